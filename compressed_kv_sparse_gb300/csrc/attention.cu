@@ -88,7 +88,10 @@ __global__ void __launch_bounds__(kThreads)
   float *mrow = ps + (size_t)HG * S;                   // [HG] running max
   float *lrow = mrow + HG;                             // [HG] running sum
   float *alpha = lrow + HG;                            // [HG] rescale of this tile
-  long long *roff = reinterpret_cast<long long *>(alpha + 2 * HG);  // [S] row offsets (-1 masked)
+  // [S] row offsets (-1 masked), on the next 8 bytes (the floats before it may be
+  // odd in number: D 192 takes tiles of 85 rows)
+  const uint32_t n_float = HG * D + S * ks_stride + HG * S + 4 * HG;
+  long long *roff = reinterpret_cast<long long *>(qs + n_float + (n_float & 1));
   __shared__ uint32_t s_nlist;
 
   const uint32_t qi = blockIdx.z, b = qi / a.T, t = qi % a.T;
