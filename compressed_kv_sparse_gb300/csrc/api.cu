@@ -5,6 +5,7 @@
 #include <cmath>
 #include <cstring>
 
+#include "fp4rows.cuh"
 #include "internal.h"
 
 using namespace ds4a;
@@ -46,11 +47,17 @@ ds4a_status check_cache(const ds4a_layer_cache *c) {
     if (c->ratio == 0 || c->max_blocks == 0 || c->n_blocks == 0) return DS4A_ERR_ARG;
     if ((uint64_t)c->max_blocks * (256u / c->ratio) != c->comp_cap) return DS4A_ERR_SHAPE;
   }
-  if (c->qat & ~(DS4A_QAT_FP8_ATTN | DS4A_QAT_FP4_INDEX)) return DS4A_ERR_ARG;
+  if (c->qat & ~(DS4A_QAT_FP8_ATTN | DS4A_QAT_FP4_INDEX | DS4A_FP4_ROWS | DS4A_Q_ROTATED))
+    return DS4A_ERR_ARG;
   if ((c->qat & DS4A_QAT_FP8_ATTN) && c->ratio == 0) return DS4A_ERR_ARG;
   if (c->qat & DS4A_QAT_FP4_INDEX) {
     if (c->ratio != 4) return DS4A_ERR_ARG;
     if (c->index_dim < 32 || (c->index_dim & (c->index_dim - 1))) return DS4A_ERR_SHAPE;
+  }
+  if (c->qat & DS4A_FP4_ROWS) {
+    if (c->ratio == 0 || (c->qat & DS4A_QAT_FP8_ATTN)) return DS4A_ERR_ARG;
+    if (ds4a_row_bytes(c->head_dim, c->n_rot, c->dtype) == 0) return DS4A_ERR_SHAPE;
+    if (reinterpret_cast<uintptr_t>(c->attn_comp_kv) % 16) return DS4A_ERR_ARG;
   }
   return DS4A_OK;
 }
@@ -71,6 +78,11 @@ RowMap index_map(const ds4a_layer_cache *c) {
 
 // c = 1/sqrt(n) rounded to fp32, the Hadamard normalisation of the FP4 round trip.
 float hadamard_scale(uint32_t n) { return (float)(1.0 / std::sqrt((double)n)); }
+
+// Bytes of a 4-bit attention row of this cache; 0: rows are in the cache's type.
+uint32_t packed_row_bytes(const ds4a_layer_cache *c) {
+  return (c->qat & DS4A_FP4_ROWS) ? (uint32_t)ds4a_row_bytes(c->head_dim, c->n_rot, c->dtype) : 0u;
+}
 
 uint32_t comp_rows(const ds4a_layer_cache *c, uint32_t n_tokens) {
   return c->ratio ? n_tokens / c->ratio : 0;
@@ -214,7 +226,8 @@ ds4a_status append_parts(ds4a_layer_cache *c, uint32_t pos0, uint32_t T, uint32_
     a.lane[a.n_lanes++] =
         LaneArgs{c->head_dim, c->n_rot, c->attn_comp_kv, c->attn_state_kv, c->attn_state_score,
                  c->rope_cos, c->rope_sin, attn_cand, attn_score, ape_attn, gamma_attn,
-                 nullptr, nullptr, (c->qat & DS4A_QAT_FP8_ATTN) ? 1u : 0u, 0.f, attn_map(c)};
+                 nullptr, nullptr, (c->qat & DS4A_QAT_FP8_ATTN) ? 1u : 0u, 0.f, attn_map(c),
+                 packed_row_bytes(c)};
   }
   if (li) {
     a.lane[a.n_lanes++] =
@@ -222,7 +235,7 @@ ds4a_status append_parts(ds4a_layer_cache *c, uint32_t pos0, uint32_t T, uint32_
                  c->index_state_score, c->index_rope_cos, c->index_rope_sin, idx_cand,
                  idx_score, ape_idx, gamma_idx, c->index_norm, c->index_norm_max,
                  (c->qat & DS4A_QAT_FP4_INDEX) ? 2u : 0u, hadamard_scale(c->index_dim),
-                 index_map(c)};
+                 index_map(c), 0u};
   }
   st = cuda_status(launch_append(a, reinterpret_cast<cudaStream_t>(stream)));
   if (st) return st;
@@ -262,15 +275,16 @@ ds4a_status ds4a_compress_append_lanes(ds4a_layer_cache *c, uint32_t pos0, uint3
 size_t ds4a_workspace_bytes(int call, const ds4a_layer_cache *c, uint32_t T, uint32_t n_heads,
                             uint32_t top_k) {
   if (!c) return 0;
+  const bool fp4 = (c->qat & DS4A_FP4_ROWS) != 0;
   switch (call) {
     case DS4A_CALL_INDEX_TOPK:
       return index_ws_bytes(c->dtype, c->batch, T, n_heads, c->index_dim, c->comp_cap);
     case DS4A_CALL_ATTN_DECODE:
       return attn_ws_bytes(c->dtype, c->ratio, c->batch, 1, n_heads, c->head_dim, c->n_rot,
-                           c->cap_raw, c->comp_cap, c->ratio == 4 ? top_k : 0);
+                           c->cap_raw, c->comp_cap, c->ratio == 4 ? top_k : 0, fp4);
     case DS4A_CALL_ATTN_PREFILL:
       return attn_ws_bytes(c->dtype, c->ratio, c->batch, T, n_heads, c->head_dim, c->n_rot,
-                           c->cap_raw, c->comp_cap, c->ratio == 4 ? top_k : 0);
+                           c->cap_raw, c->comp_cap, c->ratio == 4 ? top_k : 0, fp4);
     default:
       return 0;
   }
@@ -343,7 +357,8 @@ static ds4a_status attn_common(const ds4a_layer_cache *c, uint32_t pos0, uint32_
   if (!std::isfinite(scale)) return DS4A_ERR_ARG;
   if (c->ratio == 4 && (!topk || top_k == 0 || top_k > 2048)) return DS4A_ERR_ARG;
   const size_t need = attn_ws_bytes(c->dtype, c->ratio, c->batch, T, n_heads, c->head_dim,
-                                    c->n_rot, c->cap_raw, c->comp_cap, c->ratio == 4 ? top_k : 0);
+                                    c->n_rot, c->cap_raw, c->comp_cap, c->ratio == 4 ? top_k : 0,
+                                    (c->qat & DS4A_FP4_ROWS) != 0);
   if (need && (!ws || ws_bytes < need)) return DS4A_ERR_WORKSPACE;
   AttnArgs a;
   a.ratio = c->ratio;
@@ -371,6 +386,8 @@ static ds4a_status attn_common(const ds4a_layer_cache *c, uint32_t pos0, uint32_
   a.ws_bytes = ws_bytes;
   a.map = attn_map(c);
   a.seq_pos = c->seq_pos;
+  a.fp4 = (c->qat & DS4A_FP4_ROWS) != 0;
+  a.q_rotated = (c->qat & DS4A_Q_ROTATED) != 0;
   return cuda_status(launch_attention(a, s));
 }
 
@@ -396,7 +413,140 @@ uint32_t ds4a_decode_cluster_size(const ds4a_layer_cache *c, uint32_t n_heads, u
   // (a decode call's token is at n_tokens - 1)
   return attn_decode_cluster(c->dtype, c->ratio, c->batch, n_heads, c->head_dim, c->n_rot,
                              c->cap_raw, c->comp_cap, c->ratio == 4 ? top_k : 0,
-                             comp_rows(c, c->n_tokens), c->n_tokens);
+                             comp_rows(c, c->n_tokens), c->n_tokens,
+                             (c->qat & DS4A_FP4_ROWS) != 0);
+}
+
+size_t ds4a_row_bytes(uint32_t head_dim, uint32_t n_rot, int dtype) {
+  if (dtype != DS4A_F32 && dtype != DS4A_BF16) return 0;
+  if (head_dim == 0 || head_dim > 1024 || head_dim % 4 || n_rot % 2 || n_rot >= head_dim) return 0;
+  if ((head_dim - n_rot) % kFp4Block) return 0;
+  return fp4_layout(head_dim, n_rot, dtype == DS4A_BF16 ? 2u : 4u).row_bytes;
+}
+
+}  // extern "C"
+
+namespace {
+
+ds4a_status rows_call(bool pack, const ds4a_layer_cache *c, uint32_t n, const void *rows,
+                      const int32_t *slots, ds4a_stream_t stream) {
+  ds4a_status st = check_cache(c);
+  if (st) return st;
+  if (!(c->qat & DS4A_FP4_ROWS)) return DS4A_ERR_ARG;
+  if (n == 0) return DS4A_OK;
+  if (!rows || reinterpret_cast<uintptr_t>(rows) % (c->dtype == DS4A_BF16 ? 2 : 4))
+    return DS4A_ERR_ARG;
+  const uint64_t pool = c->block_table ? (uint64_t)c->n_blocks * (256u / c->ratio)
+                                       : (uint64_t)c->batch * c->comp_cap;
+  if (!slots && n > pool) return DS4A_ERR_CAPACITY;
+  return cuda_status(launch_rows_fp4(pack, c->dtype, c->attn_comp_kv, pool,
+                                     const_cast<void *>(rows), slots, n, c->head_dim, c->n_rot,
+                                     reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+ds4a_status ds4a_pack_rows(ds4a_layer_cache *c, uint32_t n, const void *rows,
+                           const int32_t *slots, ds4a_stream_t stream) {
+  return rows_call(true, c, n, rows, slots, stream);
+}
+
+ds4a_status ds4a_unpack_rows(const ds4a_layer_cache *c, uint32_t n, void *rows,
+                             const int32_t *slots, ds4a_stream_t stream) {
+  return rows_call(false, c, n, rows, slots, stream);
+}
+
+ds4a_status ds4a_norm_rope(ds4a_layer_cache *c, uint32_t n, const int32_t *pos, const void *q,
+                           uint64_t q_stride, uint32_t n_heads, const void *gamma_q, void *q_out,
+                           const void *kv, uint64_t kv_stride, const void *gamma_kv,
+                           void *kv_out, const int32_t *slots, uint32_t flags,
+                           ds4a_stream_t stream) {
+  ds4a_status st = check_cache(c);
+  if (st) return st;
+  if (flags & ~DS4A_NORM_ROTATE_Q) return DS4A_ERR_ARG;
+  if (n > 0x7fffffffu) return DS4A_ERR_SHAPE;
+  if ((!q && !kv) || !pos) return DS4A_ERR_ARG;
+  const uint32_t es = c->dtype == DS4A_BF16 ? 2 : 4;
+  uintptr_t ptrs = 0;
+  if (q) {
+    if (n_heads == 0 || n_heads > 128) return DS4A_ERR_SHAPE;
+    if (!q_out) return DS4A_ERR_ARG;
+    const uint64_t row = (uint64_t)n_heads * c->head_dim;
+    if (q_stride < row) return DS4A_ERR_SHAPE;
+    // in place: only where every row is written where it was read
+    if (q == q_out && q_stride != row) return DS4A_ERR_ARG;
+    ptrs |= reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(q_out) |
+            reinterpret_cast<uintptr_t>(gamma_q);
+  }
+  uint64_t n_dst = n;
+  if (kv) {
+    if (kv_stride < c->head_dim) return DS4A_ERR_SHAPE;
+    if (!kv_out && !slots) return DS4A_ERR_ARG;
+    if (kv_out && slots) return DS4A_ERR_ARG;
+    if (kv == kv_out && kv_stride != c->head_dim) return DS4A_ERR_ARG;
+    if (!kv_out) n_dst = (uint64_t)c->batch * c->cap_raw;
+    if (n_dst > 0x7fffffffu) return DS4A_ERR_SHAPE;
+    ptrs |= reinterpret_cast<uintptr_t>(kv) | reinterpret_cast<uintptr_t>(kv_out) |
+            reinterpret_cast<uintptr_t>(gamma_kv) | reinterpret_cast<uintptr_t>(c->raw_kv);
+  }
+  if (ptrs % es) return DS4A_ERR_ARG;
+  if (n == 0) return DS4A_OK;
+  NormRopeArgs a;
+  a.dtype = c->dtype;
+  a.n = n;
+  a.n_heads = n_heads;
+  a.head_dim = c->head_dim;
+  a.n_rot = c->n_rot;
+  a.rope_max_pos = c->rope_max_pos;
+  a.pos = pos;
+  a.q = q;
+  a.gamma_q = gamma_q;
+  a.kv = kv;
+  a.gamma_kv = gamma_kv;
+  a.q_out = q_out;
+  a.kv_dst = kv_out ? kv_out : c->raw_kv;
+  a.q_stride = q_stride;
+  a.kv_stride = kv_stride;
+  a.slots = kv_out ? nullptr : slots;
+  a.n_dst = (uint32_t)n_dst;
+  a.rot_q = (flags & DS4A_NORM_ROTATE_Q) != 0;
+  a.cos = c->rope_cos;
+  a.sin = c->rope_sin;
+  return cuda_status(launch_norm_rope(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+ds4a_status ds4a_block_tables(const ds4a_block_pool *p, const uint32_t *ctx_len,
+                              const uint32_t *new_len, uint32_t cap_raw,
+                              const ds4a_step_tables *out, ds4a_stream_t stream) {
+  if (!p || !out || !ctx_len || !new_len) return DS4A_ERR_ARG;
+  if (!p->table || !p->held || !p->free_list || !p->state) return DS4A_ERR_ARG;
+  if (p->rows == 0 || p->rows > DS4A_MAX_TABLE_ROWS || p->max_blocks == 0 || p->n_blocks == 0)
+    return DS4A_ERR_SHAPE;
+  // slots (blk * 64 + ..) and positions (< 256 * max_blocks) are int32
+  if (p->n_blocks > (1u << 25) || p->max_blocks > (1u << 23)) return DS4A_ERR_SHAPE;
+  if (cap_raw == 0 || cap_raw > 1024 || out->max_tokens > 0x7fffffffu) return DS4A_ERR_SHAPE;
+  TablesArgs a;
+  a.rows = p->rows;
+  a.max_blocks = p->max_blocks;
+  a.n_blocks = p->n_blocks;
+  a.cap_raw = cap_raw;
+  a.max_tokens = out->max_tokens;
+  a.ctx_len = ctx_len;
+  a.new_len = new_len;
+  a.table = p->table;
+  a.held = p->held;
+  a.free_list = p->free_list;
+  a.state = p->state;
+  a.seq_pos = out->seq_pos;
+  a.cu_len = out->cu_len;
+  a.tok_seq = out->tok_seq;
+  a.tok_pos = out->tok_pos;
+  a.raw_slot = out->raw_slot;
+  a.slot4 = out->comp_slot4;
+  a.slot128 = out->comp_slot128;
+  return cuda_status(launch_block_tables(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 ds4a_status ds4a_sparse_attn_prefill_chunk(ds4a_layer_cache *c, uint32_t pos0, uint32_t T,

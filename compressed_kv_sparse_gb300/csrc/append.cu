@@ -16,6 +16,7 @@
 // parallel, one block per row, reading window tokens from the chunk inputs or,
 // for tokens before pos0, from the state as it was before the chunk; a second
 // launch then writes the state as the token-by-token process would leave it.
+#include "fp4rows.cuh"
 #include "quant.cuh"
 #include "tc.cuh"
 
@@ -34,8 +35,9 @@ struct SlotVal {
 // Pool window slots per channel, RMS-normalise, rotate at `pos`, apply the
 // lane's step-8 round trip (if any) and store row i of the lane. get(s, c)
 // returns slot s of channel c (score without APE, -inf when empty). Called by
-// every thread of the block (uniform).
-template <typename T, typename Get>
+// every thread of the block (uniform). FP4: the attention lane's rows are held in
+// 4 bits (an instantiation of its own, so that the others carry none of it).
+template <typename T, bool FP4, typename Get>
 __device__ void pool_norm_rope_store(const LaneArgs &L, uint32_t W, uint32_t b, uint32_t i,
                                      uint32_t pos, Get get, float *red) {
   const T *ape = static_cast<const T *>(L.ape);
@@ -134,6 +136,23 @@ __device__ void pool_norm_rope_store(const LaneArgs &L, uint32_t W, uint32_t b, 
       }
     }
   }
+  if (FP4 && L.row_bytes) {   // uniform: the row is held in 4 bits
+    __shared__ float rbuf[2 * kThreads * kMaxPairsPerThread];
+#pragma unroll
+    for (int k = 0; k < kMaxPairsPerThread; ++k) {
+      const uint32_t j = threadIdx.x + k * blockDim.x;
+      if (j < npair) {
+        rbuf[2 * j] = y[k][0];
+        rbuf[2 * j + 1] = y[k][1];
+      }
+    }
+    __syncthreads();
+    if (mapped)
+      fp4_store_row<T>(rbuf, static_cast<uint8_t *>(L.comp) + prow * L.row_bytes,
+                       fp4_layout(width, L.n_rot, sizeof(T)), L.n_rot, threadIdx.x, blockDim.x);
+    __syncthreads();   // (rbuf and red are free again)
+    return;
+  }
   float st[kMaxPairsPerThread][2];   // the stored (rounded) values, for the row norm
   float mx = 0.f;
 #pragma unroll
@@ -225,7 +244,7 @@ __device__ void raw_row(const T *src, T *dst, uint32_t D, uint32_t n_rot, uint32
 // One lane's decode step in one block: store the token into its window slot
 // and, at a ratio boundary, pool, normalise, rotate and append the row, then
 // (ratio 4) move slots 4..7 to 0..3.
-template <typename T>
+template <typename T, bool FP4>
 __device__ void lane_step_block(const AppendArgs &a, const LaneArgs &L, uint32_t b, uint32_t p,
                                 float *red) {
   const uint32_t r = a.ratio, W = a.window, width = L.width;
@@ -246,7 +265,7 @@ __device__ void lane_step_block(const AppendArgs &a, const LaneArgs &L, uint32_t
   // The store above gives thread t channel t; the pool gives it channels 2t
   // and 2t + 1, written by other threads: make the stores visible first.
   __syncthreads();
-  pool_norm_rope_store<T>(L, W, b, i, i * r, get, red);
+  pool_norm_rope_store<T, FP4>(L, W, b, i, i * r, get, red);
   if (r == 4) {
     __syncthreads();  // every pool read of slots 0..3 is done
     for (uint32_t c = threadIdx.x; c < width; c += blockDim.x) {
@@ -259,7 +278,7 @@ __device__ void lane_step_block(const AppendArgs &a, const LaneArgs &L, uint32_t
   }
 }
 
-template <typename T>
+template <typename T, bool FP4>
 __global__ void __launch_bounds__(kThreads) append_step_kernel(AppendArgs a) {
   __shared__ float red[32];
   pdl_wait();
@@ -272,7 +291,7 @@ __global__ void __launch_bounds__(kThreads) append_step_kernel(AppendArgs a) {
     raw_row(src, dst, a.head_dim, a.n_rot, p, a.cos, a.sin);
     return;
   }
-  lane_step_block<T>(a, a.lane[role - 1], b, p, red);
+  lane_step_block<T, FP4>(a, a.lane[role - 1], b, p, red);
 }
 
 // Decode step on clusters of kSplit CTAs, for compressed layers whose
@@ -293,7 +312,7 @@ __global__ void __launch_bounds__(kThreads) append_step_kernel(AppendArgs a) {
 constexpr uint32_t kSplit = 8;
 constexpr uint32_t kSlotGroups = kThreads / 32;   // 8 warps x 32 channel pairs
 
-template <typename T, uint32_t W>
+template <typename T, uint32_t W, bool FP4>
 __global__ void __launch_bounds__(kThreads) append_step_split_kernel(AppendArgs a) {
   constexpr uint32_t SPT = W / kSlotGroups;   // slots per thread
   __shared__ float sm_max[kSlotGroups][64], sm_den[kSlotGroups][64], sm_num[kSlotGroups][64];
@@ -326,7 +345,7 @@ __global__ void __launch_bounds__(kThreads) append_step_split_kernel(AppendArgs 
   }
   const LaneArgs &L = a.lane[role - 1];
   if (L.norm) {   // the indexer lane: whole rows in the first CTA
-    if (rank == 0) lane_step_block<T>(a, L, b, p, red);
+    if (rank == 0) lane_step_block<T, FP4>(a, L, b, p, red);
     return;
   }
   const uint32_t r = a.ratio, width = L.width, cpc = width / kSplit;   // channels per CTA
@@ -464,6 +483,14 @@ __global__ void __launch_bounds__(kThreads) append_step_split_kernel(AppendArgs 
         v1 = quant_dequant(v1, ke, kE4M3);
       }
     }
+    if (FP4 && L.row_bytes) {   // 4 bits: 16 dims (a scale) are eight neighbouring lanes' pairs
+      float am = c < n_nope ? fp4_amax(v0, v1) : 0.f;
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) am = fp4_amax(am, __shfl_xor_sync(0xffffffffu, am, o));
+      fp4_store_pair<T>(v0, v1, c, am, static_cast<uint8_t *>(L.comp) + prow * L.row_bytes,
+                        fp4_layout(width, L.n_rot, sizeof(T)), mapped);
+      continue;
+    }
     if (mapped) {
       st_elem(row, c, v0);
       st_elem(row, c + 1, v1);
@@ -500,7 +527,7 @@ struct ChunkSlot {
 // n_emit: compressed rows per lane the grid has room for (the most any
 // sequence completes in the chunk); sequence b, whose chunk starts at p0 (its
 // own position in a ragged batch), completes (p0 + T) / r - p0 / r of them.
-template <typename T>
+template <typename T, bool FP4>
 __global__ void __launch_bounds__(kThreads)
     append_rows_kernel(AppendArgs a, uint32_t n_raw, uint32_t n_emit) {
   __shared__ float red[32];
@@ -523,7 +550,7 @@ __global__ void __launch_bounds__(kThreads)
   const uint32_t r = a.ratio, i = p0 / r + e;
   if (e >= (p0 + a.T) / r - p0 / r) return;   // (ragged: fewer rows in this sequence)
   ChunkSlot<T> get{&L, r, a.window, b, i, p0, a.T};
-  pool_norm_rope_store<T>(L, a.window, b, i, i * r, get, red);
+  pool_norm_rope_store<T, FP4>(L, a.window, b, i, i * r, get, red);
 }
 
 // State after the chunk, as the token-by-token process leaves it.
@@ -595,7 +622,7 @@ __global__ void state_reset_kernel(float *kv, float *score, size_t n) {
   }
 }
 
-template <typename T>
+template <typename T, bool FP4>
 cudaError_t launch_append_t(const AppendArgs &a, cudaStream_t s) {
   // compressed-layer decode with 512- or 1024-wide rows: one cluster per
   // (sequence, role)
@@ -617,8 +644,8 @@ cudaError_t launch_append_t(const AppendArgs &a, cudaStream_t s) {
     cfg.stream = s;
     cfg.attrs = at;
     cfg.numAttrs = 2;
-    cudaError_t e = a.ratio == 4 ? cudaLaunchKernelEx(&cfg, append_step_split_kernel<T, 8>, a)
-                                 : cudaLaunchKernelEx(&cfg, append_step_split_kernel<T, 128>, a);
+    cudaError_t e = a.ratio == 4 ? cudaLaunchKernelEx(&cfg, append_step_split_kernel<T, 8, FP4>, a)
+                                 : cudaLaunchKernelEx(&cfg, append_step_split_kernel<T, 128, FP4>, a);
     if (e != cudaSuccess) return e;
     note_launches(1);
     return cudaGetLastError();
@@ -626,7 +653,7 @@ cudaError_t launch_append_t(const AppendArgs &a, cudaStream_t s) {
   if (a.T == 1 && a.direct) {
     const uint32_t roles = (a.y0 ? 0u : 1u) + (uint32_t)a.n_lanes;
     if (!roles) return cudaSuccess;
-    cudaError_t e = launch_pdl(append_step_kernel<T>, dim3(a.batch, roles), dim3(kThreads), 0,
+    cudaError_t e = launch_pdl(append_step_kernel<T, FP4>, dim3(a.batch, roles), dim3(kThreads), 0,
                                s, a);
     if (e != cudaSuccess) return e;
     note_launches(1);
@@ -640,7 +667,7 @@ cudaError_t launch_append_t(const AppendArgs &a, cudaStream_t s) {
                                       : (a.pos0 + a.T) / a.ratio - a.pos0 / a.ratio;
   const uint32_t nblk = n_raw + n_emit * a.n_lanes;
   if (nblk) {
-    append_rows_kernel<T><<<dim3(nblk, a.batch), kThreads, 0, s>>>(a, n_raw, n_emit ? n_emit : 1);
+    append_rows_kernel<T, FP4><<<dim3(nblk, a.batch), kThreads, 0, s>>>(a, n_raw, n_emit ? n_emit : 1);
     note_launches(1);
   }
   if (a.n_lanes) {
@@ -653,7 +680,11 @@ cudaError_t launch_append_t(const AppendArgs &a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_append(const AppendArgs &a, cudaStream_t s) {
-  return a.dtype == DS4A_BF16 ? launch_append_t<__nv_bfloat16>(a, s) : launch_append_t<float>(a, s);
+  // (the attention lane, when it is part of the call, is the first one)
+  const bool fp4 = a.n_lanes && a.lane[0].row_bytes;
+  if (a.dtype == DS4A_BF16)
+    return fp4 ? launch_append_t<__nv_bfloat16, true>(a, s) : launch_append_t<__nv_bfloat16, false>(a, s);
+  return fp4 ? launch_append_t<float, true>(a, s) : launch_append_t<float, false>(a, s);
 }
 
 cudaError_t launch_state_reset(float *kv, float *score, size_t n, cudaStream_t s) {

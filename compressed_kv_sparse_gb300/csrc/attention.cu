@@ -18,6 +18,7 @@
 // also applies the inverse rotation. Prefill has one split per query and
 // finishes in place.
 #include "common.cuh"
+#include "fp4rows.cuh"
 
 namespace ds4a {
 namespace {
@@ -77,7 +78,9 @@ inline size_t smem_bytes(const Plan &pl, uint32_t D) {
           4 * pl.hg) * sizeof(float) + (size_t)pl.tile * sizeof(long long) + 16;
 }
 
-template <typename T>
+// FP4: the compressed rows are 4-bit rows (fp4rows.cuh), read back to fp32 as
+// they enter the tile. The instantiation without it is the one for rows in T.
+template <typename T, bool FP4>
 __global__ void __launch_bounds__(kThreads)
     attn_kernel(AttnArgs a, Plan pl, float *part) {
   extern __shared__ float4 smem4[];
@@ -93,6 +96,7 @@ __global__ void __launch_bounds__(kThreads)
   const uint32_t n_float = HG * D + S * ks_stride + HG * S + 4 * HG;
   long long *roff = reinterpret_cast<long long *>(qs + n_float + (n_float & 1));
   __shared__ uint32_t s_nlist;
+  const Fp4Layout L4 = FP4 ? fp4_layout(D, a.n_rot, sizeof(T)) : Fp4Layout{};
 
   const uint32_t qi = blockIdx.z, b = qi / a.T, t = qi % a.T;
   const uint32_t p = seq_base(a.seq_pos, a.pos0, b) + t;
@@ -123,7 +127,7 @@ __global__ void __launch_bounds__(kThreads)
   for (uint32_t pr = threadIdx.x; pr < HG * D / 2; pr += blockDim.x) {
     const uint32_t h = pr / (D / 2), c = 2 * (pr % (D / 2));
     float x0 = ld_f32(q, (size_t)h * D + c), x1 = ld_f32(q, (size_t)h * D + c + 1);
-    if (c >= n_nope) {
+    if (c >= n_nope && !a.q_rotated) {
       const uint32_t fi = (c - n_nope) / 2;
       const float co = a.cos[(size_t)p * (a.n_rot / 2) + fi];
       const float si = a.sin[(size_t)p * (a.n_rot / 2) + fi];
@@ -165,13 +169,42 @@ __global__ void __launch_bounds__(kThreads)
         } else {
           const uint32_t j = g - n_w;
           const int32_t idx = a.ratio == 4 ? tk[j] : (int32_t)j;
-          if (idx >= 0) off = (1ll << 61) | (long long)(a.map.row_of(b, (uint32_t)idx) * D);
+          const size_t per = FP4 ? L4.row_bytes : D;   // bytes, or elements of T
+          if (idx >= 0) off = (1ll << 61) | (long long)(a.map.row_of(b, (uint32_t)idx) * per);
         }
       }
       roff[r] = off;
     }
     __syncthreads();
-    for (uint32_t i = threadIdx.x; i < S * D; i += blockDim.x) {
+    if (FP4) {   // four dims at a time (codes and tail are both in fours)
+      for (uint32_t i = threadIdx.x; i < S * D / 4; i += blockDim.x) {
+        const uint32_t r = i / (D / 4), d = 4 * (i % (D / 4));
+        const long long off = roff[r];
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        if (off >= 0 && (off & (1ll << 61)) && !(off & (1ll << 62))) {
+          const uint8_t *row = static_cast<const uint8_t *>(a.comp) + (off & ((1ll << 61) - 1));
+          if (d < L4.nope) {
+            const uint32_t kb = d / 64;
+            float e[8];
+            fp4_decode(*reinterpret_cast<const uint32_t *>(row + fp4_word_at(kb, (d % 64) / 8)),
+                       row[fp4_scale_at(L4, kb, (d % 64) / 16)], e);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = d & 4 ? e[4 + k] : e[k];
+          } else {
+            const T *t4 = reinterpret_cast<const T *>(row + L4.tail) + (d - L4.nope);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = ld_f32(t4, k);
+          }
+        } else if (off >= 0) {
+          const T *src = off & (1ll << 62) ? chunk : ring;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[k] = ld_f32(src, (size_t)(off & ((1ll << 61) - 1)) + d + k);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) ks[(size_t)r * ks_stride + d + k] = v[k];
+      }
+    }
+    for (uint32_t i = threadIdx.x; !FP4 && i < S * D; i += blockDim.x) {
       const uint32_t r = i / D, d = i % D;
       const long long off = roff[r];
       float v = 0.f;
@@ -336,14 +369,15 @@ cudaError_t launch_attention_t(const AttnArgs &a, cudaStream_t s) {
   const Plan pl = make_plan(a.ratio, a.batch, a.T, a.n_heads, a.head_dim, a.cap_raw,
                             a.comp_cap, a.top_k);
   const size_t smem = smem_bytes(pl, a.head_dim);
-  static int smem_set = 0;
-  cudaError_t e = ensure_smem(attn_kernel<T>, smem, &smem_set);
+  static DeviceSmem smem_set[2];
+  auto *kernel = a.fp4 ? attn_kernel<T, true> : attn_kernel<T, false>;
+  cudaError_t e = ensure_smem(kernel, smem, smem_set[a.fp4].here());
   if (e != cudaSuccess) return e;
   // (the first 256 bytes: the error word of the workspace; this path has no
   // device waits and leaves it alone)
   float *part = a.ws ? reinterpret_cast<float *>(static_cast<uint8_t *>(a.ws) + 256) : nullptr;
   dim3 grid(pl.n_splits, pl.n_hg, a.batch * a.T);
-  attn_kernel<T><<<grid, kThreads, smem, s>>>(a, pl, part);
+  kernel<<<grid, kThreads, smem, s>>>(a, pl, part);
   note_launches(1);
   if (pl.n_splits > 1) {
     attn_merge_kernel<T><<<dim3(a.n_heads, a.batch * a.T), 128, 0, s>>>(a, pl, part);
@@ -368,8 +402,8 @@ cudaError_t launch_attention_tc_path(const AttnArgs &a, cudaStream_t s) {
 
 size_t attn_ws_bytes(int dtype, uint32_t ratio, uint32_t batch, uint32_t T, uint32_t n_heads,
                      uint32_t head_dim, uint32_t n_rot, uint32_t cap_raw, uint32_t comp_cap,
-                     uint32_t top_k) {
-  if (attn_tc_supported(dtype, n_heads, head_dim, n_rot))
+                     uint32_t top_k, bool fp4) {
+  if (!fp4 && attn_tc_supported(dtype, n_heads, head_dim, n_rot))
     return attn_tc_ws_bytes(batch, T, rows_max(ratio, cap_raw, comp_cap, top_k));
   const Plan pl = make_plan(ratio, batch, T, n_heads, head_dim, cap_raw, comp_cap, top_k);
   if (pl.n_splits == 1) return 0;
@@ -379,13 +413,13 @@ size_t attn_ws_bytes(int dtype, uint32_t ratio, uint32_t batch, uint32_t T, uint
 uint32_t attn_decode_cluster(int dtype, uint32_t ratio, uint32_t batch, uint32_t n_heads,
                              uint32_t head_dim, uint32_t n_rot, uint32_t cap_raw,
                              uint32_t comp_cap, uint32_t top_k, uint32_t n_comp,
-                             uint64_t pos_end) {
-  if (!attn_tc_supported(dtype, n_heads, head_dim, n_rot)) return 0;
+                             uint64_t pos_end, bool fp4) {
+  if (fp4 || !attn_tc_supported(dtype, n_heads, head_dim, n_rot)) return 0;
   return attn_tc_decode_cluster(rows_at(ratio, cap_raw, comp_cap, top_k, n_comp, pos_end), batch);
 }
 
 cudaError_t launch_attention(const AttnArgs &a, cudaStream_t s) {
-  if (attn_tc_supported(a.dtype, a.n_heads, a.head_dim, a.n_rot))
+  if (!a.fp4 && attn_tc_supported(a.dtype, a.n_heads, a.head_dim, a.n_rot))
     return launch_attention_tc_path(a, s);
   return a.dtype == DS4A_BF16 ? launch_attention_t<__nv_bfloat16>(a, s)
                               : launch_attention_t<float>(a, s);

@@ -81,6 +81,7 @@ struct TcAttnParams {
   uint32_t tma_rows;
   uint32_t n_q;       // queries = batch * T
   float c2;           // softmax scale * log2(e)
+  uint32_t q_rotated; // q is rotated already
   const __nv_bfloat16 *q, *ring, *chunk, *comp;
   const int32_t *topk;
   const float *cos, *sin;
@@ -496,6 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // rotate the tail (dims 448..511 = block 7) at position p, in place
 #pragma unroll
         for (uint32_t i = 0; i < kQC; ++i) {
+          if (P.q_rotated) break;
           const uint32_t id = lt + 128 * i, h = id >> 3, pc = id & 7;
           uint4 *ptr = reinterpret_cast<uint4 *>(S.q + 7 * QBLK + h * 128 + pc * 16);
           uint4 v = *ptr;
@@ -995,6 +997,7 @@ cudaError_t launch_attention_tc(const AttnArgs &a, uint32_t rows_max, int *err, 
   P.top_k = a.top_k;
   P.n_q = a.batch * a.T;
   P.c2 = a.scale * 1.4426950408889634f;
+  P.q_rotated = a.q_rotated ? 1u : 0u;
   P.q = static_cast<const __nv_bfloat16 *>(a.q);
   P.ring = static_cast<const __nv_bfloat16 *>(a.ring);
   P.chunk = static_cast<const __nv_bfloat16 *>(a.chunk);

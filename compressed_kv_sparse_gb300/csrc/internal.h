@@ -26,6 +26,16 @@ cudaError_t ensure_smem(F *func, size_t bytes, int *done) {
   return e;
 }
 
+// A kernel's ensure_smem record per device (the limit is set on the current one).
+struct DeviceSmem {
+  int done[64] = {};
+  int *here() {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
+    return done + dev;
+  }
+};
+
 // Launch with programmatic stream serialization (see pdl_wait in common.cuh).
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
@@ -97,6 +107,8 @@ struct LaneArgs {
   uint32_t quant;                 // step 8: 0 none, 1 FP8 non-RoPE dims, 2 FP4 QAT
   float had_c;                    // 1/sqrt(width) in fp32 (quant 2)
   RowMap map;                     // rows of comp (and norm)
+  uint32_t row_bytes;             // 0: rows of comp are `width` elements; else 4-bit rows of
+                                  // this many bytes (fp4rows.cuh)
 };
 
 struct AppendArgs {
@@ -163,10 +175,12 @@ struct AttnArgs {
   size_t ws_bytes;
   RowMap map;             // rows of comp
   const uint32_t *seq_pos;  // [B] per-sequence positions (ragged decode) or NULL
+  bool fp4;               // comp holds 4-bit rows (fp4rows.cuh)
+  bool q_rotated;         // q is rotated already
 };
 size_t attn_ws_bytes(int dtype, uint32_t ratio, uint32_t batch, uint32_t T, uint32_t n_heads,
                      uint32_t head_dim, uint32_t n_rot, uint32_t cap_raw, uint32_t comp_cap,
-                     uint32_t top_k);
+                     uint32_t top_k, bool fp4);
 cudaError_t launch_attention(const AttnArgs &a, cudaStream_t s);
 
 // Tensor-core attention (attention_tc.cu): bf16, 64 heads x 512 dims, 64-dim tail.
@@ -182,10 +196,41 @@ uint32_t attn_tc_decode_cluster(uint32_t rows_max, uint32_t n_q);
 uint32_t attn_decode_cluster(int dtype, uint32_t ratio, uint32_t batch, uint32_t n_heads,
                              uint32_t head_dim, uint32_t n_rot, uint32_t cap_raw,
                              uint32_t comp_cap, uint32_t top_k, uint32_t n_comp,
-                             uint64_t pos_end);
+                             uint64_t pos_end, bool fp4);
 cudaError_t launch_ring_commit(int dtype, uint32_t batch, uint32_t T, uint32_t pos0,
                                const uint32_t *seq_pos, uint32_t cap_raw, uint32_t head_dim,
                                const void *chunk, void *ring, cudaStream_t s);
+// Compressed rows to (pack) and from their 4-bit form; slots NULL: row i.
+cudaError_t launch_rows_fp4(bool pack, int dtype, void *packed, uint64_t n_pool, void *rows,
+                            const int32_t *slots, uint32_t n, uint32_t D, uint32_t n_rot,
+                            cudaStream_t s);
+
+struct NormRopeArgs {
+  int dtype;
+  uint32_t n, n_heads, head_dim, n_rot, rope_max_pos;
+  const int32_t *pos;             // [n]
+  const void *q, *gamma_q, *kv, *gamma_kv;
+  void *q_out, *kv_dst;           // kv_dst: n_dst rows of head_dim
+  uint64_t q_stride, kv_stride;   // elements between tokens
+  const int32_t *slots;           // [n] rows of kv_dst, or NULL: row i
+  uint32_t n_dst;
+  bool rot_q;
+  const float *cos, *sin;
+};
+cudaError_t launch_norm_rope(const NormRopeArgs &a, cudaStream_t s);
+
+struct TablesArgs {
+  uint32_t rows, max_blocks, n_blocks, cap_raw, max_tokens;
+  const uint32_t *ctx_len, *new_len;
+  int32_t *table;
+  uint32_t *held;
+  int32_t *free_list;
+  uint32_t *state;
+  uint32_t *seq_pos, *cu_len;
+  int32_t *tok_seq, *tok_pos, *raw_slot, *slot4, *slot128;
+};
+cudaError_t launch_block_tables(const TablesArgs &a, cudaStream_t s);
+
 cudaError_t launch_state_reset(float *kv, float *score, size_t n, cudaStream_t s);
 cudaError_t launch_index_norms(int dtype, const void *rows, const RowMap &map, uint32_t dim,
                                uint32_t batch, uint32_t n_rows, float *norm, uint32_t *norm_max,

@@ -51,6 +51,21 @@ class LayerCacheC(ctypes.Structure):
 
 QAT_FP8_ATTN = 1    # DS4A_QAT_FP8_ATTN
 QAT_FP4_INDEX = 2   # DS4A_QAT_FP4_INDEX
+FP4_ROWS = 0x10000  # DS4A_FP4_ROWS: attn_comp_kv holds 4-bit rows
+Q_ROTATED = 0x20000  # DS4A_Q_ROTATED: the attention's queries are rotated already
+
+
+class BlockPoolC(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_uint32), ("max_blocks", ctypes.c_uint32),
+                ("n_blocks", ctypes.c_uint32), ("table", ctypes.c_void_p),
+                ("held", ctypes.c_void_p), ("free_list", ctypes.c_void_p),
+                ("state", ctypes.c_void_p)]
+
+
+class StepTablesC(ctypes.Structure):
+    _fields_ = [("max_tokens", ctypes.c_uint32)] + [
+        (n, ctypes.c_void_p) for n in ("seq_pos", "cu_len", "tok_seq", "tok_pos", "raw_slot",
+                                       "comp_slot4", "comp_slot128")]
 
 
 EXPORTS = {
@@ -77,6 +92,16 @@ EXPORTS = {
                                                       ctypes.c_float, ctypes.c_void_p,
                                                       ctypes.c_void_p, ctypes.c_size_t,
                                                       ctypes.c_void_p]),
+    "ds4a_row_bytes": (ctypes.c_size_t, [ctypes.c_uint32, ctypes.c_uint32, ctypes.c_int]),
+    "ds4a_pack_rows": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_uint32] + [ctypes.c_void_p] * 3),
+    "ds4a_unpack_rows": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_uint32] + [ctypes.c_void_p] * 3),
+    "ds4a_norm_rope": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_uint32, ctypes.c_void_p,
+                                      ctypes.c_void_p, ctypes.c_uint64, ctypes.c_uint32,
+                                      ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                      ctypes.c_uint64, ctypes.c_void_p, ctypes.c_void_p,
+                                      ctypes.c_void_p, ctypes.c_uint32, ctypes.c_void_p]),
+    "ds4a_block_tables": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                         ctypes.c_uint32, ctypes.c_void_p, ctypes.c_void_p]),
     "ds4a_index_topk_noalloc": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_uint32, ctypes.c_uint32,
                                                ctypes.c_void_p, ctypes.c_void_p, ctypes.c_uint32,
                                                ctypes.c_uint32, ctypes.c_void_p, ctypes.c_void_p]),
@@ -181,6 +206,7 @@ class LayerCache:
             assert block_table.dtype == torch.int32 and block_table.shape[0] == batch
             assert comp_cap == block_table.shape[1] * (256 // ratio)
         rpb = 256 // ratio if ratio else 0
+        self.fp4_rows = bool(qat & FP4_ROWS)   # attn_comp_kv: 4-bit rows, as bytes
         # comp rows: [B][comp_cap][w] or a pool [n_blocks][rows per block][w]
         rows = (lambda w, r, dt=td: z(n_blocks, r, w, dt=dt)) if paged else \
                (lambda w, r, dt=td: z(batch, comp_cap, w, dt=dt))
@@ -189,7 +215,10 @@ class LayerCache:
         self.index_comp_kv = self.index_state_kv = self.index_state_score = None
         self.index_norm = self.index_norm_max = None
         if ratio:
-            self.attn_comp_kv = rows(head_dim, rpb)
+            if self.fp4_rows:
+                self.attn_comp_kv = rows(row_bytes(head_dim, n_rot, dtype), rpb, torch.uint8)
+            else:
+                self.attn_comp_kv = rows(head_dim, rpb)
             self.attn_state_kv = z(batch, W, head_dim, dt=torch.float32)
             self.attn_state_score = torch.full((batch, W, head_dim), float("-inf"),
                                                device=device)
@@ -238,6 +267,17 @@ class LayerCache:
         g = t[tb.clamp(0, self.n_blocks - 1)]              # [B][max_blocks][rpb](...)
         return g.reshape((self.batch, self.comp_cap) + tuple(t.shape[2:]))
 
+    def slots(self, n: int) -> torch.Tensor:
+        """[B][n] int32: the pool row of compressed rows 0 .. n - 1 of each sequence."""
+        dev = self.raw_kv.device
+        r = torch.arange(n, device=dev)
+        if self.block_table is None:
+            s = torch.arange(self.batch, device=dev)[:, None] * self.comp_cap + r
+        else:
+            rpb = 256 // self.ratio
+            s = self.block_table.to(dev).long()[:, r // rpb] * rpb + r % rpb
+        return s.int().contiguous()
+
     @property
     def n_tokens(self) -> int:
         return self.c.n_tokens
@@ -251,10 +291,14 @@ class LayerCache:
 
     def load_state(self, hist: Dict[str, torch.Tensor], n_tokens: int):
         """Copy a cache snapshot (same layout as the tensors here) in, set
-        n_tokens and rebuild the indexer row norms (ds4a_index_norms)."""
+        n_tokens and rebuild the indexer row norms (ds4a_index_norms). With 4-bit
+        rows, attn_comp_kv may be given as values [B][n][D]: they are packed."""
         for name, t in hist.items():
             dst = getattr(self, name)
-            if self.block_table is not None and name in ("attn_comp_kv", "index_comp_kv"):
+            if name == "attn_comp_kv" and self.fp4_rows and t.dtype != torch.uint8:
+                ds4a_pack_rows(self, t.reshape(-1, self.head_dim).to(dst.device, self.torch_dtype),
+                               self.slots(t.shape[1]).reshape(-1))
+            elif self.block_table is not None and name in ("attn_comp_kv", "index_comp_kv"):
                 rpb, nb = dst.shape[1], (t.shape[1] + dst.shape[1] - 1) // dst.shape[1]
                 src = torch.zeros((self.batch, nb * rpb) + tuple(t.shape[2:]), dtype=t.dtype,
                                   device=t.device)
@@ -316,6 +360,92 @@ def ds4a_index_topk(cache: LayerCache, pos0: int, T: int, q_idx: torch.Tensor, w
     _check(load().ds4a_index_topk(cache.ref(), pos0, T, _ptr(q_idx), _ptr(w), n_heads, top_k,
                                   _ptr(topk), _ptr(ws), ws.numel() * ws.element_size(),
                                   _stream(stream)), "ds4a_index_topk")
+
+
+def row_bytes(head_dim: int, n_rot: int, dtype: str) -> int:
+    """Bytes of a compressed row held in 4 bits (ds4a_row_bytes)."""
+    n = load().ds4a_row_bytes(head_dim, n_rot, DS4A_BF16 if dtype == "bf16" else DS4A_F32)
+    if n == 0:
+        raise Ds4aError(-2, "ds4a_row_bytes")
+    return n
+
+
+def ds4a_pack_rows(cache: LayerCache, rows: torch.Tensor, slots: Optional[torch.Tensor] = None,
+                   stream=None):
+    """rows [n][D] into the 4-bit rows `slots` (None: 0 .. n - 1) of the cache's pool."""
+    _check(load().ds4a_pack_rows(cache.ref(), rows.shape[0], _ptr(rows), _ptr(slots),
+                                 _stream(stream)), "ds4a_pack_rows")
+
+
+def ds4a_unpack_rows(cache: LayerCache, rows: torch.Tensor, slots: Optional[torch.Tensor] = None,
+                     stream=None):
+    """The values of 4-bit rows `slots` (None: 0 .. n - 1) into rows [n][D]."""
+    _check(load().ds4a_unpack_rows(cache.ref(), rows.shape[0], _ptr(rows), _ptr(slots),
+                                   _stream(stream)), "ds4a_unpack_rows")
+
+
+NORM_ROTATE_Q = 1   # DS4A_NORM_ROTATE_Q
+
+
+def ds4a_norm_rope(cache: LayerCache, pos: torch.Tensor, *, q: Optional[torch.Tensor] = None,
+                   gamma_q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                   kv: Optional[torch.Tensor] = None, gamma_kv: Optional[torch.Tensor] = None,
+                   kv_out: Optional[torch.Tensor] = None, slots: Optional[torch.Tensor] = None,
+                   rot_q: bool = False, stream=None):
+    """Norms of q [n][H][D] and kv [n][D] with the tail rotation. The tokens of q and kv
+    may be strided (a slice of one projection's output); a token's own elements
+    are contiguous. kv goes to kv_out [n][D] or, kv_out None, to rows `slots` of
+    the raw window."""
+    n, H = pos.shape[0], 0
+    if q is not None:
+        H = q.shape[1]
+        assert q.shape[0] == n and q.stride(2) == 1 and (H == 1 or q.stride(1) == q.shape[2])
+    assert kv is None or (kv.shape[0] == n and kv.stride(1) == 1)
+    _check(load().ds4a_norm_rope(
+        cache.ref(), n, _ptr(pos), None if q is None else q.data_ptr(),
+        0 if q is None else (q.stride(0) if n > 1 else H * q.shape[2]), H, _ptr(gamma_q),
+        _ptr(q_out), None if kv is None else kv.data_ptr(),
+        0 if kv is None else (kv.stride(0) if n > 1 else kv.shape[1]), _ptr(gamma_kv),
+        _ptr(kv_out), _ptr(slots), NORM_ROTATE_Q if rot_q else 0, _stream(stream)),
+        "ds4a_norm_rope")
+
+
+class BlockPool:
+    """Blocks of a paged cache and who holds them (ds4a_block_pool); all free at first."""
+
+    def __init__(self, rows: int, max_blocks: int, n_blocks: int, device="cuda"):
+        self.rows, self.max_blocks, self.n_blocks = rows, max_blocks, n_blocks
+        i32 = dict(dtype=torch.int32, device=device)
+        self.table = torch.full((rows, max_blocks), -1, **i32)
+        self.held = torch.zeros(rows, **i32)
+        self.free_list = torch.arange(n_blocks, **i32)
+        self.state = torch.tensor([0, n_blocks, 0, 0], **i32)
+        self.c = BlockPoolC(rows=rows, max_blocks=max_blocks, n_blocks=n_blocks,
+                            table=_ptr(self.table), held=_ptr(self.held),
+                            free_list=_ptr(self.free_list), state=_ptr(self.state))
+
+
+class StepTables:
+    """What ds4a_block_tables writes for a step (ds4a_step_tables)."""
+
+    def __init__(self, rows: int, max_tokens: int, device="cuda"):
+        i32 = dict(dtype=torch.int32, device=device)
+        self.rows, self.max_tokens = rows, max_tokens
+        self.seq_pos = torch.zeros(rows, **i32)
+        self.cu_len = torch.zeros(rows + 1, **i32)
+        tok = torch.full((5, max_tokens), -1, **i32)
+        self.tok_seq, self.tok_pos, self.raw_slot, self.comp_slot4, self.comp_slot128 = tok
+        self.c = StepTablesC(max_tokens=max_tokens, **{
+            n: _ptr(getattr(self, n)) for n in ("seq_pos", "cu_len", "tok_seq", "tok_pos",
+                                                "raw_slot", "comp_slot4", "comp_slot128")})
+
+
+def ds4a_block_tables(pool: BlockPool, ctx_len: torch.Tensor, new_len: torch.Tensor, cap_raw: int,
+                      step: StepTables, stream=None):
+    """Blocks for rows of ctx_len [B] tokens (the last new_len [B] of them new), int32."""
+    assert ctx_len.numel() == pool.rows == new_len.numel() == step.rows
+    _check(load().ds4a_block_tables(ctypes.byref(pool.c), _ptr(ctx_len), _ptr(new_len), cap_raw,
+                                    ctypes.byref(step.c), _stream(stream)), "ds4a_block_tables")
 
 
 STATIC_SCRATCH_BYTES = 8 << 20

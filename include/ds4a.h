@@ -10,6 +10,12 @@
  *   ds4a_sparse_attn_decode       attention of one new token per sequence
  *   ds4a_sparse_attn_prefill_chunk attention of a chunk of T tokens
  *
+ * and around them, for serving:
+ *
+ *   ds4a_block_tables             block tables, positions and slot maps of a step
+ *   ds4a_norm_rope                query-head and K = V norms, rotation, insert
+ *   ds4a_pack_rows / _unpack_rows compressed rows to and from 4 bits
+ *
  * Sources ("page §n" below): "【#3】ds4.c を読み解く" (qiita, DwarfStar series
  * part 3) and "vLLM DeepSeek V4 サポート: 効率的な長文コンテキスト注意機構"
  * (section "DeepSeek V4 アテンションアーキテクチャ").
@@ -100,6 +106,11 @@ typedef enum { DS4A_F32 = 0, DS4A_BF16 = 1 } ds4a_dtype;
  *                    compressed indexer rows, and in ds4a_index_topk the
  *                    rotated queries, take the FP4 QAT round trip. 0 = off.
  *                    Scales and arithmetic: see DS4A_QAT_FP8_ATTN below.
+ *                    Two further bits say how rows and queries are held:
+ *                    DS4A_FP4_ROWS (ratio != 0, not with DS4A_QAT_FP8_ATTN):
+ *                    attn_comp_kv holds 4-bit rows of ds4a_row_bytes bytes
+ *                    (16-byte aligned); DS4A_Q_ROTATED: the queries given to
+ *                    the attention calls are rotated already. See below.
  *  block_table       NULL: compressed rows are contiguous per sequence as laid
  *                    out above. Non-NULL (ratio != 0): a paged cache (vLLM's
  *                    page: one logical block = 256 token positions on every
@@ -172,6 +183,40 @@ typedef struct {
  */
 #define DS4A_QAT_FP8_ATTN 1u
 #define DS4A_QAT_FP4_INDEX 2u
+
+/*
+ * Compressed attention rows held in 4 bits. With DS4A_FP4_ROWS the compressor
+ * writes, and the attention calls read, rows of ds4a_row_bytes(head_dim, n_rot,
+ * dtype) bytes in place of head_dim elements: attn_comp_kv is then
+ * [B][comp_cap][row_bytes] or, paged, [n_blocks][256/ratio][row_bytes]. The
+ * raw window, the indexer rows and every other call are as without it. The
+ * leading nope = head_dim - n_rot dims (a multiple of 16, > 0) are E2M1 codes
+ * with one scale 2^k per 16 dims, k the smallest integer >= -127 such that
+ * amax <= 6 * 2^k; a value is the nearest E2M1 value times 2^k, ties to the even
+ * code (a block with amax > 1.5 * 2^127 tops out at 1.5 * 2^127, a block that
+ * holds an infinity or a NaN reads back as NaN). The rotated dims keep the
+ * cache's dtype. The fp32 row (after RMSNorm and tail RoPE) is what is rounded.
+ * For head_dim 512, n_rot 64, bf16 a row is 384 bytes against 1024.
+ *
+ * Bytes of a row, with nb = ceil(nope / 64), ns = ceil(nb / 8), R = nb + ns
+ * rounded up to a multiple of 4: lane j (0..7) owns dims 64 kb + 8 j + i (i < 8) as
+ * 32-bit word kb; words nb .. nb + ns - 1 hold scale bytes k + 127 (255: NaN): lanes
+ * 2 q and 2 q + 1 share those of dims 64 kb + 16 q .., the byte of block kb being
+ * byte kb % 4 of word nb + (kb % (4 ns)) / 4 of lane 2 q + kb / (4 ns). Word w of lane j is
+ * at byte 128 (w / 4) + 16 j + 4 (w % 4), little endian. In a code word dim i is
+ * in half-word i % 2 with its sign at bit {15, 12, 14, 13}[i / 2] of it and its
+ * magnitude code at bits {6, 3, 0, 9}[i / 2] and up. The n_rot rotated dims
+ * follow at byte 32 R; the row is padded to a multiple of 32 bytes.
+ *
+ * DS4A_Q_ROTATED: the attention calls take q as ds4a_norm_rope leaves it with
+ * DS4A_NORM_ROTATE_Q (rounded to dtype once, after the rotation) and do not
+ * rotate it; the output is rotated back as before.
+ */
+#define DS4A_FP4_ROWS 0x10000u
+#define DS4A_Q_ROTATED 0x20000u
+
+/* Bytes of one 4-bit compressed row (0: sizes or dtype not supported). */
+size_t ds4a_row_bytes(uint32_t head_dim, uint32_t n_rot, int dtype);
 
 /* Workspace selectors for ds4a_workspace_bytes. */
 enum { DS4A_CALL_APPEND = 0, DS4A_CALL_INDEX_TOPK = 1, DS4A_CALL_ATTN_DECODE = 2,
@@ -319,6 +364,116 @@ ds4a_status ds4a_sparse_attn_prefill_chunk(ds4a_layer_cache *cache, uint32_t pos
                                            const void *raw_chunk, const int32_t *topk,
                                            uint32_t top_k, float scale, void *out, void *ws,
                                            size_t ws_bytes, ds4a_stream_t stream);
+
+/*
+ * Compressed rows into and out of a cache with DS4A_FP4_ROWS (a restored prefix,
+ * a row computed elsewhere).
+ *
+ *  rows  [n][head_dim] (dtype)
+ *  slots [n] int32 DEVICE: row slots[i] of the pool (b * comp_cap + r, or paged
+ *        block * 256/ratio + r); entries outside the pool are skipped (unpack
+ *        leaves rows[i] as it was). NULL: row i. ds4a_pack_rows needs distinct
+ *        slots: of two rows for one slot either one, or a mix of both, remains.
+ * n = 0 does nothing. Neither changes n_tokens. Errors: DS4A_ERR_ARG (no
+ * DS4A_FP4_ROWS, a missing or misaligned pointer), DS4A_ERR_CAPACITY (no slots and n
+ * beyond the pool), DS4A_ERR_CUDA.
+ */
+ds4a_status ds4a_pack_rows(ds4a_layer_cache *cache, uint32_t n, const void *rows,
+                           const int32_t *slots, ds4a_stream_t stream);
+ds4a_status ds4a_unpack_rows(const ds4a_layer_cache *cache, uint32_t n, void *rows,
+                             const int32_t *slots, ds4a_stream_t stream);
+
+/*
+ * Norms of n tokens' query heads and K = V rows with the tail rotation in the
+ * same pass (vLLM page, "GPU 計算飽和": fused Q norm + KV RoPE + K insert):
+ *   y = x / sqrt(mean(x^2) + 1e-6) * gamma over the head_dim dims of a row, then
+ *   the tail rotated at the token's position; fp32 throughout, rounded once.
+ *
+ *  pos      [n] int32 DEVICE: position of each token; a token whose position is
+ *           negative or >= rope_max_pos is skipped (its outputs stay as they were)
+ *  q        [n][H][D] (dtype), q_stride elements from token to token (>= H * D;
+ *           the heads of a token are contiguous); NULL: no queries
+ *  gamma_q  [D] (dtype) or NULL: no gain
+ *  q_out    [n][H][D], contiguous; may be q itself when q_stride == H * D
+ *  kv       [n][D] (dtype), kv_stride elements from token to token; NULL: none
+ *  gamma_kv [D] or NULL
+ *  kv_out   [n][D]: the rows, token by token (raw_chunk of a prefill); may be kv
+ *           itself when kv_stride == D. NULL: each row goes to row slots[i] of
+ *           the raw window raw_kv (b * cap_raw + p % cap_raw for sequence b).
+ *  slots    [n] int32 DEVICE, with kv_out NULL only; a slot outside
+ *           [0, B * cap_raw) drops the row. Slots must be distinct.
+ *  flags    DS4A_NORM_ROTATE_Q: rotate the queries too (the attention of a cache
+ *           with DS4A_Q_ROTATED); 0: norm only (it rotates them itself).
+ *
+ * Replaces DS4A_LANE_RAW of the append; n_tokens is left for the append of the
+ * other lanes, or for the caller (ds4a_compress_append_lanes). Errors:
+ * DS4A_ERR_ARG (nothing to do, a missing or misaligned pointer, kv_out and slots
+ * both given or neither, an overlapping in-place call), DS4A_ERR_SHAPE (strides, n_heads,
+ * sizes), DS4A_ERR_CUDA.
+ */
+#define DS4A_NORM_ROTATE_Q 1u
+ds4a_status ds4a_norm_rope(ds4a_layer_cache *cache, uint32_t n, const int32_t *pos, const void *q,
+                           uint64_t q_stride, uint32_t n_heads, const void *gamma_q, void *q_out,
+                           const void *kv, uint64_t kv_stride, const void *gamma_kv,
+                           void *kv_out, const int32_t *slots, uint32_t flags,
+                           ds4a_stream_t stream);
+
+/*
+ * Block tables, positions and slot maps of a step, from the requests' lengths,
+ * on the GPU (vLLM page: logical blocks of 256 token positions).
+ *
+ * ds4a_block_pool: the blocks of a paged cache and who holds them (DEVICE arrays).
+ *  rows        B, at most DS4A_MAX_TABLE_ROWS
+ *  max_blocks  logical blocks per row (<= 2^23)
+ *  n_blocks    physical blocks of the pool (<= 2^25)
+ *  table       [B][max_blocks] int32: the block_table of the layers' caches
+ *  held        [B] uint32: blocks each row holds (table entries 0 .. held - 1)
+ *  free_list   [n_blocks] int32: a ring of free block numbers
+ *  state       [4] uint32: 0 the ring's head, 1 how many blocks are free, 2 (out)
+ *              blocks that the last call could not supply, 3 zero between calls.
+ * A new pool: held 0, free_list = all blocks, state = {0, n_blocks, 0, 0}.
+ *
+ * ds4a_step_tables: what a step needs (DEVICE arrays, each may be NULL).
+ *  max_tokens  entries of the four token arrays; tokens beyond it get none
+ *  seq_pos     [B] position of each row's first new token (a cache's seq_pos)
+ *  cu_len      [B + 1] new tokens of the rows before each row; the total last
+ *  tok_seq, tok_pos  [max_tokens] row and position of each packed token
+ *  raw_slot    its row in raw_kv, b * cap_raw + p % cap_raw; -1 when a later
+ *              token of the same row takes that slot
+ *  comp_slot4, comp_slot128  the row of a ratio-4 / ratio-128 pool that the token
+ *              completes (block * 64 + .., block * 2 + ..), -1 when it completes none
+ *  Entries behind the last token are -1.
+ *
+ * ds4a_block_tables: row b is to hold ctx_len[b] tokens (0: the row is free) of
+ * which the last min(new_len[b], ctx_len[b]) are new. It takes blocks from the
+ * ring's head until it holds ceil(ctx_len / 256) of them (at most max_blocks), in
+ * the order of the rows, or gives the surplus back to the ring's tail (available
+ * from the next call on), table entries of blocks given back becoming -1. Where the ring
+ * runs out the entries are -1 (rows there are not written by the append), held counts
+ * what was supplied, and the next call asks again. Every other table entry is left as it
+ * was. A row whose blocks other rows share must not shrink below the shared part.
+ * The result depends on the inputs alone. Calls on one pool must be ordered (they
+ * change it), captured ones too. The lengths' sum must be below 2^31.
+ * Errors: DS4A_ERR_ARG (a missing pointer), DS4A_ERR_SHAPE (sizes), DS4A_ERR_CUDA.
+ */
+#define DS4A_MAX_TABLE_ROWS 8192u
+typedef struct {
+  uint32_t rows, max_blocks, n_blocks;
+  int32_t *table;
+  uint32_t *held;
+  int32_t *free_list;
+  uint32_t *state;
+} ds4a_block_pool;
+
+typedef struct {
+  uint32_t max_tokens;
+  uint32_t *seq_pos, *cu_len;
+  int32_t *tok_seq, *tok_pos, *raw_slot, *comp_slot4, *comp_slot128;
+} ds4a_step_tables;
+
+ds4a_status ds4a_block_tables(const ds4a_block_pool *pool, const uint32_t *ctx_len,
+                              const uint32_t *new_len, uint32_t cap_raw,
+                              const ds4a_step_tables *step, ds4a_stream_t stream);
 
 /*
  * ds4a_index_topk for callers that cannot allocate device memory (the pages
