@@ -403,8 +403,8 @@ cudaError_t launch_attention_tc_path(const AttnArgs &a, cudaStream_t s) {
 size_t attn_ws_bytes(int dtype, uint32_t ratio, uint32_t batch, uint32_t T, uint32_t n_heads,
                      uint32_t head_dim, uint32_t n_rot, uint32_t cap_raw, uint32_t comp_cap,
                      uint32_t top_k, bool fp4) {
-  if (!fp4 && attn_tc_supported(dtype, n_heads, head_dim, n_rot))
-    return attn_tc_ws_bytes(batch, T, rows_max(ratio, cap_raw, comp_cap, top_k));
+  if (attn_tc_supported(dtype, n_heads, head_dim, n_rot, fp4))
+    return attn_tc_ws_bytes(batch, T, rows_max(ratio, cap_raw, comp_cap, top_k), n_heads);
   const Plan pl = make_plan(ratio, batch, T, n_heads, head_dim, cap_raw, comp_cap, top_k);
   if (pl.n_splits == 1) return 0;
   return 256 + (size_t)batch * T * pl.n_splits * n_heads * (head_dim + 2) * sizeof(float);
@@ -414,12 +414,13 @@ uint32_t attn_decode_cluster(int dtype, uint32_t ratio, uint32_t batch, uint32_t
                              uint32_t head_dim, uint32_t n_rot, uint32_t cap_raw,
                              uint32_t comp_cap, uint32_t top_k, uint32_t n_comp,
                              uint64_t pos_end, bool fp4) {
-  if (fp4 || !attn_tc_supported(dtype, n_heads, head_dim, n_rot)) return 0;
-  return attn_tc_decode_cluster(rows_at(ratio, cap_raw, comp_cap, top_k, n_comp, pos_end), batch);
+  if (!attn_tc_supported(dtype, n_heads, head_dim, n_rot, fp4)) return 0;
+  return attn_tc_decode_cluster(rows_at(ratio, cap_raw, comp_cap, top_k, n_comp, pos_end), batch,
+                                n_heads);
 }
 
 cudaError_t launch_attention(const AttnArgs &a, cudaStream_t s) {
-  if (!a.fp4 && attn_tc_supported(a.dtype, a.n_heads, a.head_dim, a.n_rot))
+  if (attn_tc_supported(a.dtype, a.n_heads, a.head_dim, a.n_rot, a.fp4))
     return launch_attention_tc_path(a, s);
   return a.dtype == DS4A_BF16 ? launch_attention_t<__nv_bfloat16>(a, s)
                               : launch_attention_t<float>(a, s);

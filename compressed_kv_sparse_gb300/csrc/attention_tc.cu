@@ -45,8 +45,10 @@
 #include <cuda_bf16.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "common.cuh"
+#include "fp4rows.cuh"
 #include "tc.cuh"
 
 namespace ds4a {
@@ -56,15 +58,24 @@ constexpr int kH = 64, kD = 512, kNope = 448, kRows = 128;
 constexpr int kQBlk = kH * 128;        // one 64-dim block of Q: 64 heads x 128 B
 // Heads per CTA: decode splits a query's 64 heads over two clusters (every
 // rank reads the same rows for half the heads); prefill keeps all 64.
-template <bool DEC>
+template <int NH_>
 struct Heads {
-  static constexpr int NH = DEC ? 32 : 64;   // heads of this CTA
+  static constexpr int NH = NH_;             // heads of this CTA
   static constexpr int HG = kH / NH;         // head groups per query
   static constexpr int NHF = NH / 32;        // 32-column halves of the S accumulator
   static constexpr int QBLK = NH * 128;      // one 64-dim block of this CTA's Q
 };
 constexpr int kKBlk = kRows * 128;     // one 64-dim block of the row tile
-constexpr int kThreads = 288;
+// Warps: 0-3 softmax and epilogue, then the loaders, then the MMA issuer. 4-bit
+// rows take eight loader warps: they convert every element of a tile.
+template <bool FP4>
+struct Warps {
+  static constexpr uint32_t NL = FP4 ? 8 : 4;          // loader warps
+  static constexpr uint32_t LT = 32 * NL;              // loader threads
+  static constexpr uint32_t MMA = 4 + NL;              // the MMA issuer's warp
+  static constexpr uint32_t THREADS = 32 * (MMA + 1);  // 288 or 416
+};
+constexpr int kNhDec = 32;             // heads per CTA in decode
 constexpr uint32_t kMaxCluster = 16;   // cluster size; beyond 8 (the portable limit) when the
                                        // device allows non-portable sizes
 constexpr float kRaiseLog2 = 8.0f;     // raise the running max beyond 2^8
@@ -82,7 +93,8 @@ struct TcAttnParams {
   uint32_t n_q;       // queries = batch * T
   float c2;           // softmax scale * log2(e)
   uint32_t q_rotated; // q is rotated already
-  const __nv_bfloat16 *q, *ring, *chunk, *comp;
+  uint32_t n_heads, hg;   // 4-bit rows: heads of a query (1 .. 128), head groups of a query
+  const __nv_bfloat16 *q, *ring, *chunk, *comp;   // (comp: bytes of 4-bit rows where FP4)
   const int32_t *topk;
   const float *cos, *sin;
   __nv_bfloat16 *out;
@@ -225,10 +237,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // weights 2^(m_j - M) / sum_j 2^(m_j - M) l_j. A rank without rows left
 // m = -inf and zeros; one with only masked rows left m = -inf and O = 0.
 // CM: compile-time bound on the cluster size C (the loops over ranks unroll)
-template <uint32_t CM, int NH>
+template <uint32_t CM, int NH, bool FP4>
 __device__ __forceinline__ bool merge_heads(const TcAttnParams &P, Smem &S, uint32_t vq,
                                             uint32_t rank, uint32_t C, ErrWord ew) {
-  const uint32_t t = threadIdx.x, qi = vq / (kH / NH), hq0 = (vq % (kH / NH)) * NH;
+  const uint32_t HG = FP4 ? P.hg : (uint32_t)(kH / NH), HQ = FP4 ? P.n_heads : (uint32_t)kH;
+  const uint32_t t = threadIdx.x, qi = vq / HG, hq0 = (vq % HG) * NH;
   const uint32_t h0 = rank * NH / C, h1 = (rank + 1) * NH / C, nh = h1 - h0;
   const __nv_bfloat16 *part = P.part + (size_t)vq * C * NH * kD;
   const float *ml = P.ml + (size_t)vq * C * NH * 2;
@@ -292,16 +305,54 @@ __device__ __forceinline__ bool merge_heads(const TcAttnParams &P, Smem &S, uint
     // rotate back by -p: (x0, x1) -> (x0 c + x1 s, -x0 s + x1 c)
     const float r0 = a0 * co0 + a1 * si0, r1 = -a0 * si0 + a1 * co0;
     const float r2 = a2 * co1 + a3 * si1, r3 = -a2 * si1 + a3 * co1;
-    *reinterpret_cast<uint2 *>(P.out + ((size_t)qi * kH + hq0 + h0 + i) * kD + d) =
-        make_uint2(pack_bf16(r0, r1), pack_bf16(r2, r3));
+    if (!FP4 || hq0 + h0 + i < HQ)   // (a last group of heads may be part-filled)
+      *reinterpret_cast<uint2 *>(P.out + ((size_t)qi * HQ + hq0 + h0 + i) * kD + d) =
+          make_uint2(pack_bf16(r0, r1), pack_bf16(r2, r3));
   }
   return true;
 }
 
+// One query row of the tile from its 4-bit form (rec: this lane's 32-byte record,
+// tail: its 16 bytes of rotated dims) into 64-dim blocks kb0, kb0 + 1 of the tile, as
+// 16-byte chunk `at` of each. sl, sh: the scale bytes of blocks 0 .. 3 and 4 .. 6.
+// E2M1 times 2^-126 (fp4_pair_raw) becomes the bf16 value by one exact product with
+// 2^(k + 126), a bf16 number while k <= 1 (byte <= 128: largest magnitude up to 12);
+// `wide`: the row has a larger scale and takes two products.
+template <uint32_t KB>
+__device__ __forceinline__ uint4 fp4_chunk(uint32_t w, uint32_t sl, uint32_t sh, bool wide) {
+  const uint32_t byte = ((KB < 4 ? sl : sh) >> (8 * (KB % 4))) & 255u;
+  uint32_t o[4] = {fp4_pair_raw<0>(w), fp4_pair_raw<1>(w), fp4_pair_raw<2>(w), fp4_pair_raw<3>(w)};
+  uint32_t m = byte * 0x00800080u + 0x3F003F00u;   // 2^(k + 126), twice
+  if (wide) {
+    const uint32_t up = 0x7E807E80u;               // 2^126, twice
+    m = byte ? byte * 0x00800080u : 0x00400040u;   // 2^k
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&o[i]),
+                                       *reinterpret_cast<const __nv_bfloat162 *>(&up));
+      o[i] = *reinterpret_cast<const uint32_t *>(&v);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&o[i]),
+                                     *reinterpret_cast<const __nv_bfloat162 *>(&m));
+    o[i] = *reinterpret_cast<const uint32_t *>(&v);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+// A scale byte above 128 among the four of a word.
+__device__ __forceinline__ uint32_t fp4_wide(uint32_t s) {
+  return ((s & 0x7F7F7F7Fu) + 0x7F7F7F7Fu) & s & 0x80808080u;
+}
+constexpr uint32_t kFp4RowBytes = 384;   // D 512, n_rot 64, bf16
+
 // DEC: decode (clusters of P.cluster CTAs per query) or prefill (persistent
-// CTAs); two instantiations keep each path's code to itself
-template <bool DEC, bool PAGED>
-__global__ void __launch_bounds__(kThreads, 1)
+// CTAs); PAGED: rows through the block table (4-bit rows look at it at run time);
+// FP4: compressed rows in 4 bits; NH: heads per CTA. Instantiations keep each path's
+// code to itself.
+template <bool DEC, bool PAGED, bool FP4, int NH>
+__global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                    const __grid_constant__ CUtensorMap tmap_ring,
                    const __grid_constant__ CUtensorMap tmap_comp, TcAttnParams P) {
@@ -322,14 +373,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   // decode: cluster of C CTAs per (query, head group), rank c takes tiles
   // c, c + C, ...; prefill: one whole query at a time per CTA
   constexpr bool dec = DEC;
-  using HS = Heads<DEC>;
-  constexpr int NH = HS::NH, NHF = HS::NHF, QBLK = HS::QBLK;
+  using HS = Heads<NH>;
+  using WP = Warps<FP4>;
+  constexpr int NHF = HS::NHF, QBLK = HS::QBLK;
+  // head groups of a query and its heads; 4-bit rows take any number of heads
+  const uint32_t HG = FP4 ? P.hg : (uint32_t)HS::HG, HQ = FP4 ? P.n_heads : (uint32_t)kH;
+  constexpr bool kScan = !DEC || FP4;   // read the list for its end (see query_geo)
   const uint32_t C = dec ? P.cluster : 1u;
   const uint32_t rank = dec ? cluster_ctarank() : 0u;
   const uint32_t vq = dec ? blockIdx.x / C : 0u;          // decode: (query, head group)
-  const uint32_t hq0 = dec ? (vq % HS::HG) * NH : 0u;     // first head of this CTA
-  const uint32_t q_first = dec ? vq / HS::HG : blockIdx.x;
-  const uint32_t q_step = dec ? P.n_q : gridDim.x;
+  // items (query, head group) i0, i0 + i_step, ... < n_items: one in decode; prefill
+  // of bf16 rows has one group, so that an item is a query
+  const uint32_t n_items = FP4 ? P.n_q * P.hg : dec ? P.n_q * HS::HG : P.n_q;
+  const uint32_t i0 = dec ? vq : blockIdx.x, i_step = dec ? n_items : gridDim.x;
+  auto item_q = [&](uint32_t it) { return FP4 || dec ? it / HG : it; };
+  auto item_h = [&](uint32_t it) { return FP4 || dec ? (it % HG) * NH : 0u; };   // first head
   const int err_base = *(volatile int *)P.err;
   if (NH < kH) {
     // heads NH .. 63 of every P row stay zero: the PV and sum MMAs read all
@@ -341,9 +399,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   if (threadIdx.x == 0) {
-    mbar_init(&S.kv_full, 128);
+    mbar_init(&S.kv_full, WP::LT);
     for (int i = 0; i < 4; ++i) mbar_init(&S.kv_empty[i], 1);
-    mbar_init(&S.q_full, 128);
+    mbar_init(&S.q_full, WP::LT);
     mbar_init(&S.q_empty, 1);
     mbar_init(&S.s_full, 1);
     mbar_init(&S.p_full, 128);
@@ -362,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       prefetch_tmap(&tmap_comp);
     }
   }
-  if (warp == 8) tmem_alloc(&S.tmem, 512);
+  if (warp == WP::MMA) tmem_alloc(&S.tmem, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -382,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   // the loaders wait for the previous launch themselves, after they have
   // started the first query's Q load
-  const bool loader = warp >= 4 && warp < 8;
+  const bool loader = warp >= 4 && warp < WP::MMA;
   if (!loader) {
     pdl_wait();
     pdl_trigger();
@@ -391,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // so that its latency overlaps the previous launch
   const ErrWord ew{P.err, err_base};
 
-  if (warp >= 4 && warp < 8) {
+  if (warp >= 4 && warp < WP::MMA) {
     // ------------------------------------------------------------ loaders
     const uint32_t lt = threadIdx.x - 128, lw = warp - 4;
     uint32_t n = 0, qn = 0, qt = 0, nk = 0;   // qt: Q loads issued, nk: TMA tiles issued
@@ -433,21 +491,111 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return true;
     };
+    // ---- 4-bit rows: thread lt holds lane lt % 8 of rows lt / 8 + 32 i. fetch_tile
+    // loads their records into registers (12 16-byte loads in flight, each warp
+    // load 128 contiguous bytes of four rows); store_tile converts them block pair by
+    // block pair as the tile's slots free up. The next tile's records load while
+    // this one's MMAs run.
+    constexpr uint32_t kFR = FP4 ? kRows * 8 / WP::LT : 1;   // rows per thread
+    uint4 rec[kFR][3];
+    const __nv_bfloat16 *fsrc[kFR];   // a row in bf16 (the window), or NULL
+    uint32_t fpk = 0;                 // bit i: row i is in 4 bits
+    auto fetch_tile = [&](const QueryGeo &g, uint32_t tile) {
+      const uint32_t j = lt & 7;
+      fpk = 0;
+#pragma unroll
+      for (uint32_t i = 0; i < kFR; ++i) {
+        const uint32_t r = tile * kRows + (lt >> 3) + 32 * i;
+        fsrc[i] = nullptr;
+        if (r < g.n_w) {
+          fsrc[i] = row_src<false>(P, g, r);
+        } else if (r < g.N) {
+          const uint32_t e = r - g.n_w;
+          const int32_t idx = P.ratio == 4 ? g.tk[e] : (int32_t)e;
+          if (idx >= 0) {
+            const uint4 *src = reinterpret_cast<const uint4 *>(
+                reinterpret_cast<const uint8_t *>(P.comp) +
+                P.map.row_of(g.b, (uint32_t)idx) * kFp4RowBytes) + j;
+            fpk |= 1u << i;
+#pragma unroll
+            for (uint32_t v = 0; v < 3; ++v) rec[i][v] = __ldg(src + 8 * v);
+          }
+        }
+      }
+    };
+    auto store_tile = [&](const QueryGeo &g, uint32_t tile, uint32_t n) -> bool {
+      if (tile_kind<DEC, true>(P, g, tile)) {   // the whole window ring by TMA
+        for (uint32_t kb = 0; kb < 8; ++kb) {
+          if ((kb & 1) == 0 && !mbar_wait_warp(&S.kv_empty[kb >> 1], (n & 1) ^ 1, ew)) return false;
+          if (lt == 0) {
+            if (kb == 0) mbar_arrive_expect_tx(&S.kv_tma, 8 * kKBlk);
+            tma_load_3d(S.kv + kb * kKBlk, &tmap_ring, &S.kv_tma, (int)(64 * kb), 0, (int)g.b);
+          }
+        }
+        return true;
+      }
+      const uint32_t j = lt & 7, r0 = lt >> 3;
+      uint32_t sl[kFR], sh[kFR], wide = 0;
+#pragma unroll
+      for (uint32_t i = 0; i < kFR; ++i) {   // a pair of lanes shares its scale bytes
+        const uint32_t mine = rec[i][1].w, other = __shfl_xor_sync(0xffffffffu, mine, 1);
+        sl[i] = j & 1 ? other : mine;
+        sh[i] = j & 1 ? mine : other;
+        if (fp4_wide(sl[i]) | fp4_wide(sh[i])) wide |= 1u << i;
+      }
+      auto block = [&](auto kb_c) -> bool {
+        constexpr uint32_t KB = decltype(kb_c)::value;
+        if ((KB & 1) == 0 && !mbar_wait_warp(&S.kv_empty[KB >> 1], (n & 1) ^ 1, ew)) return false;
+#pragma unroll
+        for (uint32_t i = 0; i < kFR; ++i) {
+          const uint32_t r = r0 + 32 * i;
+          uint8_t *dst = S.kv + KB * kKBlk + (r >> 3) * 1024 + (r & 7) * 128 + ((j ^ (r & 7)) << 4);
+          if ((fpk >> i) & 1) {
+            const uint4 a = rec[i][0], c = rec[i][1];
+            if (KB == 7)
+              *reinterpret_cast<uint4 *>(dst) = rec[i][2];
+            else
+              *reinterpret_cast<uint4 *>(dst) =
+                  fp4_chunk<KB>(KB == 0   ? a.x
+                                : KB == 1 ? a.y
+                                : KB == 2 ? a.z
+                                : KB == 3 ? a.w
+                                : KB == 4 ? c.x
+                                : KB == 5 ? c.y
+                                          : c.z,
+                                sl[i], sh[i], (wide >> i) & 1);
+          } else {
+            cp_async16(dst, fsrc[i] ? fsrc[i] + KB * 64 + j * 8 : P.ring, fsrc[i] ? 16u : 0u);
+          }
+        }
+        return true;
+      };
+      using std::integral_constant;
+      return block(integral_constant<uint32_t, 0>{}) && block(integral_constant<uint32_t, 1>{}) &&
+             block(integral_constant<uint32_t, 2>{}) && block(integral_constant<uint32_t, 3>{}) &&
+             block(integral_constant<uint32_t, 4>{}) && block(integral_constant<uint32_t, 5>{}) &&
+             block(integral_constant<uint32_t, 6>{}) && block(integral_constant<uint32_t, 7>{});
+    };
     // Q (it needs no list): eight TMA boxes of 64 heads x 64 dims, in the
     // 128-byte swizzled K-major layout the S MMAs read. The first query's
     // is issued before the wait for the previous launch: the queries are the
     // caller's input, written before that launch began (as are the rotation
     // tables), while the top-k lists and the new raw row are not.
-    auto issue_q = [&](uint32_t qi) {
+    auto issue_q = [&](uint32_t it) {
       if (lt == 0) {
+        const uint32_t qi = item_q(it), hq0 = item_h(it);
         mbar_arrive_expect_tx(&S.q_tma, 8 * QBLK);
 #pragma unroll
-        for (uint32_t kb = 0; kb < 8; ++kb)
-          tma_load_2d(S.q + kb * QBLK, &tmap_q, &S.q_tma, (int)(64 * kb), (int)(qi * kH + hq0));
+        for (uint32_t kb = 0; kb < 8; ++kb) {
+          if (FP4)   // (heads past the last one read as zeros)
+            tma_load_3d(S.q + kb * QBLK, &tmap_q, &S.q_tma, (int)(64 * kb), (int)hq0, (int)qi);
+          else
+            tma_load_2d(S.q + kb * QBLK, &tmap_q, &S.q_tma, (int)(64 * kb), (int)(qi * kH + hq0));
+        }
       }
     };
-    const bool q_early = q_first < P.n_q && rank * kRows < rows_bound(P, q_first);
-    if (q_early) issue_q(q_first);
+    const bool q_early = i0 < n_items && rank * kRows < rows_bound(P, item_q(i0));
+    if (q_early) issue_q(i0);
     // The loaders' own wait for the previous launch. Decode reads nothing of
     // it before the first rows (the rotation coefficients are inputs and a
     // decode list is not scanned), so its first query's coefficients and
@@ -461,28 +609,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         waited = true;
       }
     };
-    if (!DEC) wait_prev();
-    for (uint32_t qi = q_first; qi < P.n_q; qi += q_step) {
+    if (kScan) wait_prev();
+    for (uint32_t it = i0; it < n_items; it += i_step) {
+      const uint32_t qi = item_q(it);
       if (rank * kRows >= rows_bound(P, qi)) continue;   // no rows for this rank
       if (!mbar_wait_warp(&S.q_empty, (qn & 1) ^ 1, ew)) goto done_loader;
-      if (!(q_early && qi == q_first)) issue_q(qi);
+      if (!(q_early && it == i0)) issue_q(it);
       {
-        // this thread's 16-byte chunks of the tail: chunk lt (+ 128 i) of
+        // this thread's 16-byte chunks of the tail: chunk lt (+ LT i) of
         // block 7 hold pairs 4 lc .. 4 lc + 3 of head id / 8; their
         // coefficients load while the list is read
         const uint32_t pq = seq_base(P.seq_pos, P.pos0, qi / P.T) + qi % P.T;
-        constexpr uint32_t kQC = NH / 16;   // tail chunks per loader thread
+        constexpr uint32_t kQC = NH * 8 / WP::LT;   // tail chunks per loader thread
         float co[4 * kQC], si[4 * kQC];
 #pragma unroll
         for (uint32_t i = 0; i < kQC; ++i) {
-          const uint32_t id = lt + 128 * i, h = id >> 3, lc = (id & 7) ^ (h & 7);
+          const uint32_t id = lt + WP::LT * i, h = id >> 3, lc = (id & 7) ^ (h & 7);
 #pragma unroll
           for (uint32_t e = 0; e < 4; ++e) {
             co[4 * i + e] = P.cos[(size_t)pq * 32 + 4 * lc + e];
             si[4 * i + e] = P.sin[(size_t)pq * 32 + 4 * lc + e];
           }
         }
-        const QueryGeo g = query_geo<!DEC>(P, qi, rank, C, lane);
+        const QueryGeo g = query_geo<kScan>(P, qi, rank, C, lane);
         if (g.t0 >= g.t1) {          // the list is shorter than the bound: nothing to do
           // (Q still lands: wait for it so the buffer is never written twice at once)
           if (!mbar_wait_warp(&S.q_tma, qt & 1, ew)) goto done_loader;
@@ -491,14 +640,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // the first tile's rows start loading before Q is rotated
         wait_prev();
-        if (!issue_tile(g, g.t0, n)) goto done_loader;
+        if (FP4) {
+          fetch_tile(g, g.t0);
+          if (!store_tile(g, g.t0, n)) goto done_loader;
+        } else if (!issue_tile(g, g.t0, n)) {
+          goto done_loader;
+        }
         if (!mbar_wait_warp(&S.q_tma, qt & 1, ew)) goto done_loader;   // Q landed
         ++qt;
         // rotate the tail (dims 448..511 = block 7) at position p, in place
 #pragma unroll
         for (uint32_t i = 0; i < kQC; ++i) {
           if (P.q_rotated) break;
-          const uint32_t id = lt + 128 * i, h = id >> 3, pc = id & 7;
+          const uint32_t id = lt + WP::LT * i, h = id >> 3, pc = id & 7;
           uint4 *ptr = reinterpret_cast<uint4 *>(S.q + 7 * QBLK + h * 128 + pc * 16);
           uint4 v = *ptr;
           uint32_t w4[4] = {v.x, v.y, v.z, v.w};
@@ -513,7 +667,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async();
         mbar_arrive(&S.q_full);
         for (uint32_t tile = g.t0; tile < g.t1; tile += g.ts, ++n) {
-          if (tile != g.t0 && !issue_tile(g, tile, n)) goto done_loader;
+          if (tile != g.t0) {
+            if (FP4 ? !store_tile(g, tile, n) : !issue_tile(g, tile, n)) goto done_loader;
+          }
           // one arrival per thread once all its rows of the tile landed: the
           // MMA issuer takes the tile whole (waits between the MMAs of one
           // accumulation halve their rate; issuing S pair by pair as the
@@ -525,22 +681,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++nk;
           }
           mbar_arrive(&S.kv_full);
+          if (FP4 && tile + g.ts < g.t1) fetch_tile(g, tile + g.ts);
         }
       }
       ++qn;
     }
   done_loader:
     cp_async_wait_all();
-  } else if (warp == 8) {
+  } else if (warp == WP::MMA) {
     // ------------------------------------------------------------ MMA issue
     constexpr uint32_t idS = idesc_bf16_f32(kRows, NH);
     constexpr uint32_t idPV = idesc_bf16_f32(kRows, kH) | kIdescMajorA_MN | kIdescMajorB_MN;
     const uint32_t q_base = smem_u32(S.q), kv_base = smem_u32(S.kv), p_base = smem_u32(S.p);
     uint32_t n = 0, qn = 0, nk = 0;
     bool ok = true;
-    for (uint32_t qi = q_first; qi < P.n_q && ok; qi += q_step) {
+    for (uint32_t it = i0; it < n_items && ok; it += i_step) {
+      const uint32_t qi = item_q(it);
       if (rank * kRows >= rows_bound(P, qi)) continue;
-      const QueryGeo g = query_geo<!DEC>(P, qi, rank, C, lane);
+      const QueryGeo g = query_geo<kScan>(P, qi, rank, C, lane);
       if (g.t0 >= g.t1) continue;
       if (lane == 0) {
         ok = mbar_wait(&S.q_full, qn & 1, ew);
@@ -622,10 +780,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return flag;
     };
-    for (uint32_t qi = q_first; qi < P.n_q; qi += q_step) {
+    for (uint32_t it = i0; it < n_items; it += i_step) {
+      const uint32_t qi = item_q(it), hq0 = item_h(it);
       const bool maybe = rank * kRows < rows_bound(P, qi);
       QueryGeo g = {};
-      if (maybe) g = query_geo<!DEC>(P, qi, rank, C, lane);
+      if (maybe) g = query_geo<kScan>(P, qi, rank, C, lane);
       const bool has_tiles = maybe && g.t0 < g.t1;
       bool any_valid = false;
       // the rotation coefficients of this thread's tail dim in the direct
@@ -775,15 +934,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         // normalise, rotate the tail back by -p and store bf16 pairs straight
         // from registers, four 128-dim chunks (no staging, no barrier)
-        float li[NH];   // 1 / L per head, for the four chunks
+        // 1 / L per head, for the four chunks (from shared memory with 4-bit rows,
+        // whose larger block has fewer registers per thread)
+        float li[FP4 ? 1 : NH];
+        if (!FP4) {
 #pragma unroll
-        for (int h = 0; h < NH; ++h) li[h] = S.linv[h];
+          for (int h = 0; h < NH; ++h) li[FP4 ? 0 : h] = S.linv[h];
+        }
+        auto linv = [&](int h) { return FP4 ? S.linv[h] : li[FP4 ? 0 : h]; };
         const bool odd = lane & 1;
 #pragma unroll 1
         for (uint32_t m = 0; m < 4; ++m) {
           const bool rot = m == 3 && r >= 64;   // warp-uniform: the rotated tail dims
           const float co = ep_co, si = ep_si;   // (the pair's coefficients: both lanes)
-          __nv_bfloat16 *o = P.out + ((size_t)qi * kH + hq0) * kD + m * 128;
+          __nv_bfloat16 *o = P.out + ((size_t)qi * HQ + hq0) * kD + m * 128;
           uint32_t ab[NHF][32];
 #pragma unroll
           for (uint32_t hf = 0; hf < (uint32_t)NHF; ++hf)
@@ -793,8 +957,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (uint32_t hf = 0; hf < (uint32_t)NHF; ++hf) {
 #pragma unroll
             for (int h = 0; h < 32; h += 2) {
-              const float v0 = __uint_as_float(ab[hf][h]) * li[32 * hf + h];
-              const float v1 = __uint_as_float(ab[hf][h + 1]) * li[32 * hf + h + 1];
+              const float v0 = __uint_as_float(ab[hf][h]) * linv(32 * hf + h);
+              const float v1 = __uint_as_float(ab[hf][h + 1]) * linv(32 * hf + h + 1);
               // lanes 2i, 2i + 1 hold dims d, d + 1 of heads h, h + 1: one
               // swap gives the even lane head h's pair and the odd lane head
               // h + 1's, rotated in place and stored as one bf16 pair
@@ -806,7 +970,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 x1 = y1;
               }
               const uint32_t row = 32 * hf + h + (odd ? 1u : 0u);
-              *reinterpret_cast<uint32_t *>(o + (size_t)row * kD + (r & ~1u)) = pack_bf16(x0, x1);
+              if (!FP4 || hq0 + row < HQ)
+                *reinterpret_cast<uint32_t *>(o + (size_t)row * kD + (r & ~1u)) = pack_bf16(x0, x1);
             }
           }
         }
@@ -863,14 +1028,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) tmem_dealloc(tmem, 512);
+  if (warp == WP::MMA) tmem_dealloc(tmem, 512);
   if (dec && C > 1) {
     cluster_sync_all();   // every rank's O and (max, sum) are in the workspace
     if (warp < 8) {
       if (C <= 8)
-        merge_heads<8, NH>(P, S, vq, rank, C, ew);
+        merge_heads<8, NH, FP4>(P, S, vq, rank, C, ew);
       else
-        merge_heads<kMaxCluster, NH>(P, S, vq, rank, C, ew);
+        merge_heads<kMaxCluster, NH, FP4>(P, S, vq, rank, C, ew);
     }
   }
 }
@@ -889,10 +1054,13 @@ int max_active_clusters(uint32_t C, size_t smem) {
   if (C > 8) {
     int np = g_nonportable[dev].load(std::memory_order_relaxed);
     if (np == 0) {
-      np = cudaFuncSetAttribute(attn_tc_kernel<true, false>,
-                                cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
-                   cudaFuncSetAttribute(attn_tc_kernel<true, true>,
-                                        cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess
+      auto allow = [](auto *k) {
+        return cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
+               cudaSuccess;
+      };
+      np = allow(attn_tc_kernel<true, false, false, kNhDec>) &&
+                   allow(attn_tc_kernel<true, true, false, kNhDec>) &&
+                   allow(attn_tc_kernel<true, true, true, kNhDec>)
                ? 1
                : -1;
       (void)cudaGetLastError();
@@ -910,11 +1078,11 @@ int max_active_clusters(uint32_t C, size_t smem) {
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
   cfg.gridDim = dim3(C * 64);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(Warps<false>::THREADS);
   cfg.dynamicSmemBytes = smem;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  if (cudaOccupancyMaxActiveClusters(&v, attn_tc_kernel<true, false>, &cfg) != cudaSuccess || v <= 0) {
+  if (cudaOccupancyMaxActiveClusters(&v, attn_tc_kernel<true, false, false, kNhDec>, &cfg) != cudaSuccess || v <= 0) {
     (void)cudaGetLastError();
     // beyond the portable size an unanswered query means the size is not used
     v = C > 8 ? -1 : num_sms() / (int)C;
@@ -966,21 +1134,23 @@ void attn_tc_force_cluster(uint32_t C) {
   g_force_cluster.store(C > kMaxCluster ? kMaxCluster : C, std::memory_order_relaxed);
 }
 
-uint32_t attn_tc_decode_cluster(uint32_t rows_max, uint32_t n_q) {
-  return decode_cluster(rows_max, n_q * Heads<true>::HG, sizeof(Smem) + 1024);
+uint32_t attn_tc_decode_cluster(uint32_t rows_max, uint32_t n_q, uint32_t n_heads) {
+  return decode_cluster(rows_max, n_q * (n_heads + kNhDec - 1) / kNhDec, sizeof(Smem) + 1024);
 }
 
-bool attn_tc_supported(int dtype, uint32_t H, uint32_t D, uint32_t n_rot) {
-  return dtype == DS4A_BF16 && H == (uint32_t)kH && D == (uint32_t)kD && n_rot == 64;
+// (4-bit rows: any number of heads)
+bool attn_tc_supported(int dtype, uint32_t H, uint32_t D, uint32_t n_rot, bool fp4) {
+  return dtype == DS4A_BF16 && (fp4 || H == (uint32_t)kH) && D == (uint32_t)kD && n_rot == 64;
 }
 
 // Error word, then (decode) room for the partials of the largest cluster.
-size_t attn_tc_ws_bytes(uint32_t batch, uint32_t T, uint32_t rows_max) {
+size_t attn_tc_ws_bytes(uint32_t batch, uint32_t T, uint32_t rows_max, uint32_t n_heads) {
   if (T != 1) return 256;
   const uint32_t n_tiles = (rows_max + kRows - 1) / kRows;
   const uint32_t cmax = n_tiles < kMaxCluster ? (n_tiles ? n_tiles : 1u) : kMaxCluster;
   if (cmax < 2) return 256;
-  return 256 + (size_t)batch * cmax * kH * (kD * sizeof(__nv_bfloat16) + 2 * sizeof(float));
+  const uint32_t heads = (n_heads + kNhDec - 1) / kNhDec * kNhDec;   // whole groups
+  return 256 + (size_t)batch * cmax * heads * (kD * sizeof(__nv_bfloat16) + 2 * sizeof(float));
 }
 
 cudaError_t launch_attention_tc(const AttnArgs &a, uint32_t rows_max, int *err, cudaStream_t s) {
@@ -1012,19 +1182,32 @@ cudaError_t launch_attention_tc(const AttnArgs &a, uint32_t rows_max, int *err, 
   const size_t smem = sizeof(Smem) + 1024;
   // paged rows: an instantiation of its own, so the contiguous gathers carry
   // no table code
-  const bool paged = a.map.table != nullptr;
-  auto *k_dec = paged ? attn_tc_kernel<true, true> : attn_tc_kernel<true, false>;
-  auto *k_pf = paged ? attn_tc_kernel<false, true> : attn_tc_kernel<false, false>;
-  static int smem_set[2][2] = {{0, 0}, {0, 0}};
-  cudaError_t e = a.T == 1 ? ensure_smem(k_dec, smem, &smem_set[1][paged])
-                           : ensure_smem(k_pf, smem, &smem_set[0][paged]);
+  const bool paged = a.map.table != nullptr, fp4 = a.fp4;
+  auto *k_dec = fp4     ? attn_tc_kernel<true, true, true, kNhDec>
+                : paged ? attn_tc_kernel<true, true, false, kNhDec>
+                        : attn_tc_kernel<true, false, false, kNhDec>;
+  auto *k_pf = fp4     ? attn_tc_kernel<false, true, true, kH>
+               : paged ? attn_tc_kernel<false, true, false, kH>
+                       : attn_tc_kernel<false, false, false, kH>;
+  const uint32_t nh = a.T == 1 ? kNhDec : kH;
+  P.n_heads = a.n_heads;
+  P.hg = (a.n_heads + nh - 1) / nh;
+  static DeviceSmem smem_set[2][3];
+  cudaError_t e = ensure_smem(a.T == 1 ? k_dec : k_pf, smem,
+                              smem_set[a.T == 1][fp4 ? 2 : paged].here());
   if (e != cudaSuccess) return e;
-  // Q as [n_q * 64 heads][512] bf16 rows; boxes of one CTA's heads x 64 dims
   CUtensorMap tq;
-  const uint64_t qd[2] = {(uint64_t)kD, (uint64_t)P.n_q * kH};
-  const uint64_t qs[1] = {(uint64_t)kD * 2};
-  const uint32_t qb[2] = {64, (uint32_t)(a.T == 1 ? Heads<true>::NH : Heads<false>::NH)};
-  e = make_tmap_bf16(&tq, a.q, 2, qd, qs, qb);
+  if (fp4) {   // Q as [n_q][H][512]: boxes of one CTA's heads, zeros past the last head
+    const uint64_t qd[3] = {(uint64_t)kD, (uint64_t)a.n_heads, (uint64_t)P.n_q};
+    const uint64_t qs[2] = {(uint64_t)kD * 2, (uint64_t)a.n_heads * kD * 2};
+    const uint32_t qb[3] = {64, nh, 1};
+    e = make_tmap_bf16(&tq, a.q, 3, qd, qs, qb);
+  } else {     // Q as [n_q * 64 heads][512] bf16 rows; boxes of one CTA's heads x 64 dims
+    const uint64_t qd[2] = {(uint64_t)kD, (uint64_t)P.n_q * kH};
+    const uint64_t qs[1] = {(uint64_t)kD * 2};
+    const uint32_t qb[2] = {64, nh};
+    e = make_tmap_bf16(&tq, a.q, 2, qd, qs, qb);
+  }
   if (e != cudaSuccess) return e;
   // decode tiles of contiguous rows: the ring [B][128][512] (one box of its
   // 128 slots per 64 dims) and, on ratio 128 with one position for every
@@ -1040,7 +1223,7 @@ cudaError_t launch_attention_tc(const AttnArgs &a, uint32_t rows_max, int *err, 
     const uint32_t rb[3] = {64, (uint32_t)kRows, 1};
     if (make_tmap_bf16(&tr, a.ring, 3, rd, rs, rb) == cudaSuccess) P.tma_rows |= 1u;
     const uint32_t n_list = a.ratio == 128 ? min((a.pos0 + 1) / 128, a.n_comp) : 0u;
-    if (a.ratio == 128 && !paged && !a.seq_pos && n_list >= (uint32_t)kRows) {
+    if (a.ratio == 128 && !paged && !fp4 && !a.seq_pos && n_list >= (uint32_t)kRows) {
       const uint64_t cd[3] = {(uint64_t)kD, (uint64_t)n_list, (uint64_t)a.batch};
       const uint64_t cs[2] = {(uint64_t)kD * 2, (uint64_t)a.comp_cap * kD * 2};
       if (make_tmap_bf16(&tcmp, a.comp, 3, cd, cs, rb) == cudaSuccess) P.tma_rows |= 2u;
@@ -1048,9 +1231,9 @@ cudaError_t launch_attention_tc(const AttnArgs &a, uint32_t rows_max, int *err, 
   }
   if (a.T == 1) {
     // one cluster of P.cluster CTAs per (query, head group)
-    const uint32_t n_vq = P.n_q * Heads<true>::HG;
+    const uint32_t n_vq = P.n_q * P.hg;
     P.cluster = decode_cluster(rows_max, n_vq, smem);
-    P.ml = reinterpret_cast<float *>(P.part + (size_t)P.n_q * P.cluster * kH * kD);
+    P.ml = reinterpret_cast<float *>(P.part + (size_t)n_vq * P.cluster * kNhDec * kD);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -1058,7 +1241,7 @@ cudaError_t launch_attention_tc(const AttnArgs &a, uint32_t rows_max, int *err, 
     at[0].val.clusterDim.y = 1;
     at[0].val.clusterDim.z = 1;
     cfg.gridDim = dim3(n_vq * P.cluster);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(fp4 ? Warps<true>::THREADS : Warps<false>::THREADS);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1070,8 +1253,9 @@ cudaError_t launch_attention_tc(const AttnArgs &a, uint32_t rows_max, int *err, 
     return e != cudaSuccess ? e : cudaGetLastError();
   }
   P.cluster = 0;
-  const uint32_t grid = min(P.n_q, (uint32_t)num_sms());
-  e = launch_pdl(k_pf, dim3(grid), dim3(kThreads), smem, s, tq, tr, tcmp, P);
+  const uint64_t items = (uint64_t)P.n_q * P.hg;
+  const uint32_t grid = (uint32_t)min(items, (uint64_t)num_sms());
+  e = launch_pdl(k_pf, dim3(grid), dim3(fp4 ? Warps<true>::THREADS : Warps<false>::THREADS), smem, s, tq, tr, tcmp, P);
   note_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

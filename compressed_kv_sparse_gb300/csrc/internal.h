@@ -183,14 +183,15 @@ size_t attn_ws_bytes(int dtype, uint32_t ratio, uint32_t batch, uint32_t T, uint
                      uint32_t top_k, bool fp4);
 cudaError_t launch_attention(const AttnArgs &a, cudaStream_t s);
 
-// Tensor-core attention (attention_tc.cu): bf16, 64 heads x 512 dims, 64-dim tail.
-bool attn_tc_supported(int dtype, uint32_t H, uint32_t D, uint32_t n_rot);
-size_t attn_tc_ws_bytes(uint32_t batch, uint32_t T, uint32_t rows_max);
+// Tensor-core attention (attention_tc.cu): bf16, 64 heads x 512 dims, 64-dim tail;
+// with 4-bit compressed rows any number of heads.
+bool attn_tc_supported(int dtype, uint32_t H, uint32_t D, uint32_t n_rot, bool fp4);
+size_t attn_tc_ws_bytes(uint32_t batch, uint32_t T, uint32_t rows_max, uint32_t n_heads);
 cudaError_t launch_attention_tc(const AttnArgs &a, uint32_t rows_max, int *err, cudaStream_t s);
 // Decode cluster size: forced process-wide (0 = automatic), and the size a
 // decode launch of `n_q` queries with at most `rows_max` rows each uses.
 void attn_tc_force_cluster(uint32_t C);
-uint32_t attn_tc_decode_cluster(uint32_t rows_max, uint32_t n_q);
+uint32_t attn_tc_decode_cluster(uint32_t rows_max, uint32_t n_q, uint32_t n_heads);
 // The same for the arguments of a decode call whose token is at position
 // pos_end - 1: 0 when it does not run on the tensor-core kernel.
 uint32_t attn_decode_cluster(int dtype, uint32_t ratio, uint32_t batch, uint32_t n_heads,
