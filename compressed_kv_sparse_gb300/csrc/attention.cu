@@ -416,7 +416,7 @@ uint32_t attn_decode_cluster(int dtype, uint32_t ratio, uint32_t batch, uint32_t
                              uint64_t pos_end, bool fp4) {
   if (!attn_tc_supported(dtype, n_heads, head_dim, n_rot, fp4)) return 0;
   return attn_tc_decode_cluster(rows_at(ratio, cap_raw, comp_cap, top_k, n_comp, pos_end), batch,
-                                n_heads);
+                                n_heads, fp4);
 }
 
 cudaError_t launch_attention(const AttnArgs &a, cudaStream_t s) {

@@ -66,14 +66,17 @@ struct Heads {
   static constexpr int QBLK = NH * 128;      // one 64-dim block of this CTA's Q
 };
 constexpr int kKBlk = kRows * 128;     // one 64-dim block of the row tile
-// Warps: 0-3 softmax and epilogue, then the loaders, then the MMA issuer. 4-bit
-// rows take eight loader warps: they convert every element of a tile.
+// Warps: softmax and epilogue, then the loaders, then the MMA issuer. 4-bit rows
+// take eight loader warps (they convert every element of a tile) and eight softmax
+// warps (two per 32 TMEM lanes, each with half the heads).
 template <bool FP4>
 struct Warps {
+  static constexpr uint32_t NS = FP4 ? 8 : 4;          // softmax warps
+  static constexpr uint32_t ST = 32 * NS;              // softmax threads
   static constexpr uint32_t NL = FP4 ? 8 : 4;          // loader warps
   static constexpr uint32_t LT = 32 * NL;              // loader threads
-  static constexpr uint32_t MMA = 4 + NL;              // the MMA issuer's warp
-  static constexpr uint32_t THREADS = 32 * (MMA + 1);  // 288 or 416
+  static constexpr uint32_t MMA = NS + NL;             // the MMA issuer's warp
+  static constexpr uint32_t THREADS = 32 * (MMA + 1);  // 288 or 544
 };
 constexpr int kNhDec = 32;             // heads per CTA in decode
 constexpr uint32_t kMaxCluster = 16;   // cluster size; beyond 8 (the portable limit) when the
@@ -113,6 +116,7 @@ struct Smem {
   uint64_t q_full, q_empty, s_full, p_full, p_empty, o_full, o_empty, sm_bar;
   uint64_t q_tma;   // the query's eight Q blocks landed (TMA transaction count)
   uint64_t kv_tma;  // a tile loaded by TMA landed
+  uint64_t kv_pair[4];   // 4-bit rows: blocks 2m, 2m+1 of the tile are written
   uint64_t mg_bar;  // decode merge: the peers' partial O slices landed
   float mref[kH], alpha[kH], lsh[kH], linv[kH];
   float tmax[4][kH];
@@ -363,13 +367,16 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
   // accesses, which measured faster for its c4a and c128a calls (14.5 / 16.7
   // against 14.8 / 17.0 us)
   uint8_t *sbase;
-  if (DEC)
+  if (DEC && !FP4)
     sbase = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                         ~(uintptr_t)1023);
   else
     sbase = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Smem &S = *reinterpret_cast<Smem *>(sbase);
-  const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (4-bit rows: the same for the compiler too, so that the MMA issuer's branch and
+  // its descriptors are warp-uniform)
+  const uint32_t warp = FP4 ? uniform(threadIdx.x >> 5) : threadIdx.x >> 5;
+  const uint32_t lane = threadIdx.x & 31;
   // decode: cluster of C CTAs per (query, head group), rank c takes tiles
   // c, c + C, ...; prefill: one whole query at a time per CTA
   constexpr bool dec = DEC;
@@ -400,15 +407,18 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
 
   if (threadIdx.x == 0) {
     mbar_init(&S.kv_full, WP::LT);
-    for (int i = 0; i < 4; ++i) mbar_init(&S.kv_empty[i], 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&S.kv_empty[i], 1);
+      mbar_init(&S.kv_pair[i], WP::LT);
+    }
     mbar_init(&S.q_full, WP::LT);
     mbar_init(&S.q_empty, 1);
     mbar_init(&S.s_full, 1);
-    mbar_init(&S.p_full, 128);
+    mbar_init(&S.p_full, WP::ST);
     mbar_init(&S.p_empty, 1);
     mbar_init(&S.o_full, 1);
-    mbar_init(&S.o_empty, 4);
-    mbar_init(&S.sm_bar, 128);
+    mbar_init(&S.o_empty, WP::NS);
+    mbar_init(&S.sm_bar, WP::ST);
     mbar_init(&S.q_tma, 1);
     mbar_init(&S.kv_tma, 1);
     mbar_init(&S.mg_bar, 1);
@@ -440,7 +450,7 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
   tc_fence_after();
   // the loaders wait for the previous launch themselves, after they have
   // started the first query's Q load
-  const bool loader = warp >= 4 && warp < WP::MMA;
+  const bool loader = warp >= WP::NS && warp < WP::MMA;
   if (!loader) {
     pdl_wait();
     pdl_trigger();
@@ -449,9 +459,9 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
   // so that its latency overlaps the previous launch
   const ErrWord ew{P.err, err_base};
 
-  if (warp >= 4 && warp < WP::MMA) {
+  if (loader) {
     // ------------------------------------------------------------ loaders
-    const uint32_t lt = threadIdx.x - 128, lw = warp - 4;
+    const uint32_t lt = threadIdx.x - WP::ST, lw = warp - WP::NS;
     uint32_t n = 0, qn = 0, qt = 0, nk = 0;   // qt: Q loads issued, nk: TMA tiles issued
     // issue all eight 64-dim blocks of a tile (one cp.async group each) as
     // their slots free up; rows of this lane: lw*32 + lane/8 + 4i, chunk lane%8.
@@ -493,35 +503,58 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
     };
     // ---- 4-bit rows: thread lt holds lane lt % 8 of rows lt / 8 + 32 i. fetch_tile
     // loads their records into registers (12 16-byte loads in flight, each warp
-    // load 128 contiguous bytes of four rows); store_tile converts them block pair by
+    // load 128 contiguous bytes of four rows; rows found by find_tile); store_tile converts them block pair by
     // block pair as the tile's slots free up. The next tile's records load while
     // this one's MMAs run.
     constexpr uint32_t kFR = FP4 ? kRows * 8 / WP::LT : 1;   // rows per thread
     uint4 rec[kFR][3];
-    const __nv_bfloat16 *fsrc[kFR];   // a row in bf16 (the window), or NULL
-    uint32_t fpk = 0;                 // bit i: row i is in 4 bits
-    auto fetch_tile = [&](const QueryGeo &g, uint32_t tile) {
-      const uint32_t j = lt & 7;
-      fpk = 0;
+    uint32_t nxt[kFR];                    // pool rows of the next tile, or kNoRow
+    uint32_t cur_raw = 0, nxt_raw = 0;    // bit i: row i is in bf16 (the window)
+    constexpr uint32_t kNoRow = 0xffffffffu;
+    // where the rows of a tile are (list and table reads: one tile further ahead)
+    auto find_tile = [&](const QueryGeo &g, uint32_t tile) {
+      nxt_raw = 0;
+      const uint32_t sh = P.ratio == 4 ? 6u : 1u;   // log2 of the rows per block
 #pragma unroll
       for (uint32_t i = 0; i < kFR; ++i) {
         const uint32_t r = tile * kRows + (lt >> 3) + 32 * i;
-        fsrc[i] = nullptr;
+        nxt[i] = kNoRow;
         if (r < g.n_w) {
-          fsrc[i] = row_src<false>(P, g, r);
+          nxt_raw |= 1u << i;
         } else if (r < g.N) {
           const uint32_t e = r - g.n_w;
           const int32_t idx = P.ratio == 4 ? g.tk[e] : (int32_t)e;
           if (idx >= 0) {
-            const uint4 *src = reinterpret_cast<const uint4 *>(
-                reinterpret_cast<const uint8_t *>(P.comp) +
-                P.map.row_of(g.b, (uint32_t)idx) * kFp4RowBytes) + j;
-            fpk |= 1u << i;
-#pragma unroll
-            for (uint32_t v = 0; v < 3; ++v) rec[i][v] = __ldg(src + 8 * v);
+            uint32_t row = g.b * P.comp_cap + (uint32_t)idx;   // (fewer than 2^32: launch check)
+            if (P.map.table) {   // (as RowMap::phys: entries outside the pool read block 0)
+              const uint32_t lb = (uint32_t)idx >> sh;
+              uint32_t blk = lb < P.map.max_blocks
+                                 ? (uint32_t)__ldg(P.map.table + (size_t)g.b * P.map.max_blocks + lb)
+                                 : 0u;
+              if (blk >= P.map.n_blocks) blk = 0;
+              row = (blk << sh) + ((uint32_t)idx & ((1u << sh) - 1));
+            }
+            nxt[i] = row;
           }
         }
       }
+    };
+    auto fetch_tile = [&]() {
+      cur_raw = nxt_raw;
+#pragma unroll
+      for (uint32_t i = 0; i < kFR; ++i) {
+        // (a masked row: zeros)
+        const uint8_t *src = reinterpret_cast<const uint8_t *>(P.comp) +
+                             (size_t)nxt[i] * kFp4RowBytes + 16 * (lt & 7);
+#pragma unroll
+        for (uint32_t v = 0; v < 3; ++v)
+          rec[i][v] = nxt[i] != kNoRow ? ld_nc_v4(src + 128 * v) : make_uint4(0u, 0u, 0u, 0u);
+      }
+    };
+    // this thread's chunk of row i in 64-dim block KB of the tile
+    auto chunk_dst = [&](uint32_t i, uint32_t KB) {
+      const uint32_t r = (lt >> 3) + 32 * i;
+      return S.kv + KB * kKBlk + (r >> 3) * 1024 + (r & 7) * 128 + (((lt & 7) ^ (r & 7)) << 4);
     };
     auto store_tile = [&](const QueryGeo &g, uint32_t tile, uint32_t n) -> bool {
       if (tile_kind<DEC, true>(P, g, tile)) {   // the whole window ring by TMA
@@ -532,9 +565,11 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
             tma_load_3d(S.kv + kb * kKBlk, &tmap_ring, &S.kv_tma, (int)(64 * kb), 0, (int)g.b);
           }
         }
+#pragma unroll
+        for (uint32_t m = 0; m < 4; ++m) mbar_arrive(&S.kv_pair[m]);
         return true;
       }
-      const uint32_t j = lt & 7, r0 = lt >> 3;
+      const uint32_t j = lt & 7;
       uint32_t sl[kFR], sh[kFR], wide = 0;
 #pragma unroll
       for (uint32_t i = 0; i < kFR; ++i) {   // a pair of lanes shares its scale bytes
@@ -543,38 +578,57 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
         sh[i] = j & 1 ? mine : other;
         if (fp4_wide(sl[i]) | fp4_wide(sh[i])) wide |= 1u << i;
       }
-      auto block = [&](auto kb_c) -> bool {
-        constexpr uint32_t KB = decltype(kb_c)::value;
-        if ((KB & 1) == 0 && !mbar_wait_warp(&S.kv_empty[KB >> 1], (n & 1) ^ 1, ew)) return false;
-#pragma unroll
-        for (uint32_t i = 0; i < kFR; ++i) {
-          const uint32_t r = r0 + 32 * i;
-          uint8_t *dst = S.kv + KB * kKBlk + (r >> 3) * 1024 + (r & 7) * 128 + ((j ^ (r & 7)) << 4);
-          if ((fpk >> i) & 1) {
-            const uint4 a = rec[i][0], c = rec[i][1];
-            if (KB == 7)
-              *reinterpret_cast<uint4 *>(dst) = rec[i][2];
-            else
-              *reinterpret_cast<uint4 *>(dst) =
-                  fp4_chunk<KB>(KB == 0   ? a.x
-                                : KB == 1 ? a.y
-                                : KB == 2 ? a.z
-                                : KB == 3 ? a.w
-                                : KB == 4 ? c.x
-                                : KB == 5 ? c.y
-                                          : c.z,
-                                sl[i], sh[i], (wide >> i) & 1);
-          } else {
-            cp_async16(dst, fsrc[i] ? fsrc[i] + KB * 64 + j * 8 : P.ring, fsrc[i] ? 16u : 0u);
-          }
-        }
-        return true;
+      auto word = [&](uint32_t i, uint32_t KB) {
+        const uint4 &v = rec[i][KB / 4];
+        return KB % 4 == 0 ? v.x : KB % 4 == 1 ? v.y : KB % 4 == 2 ? v.z : v.w;
       };
       using std::integral_constant;
-      return block(integral_constant<uint32_t, 0>{}) && block(integral_constant<uint32_t, 1>{}) &&
-             block(integral_constant<uint32_t, 2>{}) && block(integral_constant<uint32_t, 3>{}) &&
-             block(integral_constant<uint32_t, 4>{}) && block(integral_constant<uint32_t, 5>{}) &&
-             block(integral_constant<uint32_t, 6>{}) && block(integral_constant<uint32_t, 7>{});
+      if (__all_sync(0xffffffffu, cur_raw == 0 && wide == 0)) {
+        // every row of this warp in 4 bits with ordinary scales: straight code, the
+        // rows' conversions interleaved, each pair of blocks handed over at once
+        auto pair = [&](auto m_c) -> bool {
+          constexpr uint32_t M = decltype(m_c)::value;
+          if (!mbar_wait_warp(&S.kv_empty[M], (n & 1) ^ 1, ew)) return false;
+#pragma unroll
+          for (uint32_t i = 0; i < kFR; ++i)
+            *reinterpret_cast<uint4 *>(chunk_dst(i, 2 * M)) =
+                fp4_chunk<2 * M>(word(i, 2 * M), sl[i], sh[i], false);
+#pragma unroll
+          for (uint32_t i = 0; i < kFR; ++i)
+            *reinterpret_cast<uint4 *>(chunk_dst(i, 2 * M + 1)) =
+                M == 3 ? rec[i][2] : fp4_chunk<2 * M + 1>(word(i, 2 * M + 1), sl[i], sh[i], false);
+          fence_proxy_async();
+          mbar_arrive(&S.kv_pair[M]);
+          return true;
+        };
+        return pair(integral_constant<uint32_t, 0>{}) && pair(integral_constant<uint32_t, 1>{}) &&
+               pair(integral_constant<uint32_t, 2>{}) && pair(integral_constant<uint32_t, 3>{});
+      }
+#pragma unroll 1
+      for (uint32_t m = 0; m < 4; ++m) {
+        if (!mbar_wait_warp(&S.kv_empty[m], (n & 1) ^ 1, ew)) return false;
+#pragma unroll 1
+        for (uint32_t kb = 2 * m; kb < 2 * m + 2; ++kb)
+#pragma unroll
+          for (uint32_t i = 0; i < kFR; ++i) {
+            uint8_t *dst = chunk_dst(i, kb);
+            if ((cur_raw >> i) & 1) {
+              cp_async16(dst, row_src<false>(P, g, tile * kRows + (lt >> 3) + 32 * i) + 64 * kb + 8 * j,
+                         16u);
+            } else {
+              const uint4 a = rec[i][0], c = rec[i][1];
+              const uint32_t w = kb == 0 ? a.x : kb == 1 ? a.y : kb == 2 ? a.z : kb == 3 ? a.w
+                                 : kb == 4 ? c.x : kb == 5 ? c.y : c.z;
+              const uint32_t sb = ((kb < 4 ? sl[i] : sh[i]) >> (8 * (kb % 4))) << 24;
+              *reinterpret_cast<uint4 *>(dst) = kb == 7 ? rec[i][2] : fp4_chunk<3>(w, sb, 0u, true);
+            }
+          }
+      }
+      cp_async_wait_all();
+      fence_proxy_async();
+#pragma unroll
+      for (uint32_t m = 0; m < 4; ++m) mbar_arrive(&S.kv_pair[m]);
+      return true;
     };
     // Q (it needs no list): eight TMA boxes of 64 heads x 64 dims, in the
     // 128-byte swizzled K-major layout the S MMAs read. The first query's
@@ -641,7 +695,9 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
         // the first tile's rows start loading before Q is rotated
         wait_prev();
         if (FP4) {
-          fetch_tile(g, g.t0);
+          find_tile(g, g.t0);
+          fetch_tile();
+          if (g.t0 + g.ts < g.t1) find_tile(g, g.t0 + g.ts);
           if (!store_tile(g, g.t0, n)) goto done_loader;
         } else if (!issue_tile(g, g.t0, n)) {
           goto done_loader;
@@ -670,6 +726,13 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
           if (tile != g.t0) {
             if (FP4 ? !store_tile(g, tile, n) : !issue_tile(g, tile, n)) goto done_loader;
           }
+          if (FP4) {   // (store_tile has handed the tile over)
+            if (tile + g.ts < g.t1) {
+              fetch_tile();
+              if (tile + 2 * g.ts < g.t1) find_tile(g, tile + 2 * g.ts);
+            }
+            continue;
+          }
           // one arrival per thread once all its rows of the tile landed: the
           // MMA issuer takes the tile whole (waits between the MMAs of one
           // accumulation halve their rate; issuing S pair by pair as the
@@ -681,7 +744,6 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
             ++nk;
           }
           mbar_arrive(&S.kv_full);
-          if (FP4 && tile + g.ts < g.t1) fetch_tile(g, tile + g.ts);
         }
       }
       ++qn;
@@ -695,7 +757,66 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
     const uint32_t q_base = smem_u32(S.q), kv_base = smem_u32(S.kv), p_base = smem_u32(S.p);
     uint32_t n = 0, qn = 0, nk = 0;
     bool ok = true;
-    for (uint32_t it = i0; it < n_items && ok; it += i_step) {
+    // 4-bit rows: the whole warp runs this code and the instructions themselves
+    // elect a thread, every branch is uniform (votes and shuffles), so that the
+    // descriptors stay in uniform registers. Issued from a branch on lane 0 each MMA
+    // first moves its descriptors there, and the issue, not the tensor core, sets
+    // the pace (S^T 2000 to 4000 cycles a tile).
+    for (uint32_t it = i0; FP4 && it < n_items && ok; it += i_step) {
+      const uint32_t qi = item_q(it), rank_u = uniform(rank);
+      if (uniform(rank_u * kRows >= rows_bound(P, qi))) continue;
+      const QueryGeo g = query_geo<kScan>(P, qi, rank, C, lane);
+      const uint32_t t0 = uniform(g.t0), t1 = uniform(g.t1), ts = uniform(g.ts);
+      if (t0 >= t1) continue;
+      const bool tma0 = uniform(tile_kind<DEC, true>(P, g, t0)) != 0;   // (only a first tile)
+      const uint32_t qd = desc_lo(q_base), kd = desc_lo(kv_base), pd = desc_lo(p_base);
+      ok = mbar_wait_warp(&S.q_full, qn & 1, ew);
+      for (uint32_t tile = t0; ok && tile < t1; tile += ts, ++n) {
+        const bool first = tile == t0, last = tile + ts >= t1;
+        if (first && tma0) ok = mbar_wait_warp(&S.kv_tma, nk++ & 1, ew);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (uint32_t m = 0; m < 4; ++m) {   // S^T starts while the tile's last blocks convert
+          ok = ok && mbar_wait_warp(&S.kv_pair[m], n & 1, ew);
+          if (!ok) break;
+#pragma unroll
+          for (uint32_t kb = 2 * m; kb < 2 * m + 2; ++kb)
+#pragma unroll
+            for (uint32_t kk = 0; kk < 4; ++kk)
+              mma_bf16_elect(tmS, desc_at(kd + (kb * kKBlk + kk * 32) / 16 + desc_lbo(16), kDescHiK),
+                             desc_at(qd + (kb * QBLK + kk * 32) / 16 + desc_lbo(16), kDescHiK), idS,
+                             (kb | kk) ? 1u : 0u);
+        }
+        if (!ok) break;
+        mma_commit_elect(&S.s_full);
+        if (last) mma_commit_elect(&S.q_empty);
+        ok = mbar_wait_warp(&S.p_full, n & 1, ew);
+        if (ok && first) ok = mbar_wait_warp(&S.o_empty, (qn & 1) ^ 1, ew);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t acc0 = first ? 0u : 1u;
+#pragma unroll
+        for (uint32_t m = 0; m < 4; ++m) {
+#pragma unroll
+          for (uint32_t kk = 0; kk < 8; ++kk)
+            mma_bf16_elect(tmO + m * kH,
+                           desc_at(kd + (2 * m * kKBlk + kk * 2048) / 16 + desc_lbo(kKBlk), kDescHiK),
+                           desc_at(pd + kk * 2048 / 16 + desc_lbo(8192), kDescHiK), idPV,
+                           kk ? 1u : acc0);
+          mma_commit_elect(&S.kv_empty[m]);
+        }
+        constexpr uint32_t idL = idesc_bf16_f32(kRows, kH) | kIdescMajorB_MN;
+#pragma unroll
+        for (uint32_t kk = 0; kk < 8; ++kk)
+          mma_bf16_ta_elect(tmL, tmOnes, desc_at(pd + kk * 2048 / 16 + desc_lbo(8192), kDescHiK),
+                            idL, kk ? 1u : acc0);
+        mma_commit_elect(&S.p_empty);
+        if (last) mma_commit_elect(&S.o_full);
+      }
+      ++qn;
+    }
+    for (uint32_t it = i0; !FP4 && it < n_items && ok; it += i_step) {
       const uint32_t qi = item_q(it);
       if (rank * kRows >= rows_bound(P, qi)) continue;
       const QueryGeo g = query_geo<kScan>(P, qi, rank, C, lane);
@@ -745,25 +866,29 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
     }
   } else {
     // ------------------------------------------------------------ softmax + epilogue
-    const uint32_t r = threadIdx.x;          // tile row / TMEM lane, then dim within a block
-    const uint32_t lane_base = (warp * 32) << 16;
+    const uint32_t sq = warp & 3, hh = warp >> 2;   // TMEM quarter; half of the heads (4-bit rows)
+    const uint32_t r = 32 * sq + lane;       // tile row / TMEM lane, then dim within a block
+    const uint32_t lane_base = (sq * 32) << 16;
+    // heads of this thread: NPT parts of HB, the first from head hb0
+    constexpr uint32_t HB = FP4 ? NH / 2 : 32, NPT = FP4 ? 1 : NHF;
+    const uint32_t hb0 = FP4 ? hh * HB : 0u;
     uint32_t n = 0, qn = 0, sm_phase = 0;
-    // P of heads 32 hf .. + 31 of row r from their scores `a` with the current
+    // P of heads hb .. hb + HB - 1 of row r from their scores `a` with the current
     // running maxima; flags a score above its head's maximum by more than 2^8
-    auto p_half = [&](bool valid, const uint32_t (&a)[32], uint32_t hf, bool &flag) {
+    auto p_half = [&](bool valid, const uint32_t (&a)[HB], uint32_t hb, bool &flag) {
       uint8_t *prow = S.p + (r >> 3) * 1024 + (r & 7) * 128;
 #pragma unroll
-        for (uint32_t c4 = 0; c4 < 4; ++c4) {
+        for (uint32_t c4 = 0; c4 < HB / 8; ++c4) {
           uint32_t w4[4];
 #pragma unroll
           for (uint32_t e = 0; e < 4; ++e) {
-            const uint32_t hl = 8 * c4 + 2 * e, h = 32 * hf + hl;
+            const uint32_t hl = 8 * c4 + 2 * e, h = hb + hl;
             const float t0 = fmaf(__uint_as_float(a[hl]), P.c2, -S.mref[h]);
             const float t1 = fmaf(__uint_as_float(a[hl + 1]), P.c2, -S.mref[h + 1]);
             flag |= valid && (t0 > kRaiseLog2 || t1 > kRaiseLog2);
             w4[e] = valid ? pack_bf16(ex2_approx(t0), ex2_approx(t1)) : 0u;
           }
-          *reinterpret_cast<uint4 *>(prow + (((4 * hf + c4) ^ (r & 7)) << 4)) =
+          *reinterpret_cast<uint4 *>(prow + (((hb / 8 + c4) ^ (r & 7)) << 4)) =
               make_uint4(w4[0], w4[1], w4[2], w4[3]);
         }
     };
@@ -772,11 +897,11 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
     auto write_p = [&](bool valid) {
       bool flag = false;
 #pragma unroll
-      for (uint32_t hf = 0; hf < (uint32_t)NHF; ++hf) {
-        uint32_t a[32];
-        tmem_ld32(tmS + lane_base + 32 * hf, a);
+      for (uint32_t hf = 0; hf < NPT; ++hf) {
+        uint32_t a[HB];
+        tmem_ld(tmS + lane_base + hb0 + HB * hf, a);
         tmem_ld_wait();
-        p_half(valid, a, hf, flag);
+        p_half(valid, a, hb0 + HB * hf, flag);
       }
       return flag;
     };
@@ -812,7 +937,7 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
           // its code is fetched cold, and an unrolled form measured ~2 us of
           // instruction fetch
 #pragma unroll 1
-          for (uint32_t c = 0; c < (uint32_t)NH; c += 8) {
+          for (uint32_t c = hb0; c < hb0 + HB * NPT; c += 8) {
             uint32_t a8[8];
             tmem_ld8(tmS + lane_base + c, a8);
             tmem_ld_wait();
@@ -821,14 +946,14 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
               const uint32_t u = __float_as_uint(__uint_as_float(a8[j]) * P.c2);
               const uint32_t key = valid ? ((u & 0x80000000u) ? ~u : (u | 0x80000000u)) : 0u;
               const uint32_t mk = redux_max_u32(key);
-              if (lane == ((c + j) & 31)) tkey[warp * kH + c + j] = mk;
+              if (lane == ((c + j) & 31)) tkey[sq * kH + c + j] = mk;
             }
           }
-          if (r == 0) S.flagcnt[(n + 1) % 3] = 0;   // the next tile's raise count
+          if (threadIdx.x == 0) S.flagcnt[(n + 1) % 3] = 0;   // the next tile's raise count
           if (!group_sync(&S.sm_bar, sm_phase, ew)) goto done_softmax;
           const uint32_t k0 = max(max(tkey[0 * kH], tkey[1 * kH]), max(tkey[2 * kH], tkey[3 * kH]));
           any_valid = k0 != 0u;   // a valid row has a key above 0 for every head
-          if (r < (uint32_t)NH) {
+          if (threadIdx.x < (uint32_t)NH) {
             const uint32_t mk = max(max(tkey[0 * kH + r], tkey[1 * kH + r]),
                                     max(tkey[2 * kH + r], tkey[3 * kH + r]));
             const float mx = __uint_as_float((mk & 0x80000000u) ? (mk & 0x7fffffffu) : ~mk);
@@ -838,18 +963,23 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
           if (!mbar_wait_warp(&S.p_empty, (n & 1) ^ 1, ew)) goto done_softmax;
           // the scores (S stays until this tile's P is done)
           bool unused = false;
-          if (NHF == 2) {
+          if (FP4) {
+            uint32_t a0[HB];
+            tmem_ld(tmS + lane_base + hb0, a0);
+            tmem_ld_wait();
+            p_half(valid, a0, hb0, unused);
+          } else if (NHF == 2) {
             uint32_t a0[32], a1[32];
             tmem_ld32(tmS + lane_base, a0);
             tmem_ld32(tmS + lane_base + 32, a1);
             tmem_ld_wait();
-            p_half(valid, a0, 0, unused);
-            p_half(valid, a1, 1, unused);
+            p_half(valid, *reinterpret_cast<uint32_t(*)[HB]>(a0), 0, unused);
+            p_half(valid, *reinterpret_cast<uint32_t(*)[HB]>(a1), 32, unused);
           } else {
             uint32_t a0[32];
             tmem_ld32(tmS + lane_base, a0);
             tmem_ld_wait();
-            p_half(valid, a0, 0, unused);
+            p_half(valid, *reinterpret_cast<uint32_t(*)[HB]>(a0), 0, unused);
           }
           fence_proxy_async();
           tc_fence_before();
@@ -860,25 +990,26 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
         if (!mbar_wait_warp(&S.p_empty, (n & 1) ^ 1, ew)) goto done_softmax;
         const bool flag = write_p(valid);
         const uint32_t fc = n % 3;
-        if (r == 0) S.flagcnt[(n + 1) % 3] = 0;
+        if (threadIdx.x == 0) S.flagcnt[(n + 1) % 3] = 0;
         if (flag) atomicAdd(&S.flagcnt[fc], 1u);
         if (!group_sync(&S.sm_bar, sm_phase, ew)) goto done_softmax;
         if (S.flagcnt[fc] != 0) {
           // rare path: exact tile max per head, raise the running max, rescale
           // O and L, rewrite P
 #pragma unroll 1
-          for (uint32_t hf = 0; hf < (uint32_t)NHF; ++hf) {
-            uint32_t a[32];
-            tmem_ld32(tmS + lane_base + 32 * hf, a);
+          for (uint32_t hf = 0; hf < NPT; ++hf) {
+            const uint32_t hb = hb0 + HB * hf;
+            uint32_t a[HB];
+            tmem_ld(tmS + lane_base + hb, a);
             tmem_ld_wait();
 #pragma unroll
-            for (int h = 0; h < 32; ++h) {
+            for (uint32_t h = 0; h < HB; ++h) {
               const float v = warp_max(valid ? __uint_as_float(a[h]) * P.c2 : -INFINITY);
-              if (lane == (uint32_t)h) S.tmax[warp][32 * hf + h] = v;
+              if (lane == h) S.tmax[sq][hb + h] = v;
             }
           }
           if (!group_sync(&S.sm_bar, sm_phase, ew)) goto done_softmax;
-          if (r < (uint32_t)NH) {
+          if (threadIdx.x < (uint32_t)NH) {
             const float M = fmaxf(fmaxf(S.tmax[0][r], S.tmax[1][r]), fmaxf(S.tmax[2][r], S.tmax[3][r]));
             const float mo = S.mref[r], mn = fmaxf(mo, M);
             S.alpha[r] = exp2f(mo - mn);
@@ -887,7 +1018,7 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
           if (!group_sync(&S.sm_bar, sm_phase, ew)) goto done_softmax;
           if (!first) {
 #pragma unroll 1
-            for (uint32_t m = 0; m < 5 * (uint32_t)NHF; ++m) {   // O^T (4 dim blocks) then L
+            for (uint32_t m = FP4 ? hh : 0u; m < 5 * (uint32_t)NHF; m += FP4 ? 2 : 1) {   // O^T (4 dim blocks) then L
               uint32_t a[32];
               const uint32_t blk = m / NHF, hf = m % NHF;
               const uint32_t ta = (blk < 4 ? tmO + blk * kH : tmL) + 32 * hf + lane_base;
@@ -925,12 +1056,12 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
       if (!group_sync(&S.sm_bar, sm_phase, ew)) goto done_softmax;
       if (dec && C > 1) {
         // (max, sum) of this rank for the cluster merge; O follows from TMEM
-        if (r < (uint32_t)NH) {
+        if (threadIdx.x < (uint32_t)NH) {
           float *ml = P.ml + ((size_t)(vq * C + rank) * NH + r) * 2;
           ml[0] = (has_tiles && any_valid) ? S.mref[r] : -INFINITY;
           ml[1] = has_tiles ? S.lsh[r] : 0.f;
         }
-        if (r == 0) S.has_tiles = has_tiles ? 1u : 0u;
+        if (threadIdx.x == 0) S.has_tiles = has_tiles ? 1u : 0u;
       } else {
         // normalise, rotate the tail back by -p and store bf16 pairs straight
         // from registers, four 128-dim chunks (no staging, no barrier)
@@ -944,21 +1075,30 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
         auto linv = [&](int h) { return FP4 ? S.linv[h] : li[FP4 ? 0 : h]; };
         const bool odd = lane & 1;
 #pragma unroll 1
-        for (uint32_t m = 0; m < 4; ++m) {
+        for (uint32_t m = FP4 ? 2 * hh : 0u; m < (FP4 ? 2 * hh + 2 : 4u); ++m) {
           const bool rot = m == 3 && r >= 64;   // warp-uniform: the rotated tail dims
           const float co = ep_co, si = ep_si;   // (the pair's coefficients: both lanes)
           __nv_bfloat16 *o = P.out + ((size_t)qi * HQ + hq0) * kD + m * 128;
-          uint32_t ab[NHF][32];
+          // (4-bit rows: the two head halves one after the other, for the registers)
+          constexpr uint32_t NB = FP4 ? 1 : NHF;
+          uint32_t ab[NB][32];
+          if (!FP4) {
 #pragma unroll
-          for (uint32_t hf = 0; hf < (uint32_t)NHF; ++hf)
-            tmem_ld32(tmO + lane_base + m * kH + 32 * hf, ab[hf]);
-          tmem_ld_wait();
+            for (uint32_t hf = 0; hf < (uint32_t)NHF; ++hf)
+              tmem_ld32(tmO + lane_base + m * kH + 32 * hf, ab[FP4 ? 0 : hf]);
+            tmem_ld_wait();
+          }
 #pragma unroll
           for (uint32_t hf = 0; hf < (uint32_t)NHF; ++hf) {
+            uint32_t(&a32)[32] = ab[FP4 ? 0 : hf];
+            if (FP4) {
+              tmem_ld32(tmO + lane_base + m * kH + 32 * hf, a32);
+              tmem_ld_wait();
+            }
 #pragma unroll
             for (int h = 0; h < 32; h += 2) {
-              const float v0 = __uint_as_float(ab[hf][h]) * linv(32 * hf + h);
-              const float v1 = __uint_as_float(ab[hf][h + 1]) * linv(32 * hf + h + 1);
+              const float v0 = __uint_as_float(a32[h]) * linv(32 * hf + h);
+              const float v1 = __uint_as_float(a32[h + 1]) * linv(32 * hf + h + 1);
               // lanes 2i, 2i + 1 hold dims d, d + 1 of heads h, h + 1: one
               // swap gives the even lane head h's pair and the odd lane head
               // h + 1's, rotated in place and stored as one bf16 pair
@@ -1060,7 +1200,8 @@ int max_active_clusters(uint32_t C, size_t smem) {
       };
       np = allow(attn_tc_kernel<true, false, false, kNhDec>) &&
                    allow(attn_tc_kernel<true, true, false, kNhDec>) &&
-                   allow(attn_tc_kernel<true, true, true, kNhDec>)
+                   allow(attn_tc_kernel<true, true, true, kNhDec>) &&
+                   allow(attn_tc_kernel<true, true, true, kH>)
                ? 1
                : -1;
       (void)cudaGetLastError();
@@ -1128,14 +1269,22 @@ uint32_t decode_cluster(uint32_t rows_max, uint32_t n_q, size_t smem) {
   return pick_cluster(n_tiles, n_q, smem);
 }
 
+// Heads per CTA of a decode launch over 4-bit rows.
+uint32_t decode_heads(uint32_t n_heads, uint32_t rows_max, uint32_t n_q) {
+  // (twice as many CTAs of half the heads only while they all run at once)
+  const uint32_t tiles = (rows_max + kRows - 1) / kRows;
+  return n_heads > (uint32_t)kNhDec && (uint64_t)n_q * tiles * 2 > (uint64_t)num_sms() ? kH : kNhDec;
+}
+
 }  // namespace
 
 void attn_tc_force_cluster(uint32_t C) {
   g_force_cluster.store(C > kMaxCluster ? kMaxCluster : C, std::memory_order_relaxed);
 }
 
-uint32_t attn_tc_decode_cluster(uint32_t rows_max, uint32_t n_q, uint32_t n_heads) {
-  return decode_cluster(rows_max, n_q * (n_heads + kNhDec - 1) / kNhDec, sizeof(Smem) + 1024);
+uint32_t attn_tc_decode_cluster(uint32_t rows_max, uint32_t n_q, uint32_t n_heads, bool fp4) {
+  const uint32_t nh = fp4 ? decode_heads(n_heads, rows_max, n_q) : kNhDec;
+  return decode_cluster(rows_max, n_q * ((n_heads + nh - 1) / nh), sizeof(Smem) + 1024);
 }
 
 // (4-bit rows: any number of heads)
@@ -1149,7 +1298,7 @@ size_t attn_tc_ws_bytes(uint32_t batch, uint32_t T, uint32_t rows_max, uint32_t 
   const uint32_t n_tiles = (rows_max + kRows - 1) / kRows;
   const uint32_t cmax = n_tiles < kMaxCluster ? (n_tiles ? n_tiles : 1u) : kMaxCluster;
   if (cmax < 2) return 256;
-  const uint32_t heads = (n_heads + kNhDec - 1) / kNhDec * kNhDec;   // whole groups
+  const uint32_t heads = (n_heads + kH - 1) / kH * kH;   // whole groups
   return 256 + (size_t)batch * cmax * heads * (kD * sizeof(__nv_bfloat16) + 2 * sizeof(float));
 }
 
@@ -1183,18 +1332,19 @@ cudaError_t launch_attention_tc(const AttnArgs &a, uint32_t rows_max, int *err, 
   // paged rows: an instantiation of its own, so the contiguous gathers carry
   // no table code
   const bool paged = a.map.table != nullptr, fp4 = a.fp4;
-  auto *k_dec = fp4     ? attn_tc_kernel<true, true, true, kNhDec>
+  const uint32_t nh = a.T > 1 ? kH : fp4 ? decode_heads(a.n_heads, rows_max, P.n_q) : kNhDec;
+  auto *k_dec = fp4     ? (nh == kH ? attn_tc_kernel<true, true, true, kH>
+                                    : attn_tc_kernel<true, true, true, kNhDec>)
                 : paged ? attn_tc_kernel<true, true, false, kNhDec>
                         : attn_tc_kernel<true, false, false, kNhDec>;
   auto *k_pf = fp4     ? attn_tc_kernel<false, true, true, kH>
                : paged ? attn_tc_kernel<false, true, false, kH>
                        : attn_tc_kernel<false, false, false, kH>;
-  const uint32_t nh = a.T == 1 ? kNhDec : kH;
   P.n_heads = a.n_heads;
   P.hg = (a.n_heads + nh - 1) / nh;
-  static DeviceSmem smem_set[2][3];
+  static DeviceSmem smem_set[2][4];
   cudaError_t e = ensure_smem(a.T == 1 ? k_dec : k_pf, smem,
-                              smem_set[a.T == 1][fp4 ? 2 : paged].here());
+                              smem_set[a.T == 1][fp4 ? 2 + (nh == kH) : paged].here());
   if (e != cudaSuccess) return e;
   CUtensorMap tq;
   if (fp4) {   // Q as [n_q][H][512]: boxes of one CTA's heads, zeros past the last head
@@ -1233,7 +1383,7 @@ cudaError_t launch_attention_tc(const AttnArgs &a, uint32_t rows_max, int *err, 
     // one cluster of P.cluster CTAs per (query, head group)
     const uint32_t n_vq = P.n_q * P.hg;
     P.cluster = decode_cluster(rows_max, n_vq, smem);
-    P.ml = reinterpret_cast<float *>(P.part + (size_t)n_vq * P.cluster * kNhDec * kD);
+    P.ml = reinterpret_cast<float *>(P.part + (size_t)n_vq * P.cluster * nh * kD);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;

@@ -191,7 +191,7 @@ cudaError_t launch_attention_tc(const AttnArgs &a, uint32_t rows_max, int *err, 
 // Decode cluster size: forced process-wide (0 = automatic), and the size a
 // decode launch of `n_q` queries with at most `rows_max` rows each uses.
 void attn_tc_force_cluster(uint32_t C);
-uint32_t attn_tc_decode_cluster(uint32_t rows_max, uint32_t n_q, uint32_t n_heads);
+uint32_t attn_tc_decode_cluster(uint32_t rows_max, uint32_t n_q, uint32_t n_heads, bool fp4);
 // The same for the arguments of a decode call whose token is at position
 // pos_end - 1: 0 when it does not run on the tensor-core kernel.
 uint32_t attn_decode_cluster(int dtype, uint32_t ratio, uint32_t batch, uint32_t n_heads,
