@@ -89,9 +89,9 @@ struct TcAttnParams {
   const uint32_t *seq_pos;   // [B] per-sequence positions (ragged decode) or NULL
   uint32_t cluster;   // decode: CTAs per query (one cluster); 0: prefill, persistent CTAs
   // decode tiles of contiguous rows by TMA instead of row gathers (ratios 0
-  // and 128): bit 0 the window tile as the whole 128-slot ring, bit 1 (ratio
-  // 128) the compressed tiles (the visible rows, the same count for every
-  // sequence)
+  // and 128; 4-bit rows: every ratio): bit 0 the window tile as the whole 128-slot
+  // ring, bit 1 (ratio 128) the compressed tiles (the visible rows, the same count for
+  // every sequence); bit 2 (4-bit rows, chunk): a window inside the chunk
   uint32_t tma_rows;
   uint32_t n_q;       // queries = batch * T
   float c2;           // softmax scale * log2(e)
@@ -123,12 +123,22 @@ struct Smem {
   float mw[kH][kMaxCluster];        // decode merge: weight of each rank, per owned head
   uint32_t flagcnt[3], tmem, has_tiles;
 };
+// 4-bit rows, ratio 4: the top-k lists of the query in work and the next one as pool
+// rows (kNoRow: masked), staged by the loaders for every role; lists above kList entries
+// take both halves, one query at a time
+constexpr uint32_t kList = 1024, kNoRow = 0xffffffffu;
+struct SmemFp4 : Smem {
+  uint32_t rows[2 * kList];
+  uint32_t wend[2][8];            // per loader warp: first entry that ends the list
+  uint64_t geo_full[2], geo_empty[2], ld_bar;
+};
 // the merge pulls at most C * ceil(64 / C) rows of 1 KiB (75 at C = 15)
 constexpr uint32_t max_pulled_rows(uint32_t C = 1) {
   return C > kMaxCluster ? 0u
                          : (C * ((kH + C - 1) / C) > max_pulled_rows(C + 1) ? C * ((kH + C - 1) / C)
                                                                              : max_pulled_rows(C + 1));
 }
+static_assert(sizeof(SmemFp4) + 1024 <= 227 * 1024, "one block's shared memory");
 static_assert(8 * kKBlk >= max_pulled_rows() * kD * 2, "pulled slices fit the row buffer");
 static_assert(2 * kH * 128 == kRows * 128, "output staging fills the P buffer");
 
@@ -151,9 +161,11 @@ struct QueryGeo {
 // rows past its visible ones). A decode list holds visible rows, then -1, so
 // decode takes the bound min(top_k, visible) and masks the -1 entries row by
 // row, with no dependent list read before the first gather.
+// n_list: the length of a ratio-4 list where it is known (4-bit rows).
 template <bool SCAN>
 __device__ __forceinline__ QueryGeo query_geo(const TcAttnParams &P, uint32_t qi, uint32_t t0,
-                                              uint32_t ts, uint32_t lane) {
+                                              uint32_t ts, uint32_t lane,
+                                              uint32_t n_list = kNoRow) {
   QueryGeo g;
   g.qi = qi;
   g.b = qi / P.T;
@@ -162,7 +174,9 @@ __device__ __forceinline__ QueryGeo query_geo(const TcAttnParams &P, uint32_t qi
   g.n_w = min(g.p + 1, P.cap_raw);
   g.tk = P.topk ? P.topk + (size_t)qi * P.top_k : nullptr;
   g.n_list = 0;
-  if (P.ratio == 4 && !SCAN) {
+  if (n_list != kNoRow) {
+    g.n_list = n_list;
+  } else if (P.ratio == 4 && !SCAN) {
     g.n_list = min(P.top_k, min((g.p + 1) / 4, P.n_comp));
   } else if (P.ratio == 4) {
     const uint32_t vis = min((g.p + 1) / 4, P.n_comp);
@@ -198,10 +212,13 @@ __device__ __forceinline__ QueryGeo query_geo(const TcAttnParams &P, uint32_t qi
 
 // How tile `tile` of a decode query loads: 0 row gathers, 1 the whole ring
 // by TMA (the window of 128 rows, in slot order: the softmax does not depend
-// on the order of the rows), 2 compressed rows 128 (tile - 1) .. by TMA.
-template <bool DEC, bool PAGED>
+// on the order of the rows), 2 compressed rows 128 (tile - 1) .. by TMA, 3 (4-bit
+// rows, chunk) a window that lies in the chunk, by TMA.
+template <bool DEC, bool PAGED, bool FP4 = false>
 __device__ __forceinline__ uint32_t tile_kind(const TcAttnParams &P, const QueryGeo &g,
                                               uint32_t tile) {
+  if (FP4 && !DEC)
+    return tile == 0 && (P.tma_rows & 4u) && g.p - g.p0 >= (uint32_t)kRows - 1 ? 3u : 0u;
   if (!DEC || g.n_w != (uint32_t)kRows) return 0;
   if (tile == 0) return (P.tma_rows & 1u) ? 1u : 0u;
   return (!PAGED && (P.tma_rows & 2u) && P.ratio == 128) ? 2u : 0u;
@@ -372,7 +389,9 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
                                         ~(uintptr_t)1023);
   else
     sbase = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  Smem &S = *reinterpret_cast<Smem *>(sbase);
+  using SmemT = typename std::conditional<FP4, SmemFp4, Smem>::type;
+  SmemT &S = *reinterpret_cast<SmemT *>(sbase);
+  SmemFp4 &S4 = *reinterpret_cast<SmemFp4 *>(sbase);   // (4-bit rows only)
   // (4-bit rows: the same for the compiler too, so that the MMA issuer's branch and
   // its descriptors are warp-uniform)
   const uint32_t warp = FP4 ? uniform(threadIdx.x >> 5) : threadIdx.x >> 5;
@@ -385,7 +404,19 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
   constexpr int NHF = HS::NHF, QBLK = HS::QBLK;
   // head groups of a query and its heads; 4-bit rows take any number of heads
   const uint32_t HG = FP4 ? P.hg : (uint32_t)HS::HG, HQ = FP4 ? P.n_heads : (uint32_t)kH;
-  constexpr bool kScan = !DEC || FP4;   // read the list for its end (see query_geo)
+  constexpr bool kScan = !DEC && !FP4;   // read the list for its end (see query_geo)
+  // 4-bit rows, ratio 4: half `gb` of the staged lists (gn: lists before this one), the
+  // length of the list in it, and its release
+  const bool staged = FP4 && P.ratio == 4;
+  const uint32_t n_half = P.top_k <= kList ? 2u : 1u;
+  auto list_half = [&](uint32_t gn) { return n_half == 2 ? gn & 1 : 0u; };
+  auto list_phase = [&](uint32_t gn) { return (n_half == 2 ? gn >> 1 : gn) & 1; };
+  auto list_end = [&](uint32_t gb) {
+    uint32_t e = P.top_k;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) e = min(e, S4.wend[gb][w]);
+    return e;
+  };
   const uint32_t C = dec ? P.cluster : 1u;
   const uint32_t rank = dec ? cluster_ctarank() : 0u;
   const uint32_t vq = dec ? blockIdx.x / C : 0u;          // decode: (query, head group)
@@ -417,11 +448,18 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
     mbar_init(&S.p_full, WP::ST);
     mbar_init(&S.p_empty, 1);
     mbar_init(&S.o_full, 1);
-    mbar_init(&S.o_empty, WP::NS);
+    mbar_init(&S.o_empty, FP4 && !DEC ? WP::NS + WP::NL : WP::NS);
     mbar_init(&S.sm_bar, WP::ST);
     mbar_init(&S.q_tma, 1);
     mbar_init(&S.kv_tma, 1);
     mbar_init(&S.mg_bar, 1);
+    if (FP4) {
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&S4.geo_full[i], 1);
+        mbar_init(&S4.geo_empty[i], WP::NS + 1);   // softmax warps and the MMA issuer
+      }
+      mbar_init(&S4.ld_bar, WP::LT);
+    }
     S.flagcnt[0] = S.flagcnt[1] = S.flagcnt[2] = 0;
     fence_mbar_init();
     prefetch_tmap(&tmap_q);
@@ -458,6 +496,97 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
   // this launch's view of the error word (see ErrWord), read before the wait
   // so that its latency overlaps the previous launch
   const ErrWord ew{P.err, err_base};
+  auto wait_warp = [&](uint64_t *bar, uint32_t parity, ErrWord e) {
+    return FP4 ? mbar_wait_sleep(bar, parity, e) : mbar_wait_warp(bar, parity, e);
+  };
+  auto sync_group = [&](uint64_t *bar, uint32_t &phase, ErrWord e) {
+    return FP4 ? group_sync_sleep(bar, phase, e) : group_sync(bar, phase, e);
+  };
+
+  // Chunks over 4-bit rows: a query's output is written by the softmax warps (dim
+  // blocks 0 and 1) and the loaders (2 and 3), both idle between its last tile and the
+  // first tile of the next query, whose PV waits for o_empty. Warp w has TMEM quarter
+  // w % 4 and 32 heads; lanes 2 i, 2 i + 1 hold dims d, d + 1 and swap so that each
+  // stores bf16 pairs of its own heads.
+  float out_co = 1.f, out_si = 0.f;   // the rotation of this thread's dim (tail dims)
+  auto out_coef = [&](uint32_t p) {   // (TMEM quarters 2, 3: dims 64 .. 127 of a block)
+    if ((warp & 2) != 0) {
+      const uint32_t fi = (32 * (warp & 3) + lane - 64) >> 1;
+      out_co = P.cos[(size_t)p * 32 + fi];
+      out_si = P.sin[(size_t)p * 32 + fi];
+    }
+  };
+  auto write_out = [&](uint32_t it, uint32_t qn_prev, uint32_t m0) -> bool {
+    const uint32_t qi = item_q(it), sq = warp & 3, hf = (warp >> 2) & 1;
+    const uint32_t h0 = item_h(it) + 32 * hf, r = 32 * sq + lane, lane_base = (32 * sq) << 16;
+    const float co = out_co, si = out_si;
+    if (!wait_warp(&S.o_full, qn_prev & 1, ew)) return false;
+    tc_fence_after();
+    const bool odd = lane & 1;
+    uint32_t a[2][16];   // sixteen heads at a time, the next load in flight
+    float li[32];        // every TMEM row of L holds the sums
+#pragma unroll
+    for (int hs = 0; hs < 2; ++hs) tmem_ld16(tmL + lane_base + 32 * hf + 16 * hs, a[hs]);
+    tmem_ld_wait();
+#pragma unroll
+    for (int h = 0; h < 32; ++h) {
+      const float l = __uint_as_float(a[h / 16][h % 16]);
+      li[h] = l > 0.f ? __fdividef(1.f, l) : 0.f;
+    }
+    __nv_bfloat16 *o = P.out + ((size_t)qi * HQ + h0) * kD + 128 * m0 + (r & ~1u);
+    const uint32_t live = HQ > h0 ? HQ - h0 : 0u;   // heads there are
+    tmem_ld16(tmO + lane_base + m0 * kH + 32 * hf, a[0]);
+#pragma unroll 1
+    for (uint32_t m = m0; m < m0 + 2; ++m, o += 128) {
+#pragma unroll
+      for (uint32_t hs = 0; hs < 2; ++hs) {
+        tmem_ld_wait();
+        if (hs == 0)
+          tmem_ld16(tmO + lane_base + m * kH + 32 * hf + 16, a[1]);
+        else if (m == m0)
+          tmem_ld16(tmO + lane_base + (m + 1) * kH + 32 * hf, a[0]);
+        else {   // everything read: the next query's PV may start
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&S.o_empty);
+        }
+        const uint32_t(&x)[16] = a[hs];
+        if (m == 3 && sq >= 2) {   // the rotated tail, back by -p, in fp32
+#pragma unroll
+          for (uint32_t h = 0; h < 16; h += 2) {
+            const float v0 = __uint_as_float(x[h]) * li[16 * hs + h];
+            const float v1 = __uint_as_float(x[h + 1]) * li[16 * hs + h + 1];
+            const float recv = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
+            const float x0 = odd ? recv : v0, x1 = odd ? v1 : recv;
+            const uint32_t row = 16 * hs + h + (odd ? 1u : 0u);
+            if (row < live)
+              *reinterpret_cast<uint32_t *>(o + (size_t)row * kD) =
+                  pack_bf16(x0 * co + x1 * si, -x0 * si + x1 * co);
+          }
+        } else {
+#pragma unroll
+          for (uint32_t h = 0; h < 16; h += 4) {
+            const uint32_t w0 = pack_bf16(__uint_as_float(x[h]) * li[16 * hs + h],
+                                          __uint_as_float(x[h + 1]) * li[16 * hs + h + 1]);
+            const uint32_t w1 = pack_bf16(__uint_as_float(x[h + 2]) * li[16 * hs + h + 2],
+                                          __uint_as_float(x[h + 3]) * li[16 * hs + h + 3]);
+            // even lanes keep heads h, h + 2, odd lanes h + 1, h + 3
+            const uint32_t mine = __byte_perm(w0, w1, odd ? 0x7632 : 0x5410);
+            const uint32_t give = __byte_perm(w0, w1, odd ? 0x5410 : 0x7632);
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, give, 1);
+            const uint32_t lo = odd ? got : mine, hi = odd ? mine : got;
+            const uint32_t row = 16 * hs + h + (odd ? 1u : 0u);
+            if (row < live)
+              *reinterpret_cast<uint32_t *>(o + (size_t)row * kD) = __byte_perm(lo, hi, 0x5410);
+            if (row + 2 < live)
+              *reinterpret_cast<uint32_t *>(o + (size_t)(row + 2) * kD) =
+                  __byte_perm(lo, hi, 0x7632);
+          }
+        }
+      }
+    }
+    return true;
+  };
 
   if (loader) {
     // ------------------------------------------------------------ loaders
@@ -470,7 +599,7 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
     auto issue_tile = [&](const QueryGeo &g, uint32_t tile, uint32_t n) -> bool {
       if (const uint32_t kind = tile_kind<DEC, PAGED>(P, g, tile)) {
         for (uint32_t kb = 0; kb < 8; ++kb) {
-          if ((kb & 1) == 0 && !mbar_wait_warp(&S.kv_empty[kb >> 1], (n & 1) ^ 1, ew)) return false;
+          if ((kb & 1) == 0 && !wait_warp(&S.kv_empty[kb >> 1], (n & 1) ^ 1, ew)) return false;
           if (lt == 0) {
             if (kb == 0) mbar_arrive_expect_tx(&S.kv_tma, 8 * kKBlk);
             if (kind == 1)
@@ -488,7 +617,7 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
         src[i] = row_src<PAGED>(P, g, tile * kRows + lw * 32 + (lane >> 3) + 4 * i);
       const uint32_t cc = lane & 7;
       for (uint32_t kb = 0; kb < 8; ++kb) {
-        if ((kb & 1) == 0 && !mbar_wait_warp(&S.kv_empty[kb >> 1], (n & 1) ^ 1, ew)) return false;
+        if ((kb & 1) == 0 && !wait_warp(&S.kv_empty[kb >> 1], (n & 1) ^ 1, ew)) return false;
         uint8_t *slot = S.kv + kb * kKBlk;
 #pragma unroll
         for (uint32_t i = 0; i < 8; ++i) {
@@ -503,52 +632,124 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
     };
     // ---- 4-bit rows: thread lt holds lane lt % 8 of rows lt / 8 + 32 i. fetch_tile
     // loads their records into registers (12 16-byte loads in flight, each warp
-    // load 128 contiguous bytes of four rows; rows found by find_tile); store_tile converts them block pair by
+    // load 128 contiguous bytes of four rows); store_tile converts them block pair by
     // block pair as the tile's slots free up. The next tile's records load while
     // this one's MMAs run.
     constexpr uint32_t kFR = FP4 ? kRows * 8 / WP::LT : 1;   // rows per thread
     uint4 rec[kFR][3];
-    uint32_t nxt[kFR];                    // pool rows of the next tile, or kNoRow
-    uint32_t cur_raw = 0, nxt_raw = 0;    // bit i: row i is in bf16 (the window)
-    constexpr uint32_t kNoRow = 0xffffffffu;
-    // where the rows of a tile are (list and table reads: one tile further ahead)
-    auto find_tile = [&](const QueryGeo &g, uint32_t tile) {
-      nxt_raw = 0;
-      const uint32_t sh = P.ratio == 4 ? 6u : 1u;   // log2 of the rows per block
+    uint32_t tbl[kFR] = {};   // ratio 128, paged: table entries of the next tile's rows
+    uint32_t cur_raw = 0;     // bit i: row i is in bf16 (the window)
+    uint32_t gn = 0, gb = 0, ld_phase = 0;   // lists staged, the current one's half
+    uint32_t n_next = 0;                     // length of the next query's list
+    const uint32_t rsh = P.ratio == 4 ? 6u : 1u;   // log2 of the rows per block
+    auto list_row = [&](uint32_t g_b, uint32_t idx, uint32_t blk) {
+      // (as RowMap::phys: table entries outside the pool read block 0)
+      if (P.map.table) return ((blk < P.map.n_blocks ? blk : 0u) << rsh) + (idx & ((1u << rsh) - 1));
+      return g_b * P.comp_cap + idx;     // (fewer than 2^32: launch check)
+    };
+    auto table_at = [&](uint32_t g_b, uint32_t idx) -> const int32_t * {
+      const uint32_t lb = min(idx >> rsh, P.map.max_blocks - 1);
+      return P.map.table + (size_t)g_b * P.map.max_blocks + lb;
+    };
+    // The list of a ratio-4 query as pool rows in shared memory. stage_load starts the
+    // loads of up to kList entries (a chunk does so a few tiles ahead of the query),
+    // stage_list finishes them, or does it all for longer lists; it returns the list's
+    // length (kNoRow: a wait gave up).
+    auto stage_load = [&](uint32_t qi) {
+      const int32_t *tk = P.topk + (size_t)qi * P.top_k;
+#pragma unroll
+      for (uint32_t i = 0; i < kFR; ++i) {
+        const uint32_t e = lt + WP::LT * i;
+        tbl[i] = e < P.top_k ? ld_nc_u32(tk + e) : kNoRow;
+      }
+    };
+    auto stage_list = [&](uint32_t qi) -> uint32_t {
+      gb = list_half(gn);
+      const uint32_t b = qi / P.T, p = seq_base(P.seq_pos, P.pos0, b) + qi % P.T;
+      const uint32_t vis = min((p + 1) / 4, P.n_comp);
+      if (!wait_warp(&S4.geo_empty[gb], list_phase(gn) ^ 1, ew)) return kNoRow;
+      uint32_t end = kNoRow;
+      for (uint32_t base = 0; base < P.top_k; base += kList) {
+        uint32_t blk[kFR];
+        if (base) {
+#pragma unroll
+          for (uint32_t i = 0; i < kFR; ++i) {
+            const uint32_t e = base + lt + WP::LT * i;
+            tbl[i] = e < P.top_k ? ld_nc_u32(P.topk + (size_t)qi * P.top_k + e) : kNoRow;
+          }
+        }
+#pragma unroll
+        for (uint32_t i = 0; i < kFR; ++i) {
+          blk[i] = 0;
+          if ((int32_t)tbl[i] >= 0 && tbl[i] >= vis) {
+            end = min(end, base + lt + WP::LT * i);
+            tbl[i] = kNoRow;
+          }
+          if (P.map.table && (int32_t)tbl[i] >= 0) blk[i] = ld_nc_u32(table_at(b, tbl[i]));
+        }
+#pragma unroll
+        for (uint32_t i = 0; i < kFR; ++i) {
+          const uint32_t e = base + lt + WP::LT * i;
+          if (e < P.top_k)
+            S4.rows[gb * kList + e] = (int32_t)tbl[i] >= 0 ? list_row(b, tbl[i], blk[i]) : kNoRow;
+        }
+      }
+      end = redux_min_u32(end);
+      if (lane == 0) S4.wend[gb][lw] = end;
+      if (!sync_group(&S4.ld_bar, ld_phase, ew)) return kNoRow;
+      if (lt == 0) mbar_arrive(&S4.geo_full[gb]);
+      ++gn;
+      return list_end(gb);
+    };
+    // the table entries that the fetch of a tile will need (a tile ahead of it)
+    auto look_tile = [&](const QueryGeo &g, uint32_t tile) {
+      if (staged || !P.map.table) return;
 #pragma unroll
       for (uint32_t i = 0; i < kFR; ++i) {
         const uint32_t r = tile * kRows + (lt >> 3) + 32 * i;
-        nxt[i] = kNoRow;
-        if (r < g.n_w) {
-          nxt_raw |= 1u << i;
-        } else if (r < g.N) {
-          const uint32_t e = r - g.n_w;
-          const int32_t idx = P.ratio == 4 ? g.tk[e] : (int32_t)e;
-          if (idx >= 0) {
-            uint32_t row = g.b * P.comp_cap + (uint32_t)idx;   // (fewer than 2^32: launch check)
-            if (P.map.table) {   // (as RowMap::phys: entries outside the pool read block 0)
-              const uint32_t lb = (uint32_t)idx >> sh;
-              uint32_t blk = lb < P.map.max_blocks
-                                 ? (uint32_t)__ldg(P.map.table + (size_t)g.b * P.map.max_blocks + lb)
-                                 : 0u;
-              if (blk >= P.map.n_blocks) blk = 0;
-              row = (blk << sh) + ((uint32_t)idx & ((1u << sh) - 1));
-            }
-            nxt[i] = row;
-          }
-        }
+        tbl[i] = r >= g.n_w && r < g.N ? ld_nc_u32(table_at(g.b, r - g.n_w)) : 0u;
       }
     };
-    auto fetch_tile = [&]() {
-      cur_raw = nxt_raw;
+    auto fetch_tile = [&](const QueryGeo &g, uint32_t tile) {
+      cur_raw = 0;
 #pragma unroll
       for (uint32_t i = 0; i < kFR; ++i) {
-        // (a masked row: zeros)
-        const uint8_t *src = reinterpret_cast<const uint8_t *>(P.comp) +
-                             (size_t)nxt[i] * kFp4RowBytes + 16 * (lt & 7);
+        const uint32_t r = tile * kRows + (lt >> 3) + 32 * i;
+        uint32_t row = kNoRow;   // (a masked row: zeros)
+        if (r < g.n_w) cur_raw |= 1u << i;
+        else if (r < g.N)
+          row = staged ? S4.rows[gb * kList + (r - g.n_w)] : list_row(g.b, r - g.n_w, tbl[i]);
+        const uint8_t *src = reinterpret_cast<const uint8_t *>(P.comp) + (size_t)row * kFp4RowBytes +
+                             16 * (lt & 7);
 #pragma unroll
         for (uint32_t v = 0; v < 3; ++v)
-          rec[i][v] = nxt[i] != kNoRow ? ld_nc_v4(src + 128 * v) : make_uint4(0u, 0u, 0u, 0u);
+          rec[i][v] = row != kNoRow ? ld_nc_v4(src + 128 * v) : make_uint4(0u, 0u, 0u, 0u);
+      }
+    };
+    // Decode, ratio 4: the records of this rank's first tile straight from the list, so that
+    // they load while the list is staged.
+    auto fetch_first = [&](uint32_t qi) {
+      const uint32_t b = qi / P.T, p = seq_base(P.seq_pos, P.pos0, b) + qi % P.T;
+      const uint32_t n_w = min(p + 1, P.cap_raw), vis = min((p + 1) / 4, P.n_comp);
+      const int32_t *tk = P.topk + (size_t)qi * P.top_k;
+      uint32_t idx[kFR], blk[kFR];
+      cur_raw = 0;
+#pragma unroll
+      for (uint32_t i = 0; i < kFR; ++i) {
+        const uint32_t r = rank * kRows + (lt >> 3) + 32 * i;
+        if (r < n_w) cur_raw |= 1u << i;
+        idx[i] = r >= n_w && r - n_w < P.top_k ? ld_nc_u32(tk + (r - n_w)) : kNoRow;
+      }
+#pragma unroll
+      for (uint32_t i = 0; i < kFR; ++i)
+        blk[i] = P.map.table && idx[i] < vis ? ld_nc_u32(table_at(b, idx[i])) : 0u;
+#pragma unroll
+      for (uint32_t i = 0; i < kFR; ++i) {
+        const uint8_t *src = reinterpret_cast<const uint8_t *>(P.comp) +
+                             (size_t)list_row(b, idx[i], blk[i]) * kFp4RowBytes + 16 * (lt & 7);
+#pragma unroll
+        for (uint32_t v = 0; v < 3; ++v)
+          rec[i][v] = idx[i] < vis ? ld_nc_v4(src + 128 * v) : make_uint4(0u, 0u, 0u, 0u);
       }
     };
     // this thread's chunk of row i in 64-dim block KB of the tile
@@ -557,12 +758,14 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
       return S.kv + KB * kKBlk + (r >> 3) * 1024 + (r & 7) * 128 + (((lt & 7) ^ (r & 7)) << 4);
     };
     auto store_tile = [&](const QueryGeo &g, uint32_t tile, uint32_t n) -> bool {
-      if (tile_kind<DEC, true>(P, g, tile)) {   // the whole window ring by TMA
+      if (const uint32_t kind = tile_kind<DEC, true, FP4>(P, g, tile)) {   // the window by TMA
         for (uint32_t kb = 0; kb < 8; ++kb) {
-          if ((kb & 1) == 0 && !mbar_wait_warp(&S.kv_empty[kb >> 1], (n & 1) ^ 1, ew)) return false;
+          if ((kb & 1) == 0 && !wait_warp(&S.kv_empty[kb >> 1], (n & 1) ^ 1, ew)) return false;
           if (lt == 0) {
             if (kb == 0) mbar_arrive_expect_tx(&S.kv_tma, 8 * kKBlk);
-            tma_load_3d(S.kv + kb * kKBlk, &tmap_ring, &S.kv_tma, (int)(64 * kb), 0, (int)g.b);
+            // (the ring's slots 0 .. 127, or chunk rows p - p0 - 127 .. p - p0)
+            tma_load_3d(S.kv + kb * kKBlk, &tmap_ring, &S.kv_tma, (int)(64 * kb),
+                        kind == 3 ? (int)(g.p - g.p0) - (kRows - 1) : 0, (int)g.b);
           }
         }
 #pragma unroll
@@ -578,43 +781,56 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
         sh[i] = j & 1 ? mine : other;
         if (fp4_wide(sl[i]) | fp4_wide(sh[i])) wide |= 1u << i;
       }
-      auto word = [&](uint32_t i, uint32_t KB) {
-        const uint4 &v = rec[i][KB / 4];
-        return KB % 4 == 0 ? v.x : KB % 4 == 1 ? v.y : KB % 4 == 2 ? v.z : v.w;
-      };
-      using std::integral_constant;
       if (__all_sync(0xffffffffu, cur_raw == 0 && wide == 0)) {
-        // every row of this warp in 4 bits with ordinary scales: straight code, the
-        // rows' conversions interleaved, each pair of blocks handed over at once
-        auto pair = [&](auto m_c) -> bool {
-          constexpr uint32_t M = decltype(m_c)::value;
-          if (!mbar_wait_warp(&S.kv_empty[M], (n & 1) ^ 1, ew)) return false;
+        // every row of this warp in 4 bits with ordinary scales: the rows' conversions
+        // interleaved, each pair of blocks handed over at once. Two rounds of the
+        // same code over four blocks each (unrolled, the code crowds the others' out of
+        // the instruction cache); the last block is the rotated tail as it is.
+#pragma unroll 1
+        for (uint32_t v = 0; v < 2; ++v) {
 #pragma unroll
-          for (uint32_t i = 0; i < kFR; ++i)
-            *reinterpret_cast<uint4 *>(chunk_dst(i, 2 * M)) =
-                fp4_chunk<2 * M>(word(i, 2 * M), sl[i], sh[i], false);
+          for (uint32_t half = 0; half < 2; ++half) {
+            const uint32_t m = 2 * v + half;
+            if (!wait_warp(&S.kv_empty[m], (n & 1) ^ 1, ew)) return false;
 #pragma unroll
-          for (uint32_t i = 0; i < kFR; ++i)
-            *reinterpret_cast<uint4 *>(chunk_dst(i, 2 * M + 1)) =
-                M == 3 ? rec[i][2] : fp4_chunk<2 * M + 1>(word(i, 2 * M + 1), sl[i], sh[i], false);
-          fence_proxy_async();
-          mbar_arrive(&S.kv_pair[M]);
-          return true;
-        };
-        return pair(integral_constant<uint32_t, 0>{}) && pair(integral_constant<uint32_t, 1>{}) &&
-               pair(integral_constant<uint32_t, 2>{}) && pair(integral_constant<uint32_t, 3>{});
+            for (uint32_t i = 0; i < kFR; ++i)
+              *reinterpret_cast<uint4 *>(chunk_dst(i, 2 * m)) =
+                  half ? fp4_chunk<2>(rec[i][0].z, sl[i], 0u, false)
+                       : fp4_chunk<0>(rec[i][0].x, sl[i], 0u, false);
+#pragma unroll
+            for (uint32_t i = 0; i < kFR; ++i) {
+              uint4 o = half ? fp4_chunk<3>(rec[i][0].w, sl[i], 0u, false)
+                             : fp4_chunk<1>(rec[i][0].y, sl[i], 0u, false);
+              if (half && v) o = rec[i][2];
+              *reinterpret_cast<uint4 *>(chunk_dst(i, 2 * m + 1)) = o;
+            }
+            fence_proxy_async();
+            mbar_arrive(&S.kv_pair[m]);
+          }
+#pragma unroll
+          for (uint32_t i = 0; i < kFR; ++i) {
+            rec[i][0] = rec[i][1];
+            sl[i] = sh[i];
+          }
+        }
+        return true;
       }
+      const __nv_bfloat16 *raw[kFR];
+#pragma unroll
+      for (uint32_t i = 0; i < kFR; ++i)
+        raw[i] = (cur_raw >> i) & 1
+                     ? row_src<false>(P, g, tile * kRows + (lt >> 3) + 32 * i) + 8 * j
+                     : nullptr;
 #pragma unroll 1
       for (uint32_t m = 0; m < 4; ++m) {
-        if (!mbar_wait_warp(&S.kv_empty[m], (n & 1) ^ 1, ew)) return false;
+        if (!wait_warp(&S.kv_empty[m], (n & 1) ^ 1, ew)) return false;
 #pragma unroll 1
         for (uint32_t kb = 2 * m; kb < 2 * m + 2; ++kb)
 #pragma unroll
           for (uint32_t i = 0; i < kFR; ++i) {
             uint8_t *dst = chunk_dst(i, kb);
             if ((cur_raw >> i) & 1) {
-              cp_async16(dst, row_src<false>(P, g, tile * kRows + (lt >> 3) + 32 * i) + 64 * kb + 8 * j,
-                         16u);
+              cp_async16(dst, raw[i] + 64 * kb, 16u);
             } else {
               const uint4 a = rec[i][0], c = rec[i][1];
               const uint32_t w = kb == 0 ? a.x : kb == 1 ? a.y : kb == 2 ? a.z : kb == 3 ? a.w
@@ -655,6 +871,7 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
     // decode list is not scanned), so its first query's coefficients and
     // geometry are prepared before the wait; prefill scans its lists, so it
     // waits here.
+    uint32_t out_it = kNoRow;   // chunks over 4-bit rows: item whose output is to be written
     bool waited = false;
     auto wait_prev = [&]() {
       if (!waited) {
@@ -663,11 +880,11 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
         waited = true;
       }
     };
-    if (kScan) wait_prev();
+    if (kScan || FP4) wait_prev();
     for (uint32_t it = i0; it < n_items; it += i_step) {
       const uint32_t qi = item_q(it);
       if (rank * kRows >= rows_bound(P, qi)) continue;   // no rows for this rank
-      if (!mbar_wait_warp(&S.q_empty, (qn & 1) ^ 1, ew)) goto done_loader;
+      if (!wait_warp(&S.q_empty, (qn & 1) ^ 1, ew)) goto done_loader;
       if (!(q_early && it == i0)) issue_q(it);
       {
         // this thread's 16-byte chunks of the tail: chunk lt (+ LT i) of
@@ -681,28 +898,55 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
           const uint32_t id = lt + WP::LT * i, h = id >> 3, lc = (id & 7) ^ (h & 7);
 #pragma unroll
           for (uint32_t e = 0; e < 4; ++e) {
+            if (FP4 && P.q_rotated) {   // (not needed, not waited for)
+              co[4 * i + e] = si[4 * i + e] = 0.f;
+              continue;
+            }
             co[4 * i + e] = P.cos[(size_t)pq * 32 + 4 * lc + e];
             si[4 * i + e] = P.sin[(size_t)pq * 32 + 4 * lc + e];
           }
         }
-        const QueryGeo g = query_geo<kScan>(P, qi, rank, C, lane);
+        uint32_t n_list = kNoRow;
+        if (staged) {
+          if (DEC) {
+            stage_load(qi);
+            fetch_first(qi);
+            n_list = stage_list(qi);
+          } else if (it == i0) {
+            stage_load(qi);
+            n_list = stage_list(qi);
+          } else {
+            gb = list_half(gn - 1);   // (staged while the last query's tiles ran)
+            n_list = n_next;
+          }
+          if (n_list == kNoRow) goto done_loader;
+        }
+        const QueryGeo g = query_geo<kScan>(P, qi, rank, C, lane, n_list);
         if (g.t0 >= g.t1) {          // the list is shorter than the bound: nothing to do
           // (Q still lands: wait for it so the buffer is never written twice at once)
-          if (!mbar_wait_warp(&S.q_tma, qt & 1, ew)) goto done_loader;
+          if (!wait_warp(&S.q_tma, qt & 1, ew)) goto done_loader;
           ++qt;
           continue;
         }
         // the first tile's rows start loading before Q is rotated
         wait_prev();
         if (FP4) {
-          find_tile(g, g.t0);
-          fetch_tile();
-          if (g.t0 + g.ts < g.t1) find_tile(g, g.t0 + g.ts);
+          if (DEC && staged) {   // (fetched already; rows behind the list's end: none)
+#pragma unroll
+            for (uint32_t i = 0; i < kFR; ++i)
+              if (g.t0 * kRows + (lt >> 3) + 32 * i >= g.N)
+#pragma unroll
+                for (uint32_t v = 0; v < 3; ++v) rec[i][v] = make_uint4(0u, 0u, 0u, 0u);
+          } else {
+            look_tile(g, g.t0);
+            fetch_tile(g, g.t0);
+            look_tile(g, g.t0 + g.ts);
+          }
           if (!store_tile(g, g.t0, n)) goto done_loader;
         } else if (!issue_tile(g, g.t0, n)) {
           goto done_loader;
         }
-        if (!mbar_wait_warp(&S.q_tma, qt & 1, ew)) goto done_loader;   // Q landed
+        if (!wait_warp(&S.q_tma, qt & 1, ew)) goto done_loader;   // Q landed
         ++qt;
         // rotate the tail (dims 448..511 = block 7) at position p, in place
 #pragma unroll
@@ -727,9 +971,21 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
             if (FP4 ? !store_tile(g, tile, n) : !issue_tile(g, tile, n)) goto done_loader;
           }
           if (FP4) {   // (store_tile has handed the tile over)
-            if (tile + g.ts < g.t1) {
-              fetch_tile();
-              if (tile + 2 * g.ts < g.t1) find_tile(g, tile + 2 * g.ts);
+            if (!DEC && tile == g.t0) {   // the last query's output, then this one's to come
+              if (out_it != kNoRow && !write_out(out_it, qn - 1, 2)) goto done_loader;
+              out_it = it;
+              out_coef(g.p);
+            }
+            // (past the last tile every row is masked: the registers are dead until then)
+            fetch_tile(g, tile + g.ts);
+            look_tile(g, tile + 2 * g.ts);
+            if (!DEC && staged && it + i_step < n_items) {
+              // the next query's list: loads after the second tile (or the only one),
+              // the rest after the last one's hand-over
+              const uint32_t gb0 = gb, qi1 = item_q(it + i_step);
+              if (tile == g.t0 + g.ts || (tile == g.t0 && g.t0 + g.ts >= g.t1)) stage_load(qi1);
+              if (tile + g.ts >= g.t1 && (n_next = stage_list(qi1)) == kNoRow) goto done_loader;
+              gb = gb0;
             }
             continue;
           }
@@ -748,6 +1004,7 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
       }
       ++qn;
     }
+    if (FP4 && !DEC && out_it != kNoRow && !write_out(out_it, qn - 1, 2)) goto done_loader;
   done_loader:
     cp_async_wait_all();
   } else if (warp == WP::MMA) {
@@ -762,23 +1019,36 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
     // descriptors stay in uniform registers. Issued from a branch on lane 0 each MMA
     // first moves its descriptors there, and the issue, not the tensor core, sets
     // the pace (S^T 2000 to 4000 cycles a tile).
+    QueryGeo g_next = {};   // (as in the softmax warps)
+    uint32_t gn = 0;
     for (uint32_t it = i0; FP4 && it < n_items && ok; it += i_step) {
       const uint32_t qi = item_q(it), rank_u = uniform(rank);
-      if (uniform(rank_u * kRows >= rows_bound(P, qi))) continue;
-      const QueryGeo g = query_geo<kScan>(P, qi, rank, C, lane);
+      const bool ahead = !DEC && !staged && it != i0;
+      if (!ahead && uniform(rank_u * kRows >= rows_bound(P, qi))) continue;
+      uint32_t n_list = kNoRow;
+      if (staged) {
+        const uint32_t gb = list_half(gn);
+        ok = mbar_wait_issue(&S4.geo_full[gb], list_phase(gn), ew);
+        if (!ok) break;
+        n_list = list_end(gb);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S4.geo_empty[gb]);   // (this warp needs no more of it)
+        ++gn;
+      }
+      const QueryGeo g = ahead ? g_next : query_geo<kScan>(P, qi, rank, C, lane, n_list);
       const uint32_t t0 = uniform(g.t0), t1 = uniform(g.t1), ts = uniform(g.ts);
       if (t0 >= t1) continue;
-      const bool tma0 = uniform(tile_kind<DEC, true>(P, g, t0)) != 0;   // (only a first tile)
+      const bool tma0 = uniform(tile_kind<DEC, true, FP4>(P, g, t0)) != 0;   // (only a first tile)
       const uint32_t qd = desc_lo(q_base), kd = desc_lo(kv_base), pd = desc_lo(p_base);
-      ok = mbar_wait_warp(&S.q_full, qn & 1, ew);
+      ok = mbar_wait_issue(&S.q_full, qn & 1, ew);
       for (uint32_t tile = t0; ok && tile < t1; tile += ts, ++n) {
         const bool first = tile == t0, last = tile + ts >= t1;
-        if (first && tma0) ok = mbar_wait_warp(&S.kv_tma, nk++ & 1, ew);
+        if (first && tma0) ok = mbar_wait_issue(&S.kv_tma, nk++ & 1, ew);
         if (!ok) break;
         tc_fence_after();
-#pragma unroll
+#pragma unroll 1
         for (uint32_t m = 0; m < 4; ++m) {   // S^T starts while the tile's last blocks convert
-          ok = ok && mbar_wait_warp(&S.kv_pair[m], n & 1, ew);
+          ok = ok && mbar_wait_issue(&S.kv_pair[m], n & 1, ew);
           if (!ok) break;
 #pragma unroll
           for (uint32_t kb = 2 * m; kb < 2 * m + 2; ++kb)
@@ -791,12 +1061,14 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
         if (!ok) break;
         mma_commit_elect(&S.s_full);
         if (last) mma_commit_elect(&S.q_empty);
-        ok = mbar_wait_warp(&S.p_full, n & 1, ew);
-        if (ok && first) ok = mbar_wait_warp(&S.o_empty, (qn & 1) ^ 1, ew);
+        if (!DEC && !staged && last && it + i_step < n_items)
+          g_next = query_geo<kScan>(P, item_q(it + i_step), rank, C, lane);
+        ok = mbar_wait_issue(&S.p_full, n & 1, ew);
+        if (ok && first) ok = mbar_wait_issue(&S.o_empty, (qn & 1) ^ 1, ew);
         if (!ok) break;
         tc_fence_after();
         const uint32_t acc0 = first ? 0u : 1u;
-#pragma unroll
+#pragma unroll 1
         for (uint32_t m = 0; m < 4; ++m) {
 #pragma unroll
           for (uint32_t kk = 0; kk < 8; ++kk)
@@ -905,17 +1177,29 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
       }
       return flag;
     };
+    // chunks over 4-bit rows without a list: the next query's geometry, found while
+    // waiting for a last tile
+    QueryGeo g_next = {};
+    uint32_t gn = 0;
     for (uint32_t it = i0; it < n_items; it += i_step) {
       const uint32_t qi = item_q(it), hq0 = item_h(it);
-      const bool maybe = rank * kRows < rows_bound(P, qi);
-      QueryGeo g = {};
-      if (maybe) g = query_geo<kScan>(P, qi, rank, C, lane);
+      const bool ahead = FP4 && !DEC && !staged && it != i0;
+      const bool maybe = ahead || rank * kRows < rows_bound(P, qi);
+      uint32_t n_list = kNoRow, gb = 0;
+      if (staged && maybe) {
+        gb = list_half(gn);
+        if (!wait_warp(&S4.geo_full[gb], list_phase(gn), ew)) goto done_softmax;
+        n_list = list_end(gb);
+        ++gn;
+      }
+      QueryGeo g = g_next;
+      if (maybe && !ahead) g = query_geo<kScan>(P, qi, rank, C, lane, n_list);
       const bool has_tiles = maybe && g.t0 < g.t1;
       bool any_valid = false;
       // the rotation coefficients of this thread's tail dim in the direct
       // output (dim 384 + r of the last chunk), loaded while the tiles run
       float ep_co = 1.f, ep_si = 0.f;
-      if (!(dec && C > 1) && has_tiles && 384 + r >= (uint32_t)kNope) {
+      if (!(dec && C > 1) && !(FP4 && !DEC) && has_tiles && 384 + r >= (uint32_t)kNope) {
         const uint32_t fi = (384 + r - kNope) >> 1;
         ep_co = P.cos[(size_t)g.p * 32 + fi];
         ep_si = P.sin[(size_t)g.p * 32 + fi];
@@ -924,8 +1208,12 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
         const bool first = tile == g.t0;
         const uint32_t row = tile * kRows + r;
         bool valid = row < g.n_w;
-        if (!valid && row < g.N) valid = P.ratio != 4 || g.tk[row - g.n_w] >= 0;
-        if (!mbar_wait_warp(&S.s_full, n & 1, ew)) goto done_softmax;
+        if (!valid && row < g.N)
+          valid = P.ratio != 4 || (FP4 ? S4.rows[gb * kList + (row - g.n_w)] != kNoRow
+                                       : g.tk[row - g.n_w] >= 0);
+        if (FP4 && !DEC && !staged && tile + g.ts >= g.t1 && it + i_step < n_items)
+          g_next = query_geo<kScan>(P, item_q(it + i_step), rank, C, lane);
+        if (!wait_warp(&S.s_full, n & 1, ew)) goto done_softmax;
         tc_fence_after();
         if (first) {
           // running maxima start at the exact per-head maxima of the first
@@ -933,11 +1221,43 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
           // largest of the four warps. P of this tile then has no score above
           // its maximum (no raise to check).
           uint32_t *tkey = reinterpret_cast<uint32_t *>(&S.tmax[0][0]);   // [4][kH]
+          if constexpr (FP4) {
+            // This thread's scores stay in registers for P; after one barrier each warp
+            // takes its heads' maxima from the four quarters itself (the warps with
+            // the same heads store the same values).
+            uint32_t a0[HB];
+            tmem_ld(tmS + lane_base + hb0, a0);
+            tmem_ld_wait();
+            uint32_t mine = 0u;
+#pragma unroll
+            for (uint32_t h = 0; h < HB; ++h) {
+              const uint32_t u = __float_as_uint(__uint_as_float(a0[h]) * P.c2);
+              const uint32_t key = valid ? ((u & 0x80000000u) ? ~u : (u | 0x80000000u)) : 0u;
+              const uint32_t mk = redux_max_u32(key);
+              if (lane == h) mine = mk;
+            }
+            if (lane < HB) tkey[sq * kH + hb0 + lane] = mine;
+            if (threadIdx.x == 0) S.flagcnt[(n + 1) % 3] = 0;   // the next tile's raise count
+            if (!sync_group(&S.sm_bar, sm_phase, ew)) goto done_softmax;
+            const uint32_t hm = hb0 + (lane & (HB - 1));
+            const uint32_t mk = max(max(tkey[0 * kH + hm], tkey[1 * kH + hm]),
+                                    max(tkey[2 * kH + hm], tkey[3 * kH + hm]));
+            any_valid = mk != 0u;   // a valid row has a key above 0 for every head
+            const float mx = __uint_as_float((mk & 0x80000000u) ? (mk & 0x7fffffffu) : ~mk);
+            if (lane < HB) S.mref[hm] = any_valid ? mx : 0.f;
+            __syncwarp();
+            if (!wait_warp(&S.p_empty, (n & 1) ^ 1, ew)) goto done_softmax;
+            bool unused = false;
+            p_half(valid, a0, hb0, unused);
+            fence_proxy_async();
+            tc_fence_before();
+            mbar_arrive(&S.p_full);
+          } else {
           // eight heads per step of a short loop: this runs once per query,
           // its code is fetched cold, and an unrolled form measured ~2 us of
           // instruction fetch
 #pragma unroll 1
-          for (uint32_t c = hb0; c < hb0 + HB * NPT; c += 8) {
+          for (uint32_t c = 0; c < (uint32_t)NH; c += 8) {
             uint32_t a8[8];
             tmem_ld8(tmS + lane_base + c, a8);
             tmem_ld_wait();
@@ -950,7 +1270,7 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
             }
           }
           if (threadIdx.x == 0) S.flagcnt[(n + 1) % 3] = 0;   // the next tile's raise count
-          if (!group_sync(&S.sm_bar, sm_phase, ew)) goto done_softmax;
+          if (!sync_group(&S.sm_bar, sm_phase, ew)) goto done_softmax;
           const uint32_t k0 = max(max(tkey[0 * kH], tkey[1 * kH]), max(tkey[2 * kH], tkey[3 * kH]));
           any_valid = k0 != 0u;   // a valid row has a key above 0 for every head
           if (threadIdx.x < (uint32_t)NH) {
@@ -959,16 +1279,11 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
             const float mx = __uint_as_float((mk & 0x80000000u) ? (mk & 0x7fffffffu) : ~mk);
             S.mref[r] = any_valid ? mx : 0.f;
           }
-          if (!group_sync(&S.sm_bar, sm_phase, ew)) goto done_softmax;
-          if (!mbar_wait_warp(&S.p_empty, (n & 1) ^ 1, ew)) goto done_softmax;
+          if (!sync_group(&S.sm_bar, sm_phase, ew)) goto done_softmax;
+          if (!wait_warp(&S.p_empty, (n & 1) ^ 1, ew)) goto done_softmax;
           // the scores (S stays until this tile's P is done)
           bool unused = false;
-          if (FP4) {
-            uint32_t a0[HB];
-            tmem_ld(tmS + lane_base + hb0, a0);
-            tmem_ld_wait();
-            p_half(valid, a0, hb0, unused);
-          } else if (NHF == 2) {
+          if (NHF == 2) {
             uint32_t a0[32], a1[32];
             tmem_ld32(tmS + lane_base, a0);
             tmem_ld32(tmS + lane_base + 32, a1);
@@ -984,38 +1299,40 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
           fence_proxy_async();
           tc_fence_before();
           mbar_arrive(&S.p_full);
+          }
           continue;
         }
         // P of this tile (the previous PV must be done with the buffer)
-        if (!mbar_wait_warp(&S.p_empty, (n & 1) ^ 1, ew)) goto done_softmax;
+        if (!wait_warp(&S.p_empty, (n & 1) ^ 1, ew)) goto done_softmax;
         const bool flag = write_p(valid);
         const uint32_t fc = n % 3;
         if (threadIdx.x == 0) S.flagcnt[(n + 1) % 3] = 0;
         if (flag) atomicAdd(&S.flagcnt[fc], 1u);
-        if (!group_sync(&S.sm_bar, sm_phase, ew)) goto done_softmax;
+        if (!sync_group(&S.sm_bar, sm_phase, ew)) goto done_softmax;
         if (S.flagcnt[fc] != 0) {
           // rare path: exact tile max per head, raise the running max, rescale
           // O and L, rewrite P
 #pragma unroll 1
-          for (uint32_t hf = 0; hf < NPT; ++hf) {
-            const uint32_t hb = hb0 + HB * hf;
-            uint32_t a[HB];
+          for (uint32_t hf = 0; hf < (FP4 ? HB / 8 : NPT); ++hf) {
+            constexpr uint32_t W = FP4 ? 8 : HB;   // (short code where it runs rarely)
+            const uint32_t hb = hb0 + W * hf;
+            uint32_t a[W];
             tmem_ld(tmS + lane_base + hb, a);
             tmem_ld_wait();
 #pragma unroll
-            for (uint32_t h = 0; h < HB; ++h) {
+            for (uint32_t h = 0; h < W; ++h) {
               const float v = warp_max(valid ? __uint_as_float(a[h]) * P.c2 : -INFINITY);
               if (lane == h) S.tmax[sq][hb + h] = v;
             }
           }
-          if (!group_sync(&S.sm_bar, sm_phase, ew)) goto done_softmax;
+          if (!sync_group(&S.sm_bar, sm_phase, ew)) goto done_softmax;
           if (threadIdx.x < (uint32_t)NH) {
             const float M = fmaxf(fmaxf(S.tmax[0][r], S.tmax[1][r]), fmaxf(S.tmax[2][r], S.tmax[3][r]));
             const float mo = S.mref[r], mn = fmaxf(mo, M);
             S.alpha[r] = exp2f(mo - mn);
             S.mref[r] = mn;
           }
-          if (!group_sync(&S.sm_bar, sm_phase, ew)) goto done_softmax;
+          if (!sync_group(&S.sm_bar, sm_phase, ew)) goto done_softmax;
           if (!first) {
 #pragma unroll 1
             for (uint32_t m = FP4 ? hh : 0u; m < 5 * (uint32_t)NHF; m += FP4 ? 2 : 1) {   // O^T (4 dim blocks) then L
@@ -1037,9 +1354,19 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
         tc_fence_before();
         mbar_arrive(&S.p_full);
       }
+      if (staged && maybe) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S4.geo_empty[gb]);
+      }
+      if (FP4 && !DEC) {
+        out_coef(g.p);
+        if (!write_out(it, qn, 0)) goto done_softmax;
+        ++qn;
+        continue;
+      }
       // ---- query end: per-head sums (any lane of L), then the output
       if (has_tiles) {
-        if (!mbar_wait_warp(&S.o_full, qn & 1, ew)) goto done_softmax;
+        if (!wait_warp(&S.o_full, qn & 1, ew)) goto done_softmax;
         tc_fence_after();
         if (warp < (uint32_t)NHF) {   // every row of L holds the sums: warp w keeps heads 32w + lane
           uint32_t a[32];
@@ -1053,7 +1380,7 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
           S.linv[32 * warp + lane] = l > 0.f ? 1.f / l : 0.f;
         }
       }
-      if (!group_sync(&S.sm_bar, sm_phase, ew)) goto done_softmax;
+      if (!sync_group(&S.sm_bar, sm_phase, ew)) goto done_softmax;
       if (dec && C > 1) {
         // (max, sum) of this rank for the cluster merge; O follows from TMEM
         if (threadIdx.x < (uint32_t)NH) {
@@ -1123,7 +1450,7 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
         ++qn;
       }
       // keep the shared sums alive until every thread has read them
-      if (!group_sync(&S.sm_bar, sm_phase, ew)) goto done_softmax;
+      if (!sync_group(&S.sm_bar, sm_phase, ew)) goto done_softmax;
     }
   done_softmax:;
   }
@@ -1328,7 +1655,7 @@ cudaError_t launch_attention_tc(const AttnArgs &a, uint32_t rows_max, int *err, 
   P.part = reinterpret_cast<__nv_bfloat16 *>(static_cast<uint8_t *>(a.ws) + 256);
   P.ml = nullptr;
   P.err = err;
-  const size_t smem = sizeof(Smem) + 1024;
+  const size_t smem = (a.fp4 ? sizeof(SmemFp4) : sizeof(Smem)) + 1024;
   // paged rows: an instantiation of its own, so the contiguous gathers carry
   // no table code
   const bool paged = a.map.table != nullptr, fp4 = a.fp4;
@@ -1367,7 +1694,15 @@ cudaError_t launch_attention_tc(const AttnArgs &a, uint32_t rows_max, int *err, 
   P.tma_rows = 0;
   // (ratio 4 keeps its window on the gathers: its first rank runs the window
   // tile beside the list tiles, and by TMA it measured slower)
-  if (a.T == 1 && a.cap_raw == (uint32_t)kRows && a.ratio != 4) {
+  // (with 4-bit rows the window is the largest tile: always by TMA; in a chunk, the
+  // windows that lie inside it)
+  if (fp4 && a.T >= (uint32_t)kRows && a.cap_raw == (uint32_t)kRows) {
+    const uint64_t rd[3] = {(uint64_t)kD, (uint64_t)a.T, (uint64_t)a.batch};
+    const uint64_t rs[2] = {(uint64_t)kD * 2, (uint64_t)a.T * kD * 2};
+    const uint32_t rb[3] = {64, (uint32_t)kRows, 1};
+    if (make_tmap_bf16(&tr, a.chunk, 3, rd, rs, rb) == cudaSuccess) P.tma_rows |= 4u;
+  }
+  if (a.T == 1 && a.cap_raw == (uint32_t)kRows && (a.ratio != 4 || fp4)) {
     const uint64_t rd[3] = {(uint64_t)kD, (uint64_t)a.cap_raw, (uint64_t)a.batch};
     const uint64_t rs[2] = {(uint64_t)kD * 2, (uint64_t)a.cap_raw * kD * 2};
     const uint32_t rb[3] = {64, (uint32_t)kRows, 1};

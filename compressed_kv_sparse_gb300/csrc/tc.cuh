@@ -113,6 +113,46 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity, E
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, err));
 }
 
+// The same wait in little code for kernels with many waiting warps: the thread
+// sleeps on the barrier for up to kSleepNs at a time instead of polling, and everything
+// beyond the first sleep is one function. (Seventeen polling warps took more than
+// a third of the issue slots of the 4-bit cache attention, and the inlined loops
+// a good part of its instruction cache.)
+constexpr uint32_t kSleepNs = 20000;
+__device__ __forceinline__ bool mbar_sleep(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(kSleepNs)
+      : "memory");
+  return ok != 0;
+}
+static __device__ __noinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, int *err, int base) {
+  const uint64_t t0 = global_ns();
+  for (;;) {
+    if (mbar_sleep(bar, parity)) return true;
+    if (global_ns() - t0 > kWaitLimitNs) {
+      atomicAdd(err, 1);
+      return false;
+    }
+    if (*(volatile int *)err != base) return false;
+  }
+}
+// One outcome for the whole (converged) warp, as mbar_wait_warp.
+__device__ __forceinline__ bool mbar_wait_sleep(uint64_t *bar, uint32_t parity, ErrWord err) {
+  const uint32_t b = smem_u32(bar);
+  if (__all_sync(0xffffffffu, mbar_sleep(b, parity))) return true;
+  return __all_sync(0xffffffffu, mbar_wait_long(b, parity, err.p, err.base));
+}
+// For the thread that issues MMAs: test first (see mbar_test_wait).
+__device__ __forceinline__ bool mbar_wait_issue(uint64_t *bar, uint32_t parity, ErrWord err) {
+  if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, mbar_wait_long(smem_u32(bar), parity, err.p, err.base));
+}
+
 // 2D / 3D tiled TMA loads into shared memory, completing on `bar`.
 __device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, uint64_t *bar,
                                             int x, int y) {
@@ -206,6 +246,12 @@ __device__ __forceinline__ uint4 ld_nc_v4(const void *p) {
   return v;
 }
 
+__device__ __forceinline__ uint32_t ld_nc_u32(const void *p) {
+  uint32_t v;
+  asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+
 // 16-byte cp.async (L2 only); src_bytes = 0 fills the 16 bytes with zeros.
 __device__ __forceinline__ void cp_async16(void *dst, const void *src, uint32_t src_bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
@@ -232,6 +278,12 @@ template <typename E>
 __device__ __forceinline__ bool group_sync(uint64_t *bar, uint32_t &phase, E err) {
   mbar_arrive(bar);
   const bool ok = mbar_wait_warp(bar, phase, err);
+  phase ^= 1;
+  return ok;
+}
+__device__ __forceinline__ bool group_sync_sleep(uint64_t *bar, uint32_t &phase, ErrWord err) {
+  mbar_arrive(bar);
+  const bool ok = mbar_wait_sleep(bar, phase, err);
   phase ^= 1;
   return ok;
 }
@@ -413,6 +465,11 @@ __device__ __forceinline__ uint32_t redux_max_u32(uint32_t v) {
   asm volatile("redux.sync.max.u32 %0, %1, 0xffffffff;" : "=r"(r) : "r"(v));
   return r;
 }
+__device__ __forceinline__ uint32_t redux_min_u32(uint32_t v) {
+  uint32_t r;
+  asm volatile("redux.sync.min.u32 %0, %1, 0xffffffff;" : "=r"(r) : "r"(v));
+  return r;
+}
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
@@ -428,6 +485,7 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
 }
 
 // By the array's size.
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[8]) { tmem_ld8(taddr, r); }
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld16(taddr, r); }
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld32(taddr, r); }
 
