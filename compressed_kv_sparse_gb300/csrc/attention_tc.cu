@@ -118,7 +118,7 @@ struct Smem {
   uint64_t kv_tma;  // a tile loaded by TMA landed
   uint64_t kv_pair[4];   // 4-bit rows: blocks 2m, 2m+1 of the tile are written
   uint64_t mg_bar;  // decode merge: the peers' partial O slices landed
-  float mref[kH], alpha[kH], lsh[kH], linv[kH];
+  alignas(16) float mref[kH], alpha[kH], lsh[kH], linv[kH];
   float tmax[4][kH];
   float mw[kH][kMaxCluster];        // decode merge: weight of each rank, per owned head
   uint32_t flagcnt[3], tmem, has_tiles;
@@ -523,15 +523,26 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
     if (!wait_warp(&S.o_full, qn_prev & 1, ew)) return false;
     tc_fence_after();
     const bool odd = lane & 1;
+    // 1 / L of head 32 hf + lane from this lane's copy (every TMEM row of L holds the
+    // sums), then all 32 by broadcast; warps with the same heads write the same values
     uint32_t a[2][16];   // sixteen heads at a time, the next load in flight
-    float li[32];        // every TMEM row of L holds the sums
+    float li[32];
 #pragma unroll
     for (int hs = 0; hs < 2; ++hs) tmem_ld16(tmL + lane_base + 32 * hf + 16 * hs, a[hs]);
     tmem_ld_wait();
+    float l = 0.f;
 #pragma unroll
-    for (int h = 0; h < 32; ++h) {
-      const float l = __uint_as_float(a[h / 16][h % 16]);
-      li[h] = l > 0.f ? __fdividef(1.f, l) : 0.f;
+    for (uint32_t h = 0; h < 32; ++h)
+      if (lane == h) l = __uint_as_float(a[h / 16][h % 16]);
+    S.linv[32 * hf + lane] = l > 0.f ? __fdividef(1.f, l) : 0.f;
+    __syncwarp();
+#pragma unroll
+    for (uint32_t h = 0; h < 32; h += 4) {
+      const float4 v = *reinterpret_cast<const float4 *>(&S.linv[32 * hf + h]);
+      li[h] = v.x;
+      li[h + 1] = v.y;
+      li[h + 2] = v.z;
+      li[h + 3] = v.w;
     }
     __nv_bfloat16 *o = P.out + ((size_t)qi * HQ + h0) * kD + 128 * m0 + (r & ~1u);
     const uint32_t live = HQ > h0 ? HQ - h0 : 0u;   // heads there are
@@ -640,7 +651,6 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
     uint32_t tbl[kFR] = {};   // ratio 128, paged: table entries of the next tile's rows
     uint32_t cur_raw = 0;     // bit i: row i is in bf16 (the window)
     uint32_t gn = 0, gb = 0, ld_phase = 0;   // lists staged, the current one's half
-    uint32_t n_next = 0;                     // length of the next query's list
     const uint32_t rsh = P.ratio == 4 ? 6u : 1u;   // log2 of the rows per block
     auto list_row = [&](uint32_t g_b, uint32_t idx, uint32_t blk) {
       // (as RowMap::phys: table entries outside the pool read block 0)
@@ -758,16 +768,14 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
       return S.kv + KB * kKBlk + (r >> 3) * 1024 + (r & 7) * 128 + (((lt & 7) ^ (r & 7)) << 4);
     };
     auto store_tile = [&](const QueryGeo &g, uint32_t tile, uint32_t n) -> bool {
-      if (const uint32_t kind = tile_kind<DEC, true, FP4>(P, g, tile)) {   // the window by TMA
-        for (uint32_t kb = 0; kb < 8; ++kb) {
-          if ((kb & 1) == 0 && !wait_warp(&S.kv_empty[kb >> 1], (n & 1) ^ 1, ew)) return false;
-          if (lt == 0) {
-            if (kb == 0) mbar_arrive_expect_tx(&S.kv_tma, 8 * kKBlk);
-            // (the ring's slots 0 .. 127, or chunk rows p - p0 - 127 .. p - p0)
-            tma_load_3d(S.kv + kb * kKBlk, &tmap_ring, &S.kv_tma, (int)(64 * kb),
-                        kind == 3 ? (int)(g.p - g.p0) - (kRows - 1) : 0, (int)g.b);
-          }
-        }
+      if (const uint32_t kind = tile_kind<DEC, true, FP4>(P, g, tile)) {
+        // the window by TMA, a box per loader warp: the ring's slots 0 .. 127, or chunk
+        // rows p - p0 - 127 .. p - p0
+        if (lt == 0) mbar_arrive_expect_tx(&S.kv_tma, 8 * kKBlk);
+        if (!wait_warp(&S.kv_empty[lw >> 1], (n & 1) ^ 1, ew)) return false;
+        if (lane == 0)
+          tma_load_3d(S.kv + lw * kKBlk, &tmap_ring, &S.kv_tma, (int)(64 * lw),
+                      kind == 3 ? (int)(g.p - g.p0) - (kRows - 1) : 0, (int)g.b);
 #pragma unroll
         for (uint32_t m = 0; m < 4; ++m) mbar_arrive(&S.kv_pair[m]);
         return true;
@@ -852,16 +860,19 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
     // caller's input, written before that launch began (as are the rotation
     // tables), while the top-k lists and the new raw row are not.
     auto issue_q = [&](uint32_t it) {
+      if (FP4) {   // a box per loader warp; heads past the last one read as zeros
+        if (lt == 0) mbar_arrive_expect_tx(&S.q_tma, 8 * QBLK);
+        if (lane == 0)
+          tma_load_3d(S.q + lw * QBLK, &tmap_q, &S.q_tma, (int)(64 * lw), (int)item_h(it),
+                      (int)item_q(it));
+        return;
+      }
       if (lt == 0) {
         const uint32_t qi = item_q(it), hq0 = item_h(it);
         mbar_arrive_expect_tx(&S.q_tma, 8 * QBLK);
 #pragma unroll
-        for (uint32_t kb = 0; kb < 8; ++kb) {
-          if (FP4)   // (heads past the last one read as zeros)
-            tma_load_3d(S.q + kb * QBLK, &tmap_q, &S.q_tma, (int)(64 * kb), (int)hq0, (int)qi);
-          else
-            tma_load_2d(S.q + kb * QBLK, &tmap_q, &S.q_tma, (int)(64 * kb), (int)(qi * kH + hq0));
-        }
+        for (uint32_t kb = 0; kb < 8; ++kb)
+          tma_load_2d(S.q + kb * QBLK, &tmap_q, &S.q_tma, (int)(64 * kb), (int)(qi * kH + hq0));
       }
     };
     const bool q_early = i0 < n_items && rank * kRows < rows_bound(P, item_q(i0));
@@ -908,17 +919,9 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
         }
         uint32_t n_list = kNoRow;
         if (staged) {
-          if (DEC) {
-            stage_load(qi);
-            fetch_first(qi);
-            n_list = stage_list(qi);
-          } else if (it == i0) {
-            stage_load(qi);
-            n_list = stage_list(qi);
-          } else {
-            gb = list_half(gn - 1);   // (staged while the last query's tiles ran)
-            n_list = n_next;
-          }
+          if (DEC || it == i0) stage_load(qi);   // (else started a few tiles ago)
+          if (DEC) fetch_first(qi);
+          n_list = stage_list(qi);
           if (n_list == kNoRow) goto done_loader;
         }
         const QueryGeo g = query_geo<kScan>(P, qi, rank, C, lane, n_list);
@@ -979,14 +982,10 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
             // (past the last tile every row is masked: the registers are dead until then)
             fetch_tile(g, tile + g.ts);
             look_tile(g, tile + 2 * g.ts);
-            if (!DEC && staged && it + i_step < n_items) {
-              // the next query's list: loads after the second tile (or the only one),
-              // the rest after the last one's hand-over
-              const uint32_t gb0 = gb, qi1 = item_q(it + i_step);
-              if (tile == g.t0 + g.ts || (tile == g.t0 && g.t0 + g.ts >= g.t1)) stage_load(qi1);
-              if (tile + g.ts >= g.t1 && (n_next = stage_list(qi1)) == kNoRow) goto done_loader;
-              gb = gb0;
-            }
+            // the next query's list starts loading after the second tile (or the only one)
+            if (!DEC && staged && it + i_step < n_items &&
+                (tile == g.t0 + g.ts || (tile == g.t0 && g.t0 + g.ts >= g.t1)))
+              stage_load(item_q(it + i_step));
             continue;
           }
           // one arrival per thread once all its rows of the tile landed: the
