@@ -66,22 +66,32 @@ __device__ __forceinline__ float fp4_amax(float a, float b) {
   return __uint_as_float(max(__float_as_uint(a) & 0x7FFFFFFFu, __float_as_uint(b) & 0x7FFFFFFFu));
 }
 
-// The code word of eight dims under the scale byte sb. |x| * 2^-k is exact or
-// far below the smallest decision point; the nearest of 0, .5, 1, 1.5, 2, 3, 4,
-// 6 with ties to the even code. 6 * 2^126 is beyond fp32: there the largest
-// finite value, 3 * 2^126, is taken.
+// Two fp32 values to E2M1 codes (nearest, ties to the even code): lo in bits 0 .. 3
+// of the result, hi in bits 4 .. 7.
+__device__ __forceinline__ uint32_t fp4_codes2(float lo, float hi) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 b;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\t"
+      "cvt.u32.u8 %0, b;\n\t}"
+      : "=r"(r)
+      : "f"(hi), "f"(lo));
+  return r;
+}
+
+// The code word of eight dims under the scale byte sb. x * 2^-k is exact or far
+// below the smallest decision point. 6 * 2^126 is beyond fp32: there the largest finite
+// value, 3 * 2^126, is taken.
 __device__ __forceinline__ uint32_t fp4_encode(const float (&v)[8], uint32_t sb) {
   if (sb == 255u) return 0u;
-  const float inv = pow2f(127 - (int)sb);
+  const float inv = pow2f(127 - (int)sb), top = sb == 253u ? 3.f : 6.f;
   uint32_t w = 0;
 #pragma unroll
-  for (uint32_t i = 0; i < 8; ++i) {
-    const float r = __fmul_rn(fabsf(v[i]), inv);
-    uint32_t c = (r > 0.25f) + (r >= 0.75f) + (r > 1.25f) + (r >= 1.75f) + (r > 2.5f) +
-                 (r >= 3.5f) + (r > 5.0f);
-    if (sb == 253u && c > 5u) c = 5u;
-    const uint32_t t = i / 2, h = 16 * (i % 2);
-    w |= (c << (fp4_mag_bit(t) + h)) | ((__float_as_uint(v[i]) >> 31) << (fp4_sign_bit(t) + h));
+  for (uint32_t t = 0; t < 4; ++t) {
+    const float lo = fminf(fmaxf(__fmul_rn(v[2 * t], inv), -top), top);
+    const float hi = fminf(fmaxf(__fmul_rn(v[2 * t + 1], inv), -top), top);
+    // dim 2 t to bits 0 .. 3, dim 2 t + 1 to bits 16 .. 19
+    const uint32_t y = (fp4_codes2(lo, hi) * 0x1001u) & 0x000F000Fu;
+    w |= ((y & 0x00070007u) << fp4_mag_bit(t)) | ((y & 0x00080008u) << (fp4_sign_bit(t) - 3));
   }
   return w;
 }

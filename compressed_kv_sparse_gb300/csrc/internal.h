@@ -229,8 +229,9 @@ struct TablesArgs {
   uint32_t *state;
   uint32_t *seq_pos, *cu_len;
   int32_t *tok_seq, *tok_pos, *raw_slot, *slot4, *slot128;
+  uint32_t search, shift;   // (set by the launch)
 };
-cudaError_t launch_block_tables(const TablesArgs &a, cudaStream_t s);
+cudaError_t launch_block_tables(TablesArgs a, cudaStream_t s);
 
 cudaError_t launch_state_reset(float *kv, float *score, size_t n, cudaStream_t s);
 cudaError_t launch_index_norms(int dtype, const void *rows, const RowMap &map, uint32_t dim,

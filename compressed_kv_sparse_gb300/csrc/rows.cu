@@ -13,8 +13,6 @@ namespace ds4a {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr uint32_t kMaxBlocks = 16;                 // 64-dim blocks of a row (D <= 1024)
-constexpr uint32_t kMaxWords = kMaxBlocks + 4;      // record words (16 + 2, padded)
 
 struct RowsArgs {
   uint8_t *packed;        // the pool
@@ -26,19 +24,14 @@ struct RowsArgs {
 };
 
 template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const T *p, float (&v)[8]) {
+__device__ __forceinline__ void copy8(const T *p, T (&v)[8]) {
   if (VEC) {
-    constexpr int E = 16 / sizeof(T);
 #pragma unroll
-    for (int h = 0; h < 8 / E; ++h) {
-      const uint4 u = *reinterpret_cast<const uint4 *>(p + h * E);
-      const T *e = reinterpret_cast<const T *>(&u);
-#pragma unroll
-      for (int i = 0; i < E; ++i) v[h * E + i] = ld_f32(e, i);
-    }
+    for (uint32_t h = 0; h < 8 * sizeof(T) / 16; ++h)
+      reinterpret_cast<uint4 *>(v)[h] = reinterpret_cast<const uint4 *>(p)[h];
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = ld_f32(p, i);
+    for (int i = 0; i < 8; ++i) v[i] = p[i];
   }
 }
 
@@ -68,96 +61,152 @@ __device__ __forceinline__ bool pool_row(const RowsArgs &a, uint32_t i, uint64_t
   return s >= 0 && row < a.n_pool;
 }
 
-template <typename T, bool VEC>
+// NB: 64-dim blocks that the code has room for (8: 512-wide rows and narrower, all
+// loads of a row in flight at once; 16: any).
+template <typename T, bool VEC, int NB>
 __global__ void __launch_bounds__(kThreads) rows_pack_kernel(RowsArgs a) {
+  constexpr uint32_t NW = NB + 4;   // record words
   const uint32_t i = blockIdx.x * (kThreads / 8) + threadIdx.x / 8, j = threadIdx.x & 7;
   uint64_t row;
   const bool live = pool_row(a, i, row);   // (the same for a row's eight lanes)
   const T *src = static_cast<const T *>(a.rows) + (size_t)(live ? i : 0) * a.D;
-  uint32_t rec[kMaxWords];
+  alignas(16) T raw[NB][8];
 #pragma unroll
-  for (uint32_t w = 0; w < kMaxWords; ++w) rec[w] = 0;
-  uint32_t own[kMaxBlocks / 4] = {0, 0, 0, 0};   // scale bytes, four per word, of every block
-#pragma unroll
-  for (uint32_t kb = 0; kb < kMaxBlocks; ++kb) {
-    if (kb >= a.L.nb) break;
+  for (uint32_t kb = 0; kb < NB; ++kb) {
     const uint32_t d = 64 * kb + 8 * j;
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (live && d < a.L.nope) load8<T, VEC>(src + d, v);
-    float am = 0.f;
+    if (live && d < a.L.nope) copy8<T, VEC>(src + d, raw[kb]);
+    else
 #pragma unroll
-    for (int e = 0; e < 8; ++e) am = fp4_amax(am, v[e]);
+      for (int e = 0; e < 8; ++e) st_elem(raw[kb], e, 0.f);
+  }
+  constexpr uint32_t E = 16 / sizeof(T);
+  uint4 tail0 = make_uint4(0u, 0u, 0u, 0u);
+  if (VEC && live && j < a.n_rot / E) tail0 = reinterpret_cast<const uint4 *>(src + a.L.nope)[j];
+  uint32_t rec[NW];
+#pragma unroll
+  for (uint32_t w = 0; w < NW; ++w) rec[w] = 0;
+  uint32_t own[NB / 4];   // scale bytes, four per word, of every block
+#pragma unroll
+  for (uint32_t q = 0; q < NB / 4; ++q) own[q] = 0;
+#pragma unroll
+  for (uint32_t kb = 0; kb < NB; ++kb) {
+    float v[8], am = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      v[e] = ld_f32(raw[kb], e);
+      am = fp4_amax(am, v[e]);
+    }
     am = fp4_amax(am, __shfl_xor_sync(0xffffffffu, am, 1));
     const uint32_t sb = fp4_scale_byte(am);
-    rec[kb] = fp4_encode(v, sb);
-    own[kb / 4] |= sb << (8 * (kb % 4));
+    if (kb < a.L.nb) {
+      rec[kb] = fp4_encode(v, sb);
+      own[kb / 4] |= sb << (8 * (kb % 4));
+    }
   }
   if (!live) return;
   // this lane's scale words: blocks 4 ns (j % 2) + 4 s ..
   const uint32_t first = (j & 1) * a.L.ns;
 #pragma unroll
-  for (uint32_t w = 0; w < kMaxWords; ++w) {
+  for (uint32_t w = 0; w < NW; ++w) {
     const uint32_t s = w - a.L.nb;
     if (w >= a.L.nb && s < a.L.ns) {
       uint32_t x = 0;
 #pragma unroll
-      for (uint32_t q = 0; q < kMaxBlocks / 4; ++q)
+      for (uint32_t q = 0; q < NB / 4; ++q)
         if (q == first + s) x = own[q];
       rec[w] = x;
     }
   }
   uint8_t *dst = a.packed + row * a.L.row_bytes;
 #pragma unroll
-  for (uint32_t g = 0; g < kMaxWords / 4; ++g)
+  for (uint32_t g = 0; g < NW / 4; ++g)
     if (4 * g < a.L.R)
       *reinterpret_cast<uint4 *>(dst + 128 * g + 16 * j) =
           make_uint4(rec[4 * g], rec[4 * g + 1], rec[4 * g + 2], rec[4 * g + 3]);
   T *tail = reinterpret_cast<T *>(dst + a.L.tail);
   if (VEC) {
-    constexpr uint32_t E = 16 / sizeof(T);
-    for (uint32_t c = j; c < a.n_rot / E; c += 8)
+    if (j < a.n_rot / E) reinterpret_cast<uint4 *>(tail)[j] = tail0;
+    for (uint32_t c = j + 8; c < a.n_rot / E; c += 8)
       reinterpret_cast<uint4 *>(tail)[c] = reinterpret_cast<const uint4 *>(src + a.L.nope)[c];
   } else {
     for (uint32_t c = j; c < a.n_rot; c += 8) tail[c] = src[a.L.nope + c];
   }
 }
 
-template <typename T, bool VEC>
+template <typename T, bool VEC, int NB>
 __global__ void __launch_bounds__(kThreads) rows_unpack_kernel(RowsArgs a) {
+  constexpr uint32_t NW = NB + 4;
   const uint32_t i = blockIdx.x * (kThreads / 8) + threadIdx.x / 8, j = threadIdx.x & 7;
   uint64_t row;
-  if (!pool_row(a, i, row)) return;
-  const uint8_t *src = a.packed + row * a.L.row_bytes;
-  T *dst = static_cast<T *>(a.rows) + (size_t)i * a.D;
-  for (uint32_t kb = 0; kb < a.L.nb; ++kb) {
-    const uint32_t d = 64 * kb + 8 * j;
-    if (d >= a.L.nope) break;
-    float v[8];
-    fp4_decode(*reinterpret_cast<const uint32_t *>(src + fp4_word_at(kb, j)),
-               src[fp4_scale_at(a.L, kb, j / 2)], v);
-    store8<T, VEC>(dst + d, v);
+  const bool live = pool_row(a, i, row);
+  const uint8_t *src = a.packed + (live ? row : 0) * a.L.row_bytes;
+  T *dst = static_cast<T *>(a.rows) + (size_t)(live ? i : 0) * a.D;
+  constexpr uint32_t E = 16 / sizeof(T);
+  // (vectors by 4 words per lane; the pool's row 0 stands in for a skipped one)
+  uint32_t rec[NW];
+#pragma unroll
+  for (uint32_t g = 0; g < NW / 4; ++g) {
+    uint4 u = make_uint4(0u, 0u, 0u, 0u);
+    if (4 * g < a.L.R) u = *reinterpret_cast<const uint4 *>(src + 128 * g + 16 * j);
+    rec[4 * g] = u.x;
+    rec[4 * g + 1] = u.y;
+    rec[4 * g + 2] = u.z;
+    rec[4 * g + 3] = u.w;
   }
   const T *tail = reinterpret_cast<const T *>(src + a.L.tail);
+  uint4 tail0 = make_uint4(0u, 0u, 0u, 0u);
+  if (VEC && live && j < a.n_rot / E) tail0 = reinterpret_cast<const uint4 *>(tail)[j];
+  // the pair's scale words: the even lane's, then the odd lane's
+  uint32_t sc[NB / 4];
+#pragma unroll
+  for (uint32_t q = 0; q < NB / 4; ++q) sc[q] = 0;
+#pragma unroll
+  for (uint32_t w = 0; w < NW; ++w) {
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, rec[w], 1), s = w - a.L.nb;
+    if (w >= a.L.nb && s < a.L.ns) {
+      const uint32_t even = j & 1 ? other : rec[w], odd = j & 1 ? rec[w] : other;
+#pragma unroll
+      for (uint32_t q = 0; q < NB / 4; ++q) {
+        if (q == s) sc[q] = even;
+        if (q == a.L.ns + s) sc[q] = odd;
+      }
+    }
+  }
+  if (!live) return;
+#pragma unroll
+  for (uint32_t kb = 0; kb < NB; ++kb) {
+    const uint32_t d = 64 * kb + 8 * j;
+    if (d < a.L.nope) {
+      float v[8];
+      fp4_decode(rec[kb], (sc[kb / 4] >> (8 * (kb % 4))) & 255u, v);
+      store8<T, VEC>(dst + d, v);
+    }
+  }
   if (VEC) {
-    constexpr uint32_t E = 16 / sizeof(T);
-    for (uint32_t c = j; c < a.n_rot / E; c += 8)
+    if (j < a.n_rot / E) reinterpret_cast<uint4 *>(dst + a.L.nope)[j] = tail0;
+    for (uint32_t c = j + 8; c < a.n_rot / E; c += 8)
       reinterpret_cast<uint4 *>(dst + a.L.nope)[c] = reinterpret_cast<const uint4 *>(tail)[c];
   } else {
     for (uint32_t c = j; c < a.n_rot; c += 8) dst[a.L.nope + c] = tail[c];
   }
 }
 
-template <typename T>
-cudaError_t launch_t(bool pack, const RowsArgs &a, cudaStream_t s) {
+template <typename T, int NB>
+cudaError_t launch_nb(bool pack, const RowsArgs &a, cudaStream_t s) {
   // 16-byte vectors where every row and its tail start on 16 bytes
   const bool vec = reinterpret_cast<uintptr_t>(a.rows) % 16 == 0 &&
                    a.D * sizeof(T) % 16 == 0 && a.n_rot * sizeof(T) % 16 == 0;
-  auto *k = pack ? (vec ? rows_pack_kernel<T, true> : rows_pack_kernel<T, false>)
-                 : (vec ? rows_unpack_kernel<T, true> : rows_unpack_kernel<T, false>);
+  auto *k = pack ? (vec ? rows_pack_kernel<T, true, NB> : rows_pack_kernel<T, false, NB>)
+                 : (vec ? rows_unpack_kernel<T, true, NB> : rows_unpack_kernel<T, false, NB>);
   const uint32_t per = kThreads / 8;
   k<<<(a.n + per - 1) / per, kThreads, 0, s>>>(a);
   note_launches(1);
   return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_t(bool pack, const RowsArgs &a, cudaStream_t s) {
+  return a.L.nb <= 8 ? launch_nb<T, 8>(pack, a, s) : launch_nb<T, 16>(pack, a, s);
 }
 
 }  // namespace

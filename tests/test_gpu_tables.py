@@ -36,7 +36,8 @@ def step(pool, ctx, new, cap_raw, max_tokens):
 
 
 @pytest.mark.parametrize("B,M,n_blocks,cap_raw", [(1, 4, 4, 128), (5, 6, 30, 128), (33, 9, 120, 7),
-                                                  (300, 5, 1700, 1024), (8192, 2, 9000, 128)])
+                                                  (300, 5, 1700, 1024), (2040, 2, 3000, 128), (2048, 3, 6500, 128),
+                                                  (8192, 2, 9000, 128)])
 def test_steps_on_one_pool(B, M, n_blocks, cap_raw):
     lib = lib_()
     rng = np.random.default_rng(B)
