@@ -1148,6 +1148,7 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
     // running maxima; flags a score above its head's maximum by more than 2^8
     auto p_half = [&](bool valid, const uint32_t (&a)[HB], uint32_t hb, bool &flag) {
       uint8_t *prow = S.p + (r >> 3) * 1024 + (r & 7) * 128;
+      float top = -INFINITY;
 #pragma unroll
         for (uint32_t c4 = 0; c4 < HB / 8; ++c4) {
           uint32_t w4[4];
@@ -1156,12 +1157,14 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
             const uint32_t hl = 8 * c4 + 2 * e, h = hb + hl;
             const float t0 = fmaf(__uint_as_float(a[hl]), P.c2, -S.mref[h]);
             const float t1 = fmaf(__uint_as_float(a[hl + 1]), P.c2, -S.mref[h + 1]);
-            flag |= valid && (t0 > kRaiseLog2 || t1 > kRaiseLog2);
+            if (FP4) top = fmaxf(top, fmaxf(t0, t1));
+            else flag |= valid && (t0 > kRaiseLog2 || t1 > kRaiseLog2);
             w4[e] = valid ? pack_bf16(ex2_approx(t0), ex2_approx(t1)) : 0u;
           }
           *reinterpret_cast<uint4 *>(prow + (((hb / 8 + c4) ^ (r & 7)) << 4)) =
               make_uint4(w4[0], w4[1], w4[2], w4[3]);
         }
+      if (FP4) flag |= valid && top > kRaiseLog2;
     };
     // P row r from the scores in TMEM; returns whether a score exceeds its
     // head's running maximum by more than 2^8
