@@ -1528,9 +1528,7 @@ int max_active_clusters(uint32_t C, size_t smem) {
                cudaSuccess;
       };
       np = allow(attn_tc_kernel<true, false, false, kNhDec>) &&
-                   allow(attn_tc_kernel<true, true, false, kNhDec>) &&
-                   allow(attn_tc_kernel<true, true, true, kNhDec>) &&
-                   allow(attn_tc_kernel<true, true, true, kH>)
+                   allow(attn_tc_kernel<true, true, false, kNhDec>)
                ? 1
                : -1;
       (void)cudaGetLastError();
@@ -1598,11 +1596,78 @@ uint32_t decode_cluster(uint32_t rows_max, uint32_t n_q, size_t smem) {
   return pick_cluster(n_tiles, n_q, smem);
 }
 
-// Heads per CTA of a decode launch over 4-bit rows.
-uint32_t decode_heads(uint32_t n_heads, uint32_t rows_max, uint32_t n_q) {
-  // (twice as many CTAs of half the heads only while they all run at once)
-  const uint32_t tiles = (rows_max + kRows - 1) / kRows;
-  return n_heads > (uint32_t)kNhDec && (uint64_t)n_q * tiles * 2 > (uint64_t)num_sms() ? kH : kNhDec;
+// The same for the 4-bit kernels (their block and shared memory are larger): clusters
+// of C CTAs that run at once, 0 where the size cannot be launched.
+int max_active_clusters_fp4(uint32_t C) {
+  static std::atomic<int> seen[64][kMaxCluster + 1];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
+  int v = seen[dev][C].load(std::memory_order_relaxed);
+  if (v != 0) return v - 1;
+  auto *k = attn_tc_kernel<true, true, true, kH>;
+  const int smem = (int)sizeof(SmemFp4) + 1024;
+  bool ok = true;
+  for (auto *f : {k, attn_tc_kernel<true, true, true, kNhDec>}) {
+    ok = ok && cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess;
+    if (C > 8)
+      ok = ok && cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = C;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(C * 64);
+  cfg.blockDim = dim3(Warps<true>::THREADS);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  v = 0;
+  if (!ok || cudaOccupancyMaxActiveClusters(&v, k, &cfg) != cudaSuccess || v < 0) {
+    (void)cudaGetLastError();
+    v = C > 8 ? 0 : num_sms() / (int)C;   // (an unanswered query)
+  }
+  if (C == 1 && v < 1) v = 1;
+  seen[dev][C].store(v + 1, std::memory_order_relaxed);
+  return v;
+}
+
+// Heads per CTA and cluster size of a decode launch over 4-bit rows: the pair with
+// the least time by what was measured on this part (64 heads, 1 to 76 sequences, 5 to 33
+// tiles): a tile takes 2.5 us for 32 heads as for 64, and beside its tiles a wave of
+// clusters takes, in tenths of a tile, 33 (32 heads, no merge) .. 54 (64 heads merged by
+// 2 or 3 CTAs). A second wave takes as long as the first. Half the heads per CTA
+// save the output exchange (c4a, 8 sequences: 12.6 us against 14.1), until they no
+// longer fit at once (c128a, 32 sequences at 524,288: 64 us against 37).
+struct DecodePlan {
+  uint32_t nh, cluster;
+};
+DecodePlan fp4_decode_plan(uint32_t n_heads, uint32_t rows_max, uint32_t n_q) {
+  const uint32_t n_tiles = (rows_max + kRows - 1) / kRows;
+  uint32_t cmax = n_tiles < kMaxCluster ? (n_tiles ? n_tiles : 1u) : kMaxCluster;
+  const uint32_t force = g_force_cluster.load(std::memory_order_relaxed);
+  DecodePlan best{(uint32_t)kNhDec, 1};
+  uint64_t best_cost = ~0ull;
+  for (uint32_t nh : {(uint32_t)kNhDec, (uint32_t)kH}) {
+    if (nh == kH && n_heads <= (uint32_t)kNhDec) continue;
+    const uint64_t n_vq = (uint64_t)n_q * ((n_heads + nh - 1) / nh);
+    for (uint32_t C = 1; C <= cmax; ++C) {
+      if (force && C != (force < cmax ? force : cmax) && max_active_clusters_fp4(force < cmax ? force : cmax) > 0)
+        continue;
+      const int act = max_active_clusters_fp4(C);
+      if (act < 1) continue;
+      const bool half = nh == (uint32_t)kNhDec;
+      const uint32_t fixed = C == 1 ? (half ? 33 : 42) : C <= 3 ? (half ? 44 : 54) : (half ? 39 : 45);
+      const uint64_t waves = (n_vq + act - 1) / act, tiles = (n_tiles + C - 1) / C;
+      const uint64_t cost = waves * (10 * tiles + fixed);
+      if (cost < best_cost) {
+        best = DecodePlan{nh, C};
+        best_cost = cost;
+      }
+    }
+  }
+  return best;
 }
 
 }  // namespace
@@ -1612,8 +1677,8 @@ void attn_tc_force_cluster(uint32_t C) {
 }
 
 uint32_t attn_tc_decode_cluster(uint32_t rows_max, uint32_t n_q, uint32_t n_heads, bool fp4) {
-  const uint32_t nh = fp4 ? decode_heads(n_heads, rows_max, n_q) : kNhDec;
-  return decode_cluster(rows_max, n_q * ((n_heads + nh - 1) / nh), sizeof(Smem) + 1024);
+  if (fp4) return fp4_decode_plan(n_heads, rows_max, n_q).cluster;
+  return decode_cluster(rows_max, n_q * Heads<kNhDec>::HG, sizeof(Smem) + 1024);
 }
 
 // (4-bit rows: any number of heads)
@@ -1661,7 +1726,9 @@ cudaError_t launch_attention_tc(const AttnArgs &a, uint32_t rows_max, int *err, 
   // paged rows: an instantiation of its own, so the contiguous gathers carry
   // no table code
   const bool paged = a.map.table != nullptr, fp4 = a.fp4;
-  const uint32_t nh = a.T > 1 ? kH : fp4 ? decode_heads(a.n_heads, rows_max, P.n_q) : kNhDec;
+  const DecodePlan plan = fp4 && a.T == 1 ? fp4_decode_plan(a.n_heads, rows_max, P.n_q)
+                                          : DecodePlan{(uint32_t)kNhDec, 0u};
+  const uint32_t nh = a.T > 1 ? (uint32_t)kH : plan.nh;
   auto *k_dec = fp4     ? (nh == kH ? attn_tc_kernel<true, true, true, kH>
                                     : attn_tc_kernel<true, true, true, kNhDec>)
                 : paged ? attn_tc_kernel<true, true, false, kNhDec>
@@ -1719,7 +1786,7 @@ cudaError_t launch_attention_tc(const AttnArgs &a, uint32_t rows_max, int *err, 
   if (a.T == 1) {
     // one cluster of P.cluster CTAs per (query, head group)
     const uint32_t n_vq = P.n_q * P.hg;
-    P.cluster = decode_cluster(rows_max, n_vq, smem);
+    P.cluster = fp4 ? plan.cluster : decode_cluster(rows_max, n_vq, smem);
     P.ml = reinterpret_cast<float *>(P.part + (size_t)n_vq * P.cluster * nh * kD);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[2];
