@@ -58,6 +58,10 @@ ds4a_status check_cache(const ds4a_layer_cache *c) {
     if (c->ratio == 0 || (c->qat & DS4A_QAT_FP8_ATTN)) return DS4A_ERR_ARG;
     if (ds4a_row_bytes(c->head_dim, c->n_rot, c->dtype) == 0) return DS4A_ERR_SHAPE;
     if (reinterpret_cast<uintptr_t>(c->attn_comp_kv) % 16) return DS4A_ERR_ARG;
+    // (the kernels number the pool's rows in 32 bits)
+    const uint64_t pool = c->block_table ? (uint64_t)c->n_blocks * (256u / c->ratio)
+                                         : (uint64_t)c->batch * c->comp_cap;
+    if (pool >= 0xffffffffu) return DS4A_ERR_SHAPE;
   }
   return DS4A_OK;
 }

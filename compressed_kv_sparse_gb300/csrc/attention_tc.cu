@@ -82,6 +82,9 @@ constexpr int kNhDec = 32;             // heads per CTA in decode
 constexpr uint32_t kMaxCluster = 16;   // cluster size; beyond 8 (the portable limit) when the
                                        // device allows non-portable sizes
 constexpr float kRaiseLog2 = 8.0f;     // raise the running max beyond 2^8
+// The maximum of a first tile without a valid row: any later score raises it (O and L
+// are zeros until then).
+constexpr float kNoMax = -1e30f;
 
 struct TcAttnParams {
   uint32_t ratio, batch, T, pos0, cap_raw, comp_cap, n_comp, top_k;
@@ -655,7 +658,7 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
     auto list_row = [&](uint32_t g_b, uint32_t idx, uint32_t blk) {
       // (as RowMap::phys: table entries outside the pool read block 0)
       if (P.map.table) return ((blk < P.map.n_blocks ? blk : 0u) << rsh) + (idx & ((1u << rsh) - 1));
-      return g_b * P.comp_cap + idx;     // (fewer than 2^32: launch check)
+      return g_b * P.comp_cap + idx;     // (below 2^32: checked on the host)
     };
     auto table_at = [&](uint32_t g_b, uint32_t idx) -> const int32_t * {
       const uint32_t lb = min(idx >> rsh, P.map.max_blocks - 1);
@@ -1197,7 +1200,6 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
       QueryGeo g = g_next;
       if (maybe && !ahead) g = query_geo<kScan>(P, qi, rank, C, lane, n_list);
       const bool has_tiles = maybe && g.t0 < g.t1;
-      bool any_valid = false;
       // the rotation coefficients of this thread's tail dim in the direct
       // output (dim 384 + r of the last chunk), loaded while the tiles run
       float ep_co = 1.f, ep_si = 0.f;
@@ -1244,9 +1246,9 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
             const uint32_t hm = hb0 + (lane & (HB - 1));
             const uint32_t mk = max(max(tkey[0 * kH + hm], tkey[1 * kH + hm]),
                                     max(tkey[2 * kH + hm], tkey[3 * kH + hm]));
-            any_valid = mk != 0u;   // a valid row has a key above 0 for every head
+            const bool any_valid = mk != 0u;   // a valid row has a key above 0 for every head
             const float mx = __uint_as_float((mk & 0x80000000u) ? (mk & 0x7fffffffu) : ~mk);
-            if (lane < HB) S.mref[hm] = any_valid ? mx : 0.f;
+            if (lane < HB) S.mref[hm] = any_valid ? mx : kNoMax;
             __syncwarp();
             if (!wait_warp(&S.p_empty, (n & 1) ^ 1, ew)) goto done_softmax;
             bool unused = false;
@@ -1274,12 +1276,12 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
           if (threadIdx.x == 0) S.flagcnt[(n + 1) % 3] = 0;   // the next tile's raise count
           if (!sync_group(&S.sm_bar, sm_phase, ew)) goto done_softmax;
           const uint32_t k0 = max(max(tkey[0 * kH], tkey[1 * kH]), max(tkey[2 * kH], tkey[3 * kH]));
-          any_valid = k0 != 0u;   // a valid row has a key above 0 for every head
+          const bool any_valid = k0 != 0u;   // a valid row has a key above 0 for every head
           if (threadIdx.x < (uint32_t)NH) {
             const uint32_t mk = max(max(tkey[0 * kH + r], tkey[1 * kH + r]),
                                     max(tkey[2 * kH + r], tkey[3 * kH + r]));
             const float mx = __uint_as_float((mk & 0x80000000u) ? (mk & 0x7fffffffu) : ~mk);
-            S.mref[r] = any_valid ? mx : 0.f;
+            S.mref[r] = any_valid ? mx : kNoMax;
           }
           if (!sync_group(&S.sm_bar, sm_phase, ew)) goto done_softmax;
           if (!wait_warp(&S.p_empty, (n & 1) ^ 1, ew)) goto done_softmax;
@@ -1387,7 +1389,7 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
         // (max, sum) of this rank for the cluster merge; O follows from TMEM
         if (threadIdx.x < (uint32_t)NH) {
           float *ml = P.ml + ((size_t)(vq * C + rank) * NH + r) * 2;
-          ml[0] = (has_tiles && any_valid) ? S.mref[r] : -INFINITY;
+          ml[0] = has_tiles && !(S.mref[r] <= kNoMax) ? S.mref[r] : -INFINITY;
           ml[1] = has_tiles ? S.lsh[r] : 0.f;
         }
         if (threadIdx.x == 0) S.has_tiles = has_tiles ? 1u : 0u;

@@ -196,7 +196,8 @@ typedef struct {
  * code (a block with amax > 1.5 * 2^127 tops out at 1.5 * 2^127, a block that
  * holds an infinity or a NaN reads back as NaN). The rotated dims keep the
  * cache's dtype. The fp32 row (after RMSNorm and tail RoPE) is what is rounded.
- * For head_dim 512, n_rot 64, bf16 a row is 384 bytes against 1024.
+ * For head_dim 512, n_rot 64, bf16 a row is 384 bytes against 1024. The pool must
+ * hold fewer than 2^32 - 1 rows (DS4A_ERR_SHAPE otherwise).
  *
  * Bytes of a row, with nb = ceil(nope / 64), ns = ceil(nb / 8), R = nb + ns
  * rounded up to a multiple of 4: lane j (0..7) owns dims 64 kb + 8 j + i (i < 8) as
@@ -404,6 +405,7 @@ ds4a_status ds4a_unpack_rows(const ds4a_layer_cache *cache, uint32_t n, void *ro
  *           [0, B * cap_raw) drops the row. Slots must be distinct.
  *  flags    DS4A_NORM_ROTATE_Q: rotate the queries too (the attention of a cache
  *           with DS4A_Q_ROTATED); 0: norm only (it rotates them itself).
+ * Outputs overlap no input but as said. The attention may be the next launch.
  *
  * Replaces DS4A_LANE_RAW of the append; n_tokens is left for the append of the
  * other lanes, or for the caller (ds4a_compress_append_lanes). Errors:

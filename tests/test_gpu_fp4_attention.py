@@ -157,6 +157,14 @@ def ends_early(rng, row, vis):
         row[m] = vis
 
 
+def late(rng, row, vis):
+    """Nothing in the first 400 places, so that whole tiles have no row."""
+    m = int((row >= 0).sum())
+    keep = row[:m].copy()
+    row[:] = -1
+    row[400:] = np.sort(rng.choice(keep, len(row) - 400, replace=False))
+
+
 DECODE = [  # ratio, B, pos, H, dtype, ragged, paged, rot_q, top_k
     (4, 1, 0, 64, "bf16", None, False, True, 512),
     (4, 2, 2, 64, "bf16", None, True, False, 512),
@@ -303,3 +311,104 @@ def test_decode_is_repeatable_on_one_workspace():
     torch.cuda.synchronize()
     assert torch.equal(a.out, want)
     b.check()
+
+
+@pytest.mark.parametrize("cluster", [1, 2, 3, 5, 0])
+@pytest.mark.parametrize("T", [1, 5])
+def test_tiles_without_a_row_before_ones_with_rows(T, cluster):
+    """The first rows that a block meets may come tiles after its first tile: scores
+    far below zero must not be lost against a maximum that no row had."""
+    lib = lib_()
+    c = Case(4, 2, T, 9000, 64, top_k=512, lists=late, rot_q=True, q_std=0.05)
+    # every row close to -20 times the queries' mean: scores around -450
+    big = torch.randn((1, 512), generator=torch.Generator().manual_seed(5)).to(DEV)
+    cap = c.rows.shape[1]
+    x = (0.1 * torch.randn((2 * cap, 512), device=DEV) - 20 * big).bfloat16()
+    lib.ds4a_pack_rows(c.c, x, c.c.slots(cap).reshape(-1))
+    back = torch.empty_like(x)
+    lib.ds4a_unpack_rows(c.c, back, c.c.slots(cap).reshape(-1))
+    c.rows = np_(back).reshape(2, cap, 512).astype(np.float64)
+    c.q = (c.q.float() + big).bfloat16()
+    c.ring.copy_((-21 * big).bfloat16().expand_as(c.ring))
+    c.chunk.copy_((-21 * big).bfloat16().expand_as(c.chunk))
+    c.c.raw_kv.copy_(c.ring)
+    lib.ds4a_set_decode_cluster(cluster)
+    try:
+        c.run()
+        c.check()
+    finally:
+        lib.ds4a_set_decode_cluster(0)
+
+
+@pytest.mark.parametrize("ratio,pos", [(4, 9000), (128, 60000)])
+def test_every_cluster_size(ratio, pos):
+    lib = lib_()
+    c = Case(ratio, 2, 1, pos, 40, top_k=1500, paged=True, rot_q=True)
+    try:
+        for C in range(1, 17):
+            lib.ds4a_set_decode_cluster(C)
+            c.out.fill_(9)
+            c.run()
+            c.check()
+    finally:
+        lib.ds4a_set_decode_cluster(0)
+
+
+def test_chunk_with_lists_of_2048():
+    c = Case(4, 1, 12, 12000, 64, top_k=2048, paged=True)
+    c.run()
+    c.check()
+
+
+@pytest.mark.parametrize("ratio", [0, 128])
+def test_queries_and_rows_written_by_the_launch_before(ratio):
+    """ds4a_norm_rope, then the attention at once, again and again with other inputs: the
+    results are those of the same calls with a wait between them."""
+    lib = lib_()
+    B, H, D, pos = 8, 64, 512, 3000
+    qat = lib.Q_ROTATED | (lib.FP4_ROWS if ratio else 0)
+    c = lib.LayerCache(ratio=ratio, head_dim=D, n_rot=64, batch=B, comp_cap=24 if ratio else 0,
+                       dtype="bf16", base=BASE, rope_max_pos=pos + 1, qat=qat, device=DEV)
+    c.n_tokens = pos + 1
+    c.raw_kv.normal_()
+    if ratio:
+        lib.ds4a_pack_rows(c, torch.randn((B * 24, D), device=DEV).bfloat16())
+    p = torch.full((B,), pos, dtype=torch.int32, device=DEV)
+    slots = (torch.arange(B, device=DEV) * 128 + pos % 128).int()
+    x = [torch.randn((B, (H + 1) * D), device=DEV).bfloat16() for _ in range(40)]
+    q = torch.empty((B, H, D), dtype=torch.bfloat16, device=DEV)
+    ws = lib.workspace(c.workspace_bytes(lib.CALL_ATTN_DECODE, 1, H, 1))
+    got = [torch.empty_like(q) for _ in x]
+    want = [torch.empty_like(q) for _ in x]
+    for out, wait in ((want, True), (got, False), (got, False)):
+        for xi, o in zip(x, out):
+            lib.ds4a_norm_rope(c, p, q=xi[:, :H * D].view(B, H, D), q_out=q, kv=xi[:, H * D:],
+                               slots=slots, rot_q=True)
+            if wait:
+                torch.cuda.synchronize()
+            lib.ds4a_sparse_attn_decode(c, pos, q, H, None, 1, lib.default_scale(D), o, ws)
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+def test_first_call_inside_a_capture():
+    """In a process of its own: nothing of the library ran before the capture."""
+    import subprocess
+    import sys
+    code = """
+import sys; sys.path.insert(0, 'tests'); sys.path.insert(0, '.')
+import torch, test_gpu_fp4_attention as t
+from compressed_kv_sparse_gb300 import lib
+c = t.Case(4, 2, 1, 700, 64, top_k=50, rot_q=True)
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    c.run()
+g.replay()
+c.check()
+print('captured')
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]

@@ -46,6 +46,9 @@ def test_fp4_cache_checks(L):
     assert _append(L, _fp4(n_rot=60)) == -2              # 452 code dims: not in sixteens
     assert _append(L, _fp4(n_rot=512)) == -2             # no code dims at all
     assert _append(L, _fp4(attn_comp_kv=FAKE + 8)) == -1  # rows are read as 16-byte vectors
+    assert _append(L, _fp4(comp_cap=(1 << 32) - 1)) == -2   # rows are numbered in 32 bits
+    assert _append(L, _fp4(block_table=FAKE, max_blocks=1, comp_cap=64, n_blocks=1 << 26)) == -2
+    assert _append(L, _fp4(block_table=FAKE, max_blocks=1, comp_cap=64, n_blocks=1 << 25)) == -4
     ok = _fp4(qat=lib.Q_ROTATED)
     assert _append(L, ok) == -4
 
