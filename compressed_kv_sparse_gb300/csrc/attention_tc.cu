@@ -82,6 +82,10 @@ constexpr int kNhDec = 32;             // heads per CTA in decode
 constexpr uint32_t kMaxCluster = 16;   // cluster size; beyond 8 (the portable limit) when the
                                        // device allows non-portable sizes
 constexpr float kRaiseLog2 = 8.0f;     // raise the running max beyond 2^8
+// 4-bit rows start from the score of one valid row instead of the first tile's maximum
+// (any reference gives the same softmax while nothing over- or underflows) and raise it
+// beyond 2^60: P, O and L are floating point, so that only the range matters.
+constexpr float kRaiseFp4 = 60.0f;
 // The maximum of a first tile without a valid row: any later score raises it (O and L
 // are zeros until then).
 constexpr float kNoMax = -1e30f;
@@ -1167,7 +1171,7 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
           *reinterpret_cast<uint4 *>(prow + (((hb / 8 + c4) ^ (r & 7)) << 4)) =
               make_uint4(w4[0], w4[1], w4[2], w4[3]);
         }
-      if (FP4) flag |= valid && top > kRaiseLog2;
+      if (FP4) flag |= valid && top > kRaiseFp4;
     };
     // P row r from the scores in TMEM; returns whether a score exceeds its
     // head's running maximum by more than 2^8
@@ -1232,6 +1236,18 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
             uint32_t a0[HB];
             tmem_ld(tmS + lane_base + hb0, a0);
             tmem_ld_wait();
+            const uint32_t row0 = tile * kRows;
+            const bool valid0 = row0 < g.n_w ||
+                (row0 < g.N && (P.ratio != 4 || S4.rows[gb * kList + (row0 - g.n_w)] != kNoRow));
+            if (valid0) {   // (the same for every thread) the tile's first row is the reference
+              if (r == 0)
+#pragma unroll
+                for (uint32_t h = 0; h < HB; h += 4)
+                  *reinterpret_cast<float4 *>(&S.mref[hb0 + h]) =
+                      make_float4(__uint_as_float(a0[h]) * P.c2, __uint_as_float(a0[h + 1]) * P.c2,
+                                  __uint_as_float(a0[h + 2]) * P.c2, __uint_as_float(a0[h + 3]) * P.c2);
+              if (threadIdx.x == 0) S.flagcnt[n % 3] = 0;
+            } else {
             uint32_t mine = 0u;
 #pragma unroll
             for (uint32_t h = 0; h < HB; ++h) {
@@ -1241,7 +1257,6 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
               if (lane == h) mine = mk;
             }
             if (lane < HB) tkey[sq * kH + hb0 + lane] = mine;
-            if (threadIdx.x == 0) S.flagcnt[(n + 1) % 3] = 0;   // the next tile's raise count
             if (!sync_group(&S.sm_bar, sm_phase, ew)) goto done_softmax;
             const uint32_t hm = hb0 + (lane & (HB - 1));
             const uint32_t mk = max(max(tkey[0 * kH + hm], tkey[1 * kH + hm]),
@@ -1249,13 +1264,10 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
             const bool any_valid = mk != 0u;   // a valid row has a key above 0 for every head
             const float mx = __uint_as_float((mk & 0x80000000u) ? (mk & 0x7fffffffu) : ~mk);
             if (lane < HB) S.mref[hm] = any_valid ? mx : kNoMax;
-            __syncwarp();
-            if (!wait_warp(&S.p_empty, (n & 1) ^ 1, ew)) goto done_softmax;
-            bool unused = false;
-            p_half(valid, a0, hb0, unused);
-            fence_proxy_async();
-            tc_fence_before();
-            mbar_arrive(&S.p_full);
+            if (threadIdx.x == 0) S.flagcnt[n % 3] = 0;
+            }
+            if (!sync_group(&S.sm_bar, sm_phase, ew)) goto done_softmax;
+            // (then as every tile: P, with a raise where a score is far above)
           } else {
           // eight heads per step of a short loop: this runs once per query,
           // its code is fetched cold, and an unrolled form measured ~2 us of
@@ -1303,8 +1315,8 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
           fence_proxy_async();
           tc_fence_before();
           mbar_arrive(&S.p_full);
-          }
           continue;
+          }
         }
         // P of this tile (the previous PV must be done with the buffer)
         if (!wait_warp(&S.p_empty, (n & 1) ^ 1, ew)) goto done_softmax;
