@@ -55,15 +55,17 @@ __host__ __device__ inline uint32_t fp4_mag_bit(uint32_t t) { return (0x9036u >>
 
 // Scale byte of a block from its largest magnitude: k + 127; 255 when the
 // block holds an infinity or a NaN (every dim of it then reads back as NaN).
-__device__ __forceinline__ uint32_t fp4_scale_byte(float amax_bits_ok) {
-  const uint32_t b = __float_as_uint(amax_bits_ok) & 0x7FFFFFFFu;
+__device__ __forceinline__ uint32_t fp4_scale_byte(float amax) {
+  const uint32_t b = __float_as_uint(amax) & 0x7FFFFFFFu;
   if (b >= 0x7F800000u) return 255u;
-  return (uint32_t)(block_scale_exp(amax_bits_ok, kE2M1) + 127);
+  return (uint32_t)(block_scale_exp(amax, kE2M1) + 127);
 }
 
-// Larger magnitude of two, keeping a NaN (fmaxf would drop it): by the bits.
+// Larger magnitude of two; a NaN stays one (fmaxf would drop it).
 __device__ __forceinline__ float fp4_amax(float a, float b) {
-  return __uint_as_float(max(__float_as_uint(a) & 0x7FFFFFFFu, __float_as_uint(b) & 0x7FFFFFFFu));
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+  return r;
 }
 
 // Two fp32 values to E2M1 codes (nearest, ties to the even code): lo in bits 0 .. 3
@@ -83,15 +85,20 @@ __device__ __forceinline__ uint32_t fp4_codes2(float lo, float hi) {
 // value, 3 * 2^126, is taken.
 __device__ __forceinline__ uint32_t fp4_encode(const float (&v)[8], uint32_t sb) {
   if (sb == 255u) return 0u;
-  const float inv = pow2f(127 - (int)sb), top = sb == 253u ? 3.f : 6.f;
+  const float inv = pow2f(127 - (int)sb);
   uint32_t w = 0;
 #pragma unroll
   for (uint32_t t = 0; t < 4; ++t) {
-    const float lo = fminf(fmaxf(__fmul_rn(v[2 * t], inv), -top), top);
-    const float hi = fminf(fmaxf(__fmul_rn(v[2 * t + 1], inv), -top), top);
-    // dim 2 t to bits 0 .. 3, dim 2 t + 1 to bits 16 .. 19
+    float lo = __fmul_rn(v[2 * t], inv), hi = __fmul_rn(v[2 * t + 1], inv);
+    if (sb == 253u) {
+      lo = fminf(fmaxf(lo, -3.f), 3.f);
+      hi = fminf(fmaxf(hi, -3.f), 3.f);
+    }
+    // dim 2 t to bits 0 .. 3, dim 2 t + 1 to bits 16 .. 19, then each part to its place
+    // (the places are disjoint: the additions are ors)
     const uint32_t y = (fp4_codes2(lo, hi) * 0x1001u) & 0x000F000Fu;
-    w |= ((y & 0x00070007u) << fp4_mag_bit(t)) | ((y & 0x00080008u) << (fp4_sign_bit(t) - 3));
+    w += (y & 0x00070007u) * (1u << fp4_mag_bit(t));
+    w += (y & 0x00080008u) * (1u << (fp4_sign_bit(t) - 3));
   }
   return w;
 }
