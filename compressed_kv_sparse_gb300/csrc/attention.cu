@@ -443,7 +443,8 @@ size_t attn_ws_bytes(int dtype, uint32_t ratio, uint32_t batch, uint32_t T, uint
                      uint32_t head_dim, uint32_t n_rot, uint32_t cap_raw, uint32_t comp_cap,
                      uint32_t top_k, bool fp4) {
   if (attn_tc_supported(dtype, n_heads, head_dim, n_rot, fp4))
-    return attn_tc_ws_bytes(batch, T, rows_max(ratio, cap_raw, comp_cap, top_k), n_heads);
+    return attn_tc_ws_bytes(batch, T, rows_max(ratio, cap_raw, comp_cap, top_k), n_heads,
+                            fp4);
   const Plan pl = make_plan(ratio, batch, T, n_heads, head_dim, cap_raw, comp_cap, top_k, fp4);
   if (pl.n_splits == 1) return 0;
   return 256 + (size_t)batch * T * pl.n_splits * n_heads * (head_dim + 2) * sizeof(float);

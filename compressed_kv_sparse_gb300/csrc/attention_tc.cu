@@ -42,9 +42,38 @@
 // warps 4-7: gather loaders (cp.async, zero fill for masked rows) and the query
 // rotation; warp 8: MMA issue (one thread) and TMEM allocation. Every wait is
 // bounded (tc.cuh); a timeout sets the error word and the CTA winds down.
+//
+// Compressed rows in 4 bits (FP4; fp4rows.cuh) take the same two MMAs per tile, on a
+// tile that the loaders convert to bf16 on the way: E2M1 times 2^k is exact in bf16, so
+// the scores are those of the values that the rows stand for. What differs:
+// - Warps 0-7 softmax (two per 32 TMEM lanes, half the heads each), 8-15 loaders, 16 MMA
+//   issue. 544 threads of 96 registers.
+// - Loaders read the next tile's records (384 bytes a row) into registers while this
+//   tile's MMAs run, and convert and hand over the tile's blocks in pairs as PV frees
+//   them; S^T starts on the first pairs meanwhile. About 16 integer and 4 bf16 operations
+//   per eight dims.
+// - The issuing code is warp-uniform with the thread elected by the instructions: the
+//   same loop from a branch on lane 0 took twice the time per MMA.
+// - Waits sleep on their barrier (mbar_sleep), and code that all warps run again and
+//   again is kept short: the kernel is sensitive to instruction fetch (unrolled loops
+//   made the chunk 30% slower).
+// - A ratio-4 list is read once, checked for its end and turned into pool rows in
+//   shared memory, a query ahead in a chunk. A full window comes by TMA, from the ring or
+//   from the chunk, a box per loader warp.
+// - A query's reference is its first tile's first row (kRaiseFp4). In a chunk the output
+//   is written by softmax and loader warps together between two queries.
+// - Any number of heads: groups of 64 (32 in decode of small batches), the last one
+//   part-filled with zero queries that are not stored.
+// Measured (one GB300): a tile takes 5.7 thousand cycles, of which 2.9 PV and 1.5 the
+// rest of S^T; reads and writes of shared memory alone are 4.2 (S^T 192 KiB, PV 192,
+// the tile's conversion 128, P and L 32, at 128 bytes a cycle), which is what bounds it;
+// a query of a chunk costs another 4 thousand for its change of Q and O. 4096 queries of
+// 640 rows x 64 heads: 460 us (bf16 rows 645), 0.39 of the burst bf16 rate; c128a decode,
+// 32 sequences of 4,224 rows: 37 us (87); c4a decode, 8 sequences: 12.5 us (12.4).
 #include <cuda_bf16.h>
 
 #include <atomic>
+#include <cstddef>
 #include <type_traits>
 
 #include "common.cuh"
@@ -108,8 +137,8 @@ struct TcAttnParams {
   const int32_t *topk;
   const float *cos, *sin;
   __nv_bfloat16 *out;
-  // decode, C > 1: each rank's O / L as [n_q][C][64][512] bf16, and its
-  // (max, sum) per head as [n_q][C][64][2] fp32
+  // decode, C > 1: each rank's O / L as [n_q][C][64][512] bf16 (4-bit rows: fp32), and
+  // its (max, sum) per head as [n_q][C][64][2] fp32
   __nv_bfloat16 *part;
   float *ml;
   int *err;
@@ -147,6 +176,9 @@ constexpr uint32_t max_pulled_rows(uint32_t C = 1) {
 }
 static_assert(sizeof(SmemFp4) + 1024 <= 227 * 1024, "one block's shared memory");
 static_assert(8 * kKBlk >= max_pulled_rows() * kD * 2, "pulled slices fit the row buffer");
+static_assert(sizeof(Smem::q) + sizeof(Smem::kv) >= max_pulled_rows() * kD * 4 &&
+                  offsetof(Smem, kv) == sizeof(Smem::q),
+              "fp32 slices fit Q's buffer and the row buffer behind it");
 static_assert(2 * kH * 128 == kRows * 128, "output staging fills the P buffer");
 
 // Rows that a query can have at most, without reading its top-k list.
@@ -264,23 +296,28 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // row-tile buffer as [j][i][512] fp32 and are combined in rank order with
 // weights 2^(m_j - M) / sum_j 2^(m_j - M) l_j. A rank without rows left
 // m = -inf and zeros; one with only masked rows left m = -inf and O = 0.
-// CM: compile-time bound on the cluster size C (the loops over ranks unroll)
+// CM: compile-time bound on the cluster size C (the loops over ranks unroll). FP4: the
+// partials are fp32 (in bf16 they added a rounding to that of P: a c4a call's relative
+// error 0.0026 against 0.0021, at the same time), pulled into Q's buffer and the
+// tile's, and twice the threads combine them.
 template <uint32_t CM, int NH, bool FP4>
 __device__ __forceinline__ bool merge_heads(const TcAttnParams &P, Smem &S, uint32_t vq,
                                             uint32_t rank, uint32_t C, ErrWord ew) {
   const uint32_t HG = FP4 ? P.hg : (uint32_t)(kH / NH), HQ = FP4 ? P.n_heads : (uint32_t)kH;
   const uint32_t t = threadIdx.x, qi = vq / HG, hq0 = (vq % HG) * NH;
   const uint32_t h0 = rank * NH / C, h1 = (rank + 1) * NH / C, nh = h1 - h0;
-  const __nv_bfloat16 *part = P.part + (size_t)vq * C * NH * kD;
+  using PT = typename std::conditional<FP4, float, __nv_bfloat16>::type;
+  constexpr uint32_t kMT = FP4 ? 512 : 256;   // threads
+  const PT *part = reinterpret_cast<const PT *>(P.part) + (size_t)vq * C * NH * kD;
   const float *ml = P.ml + (size_t)vq * C * NH * 2;
-  __nv_bfloat16 *recv = reinterpret_cast<__nv_bfloat16 *>(S.kv);
+  PT *recv = reinterpret_cast<PT *>(FP4 ? S.q : S.kv);
   // rank j's rows h0 .. h1 - 1 are contiguous: one bulk copy per rank
   if (t == 0) {
     fence_proxy_async_global();
-    mbar_arrive_expect_tx(&S.mg_bar, C * nh * kD * 2);
+    mbar_arrive_expect_tx(&S.mg_bar, C * nh * kD * sizeof(PT));
     for (uint32_t j = 0; j < C; ++j)
-      bulk_load(recv + (size_t)j * nh * kD, part + ((size_t)j * NH + h0) * kD, nh * kD * 2,
-                &S.mg_bar);
+      bulk_load(recv + (size_t)j * nh * kD, part + ((size_t)j * NH + h0) * kD,
+                nh * kD * sizeof(PT), &S.mg_bar);
   }
   if (t < nh) {
     const uint32_t h = h0 + t;
@@ -314,15 +351,23 @@ __device__ __forceinline__ bool merge_heads(const TcAttnParams &P, Smem &S, uint
     si1 = P.sin[(size_t)p * 32 + fi + 1];
   }
   const bool ok = mbar_wait(&S.mg_bar, 0, ew);
-  named_bar_sync(1, 256);
+  named_bar_sync(1, kMT);
   if (!ok) return false;
 #pragma unroll 1
-  for (uint32_t i = t >> 7; i < nh; i += 2) {
+  for (uint32_t i = t >> 7; i < nh; i += kMT / 128) {
     float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
 #pragma unroll
     for (uint32_t j = 0; j < CM; ++j) {
       const float f = S.mw[i][j];
       if (j < C && f != 0.f) {
+        if (FP4) {
+          const float4 v = *reinterpret_cast<const float4 *>(recv + (j * nh + i) * kD + d);
+          a0 = fmaf(f, v.x, a0);
+          a1 = fmaf(f, v.y, a1);
+          a2 = fmaf(f, v.z, a2);
+          a3 = fmaf(f, v.w, a3);
+          continue;
+        }
         const uint2 v = *reinterpret_cast<const uint2 *>(recv + (j * nh + i) * kD + d);
         a0 = fmaf(f, bf16lo(v.x), a0);
         a1 = fmaf(f, bf16hi(v.x), a1);
@@ -1474,6 +1519,29 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
   __syncthreads();
   tc_fence_after();
   if (dec && C > 1) {
+    if constexpr (FP4) {
+      // this rank's O / L as [NH heads][512] fp32 straight to the workspace: warp w reads
+      // TMEM lanes 32 (w % 4) .. + 31 (dims) for 32 heads of its dim blocks (64 heads:
+      // two of the four blocks, 32 heads: one), a 128-byte line per head and store
+      if (warp < 16) {
+        float *dst = reinterpret_cast<float *>(P.part) + ((size_t)vq * C + rank) * NH * kD;
+        const uint32_t qw = warp & 3, hf = NHF == 2 ? (warp >> 2) & 1 : 0u;
+        const uint32_t m0 = NHF == 2 ? 2 * (warp >> 3) : warp >> 2, m1 = m0 + (NHF == 2 ? 2 : 1);
+        const bool had = S.has_tiles != 0;
+#pragma unroll 1
+        for (uint32_t m = m0; m < m1; ++m) {
+          uint32_t a[32];
+          if (had) {
+            tmem_ld32(tmO + ((32 * qw) << 16) + m * kH + 32 * hf, a);
+            tmem_ld_wait();
+          }
+          float *to = dst + (size_t)(32 * hf) * kD + m * 128 + 32 * qw + lane;
+#pragma unroll
+          for (int h = 0; h < 32; ++h)
+            to[(size_t)h * kD] = had ? __uint_as_float(a[h]) * S.linv[32 * hf + h] : 0.f;
+        }
+      }
+    } else {
     // this rank's O / L as [NH heads][512] bf16 straight to the workspace.
     // Warp w reads TMEM lanes 32 (w % 4) .. + 31 (dims) for heads 32 hf ..
     // + 31 of dim blocks m0 .. m1 - 1 (64 heads: hf = w / 4, every block; 32
@@ -1508,13 +1576,14 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
         }
       }
     }
+    }
   }
   tc_fence_before();
   __syncthreads();
   if (warp == WP::MMA) tmem_dealloc(tmem, 512);
   if (dec && C > 1) {
     cluster_sync_all();   // every rank's O and (max, sum) are in the workspace
-    if (warp < 8) {
+    if (warp < (FP4 ? 16 : 8)) {
       if (C <= 8)
         merge_heads<8, NH, FP4>(P, S, vq, rank, C, ew);
       else
@@ -1701,13 +1770,14 @@ bool attn_tc_supported(int dtype, uint32_t H, uint32_t D, uint32_t n_rot, bool f
 }
 
 // Error word, then (decode) room for the partials of the largest cluster.
-size_t attn_tc_ws_bytes(uint32_t batch, uint32_t T, uint32_t rows_max, uint32_t n_heads) {
+size_t attn_tc_ws_bytes(uint32_t batch, uint32_t T, uint32_t rows_max, uint32_t n_heads, bool fp4) {
   if (T != 1) return 256;
   const uint32_t n_tiles = (rows_max + kRows - 1) / kRows;
   const uint32_t cmax = n_tiles < kMaxCluster ? (n_tiles ? n_tiles : 1u) : kMaxCluster;
   if (cmax < 2) return 256;
   const uint32_t heads = (n_heads + kH - 1) / kH * kH;   // whole groups
-  return 256 + (size_t)batch * cmax * heads * (kD * sizeof(__nv_bfloat16) + 2 * sizeof(float));
+  const size_t elem = fp4 ? sizeof(float) : sizeof(__nv_bfloat16);
+  return 256 + (size_t)batch * cmax * heads * (kD * elem + 2 * sizeof(float));
 }
 
 cudaError_t launch_attention_tc(const AttnArgs &a, uint32_t rows_max, int *err, cudaStream_t s) {
@@ -1801,7 +1871,7 @@ cudaError_t launch_attention_tc(const AttnArgs &a, uint32_t rows_max, int *err, 
     // one cluster of P.cluster CTAs per (query, head group)
     const uint32_t n_vq = P.n_q * P.hg;
     P.cluster = fp4 ? plan.cluster : decode_cluster(rows_max, n_vq, smem);
-    P.ml = reinterpret_cast<float *>(P.part + (size_t)n_vq * P.cluster * nh * kD);
+    P.ml = reinterpret_cast<float *>(P.part + (size_t)n_vq * P.cluster * nh * kD * (fp4 ? 2 : 1));
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;

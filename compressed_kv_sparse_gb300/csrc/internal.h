@@ -186,7 +186,7 @@ cudaError_t launch_attention(const AttnArgs &a, cudaStream_t s);
 // Tensor-core attention (attention_tc.cu): bf16, 64 heads x 512 dims, 64-dim tail;
 // with 4-bit compressed rows any number of heads.
 bool attn_tc_supported(int dtype, uint32_t H, uint32_t D, uint32_t n_rot, bool fp4);
-size_t attn_tc_ws_bytes(uint32_t batch, uint32_t T, uint32_t rows_max, uint32_t n_heads);
+size_t attn_tc_ws_bytes(uint32_t batch, uint32_t T, uint32_t rows_max, uint32_t n_heads, bool fp4);
 cudaError_t launch_attention_tc(const AttnArgs &a, uint32_t rows_max, int *err, cudaStream_t s);
 // Decode cluster size: forced process-wide (0 = automatic), and the size a
 // decode launch of `n_q` queries with at most `rows_max` rows each uses.
