@@ -1855,7 +1855,8 @@ cudaError_t launch_attention_tc(const AttnArgs &a, uint32_t rows_max, int *err, 
     const uint32_t rb[3] = {64, (uint32_t)kRows, 1};
     if (make_tmap_bf16(&tr, a.chunk, 3, rd, rs, rb) == cudaSuccess) P.tma_rows |= 4u;
   }
-  if (a.T == 1 && a.cap_raw == (uint32_t)kRows && (a.ratio != 4 || fp4)) {
+  // (not for a chunk of one token: its row is in the chunk, not yet in the ring)
+  if (a.T == 1 && !a.chunk && a.cap_raw == (uint32_t)kRows && (a.ratio != 4 || fp4)) {
     const uint64_t rd[3] = {(uint64_t)kD, (uint64_t)a.cap_raw, (uint64_t)a.batch};
     const uint64_t rs[2] = {(uint64_t)kD * 2, (uint64_t)a.cap_raw * kD * 2};
     const uint32_t rb[3] = {64, (uint32_t)kRows, 1};

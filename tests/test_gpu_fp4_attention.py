@@ -412,3 +412,17 @@ print('captured')
 """
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("ratio,p0", [(4, 0), (4, 127), (4, 3001), (128, 130), (128, 20479)])
+def test_chunk_of_one_token(ratio, p0):
+    """The token's row is in the chunk alone, its slot of the ring still holds position
+    p - 128's."""
+    c = Case(ratio, 2, 1, p0, 64, top_k=300, rot_q=True)
+    call = lib_().CALL_ATTN_PREFILL
+    c.ws = lib_().workspace(c.c.workspace_bytes(call, 1, 64, 300))
+    c.c.raw_kv[:, p0 % 128] = -3.0
+    lib_().ds4a_sparse_attn_prefill_chunk(c.c, p0, 1, c.q, 64, c.chunk, c.topk, c.k, c.scale, c.out,
+                                          c.ws)
+    c.check()
+    assert torch.equal(c.c.raw_kv[:, p0 % 128], c.chunk[:, 0])
