@@ -165,7 +165,9 @@ struct Smem {
 constexpr uint32_t kList = 1024, kNoRow = 0xffffffffu;
 struct SmemFp4 : Smem {
   uint32_t rows[2 * kList];
-  uint32_t wend[2][8];            // per loader warp: first entry that ends the list
+  // per loader warp: bits 16 .. 31 the first place that ends the list (0xffff: none), bits
+  // 0 .. 15 the place behind the last row (lists have at most 2048 places)
+  uint32_t wend[2][8];
   uint64_t geo_full[2], geo_empty[2], ld_bar;
 };
 // the merge pulls at most C * ceil(64 / C) rows of 1 KiB (75 at C = 15)
@@ -181,11 +183,14 @@ static_assert(sizeof(Smem::q) + sizeof(Smem::kv) >= max_pulled_rows() * kD * 4 &
               "fp32 slices fit Q's buffer and the row buffer behind it");
 static_assert(2 * kH * 128 == kRows * 128, "output staging fills the P buffer");
 
-// Rows that a query can have at most, without reading its top-k list.
+// Rows that a query can have at most, without reading its top-k list. FP4: places, as the
+// rows of a list may stand anywhere in it.
+template <bool FP4>
 __device__ __forceinline__ uint32_t rows_bound(const TcAttnParams &P, uint32_t qi) {
   const uint32_t p = seq_base(P.seq_pos, P.pos0, qi / P.T) + qi % P.T;
   uint32_t n = min(p + 1, P.cap_raw);
-  if (P.ratio == 4) n += min(P.top_k, min((p + 1) / 4, P.n_comp));
+  const uint32_t vis4 = min((p + 1) / 4, P.n_comp);
+  if (P.ratio == 4) n += FP4 ? (vis4 ? P.top_k : 0u) : min(P.top_k, vis4);
   else if (P.ratio == 128) n += min((p + 1) / 128, P.n_comp);
   return n;
 }
@@ -464,10 +469,13 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
   auto list_half = [&](uint32_t gn) { return n_half == 2 ? gn & 1 : 0u; };
   auto list_phase = [&](uint32_t gn) { return (n_half == 2 ? gn >> 1 : gn) & 1; };
   auto list_end = [&](uint32_t gb) {
-    uint32_t e = P.top_k;
+    uint32_t e = 0xffffu, top = 0;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) e = min(e, S4.wend[gb][w]);
-    return e;
+    for (int w = 0; w < 8; ++w) {
+      e = min(e, S4.wend[gb][w] >> 16);
+      top = max(top, S4.wend[gb][w] & 0xffffu);
+    }
+    return min(e, top);
   };
   const uint32_t C = dec ? P.cluster : 1u;
   const uint32_t rank = dec ? cluster_ctarank() : 0u;
@@ -730,7 +738,7 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
       const uint32_t b = qi / P.T, p = seq_base(P.seq_pos, P.pos0, b) + qi % P.T;
       const uint32_t vis = min((p + 1) / 4, P.n_comp);
       if (!wait_warp(&S4.geo_empty[gb], list_phase(gn) ^ 1, ew)) return kNoRow;
-      uint32_t end = kNoRow;
+      uint32_t end = 0xffffu, top = 0;
       for (uint32_t base = 0; base < P.top_k; base += kList) {
         uint32_t blk[kFR];
         if (base) {
@@ -747,6 +755,7 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
             end = min(end, base + lt + WP::LT * i);
             tbl[i] = kNoRow;
           }
+          if ((int32_t)tbl[i] >= 0) top = base + lt + WP::LT * i + 1;
           if (P.map.table && (int32_t)tbl[i] >= 0) blk[i] = ld_nc_u32(table_at(b, tbl[i]));
         }
 #pragma unroll
@@ -757,7 +766,8 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
         }
       }
       end = redux_min_u32(end);
-      if (lane == 0) S4.wend[gb][lw] = end;
+      top = redux_max_u32(top);
+      if (lane == 0) S4.wend[gb][lw] = end << 16 | top;
       if (!sync_group(&S4.ld_bar, ld_phase, ew)) return kNoRow;
       if (lt == 0) mbar_arrive(&S4.geo_full[gb]);
       ++gn;
@@ -927,7 +937,7 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
           tma_load_2d(S.q + kb * QBLK, &tmap_q, &S.q_tma, (int)(64 * kb), (int)(qi * kH + hq0));
       }
     };
-    const bool q_early = i0 < n_items && rank * kRows < rows_bound(P, item_q(i0));
+    const bool q_early = i0 < n_items && rank * kRows < rows_bound<FP4>(P, item_q(i0));
     if (q_early) issue_q(i0);
     // The loaders' own wait for the previous launch. Decode reads nothing of
     // it before the first rows (the rotation coefficients are inputs and a
@@ -946,7 +956,7 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
     if (kScan || FP4) wait_prev();
     for (uint32_t it = i0; it < n_items; it += i_step) {
       const uint32_t qi = item_q(it);
-      if (rank * kRows >= rows_bound(P, qi)) continue;   // no rows for this rank
+      if (rank * kRows >= rows_bound<FP4>(P, qi)) continue;   // no rows for this rank
       if (!wait_warp(&S.q_empty, (qn & 1) ^ 1, ew)) goto done_loader;
       if (!(q_early && it == i0)) issue_q(it);
       {
@@ -1075,7 +1085,7 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
     for (uint32_t it = i0; FP4 && it < n_items && ok; it += i_step) {
       const uint32_t qi = item_q(it), rank_u = uniform(rank);
       const bool ahead = !DEC && !staged && it != i0;
-      if (!ahead && uniform(rank_u * kRows >= rows_bound(P, qi))) continue;
+      if (!ahead && uniform(rank_u * kRows >= rows_bound<FP4>(P, qi))) continue;
       uint32_t n_list = kNoRow;
       if (staged) {
         const uint32_t gb = list_half(gn);
@@ -1141,7 +1151,7 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
     }
     for (uint32_t it = i0; !FP4 && it < n_items && ok; it += i_step) {
       const uint32_t qi = item_q(it);
-      if (rank * kRows >= rows_bound(P, qi)) continue;
+      if (rank * kRows >= rows_bound<FP4>(P, qi)) continue;
       const QueryGeo g = query_geo<kScan>(P, qi, rank, C, lane);
       if (g.t0 >= g.t1) continue;
       if (lane == 0) {
@@ -1238,7 +1248,7 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
     for (uint32_t it = i0; it < n_items; it += i_step) {
       const uint32_t qi = item_q(it), hq0 = item_h(it);
       const bool ahead = FP4 && !DEC && !staged && it != i0;
-      const bool maybe = ahead || rank * kRows < rows_bound(P, qi);
+      const bool maybe = ahead || rank * kRows < rows_bound<FP4>(P, qi);
       uint32_t n_list = kNoRow, gb = 0;
       if (staged && maybe) {
         gb = list_half(gn);

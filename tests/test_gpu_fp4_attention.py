@@ -426,3 +426,16 @@ def test_chunk_of_one_token(ratio, p0):
                                           c.ws)
     c.check()
     assert torch.equal(c.c.raw_kv[:, p0 % 128], c.chunk[:, 0])
+
+
+@pytest.mark.parametrize("T", [1, 30])
+def test_rows_behind_as_many_places_as_are_visible(T):
+    """A list with fewer visible rows than places, all of them in its last places (entries
+    below 0 are skipped wherever they are)."""
+    def last(rng, row, vis):
+        m = int((row >= 0).sum())
+        row[:] = np.concatenate([row[m:], row[:m]])
+
+    c = Case(4, 3, T, 900, 64, top_k=512, lists=last, ragged=[900, 13, 300])
+    c.run()
+    c.check([(b, t) for b in range(3) for t in range(0, T, 7)])
