@@ -443,6 +443,7 @@ ds4a_status rows_call(bool pack, const ds4a_layer_cache *c, uint32_t n, const vo
   const uint64_t pool = c->block_table ? (uint64_t)c->n_blocks * (256u / c->ratio)
                                        : (uint64_t)c->batch * c->comp_cap;
   if (!slots && n > pool) return DS4A_ERR_CAPACITY;
+  if (n > 0x7fffffffu) return DS4A_ERR_SHAPE;
   return cuda_status(launch_rows_fp4(pack, c->dtype, c->attn_comp_kv, pool,
                                      const_cast<void *>(rows), slots, n, c->head_dim, c->n_rot,
                                      reinterpret_cast<cudaStream_t>(stream)));

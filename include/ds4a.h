@@ -377,7 +377,7 @@ ds4a_status ds4a_sparse_attn_prefill_chunk(ds4a_layer_cache *cache, uint32_t pos
  *        slots: of two rows for one slot either one, or a mix of both, remains.
  * n = 0 does nothing. Neither changes n_tokens. Errors: DS4A_ERR_ARG (no
  * DS4A_FP4_ROWS, a missing or misaligned pointer), DS4A_ERR_CAPACITY (no slots and n
- * beyond the pool), DS4A_ERR_CUDA.
+ * beyond the pool), DS4A_ERR_SHAPE (n >= 2^31), DS4A_ERR_CUDA.
  */
 ds4a_status ds4a_pack_rows(ds4a_layer_cache *cache, uint32_t n, const void *rows,
                            const int32_t *slots, ds4a_stream_t stream);

@@ -61,6 +61,7 @@ def test_rows_calls_check_arguments(L):
         assert fn(r, 3, None, FAKE, None) == -1
         assert fn(r, 3, FAKE + 1, FAKE, None) == -1
         assert fn(r, c.batch * c.comp_cap + 1, FAKE, None, None) == -3
+        assert fn(r, 1 << 31, FAKE, FAKE, None) == -2
         assert fn(None, 3, FAKE, FAKE, None) == -1
         plain = _fake_cache()
         assert fn(ctypes.byref(plain), 3, FAKE, FAKE, None) == -1
@@ -131,3 +132,35 @@ def test_fp4_cache_tensors_on_cpu(L):
     c = lib.LayerCache(ratio=128, comp_cap=6, block_table=table, n_blocks=7, **kw)
     assert c.attn_comp_kv.shape == (7, 2, 384)
     assert c.slots(5).tolist() == [[8, 9, 2, 3, 0], [4, 5, 10, 11, 6]]
+
+
+def test_bindings_check_tensors(L):
+    """Tensors of another type or size than the call reads are refused before it."""
+    import torch
+    kw = dict(head_dim=512, n_rot=64, batch=2, dtype="bf16", base=160000.0, rope_max_pos=16,
+              device="cpu", qat=lib.FP4_ROWS)
+    c = lib.LayerCache(ratio=128, comp_cap=6, **kw)
+    bf, i32 = dict(dtype=torch.bfloat16), dict(dtype=torch.int32)
+    rows = torch.zeros((3, 512), **bf)
+    for fn in (lib.ds4a_pack_rows, lib.ds4a_unpack_rows):
+        for bad in ((rows.float(), None), (rows[:, :256].contiguous(), None),
+                    (rows, torch.zeros(3, dtype=torch.int64)), (rows, torch.zeros(2, **i32))):
+            with pytest.raises(AssertionError):
+                fn(c, *bad, stream=0)
+        fn(c, rows[:0], stream=0)                       # nothing to do
+    pos, q, kv = torch.zeros(3, **i32), torch.zeros((3, 4, 512), **bf), torch.zeros((3, 512), **bf)
+    ok = dict(q=q, q_out=torch.empty_like(q), kv=kv, kv_out=torch.empty_like(kv), stream=0)
+    for bad in (dict(q=q.float()), dict(q_out=q[:2]), dict(kv=kv[:2]), dict(kv_out=kv[:2]),
+                dict(gamma_q=q[0, 0].float()), dict(gamma_kv=kv[0, :8]), dict(q=q[:, :, ::2]),
+                dict(kv_out=None, slots=pos.long()), dict(kv_out=None, slots=pos[:2]),
+                dict(q=q.transpose(0, 1).contiguous().transpose(0, 1))):
+        with pytest.raises(AssertionError):
+            lib.ds4a_norm_rope(c, pos, **{**ok, **bad})
+    with pytest.raises(AssertionError):
+        lib.ds4a_norm_rope(c, pos.long(), **ok)
+    lib.ds4a_norm_rope(c, pos[:0], q=q[:0], q_out=q[:0], kv=kv[:0], kv_out=kv[:0], stream=0)
+    pool, step = lib.BlockPool(2, 4, 8, device="cpu"), lib.StepTables(2, 16, device="cpu")
+    for ctx, new in ((torch.zeros(2, **i32), torch.zeros(3, **i32)),
+                     (torch.zeros(2, dtype=torch.int64), torch.zeros(2, **i32))):
+        with pytest.raises(AssertionError):
+            lib.ds4a_block_tables(pool, ctx, new, 128, step, stream=0)
