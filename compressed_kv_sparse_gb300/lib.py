@@ -372,30 +372,30 @@ def row_bytes(head_dim: int, n_rot: int, dtype: str) -> int:
     return n
 
 
-def _rows_match(cache: LayerCache, rows, slots):
-    _i32(slots)
-    assert rows.dtype == cache.torch_dtype and rows.shape[1] == cache.head_dim
-    assert slots is None or slots.numel() == rows.shape[0]
+_I32 = torch.int32
+
+
+def _rows_match(cache: LayerCache, rows: torch.Tensor, slots) -> int:
+    n = rows.size(0)
+    assert rows.dtype is cache.torch_dtype and rows.size(1) == cache.head_dim
+    assert slots is None or (slots.dtype is _I32 and slots.numel() == n)
+    return n
 
 
 def ds4a_pack_rows(cache: LayerCache, rows: torch.Tensor, slots: Optional[torch.Tensor] = None,
                    stream=None):
     """rows [n][D] into the 4-bit rows `slots` (None: 0 .. n - 1) of the cache's pool."""
-    _rows_match(cache, rows, slots)
-    _check(load().ds4a_pack_rows(cache.ref(), rows.shape[0], _ptr(rows), _ptr(slots),
+    n = _rows_match(cache, rows, slots)
+    _check(load().ds4a_pack_rows(cache.ref(), n, _ptr(rows), _ptr(slots),
                                  _stream(stream)), "ds4a_pack_rows")
 
 
 def ds4a_unpack_rows(cache: LayerCache, rows: torch.Tensor, slots: Optional[torch.Tensor] = None,
                      stream=None):
     """The values of 4-bit rows `slots` (None: 0 .. n - 1) into rows [n][D]."""
-    _rows_match(cache, rows, slots)
-    _check(load().ds4a_unpack_rows(cache.ref(), rows.shape[0], _ptr(rows), _ptr(slots),
+    n = _rows_match(cache, rows, slots)
+    _check(load().ds4a_unpack_rows(cache.ref(), n, _ptr(rows), _ptr(slots),
                                    _stream(stream)), "ds4a_unpack_rows")
-
-
-def _i32(*tensors):
-    assert all(t is None or t.dtype == torch.int32 for t in tensors), "int32 tensors"
 
 
 NORM_ROTATE_Q = 1   # DS4A_NORM_ROTATE_Q
@@ -410,25 +410,27 @@ def ds4a_norm_rope(cache: LayerCache, pos: torch.Tensor, *, q: Optional[torch.Te
     may be strided (a slice of one projection's output); a token's own elements
     are contiguous. kv goes to kv_out [n][D] or, kv_out None, to rows `slots` of
     the raw window."""
-    n, H, D, dt = pos.shape[0], 0, cache.head_dim, cache.torch_dtype
-    _i32(pos, slots)
-    assert slots is None or slots.numel() == n
-    for t, size in ((gamma_q, D), (gamma_kv, D), (kv_out, n * D),
-                    (q_out, None if q is None else q.numel())):
-        assert t is None or (t.dtype == dt and t.numel() == size)
+    n, H, D, dt, q_stride, kv_stride = pos.numel(), 0, cache.head_dim, cache.torch_dtype, 0, 0
+    assert pos.dtype is _I32 and (slots is None or (slots.dtype is _I32 and slots.numel() == n))
+    if q is not None:
+        (N, H, W), (q_stride, s1, s2) = q.shape, q.stride()
+        assert q.dtype is dt and N == n and W == D and s2 == 1 and (H == 1 or s1 == D)
+        assert q_out is None or (q_out.dtype is dt and q_out.numel() == n * H * D)
+        assert gamma_q is None or (gamma_q.dtype is dt and gamma_q.numel() == D)
+    if kv is not None:
+        kv_stride, s1 = kv.stride()
+        assert kv.dtype is dt and kv.shape == (n, D) and s1 == 1
+        assert kv_out is None or (kv_out.dtype is dt and kv_out.numel() == n * D)
+        assert gamma_kv is None or (gamma_kv.dtype is dt and gamma_kv.numel() == D)
+    if n == 1:   # (one token: its stride is whatever the slice left)
+        q_stride, kv_stride = H * D, D
     if n == 0:   # (empty tensors have no address)
         return
-    if q is not None:
-        H = q.shape[1]
-        assert q.dtype == dt and q.shape[0] == n and q.shape[2] == D
-        assert q.stride(2) == 1 and (H == 1 or q.stride(1) == D)
-    if kv is not None:
-        assert kv.dtype == dt and kv.shape == (n, D) and kv.stride(1) == 1
     _check(load().ds4a_norm_rope(
         cache.ref(), n, _ptr(pos), None if q is None else q.data_ptr(),
-        0 if q is None else (q.stride(0) if n > 1 else H * D), H, _ptr(gamma_q),
+        q_stride, H, _ptr(gamma_q),
         _ptr(q_out), None if kv is None else kv.data_ptr(),
-        0 if kv is None else (kv.stride(0) if n > 1 else D), _ptr(gamma_kv),
+        kv_stride, _ptr(gamma_kv),
         _ptr(kv_out), _ptr(slots), NORM_ROTATE_Q if rot_q else 0, _stream(stream)),
         "ds4a_norm_rope")
 
@@ -466,7 +468,7 @@ class StepTables:
 def ds4a_block_tables(pool: BlockPool, ctx_len: torch.Tensor, new_len: torch.Tensor, cap_raw: int,
                       step: StepTables, stream=None):
     """Blocks for rows of ctx_len [B] tokens (the last new_len [B] of them new), int32."""
-    _i32(ctx_len, new_len)
+    assert ctx_len.dtype is _I32 and new_len.dtype is _I32
     assert ctx_len.numel() == pool.rows == new_len.numel() == step.rows
     _check(load().ds4a_block_tables(ctypes.byref(pool.c), _ptr(ctx_len), _ptr(new_len), cap_raw,
                                     ctypes.byref(step.c), _stream(stream)), "ds4a_block_tables")
