@@ -11,18 +11,16 @@
 // and then writes its share of the rows and tokens. The state that all of them
 // read (held, the free list's head and count) is advanced by the block that
 // arrives last at a ticket, after every block has taken its copy; none waits.
-// Bound by the launch and the latency of the sums; by the stores of five words per
-// token beyond some 10^5 tokens.
+// Bound by the launch and a chain of latencies (8 decoding rows: 3.6 us), then by what
+// each block does for all rows (2,048 rows with 239,593 tokens: 7.7 us); by the stores of
+// five words per token beyond some 10^6 tokens.
 #include "common.cuh"
 #include "tc.cuh"
 
 namespace ds4a {
 namespace {
 
-constexpr uint32_t kThreads = 256;
-constexpr uint32_t kWarps = kThreads / 32;
 constexpr uint32_t kBlockTokens = 256;   // token positions of a logical block
-constexpr uint32_t kTokPerThread = 4;
 
 // Per row, six arrays in shared memory. A thread's consecutive rows (2^shift of them)
 // are followed by one unused place, which keeps the threads' accesses to their j-th
@@ -42,8 +40,10 @@ __device__ __forceinline__ uint32_t blocks_of(uint32_t ctx) {
 }
 
 // Exclusive sums over the block of four values per thread; totals in tot.
+template <uint32_t NT>
 __device__ __forceinline__ void block_scan4(uint32_t (&v)[4], uint32_t (&tot)[4],
                                             uint32_t (*part)[4]) {
+  constexpr uint32_t NW = NT / 32;
   const uint32_t lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   uint32_t inc[4];
 #pragma unroll
@@ -59,20 +59,55 @@ __device__ __forceinline__ void block_scan4(uint32_t (&v)[4], uint32_t (&tot)[4]
 #pragma unroll
     for (int k = 0; k < 4; ++k) part[w][k] = inc[k];
   __syncthreads();
+  if (w < 4) {   // warp k sums the warps' totals of value k
+    uint32_t x = lane < NW ? part[lane][w] : 0u;
+#pragma unroll
+    for (int o = 1; o < (int)NW; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= (uint32_t)o) x += y;
+    }
+    if (lane < NW) part[lane][w] = x;
+  }
+  __syncthreads();
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    uint32_t before = 0, all = 0;
-#pragma unroll
-    for (uint32_t i = 0; i < kWarps; ++i) {
-      if (i < w) before += part[i][k];
-      all += part[i][k];
-    }
-    v[k] = before + inc[k] - v[k];
-    tot[k] = all;
+    v[k] = (w ? part[w - 1][k] : 0u) + inc[k] - v[k];
+    tot[k] = part[NW - 1][k];
   }
 }
 
-__global__ void __launch_bounds__(kThreads) block_tables_kernel(TablesArgs a) {
+// Row of token tok, the last of the B rows whose first token is at or before it (rows
+// without new tokens share their first index with the row after them). WIDE: the warp looks
+// up its 32 tokens' first and last row together, 32 rows at a time (step: the
+// largest power of 32 below B), and the lanes search between the two, which are
+// mostly one row; else each lane by halves (step: the largest power of two below B).
+// (Whatever first[] holds, the result is below B.)
+template <bool WIDE, typename First>
+__device__ __forceinline__ uint32_t row_of_token(uint32_t tok, uint32_t B, uint32_t step,
+                                                 First first) {
+  uint32_t r0 = 0;
+  if (!WIDE) {
+    for (uint32_t w = step; w; w >>= 1)
+      if (r0 + w < B && first(r0 + w) <= tok) r0 += w;
+    return r0;
+  }
+  const uint32_t lane = threadIdx.x & 31, tok0 = tok - lane;
+  uint32_t r1 = 0;
+  for (uint32_t st = step; st; st >>= 5) {
+    const uint32_t i0 = r0 + st * lane, i1 = r1 + st * lane;
+    const bool b0 = i0 < B && first(i0) <= tok0, b1 = i1 < B && first(i1) <= tok0 + 31;
+    const int n0 = __popc(__ballot_sync(0xffffffffu, b0)), n1 = __popc(__ballot_sync(0xffffffffu, b1));
+    r0 += st * (max(n0, 1) - 1);
+    r1 += st * (max(n1, 1) - 1);
+  }
+  for (uint32_t w = r1 > r0 ? 1u << (31 - __clz(r1 - r0)) : 0u; w; w >>= 1)
+    if (r0 + w <= r1 && first(r0 + w) <= tok) r0 += w;
+  return r0;
+}
+
+template <uint32_t NT, uint32_t TPT>
+__global__ void __launch_bounds__(NT) block_tables_kernel(TablesArgs a) {
+  constexpr uint32_t kThreads = NT, kWarps = NT / 32, kTokPerThread = TPT;
   extern __shared__ uint32_t words[];
   __shared__ uint32_t part[kWarps][4], last;
   pdl_wait();
@@ -102,7 +137,7 @@ __global__ void __launch_bounds__(kThreads) block_tables_kernel(TablesArgs a) {
     v[2] += held > need ? held - need : 0u;
     v[3] += want - need;
   }
-  block_scan4(v, tot, part);
+  block_scan4<NT>(v, tot, part);
   for (uint32_t b = b0; b < b1; ++b) {
     const uint32_t need = min(blocks_of(R.ctx[at(b)]), a.max_blocks), held = R.held[at(b)];
     R.first[at(b)] = v[0];
@@ -168,18 +203,12 @@ __global__ void __launch_bounds__(kThreads) block_tables_kernel(TablesArgs a) {
   const bool maps = a.tok_seq || a.tok_pos || a.raw_slot || a.slot4 || a.slot128;
   const uint64_t step = (uint64_t)gridDim.x * kThreads * kTokPerThread;
   for (uint64_t base = (uint64_t)blockIdx.x * kThreads * kTokPerThread + t;
-       maps && base < a.max_tokens; base += step) {
-    // the row of a token: the last one whose first token is at or before it (rows
-    // without new tokens share their first index with the row after them)
+       maps && base - lane < a.max_tokens; base += step) {   // (whole warps)
     uint32_t lo[kTokPerThread];
 #pragma unroll
-    for (uint32_t e = 0; e < kTokPerThread; ++e) lo[e] = 0;
-    for (uint32_t w = a.search; w; w >>= 1)   // a.search: largest power of two < B
-#pragma unroll
-      for (uint32_t e = 0; e < kTokPerThread; ++e) {
-        const uint32_t mid = lo[e] + w;
-        if (mid < B && R.first[at(mid)] <= base + kThreads * e) lo[e] = mid;
-      }
+    for (uint32_t e = 0; e < kTokPerThread; ++e)
+      lo[e] = row_of_token<(NT > 256)>((uint32_t)base + kThreads * e, B, a.search,
+                                       [&](uint32_t b) { return R.first[at(b)]; });
     int32_t blk[kTokPerThread];
     uint32_t pos[kTokPerThread];
 #pragma unroll
@@ -234,28 +263,47 @@ __global__ void __launch_bounds__(kThreads) block_tables_kernel(TablesArgs a) {
 
 }  // namespace
 
-cudaError_t launch_block_tables(TablesArgs a, cudaStream_t s) {
-  a.search = 0;
-  for (uint32_t w = 1; w < a.rows; w <<= 1) a.search = w;
-  // one block per 1024 tokens or 256 rows, whichever asks for more
-  const uint64_t by_tok = ((uint64_t)a.max_tokens + kThreads * kTokPerThread - 1) /
-                          (kThreads * kTokPerThread);
-  const uint64_t by_row = (a.rows + 255) / 256;
+namespace {
+
+template <uint32_t NT, uint32_t TPT>
+cudaError_t launch_nt(TablesArgs a, cudaStream_t s) {
+  a.search = 1;   // (see row_of_token)
+  if (NT > 256) {
+    while (32ull * a.search < a.rows) a.search *= 32;
+  } else {
+    while (2 * a.search < a.rows) a.search *= 2;
+  }
+  // a warp per row and a thread per TPT tokens, whichever asks for more blocks, while
+  // the GPU has room for them (2,048 decoding rows: 7.2 us, in blocks of a row per
+  // thread 13.6)
+  const uint64_t by_tok = ((uint64_t)a.max_tokens + NT * TPT - 1) / (NT * TPT);
+  const uint64_t by_row = (a.rows + NT / 32 - 1) / (NT / 32);
   uint64_t g = by_tok > by_row ? by_tok : by_row;
-  const uint64_t most = 2 * (uint64_t)num_sms();
-  if (g > most) g = most;
-  if (g < 1) g = 1;
+  if (g > (uint64_t)num_sms()) g = num_sms();
+  if (NT <= 256) g = 1;   // (the call is small)
   a.shift = 0;   // rows per thread: 2^shift
-  while (((uint64_t)kThreads << a.shift) < a.rows) ++a.shift;
+  while (((uint64_t)NT << a.shift) < a.rows) ++a.shift;
   const size_t smem = (size_t)(a.rows + (a.rows >> a.shift) + 1) * kRowWords * sizeof(uint32_t);
   static DeviceSmem smem_set;
+  auto *k = block_tables_kernel<NT, TPT>;
   // (the limit without the attribute counts the static arrays too)
-  cudaError_t e = ensure_smem(block_tables_kernel, smem + 1024, smem_set.here());
+  cudaError_t e = ensure_smem(k, smem + 1024, smem_set.here());
   if (e != cudaSuccess) return e;
-  e = launch_pdl(block_tables_kernel, dim3((uint32_t)g), dim3(kThreads), smem, s, a);
+  e = launch_pdl(k, dim3((uint32_t)g), dim3(NT), smem, s, a);
   if (e != cudaSuccess) return e;
   note_launches(1);
   return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_block_tables(TablesArgs a, cudaStream_t s) {
+  // Few rows and tokens: one small block, which needs no ticket (8 decoding rows 3.2 us
+  // against 3.7 in large ones, 24 rows 4.5 in three small ones against 4.3). Otherwise up
+  // to one block of 1,024 threads per SM, which shares the sums over all rows among more
+  // threads (200 rows with 27,145 tokens: 5.6 us, in blocks of 256 threads 6.2; 2,048
+  // rows with 239,593: 7.7 against 9.9; 8,192 decoding: 9.0 against 18.8).
+  return a.rows <= 16 && a.max_tokens <= 512 ? launch_nt<256, 2>(a, s) : launch_nt<1024, 1>(a, s);
 }
 
 }  // namespace ds4a

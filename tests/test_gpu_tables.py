@@ -35,8 +35,9 @@ def step(pool, ctx, new, cap_raw, max_tokens):
     return st
 
 
-@pytest.mark.parametrize("B,M,n_blocks,cap_raw", [(1, 4, 4, 128), (5, 6, 30, 128), (33, 9, 120, 7),
-                                                  (300, 5, 1700, 1024), (2040, 2, 3000, 128), (2048, 3, 6500, 128),
+@pytest.mark.parametrize("B,M,n_blocks,cap_raw", [(1, 4, 4, 128), (5, 6, 30, 128), (16, 9, 60, 7), (17, 9, 60, 7), (33, 9, 120, 7),
+                                                  (300, 5, 1700, 1024), (1024, 3, 3300, 5),
+                                                  (1025, 3, 3300, 128), (2040, 2, 3000, 128), (2048, 3, 6500, 128),
                                                   (8192, 2, 9000, 128)])
 def test_steps_on_one_pool(B, M, n_blocks, cap_raw):
     lib = lib_()
@@ -59,7 +60,7 @@ def test_steps_on_one_pool(B, M, n_blocks, cap_raw):
     assert sorted(pool.free_list.tolist()) == list(range(n_blocks))
 
 
-@pytest.mark.parametrize("n_tok", [1, 3, 1023, 1024, 1025, 70000, 400001])
+@pytest.mark.parametrize("n_tok", [1, 3, 511, 512, 513, 1023, 1024, 1025, 70000, 400001])
 def test_token_counts(n_tok):
     lib = lib_()
     M = n_tok // 256 + 2
