@@ -11,8 +11,8 @@
 // and then writes its share of the rows and tokens. The state that all of them
 // read (held, the free list's head and count) is advanced by the block that
 // arrives last at a ticket, after every block has taken its copy; none waits.
-// Bound by the launch and a chain of latencies (8 decoding rows: 3.6 us), then by what
-// each block does for all rows (2,048 rows with 239,593 tokens: 7.7 us); by the stores of
+// Bound by the launch and a chain of latencies (8 decoding rows: 3.3 us), then by what
+// each block does for all rows (2,048 rows with 239,593 tokens: 7.8 us); by the stores of
 // five words per token beyond some 10^6 tokens.
 #include "common.cuh"
 #include "tc.cuh"

@@ -439,3 +439,48 @@ def test_rows_behind_as_many_places_as_are_visible(T):
     c = Case(4, 3, T, 900, 64, top_k=512, lists=last, ragged=[900, 13, 300])
     c.run()
     c.check([(b, t) for b in range(3) for t in range(0, T, 7)])
+
+
+@pytest.mark.parametrize("ratio,T,dtype", [(4, 1, "bf16"), (4, 9, "bf16"), (128, 1, "bf16"),
+                                           (4, 1, "f32")])
+def test_pool_offsets_pass_32_bits(ratio, T, dtype):
+    """The same rows at the far end of a pool of more than 4 GiB: the same output."""
+    lib = lib_()
+    D = 512 if dtype == "bf16" else 128
+    c = Case(ratio, 2, T, 5000, 64 if dtype == "bf16" else 5, D=D, top_k=100, dtype=dtype, paged=True)
+    c.run()
+    c.check()
+    rpb, near = 256 // ratio, c.c.n_blocks
+    far = (1 << 32) // (384 * rpb) + 1
+    table = torch.where(c.c.block_table >= 0, c.c.block_table + far, -1).int()
+    big = lib.LayerCache(ratio=ratio, head_dim=D, n_rot=64, batch=2, comp_cap=c.rows.shape[1],
+                         dtype=dtype, base=BASE, rope_max_pos=5000 + T, index_dim=32, index_rot=32,
+                         qat=lib.FP4_ROWS, device=DEV, block_table=table, n_blocks=far + near)
+    big.attn_comp_kv[far:] = c.c.attn_comp_kv
+    big.raw_kv.copy_(c.ring)
+    big.n_tokens = 5000 + T
+    want, c.c = c.out.clone(), big
+    c.out.fill_(7)
+    c.run()
+    torch.cuda.synchronize()
+    assert torch.equal(c.out, want)
+
+
+def test_two_calls_at_once():
+    """Calls on two streams, a workspace each."""
+    a = Case(128, 3, 1, 70000, 64, paged=True, rot_q=True)
+    b = Case(4, 2, 40, 700, 64, top_k=200)
+    cases, streams = (a, b), (torch.cuda.Stream(), torch.cuda.Stream())
+    for c in cases:
+        c.run()
+    torch.cuda.synchronize()
+    want = [c.out.clone() for c in cases]
+    b.c.raw_kv.copy_(b.ring)
+    for _ in range(5):
+        for c, s in zip(cases, streams):
+            c.out.zero_()
+            s.wait_stream(torch.cuda.current_stream())
+            c.run(stream=s)
+        torch.cuda.synchronize()
+        assert all(torch.equal(c.out, w) for c, w in zip(cases, want))
+        b.c.raw_kv.copy_(b.ring)

@@ -137,3 +137,18 @@ def test_many_tokens_other_stream_and_replayed_graph():
     g.replay()
     torch.cuda.synchronize()
     near(out[:64], q[:64], None, np.ones(64), 64, "bf16", True)
+
+
+def test_offsets_pass_32_bits():
+    """The last of so many tokens that their elements are numbered beyond 2^32."""
+    lib = lib_()
+    H, D = 64, 512
+    n = (1 << 32) // (H * D) + 5
+    c = make_cache(D, 64, "bf16")
+    q = torch.zeros((n, H, D), dtype=torch.bfloat16, device=DEV)
+    q[-7:] = torch.randn((7, H, D), device=DEV).bfloat16()
+    pos = torch.arange(n, dtype=torch.int32, device=DEV) % MAXP
+    out = torch.empty_like(q)
+    lib.ds4a_norm_rope(c, pos, q=q, q_out=out, rot_q=True)
+    near(out[-7:], q[-7:], None, pos[-7:].cpu().numpy(), 64, "bf16", True)
+    assert not out[:-7].any()
