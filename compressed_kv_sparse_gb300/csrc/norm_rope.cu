@@ -7,7 +7,7 @@
 // stays in registers between the sum of squares and the scaled, rotated store, so
 // each element is read once and written once. Bound by HBM at a chunk's size (4096
 // tokens of 64 heads x 512 in bf16: 92 us, 0.88 of the measured copy rate), by the
-// launch and two dependent look-ups at a decode step's (8 tokens: 2.9 us).
+// launch and two dependent look-ups at a decode step's (8 tokens: 3.1 us).
 #include "common.cuh"
 #include "tc.cuh"
 
