@@ -498,10 +498,7 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
 
   if (threadIdx.x == 0) {
     mbar_init(&S.kv_full, WP::LT);
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(&S.kv_empty[i], 1);
-      mbar_init(&S.kv_pair[i], WP::LT);
-    }
+    for (int i = 0; i < 4; ++i) mbar_init(&S.kv_empty[i], 1);
     mbar_init(&S.q_full, WP::LT);
     mbar_init(&S.q_empty, 1);
     mbar_init(&S.s_full, 1);
@@ -514,6 +511,7 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
     mbar_init(&S.kv_tma, 1);
     mbar_init(&S.mg_bar, 1);
     if (FP4) {
+      for (int i = 0; i < 4; ++i) mbar_init(&S.kv_pair[i], WP::LT);
       for (int i = 0; i < 2; ++i) {
         mbar_init(&S4.geo_full[i], 1);
         mbar_init(&S4.geo_empty[i], WP::NS + 1);   // softmax warps and the MMA issuer
