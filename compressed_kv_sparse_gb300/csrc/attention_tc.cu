@@ -158,6 +158,7 @@ struct Smem {
   float tmax[4][kH];
   float mw[kH][kMaxCluster];        // decode merge: weight of each rank, per owned head
   uint32_t flagcnt[3], tmem, has_tiles;
+  uint32_t n_end;   // decode over bf16 rows, ratio 4: rows up to the entry that ends the list
 };
 // 4-bit rows, ratio 4: the top-k lists of the query in work and the next one as pool
 // rows (kNoRow: masked), staged by the loaders for every role; lists above kList entries
@@ -183,29 +184,67 @@ static_assert(sizeof(Smem::q) + sizeof(Smem::kv) >= max_pulled_rows() * kD * 4 &
               "fp32 slices fit Q's buffer and the row buffer behind it");
 static_assert(2 * kH * 128 == kRows * 128, "output staging fills the P buffer");
 
-// Rows that a query can have at most, without reading its top-k list. FP4: places, as the
-// rows of a list may stand anywhere in it.
-template <bool FP4>
+// Places that a query's rows can take at most, without reading its top-k list (whose rows
+// may stand anywhere in it).
 __device__ __forceinline__ uint32_t rows_bound(const TcAttnParams &P, uint32_t qi) {
   const uint32_t p = seq_base(P.seq_pos, P.pos0, qi / P.T) + qi % P.T;
   uint32_t n = min(p + 1, P.cap_raw);
-  const uint32_t vis4 = min((p + 1) / 4, P.n_comp);
-  if (P.ratio == 4) n += FP4 ? (vis4 ? P.top_k : 0u) : min(P.top_k, vis4);
+  if (P.ratio == 4) n += min((p + 1) / 4, P.n_comp) ? P.top_k : 0u;
   else if (P.ratio == 128) n += min((p + 1) / 128, P.n_comp);
   return n;
 }
 
 // Query-level geometry shared by every role: tiles t0, t0 + ts, ... < t1.
 struct QueryGeo {
-  uint32_t qi, b, p0, p, n_w, n_list, N, t0, t1, ts;   // p0: the sequence's first chunk position
+  // p0: the sequence's first chunk position; vis: visible rows (ratio 4; else any number)
+  uint32_t qi, b, p0, p, n_w, n_list, N, t0, t1, ts, vis;
   const int32_t *tk;
 };
 
-// SCAN: read the list for its end (prefill: a chunk query's list may hold
-// rows past its visible ones). A decode list holds visible rows, then -1, so
-// decode takes the bound min(top_k, visible) and masks the -1 entries row by
-// row, with no dependent list read before the first gather.
-// n_list: the length of a ratio-4 list where it is known (4-bit rows).
+// A ratio-4 list ends at its first entry that is not visible. One warp: bits 16 .. 31 the
+// place of that entry (n: none), bits 0 .. 15 the place behind the last visible row (lists
+// have at most 2048 places).
+static __device__ __noinline__ uint32_t list_scan(const int32_t *tk, uint32_t n, uint32_t vis) {
+  const uint32_t lane = threadIdx.x & 31;
+  uint32_t end = n, top = 0;
+#pragma unroll 1
+  for (uint32_t base = lane; base - lane < n; base += 512) {
+    int32_t v[16];   // 16 loads in flight
+#pragma unroll
+    for (uint32_t i = 0; i < 16; ++i) v[i] = base + 32 * i < n ? tk[base + 32 * i] : -1;
+#pragma unroll
+    for (uint32_t i = 0; i < 16; ++i) {
+      if ((uint32_t)v[i] < vis) top = base + 32 * i + 1;
+      else if (v[i] >= 0) end = min(end, base + 32 * i);
+    }
+  }
+  return redux_min_u32(end) << 16 | redux_max_u32(top);
+}
+// The place of the entry that ends the list alone (n: none), in little code where there is
+// no such entry.
+static __device__ __noinline__ uint32_t list_stop(const int32_t *tk, uint32_t n, uint32_t vis) {
+  int32_t most = -1;
+#pragma unroll 1
+  for (uint32_t base = threadIdx.x & 31; base < n; base += 512) {
+    int32_t v[16];
+#pragma unroll
+    for (uint32_t i = 0; i < 16; ++i) v[i] = tk[min(base + 32 * i, n - 1)];
+#pragma unroll
+    for (uint32_t i = 0; i < 16; ++i) most = max(most, v[i]);
+  }
+  // (negative entries as unsigned would be the largest)
+  if (redux_max_u32((uint32_t)most + 1u) <= vis) return n;
+  return list_scan(tk, n, vis) >> 16;
+}
+
+// SCAN: read the list for its end (a chunk over bf16 rows). Decode over bf16 rows gives every
+// place of a list a row of a tile where as many rows are visible (the list is then full, or has
+// holes), without reading it before the first gather: entries that are no visible row are masked
+// one by one, those behind the list's end once the loaders have looked for it, while the first
+// rows are on their way (c4a, 8 sequences: 13.0 us; with the list read by every role before the
+// first gather 13.8, without any look for its end 12.6). Where fewer rows are visible than the
+// list has places, it is read for its length. n_list: the length of a ratio-4 list where it is
+// known (4-bit rows).
 template <bool SCAN>
 __device__ __forceinline__ QueryGeo query_geo(const TcAttnParams &P, uint32_t qi, uint32_t t0,
                                               uint32_t ts, uint32_t lane,
@@ -218,12 +257,17 @@ __device__ __forceinline__ QueryGeo query_geo(const TcAttnParams &P, uint32_t qi
   g.n_w = min(g.p + 1, P.cap_raw);
   g.tk = P.topk ? P.topk + (size_t)qi * P.top_k : nullptr;
   g.n_list = 0;
+  g.vis = P.ratio == 4 ? min((g.p + 1) / 4, P.n_comp) : 0x80000000u;
   if (n_list != kNoRow) {
     g.n_list = n_list;
   } else if (P.ratio == 4 && !SCAN) {
-    g.n_list = min(P.top_k, min((g.p + 1) / 4, P.n_comp));
+    g.n_list = P.top_k;
+    if (g.vis < P.top_k) {
+      const uint32_t ends = list_scan(g.tk, P.top_k, g.vis);
+      g.n_list = min(ends >> 16, ends & 0xffffu);
+    }
   } else if (P.ratio == 4) {
-    const uint32_t vis = min((g.p + 1) / 4, P.n_comp);
+    const uint32_t vis = g.vis;
     // the list ends at its first entry >= vis; 16 independent loads per round
     g.n_list = P.top_k;
     for (uint32_t base = 0; base < P.top_k; base += 512) {
@@ -281,7 +325,7 @@ __device__ __forceinline__ const __nv_bfloat16 *row_src(const TcAttnParams &P, c
   if (r < g.N) {
     const uint32_t j = r - g.n_w;
     const int32_t idx = P.ratio == 4 ? g.tk[j] : (int32_t)j;
-    if (idx >= 0) {
+    if ((uint32_t)idx < g.vis) {
       if (PAGED) return P.comp + P.map.row_of(g.b, (uint32_t)idx) * kD;
       return P.comp + ((size_t)g.b * P.comp_cap + (uint32_t)idx) * kD;
     }
@@ -699,6 +743,17 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
       }
       return true;
     };
+    // this thread's chunks of the rows from n_end on, once they have landed: zeros
+    auto zero_rows = [&](uint32_t tile, uint32_t n_end) {
+      cp_async_wait_all();
+#pragma unroll 1
+      for (uint32_t e = 0; e < 64; ++e) {
+        const uint32_t r = lw * 32 + (lane >> 3) + 4 * (e & 7), kb = e >> 3;
+        if (tile * kRows + r >= n_end)
+          *reinterpret_cast<uint4 *>(S.kv + kb * kKBlk + (r >> 3) * 1024 + (r & 7) * 128 +
+                                     (((lane & 7) ^ (r & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+      }
+    };
     // ---- 4-bit rows: thread lt holds lane lt % 8 of rows lt / 8 + 32 i. fetch_tile
     // loads their records into registers (12 16-byte loads in flight, each warp
     // load 128 contiguous bytes of four rows); store_tile converts them block pair by
@@ -935,13 +990,13 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
           tma_load_2d(S.q + kb * QBLK, &tmap_q, &S.q_tma, (int)(64 * kb), (int)(qi * kH + hq0));
       }
     };
-    const bool q_early = i0 < n_items && rank * kRows < rows_bound<FP4>(P, item_q(i0));
+    const bool q_early = i0 < n_items && rank * kRows < rows_bound(P, item_q(i0));
     if (q_early) issue_q(i0);
     // The loaders' own wait for the previous launch. Decode reads nothing of
-    // it before the first rows (the rotation coefficients are inputs and a
-    // decode list is not scanned), so its first query's coefficients and
-    // geometry are prepared before the wait; prefill scans its lists, so it
-    // waits here.
+    // it before its list (the rotation coefficients are inputs) or, without
+    // one, its first rows, so its first query's coefficients and, but for a
+    // list that is read for its length, its geometry are prepared before the
+    // wait; prefill scans its lists, so it waits here.
     uint32_t out_it = kNoRow;   // chunks over 4-bit rows: item whose output is to be written
     bool waited = false;
     auto wait_prev = [&]() {
@@ -954,7 +1009,7 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
     if (kScan || FP4) wait_prev();
     for (uint32_t it = i0; it < n_items; it += i_step) {
       const uint32_t qi = item_q(it);
-      if (rank * kRows >= rows_bound<FP4>(P, qi)) continue;   // no rows for this rank
+      if (rank * kRows >= rows_bound(P, qi)) continue;   // no rows for this rank
       if (!wait_warp(&S.q_empty, (qn & 1) ^ 1, ew)) goto done_loader;
       if (!(q_early && it == i0)) issue_q(it);
       {
@@ -978,13 +1033,14 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
           }
         }
         uint32_t n_list = kNoRow;
+        if (DEC && P.ratio == 4) wait_prev();
         if (staged) {
           if (DEC || it == i0) stage_load(qi);   // (else started a few tiles ago)
           if (DEC) fetch_first(qi);
           n_list = stage_list(qi);
           if (n_list == kNoRow) goto done_loader;
         }
-        const QueryGeo g = query_geo<kScan>(P, qi, rank, C, lane, n_list);
+        QueryGeo g = query_geo<kScan>(P, qi, rank, C, lane, n_list);
         if (g.t0 >= g.t1) {          // the list is shorter than the bound: nothing to do
           // (Q still lands: wait for it so the buffer is never written twice at once)
           if (!wait_warp(&S.q_tma, qt & 1, ew)) goto done_loader;
@@ -1052,6 +1108,17 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
           // MMA issuer takes the tile whole (waits between the MMAs of one
           // accumulation halve their rate; issuing S pair by pair as the
           // blocks land measured slower)
+          if (DEC && P.ratio == 4 && tile == g.t0) {
+            // while the rows are on their way: the entry that ends the list, for the softmax
+            // warps and the tiles to come; rows behind it (rare) become zeros after all, lest
+            // a NaN of theirs meet its weight of 0
+            const uint32_t n_end = g.n_w + list_stop(g.tk, P.top_k, g.vis);
+            if (n_end < g.N) {
+              zero_rows(tile, n_end);
+              g.N = n_end;
+            }
+            if (lt == 0) S.n_end = n_end;
+          }
           cp_async_wait_all();
           fence_proxy_async();
           if (tile_kind<DEC, PAGED>(P, g, tile)) {   // (one thread watches the TMA tile)
@@ -1083,7 +1150,7 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
     for (uint32_t it = i0; FP4 && it < n_items && ok; it += i_step) {
       const uint32_t qi = item_q(it), rank_u = uniform(rank);
       const bool ahead = !DEC && !staged && it != i0;
-      if (!ahead && uniform(rank_u * kRows >= rows_bound<FP4>(P, qi))) continue;
+      if (!ahead && uniform(rank_u * kRows >= rows_bound(P, qi))) continue;
       uint32_t n_list = kNoRow;
       if (staged) {
         const uint32_t gb = list_half(gn);
@@ -1149,7 +1216,7 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
     }
     for (uint32_t it = i0; !FP4 && it < n_items && ok; it += i_step) {
       const uint32_t qi = item_q(it);
-      if (rank * kRows >= rows_bound<FP4>(P, qi)) continue;
+      if (rank * kRows >= rows_bound(P, qi)) continue;
       const QueryGeo g = query_geo<kScan>(P, qi, rank, C, lane);
       if (g.t0 >= g.t1) continue;
       if (lane == 0) {
@@ -1246,7 +1313,7 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
     for (uint32_t it = i0; it < n_items; it += i_step) {
       const uint32_t qi = item_q(it), hq0 = item_h(it);
       const bool ahead = FP4 && !DEC && !staged && it != i0;
-      const bool maybe = ahead || rank * kRows < rows_bound<FP4>(P, qi);
+      const bool maybe = ahead || rank * kRows < rows_bound(P, qi);
       uint32_t n_list = kNoRow, gb = 0;
       if (staged && maybe) {
         gb = list_half(gn);
@@ -1271,11 +1338,16 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
         bool valid = row < g.n_w;
         if (!valid && row < g.N)
           valid = P.ratio != 4 || (FP4 ? S4.rows[gb * kList + (row - g.n_w)] != kNoRow
-                                       : g.tk[row - g.n_w] >= 0);
+                                       : (uint32_t)g.tk[row - g.n_w] < g.vis);
         if (FP4 && !DEC && !staged && tile + g.ts >= g.t1 && it + i_step < n_items)
           g_next = query_geo<kScan>(P, item_q(it + i_step), rank, C, lane);
         if (!wait_warp(&S.s_full, n & 1, ew)) goto done_softmax;
         tc_fence_after();
+        if (DEC && !FP4 && P.ratio == 4) {
+          // (kv_full's phase is complete: the test orders the loaders' store of n_end before this)
+          if (first) (void)mbar_test_wait(&S.kv_full, n & 1);
+          valid = valid && row < S.n_end;
+        }
         if (first) {
           // running maxima start at the exact per-head maxima of the first
           // tile's scaled scores: warp maxima of order-keyed values, then the
