@@ -164,7 +164,8 @@ class Runner:
                                comp_cap=cap, dtype=s.dtype, base=s.rope_base,
                                rope_max_pos=end + 1, index_dim=s.index_dim,
                                index_rot=s.index_rot, cap_raw=s.cap_raw,
-                               qat=qat_flags(s.ratio) if qat else 0, device=device,
+                               # (queries and positions are written before the append)
+                               qat=lib.Q_READY | (qat_flags(s.ratio) if qat else 0), device=device,
                                block_table=table, n_blocks=n_blocks)
             hist = synth.cache_history(seed_wl, il, self.p0, comp_cap=cap, device=device)
             c.load_state(hist, self.p0)

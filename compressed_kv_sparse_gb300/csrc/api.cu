@@ -47,7 +47,8 @@ ds4a_status check_cache(const ds4a_layer_cache *c) {
     if (c->ratio == 0 || c->max_blocks == 0 || c->n_blocks == 0) return DS4A_ERR_ARG;
     if ((uint64_t)c->max_blocks * (256u / c->ratio) != c->comp_cap) return DS4A_ERR_SHAPE;
   }
-  if (c->qat & ~(DS4A_QAT_FP8_ATTN | DS4A_QAT_FP4_INDEX | DS4A_FP4_ROWS | DS4A_Q_ROTATED))
+  if (c->qat & ~(DS4A_QAT_FP8_ATTN | DS4A_QAT_FP4_INDEX | DS4A_FP4_ROWS | DS4A_Q_ROTATED |
+                 DS4A_Q_READY))
     return DS4A_ERR_ARG;
   if ((c->qat & DS4A_QAT_FP8_ATTN) && c->ratio == 0) return DS4A_ERR_ARG;
   if (c->qat & DS4A_QAT_FP4_INDEX) {
@@ -392,6 +393,7 @@ static ds4a_status attn_common(const ds4a_layer_cache *c, uint32_t pos0, uint32_
   a.seq_pos = c->seq_pos;
   a.fp4 = (c->qat & DS4A_FP4_ROWS) != 0;
   a.q_rotated = (c->qat & DS4A_Q_ROTATED) != 0;
+  a.q_ready = (c->qat & DS4A_Q_READY) != 0;
   return cuda_status(launch_attention(a, s));
 }
 

@@ -132,6 +132,8 @@ struct TcAttnParams {
   uint32_t n_q;       // queries = batch * T
   float c2;           // softmax scale * log2(e)
   uint32_t q_rotated; // q is rotated already
+  uint32_t q_ready;   // q, positions, tables and error word may be read before the wait for the
+                      // previous launch (DS4A_Q_READY)
   uint32_t n_heads, hg;   // 4-bit rows: heads of a query (1 .. 128), head groups of a query
   const __nv_bfloat16 *q, *ring, *chunk, *comp;   // (comp: bytes of 4-bit rows where FP4)
   const int32_t *topk;
@@ -530,7 +532,14 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
   const uint32_t i0 = dec ? vq : blockIdx.x, i_step = dec ? n_items : gridDim.x;
   auto item_q = [&](uint32_t it) { return FP4 || dec ? it / HG : it; };
   auto item_h = [&](uint32_t it) { return FP4 || dec ? (it % HG) * NH : 0u; };   // first head
-  const int err_base = *(volatile int *)P.err;
+  // The wait for the previous launch: in a chunk here; in decode behind the block's own
+  // preparations or, with q_ready, in the loaders behind the first query's Q load (c4a, 8
+  // sequences, alone: 13.0 and 13.8 us; here for every call 14.3).
+  const bool ready = DEC && P.q_ready != 0;
+  if (!DEC) pdl_wait();
+  // (this launch's view of the error word: see ErrWord)
+  int err_base = 0;
+  if (ready || !DEC) err_base = *(volatile int *)P.err;
   if (NH < kH) {
     // heads NH .. 63 of every P row stay zero: the PV and sum MMAs read all
     // 64 columns, and those of the other group contribute nothing
@@ -588,15 +597,12 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  // the loaders wait for the previous launch themselves, after they have
-  // started the first query's Q load
   const bool loader = warp >= WP::NS && warp < WP::MMA;
-  if (!loader) {
+  if (!loader || (DEC && !ready)) {
     pdl_wait();
     pdl_trigger();
+    if (DEC && !ready) err_base = *(volatile int *)P.err;
   }
-  // this launch's view of the error word (see ErrWord), read before the wait
-  // so that its latency overlaps the previous launch
   const ErrWord ew{P.err, err_base};
   auto wait_warp = [&](uint64_t *bar, uint32_t parity, ErrWord e) {
     return FP4 ? mbar_wait_sleep(bar, parity, e) : mbar_wait_warp(bar, parity, e);
@@ -970,10 +976,10 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
       return true;
     };
     // Q (it needs no list): eight TMA boxes of 64 heads x 64 dims, in the
-    // 128-byte swizzled K-major layout the S MMAs read. The first query's
-    // is issued before the wait for the previous launch: the queries are the
-    // caller's input, written before that launch began (as are the rotation
-    // tables), while the top-k lists and the new raw row are not.
+    // 128-byte swizzled K-major layout the S MMAs read. With q_ready the first
+    // query's is issued before the wait for the previous launch: the queries, the
+    // positions and the rotation tables were then written before that launch
+    // began, while the top-k lists and the new raw row were not.
     auto issue_q = [&](uint32_t it) {
       if (FP4) {   // a box per loader warp; heads past the last one read as zeros
         if (lt == 0) mbar_arrive_expect_tx(&S.q_tma, 8 * QBLK);
@@ -990,15 +996,17 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
           tma_load_2d(S.q + kb * QBLK, &tmap_q, &S.q_tma, (int)(64 * kb), (int)(qi * kH + hq0));
       }
     };
-    const bool q_early = i0 < n_items && rank * kRows < rows_bound(P, item_q(i0));
+    // (without q_ready, behind the wait: before the loop all the same for bf16 rows, chunk 648
+    // against 660 us; in the loop for 4-bit rows, c4a decode 12.5 against 13.0)
+    const bool q_early = (ready || (!FP4 && i0 < n_items)) && rank * kRows < rows_bound(P, item_q(i0));
     if (q_early) issue_q(i0);
-    // The loaders' own wait for the previous launch. Decode reads nothing of
-    // it before its list (the rotation coefficients are inputs) or, without
-    // one, its first rows, so its first query's coefficients and, but for a
-    // list that is read for its length, its geometry are prepared before the
-    // wait; prefill scans its lists, so it waits here.
+    // The loaders' own wait for the previous launch (q_ready). Decode then reads
+    // nothing of it before its list or, without one, its first rows, so its first
+    // query's coefficients and, but for a list that is read for its length, its
+    // geometry are prepared before the wait; prefill scans its lists, so it waits
+    // here.
     uint32_t out_it = kNoRow;   // chunks over 4-bit rows: item whose output is to be written
-    bool waited = false;
+    bool waited = DEC && !ready;
     auto wait_prev = [&]() {
       if (!waited) {
         pdl_wait();
@@ -1875,6 +1883,7 @@ cudaError_t launch_attention_tc(const AttnArgs &a, uint32_t rows_max, int *err, 
   P.n_q = a.batch * a.T;
   P.c2 = a.scale * 1.4426950408889634f;
   P.q_rotated = a.q_rotated ? 1u : 0u;
+  P.q_ready = a.q_ready ? 1u : 0u;
   P.q = static_cast<const __nv_bfloat16 *>(a.q);
   P.ring = static_cast<const __nv_bfloat16 *>(a.ring);
   P.chunk = static_cast<const __nv_bfloat16 *>(a.chunk);

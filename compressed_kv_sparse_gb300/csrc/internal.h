@@ -177,6 +177,7 @@ struct AttnArgs {
   const uint32_t *seq_pos;  // [B] per-sequence positions (ragged decode) or NULL
   bool fp4;               // comp holds 4-bit rows (fp4rows.cuh)
   bool q_rotated;         // q is rotated already
+  bool q_ready;           // DS4A_Q_READY
 };
 size_t attn_ws_bytes(int dtype, uint32_t ratio, uint32_t batch, uint32_t T, uint32_t n_heads,
                      uint32_t head_dim, uint32_t n_rot, uint32_t cap_raw, uint32_t comp_cap,

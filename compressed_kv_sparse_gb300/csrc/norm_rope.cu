@@ -9,7 +9,6 @@
 // tokens of 64 heads x 512 in bf16: 92 us, 0.88 of the measured copy rate), by the
 // launch and two dependent look-ups at a decode step's (8 tokens: 3.1 us).
 #include "common.cuh"
-#include "tc.cuh"
 
 namespace ds4a {
 namespace {
@@ -193,13 +192,6 @@ __global__ void __launch_bounds__(kThreads, NV <= 2 ? 3 : 1) norm_rope_kernel(No
       }
     }
   }
-  // The attention starts its first query load before it waits for the previous
-  // launch (griddepcontrol.wait). When that launch is this one, it has begun only
-  // once every block here has ended, so it is enough that this thread's stores
-  // are done for the whole GPU, copies by TMA included, before it ends. For the
-  // same reason there is no early launch trigger.
-  fence_proxy_async_global();
-  __threadfence();
 }
 
 template <typename T, int E>

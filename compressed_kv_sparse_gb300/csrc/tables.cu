@@ -15,7 +15,6 @@
 // each block does for all rows (2,048 rows with 239,593 tokens: 7.8 us); by the stores of
 // five words per token beyond some 10^6 tokens.
 #include "common.cuh"
-#include "tc.cuh"
 
 namespace ds4a {
 namespace {
@@ -256,9 +255,6 @@ __global__ void __launch_bounds__(NT) block_tables_kernel(TablesArgs a) {
       advance();
     }
   }
-  // (as at the end of norm_rope_kernel: a following launch may read positions
-  // before its own wait, so the stores are done before this thread ends)
-  __threadfence();
 }
 
 }  // namespace

@@ -53,6 +53,7 @@ QAT_FP8_ATTN = 1    # DS4A_QAT_FP8_ATTN
 QAT_FP4_INDEX = 2   # DS4A_QAT_FP4_INDEX
 FP4_ROWS = 0x10000  # DS4A_FP4_ROWS: attn_comp_kv holds 4-bit rows
 Q_ROTATED = 0x20000  # DS4A_Q_ROTATED: the attention's queries are rotated already
+Q_READY = 0x80000   # DS4A_Q_READY: q and positions are written before the launch before it begins
 
 
 class BlockPoolC(ctypes.Structure):
