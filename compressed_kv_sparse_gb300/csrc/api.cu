@@ -4,6 +4,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstring>
+#include <initializer_list>
 
 #include "fp4rows.cuh"
 #include "internal.h"
@@ -23,6 +24,14 @@ cudaError_t note_error(cudaError_t e) {
 namespace {
 
 uint32_t window_of(uint32_t ratio) { return ratio == 4 ? 8u : ratio == 128 ? 128u : 0u; }
+
+// The pointers (NULL: not there) start on multiples of `align` bytes.
+bool aligned(uint32_t align, std::initializer_list<const void *> ptrs) {
+  uintptr_t all = 0;
+  for (const void *p : ptrs) all |= reinterpret_cast<uintptr_t>(p);
+  return all % align == 0;
+}
+uint32_t elem_bytes(const ds4a_layer_cache *c) { return c->dtype == DS4A_BF16 ? 2u : 4u; }
 
 ds4a_status check_cache(const ds4a_layer_cache *c) {
   if (!c) return DS4A_ERR_ARG;
@@ -206,6 +215,13 @@ ds4a_status append_parts(ds4a_layer_cache *c, uint32_t pos0, uint32_t T, uint32_
   if (c->ratio && comp_rows(c, pos0 + T) > c->comp_cap) return DS4A_ERR_CAPACITY;
   if (la && (!attn_cand || !attn_score || !ape_attn || !gamma_attn)) return DS4A_ERR_ARG;
   if (li && (!idx_cand || !idx_score || !ape_idx || !gamma_idx)) return DS4A_ERR_ARG;
+  // (the step kernel of 512- and 1024-wide rows reads the state as pairs)
+  if (la && !aligned(c->head_dim == 512 || c->head_dim == 1024 ? 8 : 4,
+                     {c->attn_state_kv, c->attn_state_score}))
+    return DS4A_ERR_ARG;
+  if (!aligned(elem_bytes(c), {raw_kv_in, raw_chunk_out, c->raw_kv, attn_cand, attn_score, ape_attn,
+                               gamma_attn, idx_cand, idx_score, ape_idx, gamma_idx}))
+    return DS4A_ERR_ARG;
 
   AppendArgs a;
   std::memset(&a, 0, sizeof(a));
@@ -309,6 +325,11 @@ ds4a_status index_topk_check(const ds4a_layer_cache *c, uint32_t pos0, uint32_t 
   if (T == 0 || n_heads == 0 || n_heads > 128 || top_k == 0 || top_k > 2048) return DS4A_ERR_SHAPE;
   if (!q_idx || !w || !topk) return DS4A_ERR_ARG;
   if ((uint64_t)pos0 + T > c->n_tokens) return DS4A_ERR_POSITION;
+  // (the tensor-core scorer reads keys by TMA)
+  const bool tc = c->dtype == DS4A_BF16 && index_tc_supported(n_heads, c->index_dim);
+  if (!aligned(tc ? 16 : elem_bytes(c), {c->index_comp_kv}) || !aligned(elem_bytes(c), {q_idx, w}) ||
+      !aligned(4, {topk, c->index_norm, c->index_norm_max, c->seq_pos, c->block_table}))
+    return DS4A_ERR_ARG;
   const uint32_t Hp = (n_heads + 7u) & ~7u;
   if (((size_t)c->index_dim * Hp + Hp + 128 * (size_t)(c->index_dim + 1)) * 4 > 227 * 1024)
     return DS4A_ERR_SHAPE;
@@ -325,6 +346,7 @@ ds4a_status ds4a_index_topk(const ds4a_layer_cache *c, uint32_t pos0, uint32_t T
   if (st) return st;
   const size_t need = index_ws_bytes(c->dtype, c->batch, T, n_heads, c->index_dim, c->comp_cap);
   if (!ws || ws_bytes < need) return DS4A_ERR_WORKSPACE;
+  if (!aligned(16, {ws})) return DS4A_ERR_ARG;
   IndexArgs a;
   a.batch = c->batch;
   a.T = T;
@@ -361,10 +383,19 @@ static ds4a_status attn_common(const ds4a_layer_cache *c, uint32_t pos0, uint32_
   if (!q || !out) return DS4A_ERR_ARG;
   if (!std::isfinite(scale)) return DS4A_ERR_ARG;
   if (c->ratio == 4 && (!topk || top_k == 0 || top_k > 2048)) return DS4A_ERR_ARG;
+  // The tensor-core kernels copy rows and queries 16 bytes at a time and store the output in
+  // 4- and 8-byte words.
+  const bool tc = attn_tc_supported(c->dtype, n_heads, c->head_dim, c->n_rot,
+                                    (c->qat & DS4A_FP4_ROWS) != 0);
+  if (!aligned(tc ? 16 : elem_bytes(c),
+               {q, out, raw_chunk, c->raw_kv, c->ratio ? c->attn_comp_kv : nullptr}) ||
+      !aligned(4, {c->ratio == 4 ? topk : nullptr, c->seq_pos, c->block_table}))
+    return DS4A_ERR_ARG;
   const size_t need = attn_ws_bytes(c->dtype, c->ratio, c->batch, T, n_heads, c->head_dim,
                                     c->n_rot, c->cap_raw, c->comp_cap, c->ratio == 4 ? top_k : 0,
                                     (c->qat & DS4A_FP4_ROWS) != 0);
   if (need && (!ws || ws_bytes < need)) return DS4A_ERR_WORKSPACE;
+  if (need && !aligned(16, {ws})) return DS4A_ERR_ARG;
   AttnArgs a;
   a.ratio = c->ratio;
   a.batch = c->batch;
@@ -440,8 +471,7 @@ ds4a_status rows_call(bool pack, const ds4a_layer_cache *c, uint32_t n, const vo
   if (st) return st;
   if (!(c->qat & DS4A_FP4_ROWS)) return DS4A_ERR_ARG;
   if (n == 0) return DS4A_OK;
-  if (!rows || reinterpret_cast<uintptr_t>(rows) % (c->dtype == DS4A_BF16 ? 2 : 4))
-    return DS4A_ERR_ARG;
+  if (!rows || !aligned(elem_bytes(c), {rows}) || !aligned(4, {slots})) return DS4A_ERR_ARG;
   const uint64_t pool = c->block_table ? (uint64_t)c->n_blocks * (256u / c->ratio)
                                        : (uint64_t)c->batch * c->comp_cap;
   if (!slots && n > pool) return DS4A_ERR_CAPACITY;
@@ -475,8 +505,8 @@ ds4a_status ds4a_norm_rope(ds4a_layer_cache *c, uint32_t n, const int32_t *pos, 
   if (flags & ~DS4A_NORM_ROTATE_Q) return DS4A_ERR_ARG;
   if (n > 0x7fffffffu) return DS4A_ERR_SHAPE;
   if ((!q && !kv) || !pos) return DS4A_ERR_ARG;
-  const uint32_t es = c->dtype == DS4A_BF16 ? 2 : 4;
-  uintptr_t ptrs = 0;
+  const uint32_t es = elem_bytes(c);
+  if (!aligned(4, {pos, slots})) return DS4A_ERR_ARG;
   if (q) {
     if (n_heads == 0 || n_heads > 128) return DS4A_ERR_SHAPE;
     if (!q_out) return DS4A_ERR_ARG;
@@ -484,8 +514,7 @@ ds4a_status ds4a_norm_rope(ds4a_layer_cache *c, uint32_t n, const int32_t *pos, 
     if (q_stride < row) return DS4A_ERR_SHAPE;
     // in place: only where every row is written where it was read
     if (q == q_out && q_stride != row) return DS4A_ERR_ARG;
-    ptrs |= reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(q_out) |
-            reinterpret_cast<uintptr_t>(gamma_q);
+    if (!aligned(es, {q, q_out, gamma_q})) return DS4A_ERR_ARG;
   }
   uint64_t n_dst = n;
   if (kv) {
@@ -495,10 +524,8 @@ ds4a_status ds4a_norm_rope(ds4a_layer_cache *c, uint32_t n, const int32_t *pos, 
     if (kv == kv_out && kv_stride != c->head_dim) return DS4A_ERR_ARG;
     if (!kv_out) n_dst = (uint64_t)c->batch * c->cap_raw;
     if (n_dst > 0x7fffffffu) return DS4A_ERR_SHAPE;
-    ptrs |= reinterpret_cast<uintptr_t>(kv) | reinterpret_cast<uintptr_t>(kv_out) |
-            reinterpret_cast<uintptr_t>(gamma_kv) | reinterpret_cast<uintptr_t>(c->raw_kv);
+    if (!aligned(es, {kv, kv_out, gamma_kv, c->raw_kv})) return DS4A_ERR_ARG;
   }
-  if (ptrs % es) return DS4A_ERR_ARG;
   if (n == 0) return DS4A_OK;
   NormRopeArgs a;
   a.dtype = c->dtype;
@@ -529,6 +556,10 @@ ds4a_status ds4a_block_tables(const ds4a_block_pool *p, const uint32_t *ctx_len,
                               const ds4a_step_tables *out, ds4a_stream_t stream) {
   if (!p || !out || !ctx_len || !new_len) return DS4A_ERR_ARG;
   if (!p->table || !p->held || !p->free_list || !p->state) return DS4A_ERR_ARG;
+  if (!aligned(4, {p->table, p->held, p->free_list, p->state, ctx_len, new_len, out->seq_pos,
+                   out->cu_len, out->tok_seq, out->tok_pos, out->raw_slot, out->comp_slot4,
+                   out->comp_slot128}))
+    return DS4A_ERR_ARG;
   if (p->rows == 0 || p->rows > DS4A_MAX_TABLE_ROWS || p->max_blocks == 0 || p->n_blocks == 0)
     return DS4A_ERR_SHAPE;
   // slots (blk * 64 + ..) and positions (< 256 * max_blocks) are int32

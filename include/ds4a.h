@@ -34,6 +34,12 @@
  *  - Row-major layouts, innermost dimension last. Element type of rows,
  *    inputs and outputs is ds4a_layer_cache.dtype (fp32 or bf16); the
  *    compressor state is always fp32.
+ *  - Every array starts on a multiple of its element's size, workspaces on 16
+ *    bytes. On 16 bytes too, where the calls run on the tensor cores (bf16): q,
+ *    out, raw_kv, raw_chunk and attn_comp_kv of the attention calls of a cache
+ *    of 512 dims with a 64-dim tail (64 heads, or 4-bit rows), index_comp_kv of
+ *    an indexer of 64 heads x 128 dims; attn_state_kv and attn_state_score on 8
+ *    bytes for 512 and 1024 dims. DS4A_ERR_ARG otherwise.
  *  - Order within a step: append -> index_topk (ratio 4) -> attention.
  */
 #ifndef DS4A_H

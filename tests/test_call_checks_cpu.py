@@ -23,3 +23,101 @@ def test_the_flag_for_ready_queries(L):
     assert append(L, cache(qat=lib.Q_READY)) == -4       # past the cache's checks (position)
     assert append(L, cache(qat=lib.Q_READY | lib.Q_ROTATED | lib.FP4_ROWS)) == -4
     assert append(L, cache(qat=lib.Q_READY << 1)) == -1
+
+
+BIG = 1 << 40
+
+
+def decode(L, c, q=FAKE, topk=FAKE, out=FAKE, ws=FAKE, nbytes=BIG, heads=64):
+    return L.ds4a_sparse_attn_decode(ctypes.byref(c), c.n_tokens - 1, q, heads, topk, 512, 0.1, out, ws,
+                                     nbytes, None)
+
+
+def chunk(L, c, q=FAKE, rows=FAKE, topk=FAKE, out=FAKE, ws=FAKE, nbytes=BIG, heads=64):
+    return L.ds4a_sparse_attn_prefill_chunk(ctypes.byref(c), c.n_tokens - 2, 2, q, heads, rows, topk, 512,
+                                            0.1, out, ws, nbytes, None)
+
+
+def test_attention_on_the_tensor_cores_wants_16_bytes(L):
+    """Rows, queries, output and workspace of the kernels that copy 16 bytes at a time."""
+    for qat, heads in ((0, 64), (lib.FP4_ROWS, 64), (lib.FP4_ROWS, 5)):
+        kw = dict(qat=qat)
+        for call in (decode, chunk):
+            assert call(L, cache(**kw), nbytes=8, heads=heads) == -8     # past the checks
+            for off in (2, 4, 8):
+                for name in ("q", "out", "ws"):
+                    assert call(L, cache(**kw), heads=heads, **{name: FAKE + off}) == -1, (name, off)
+                for name in ("raw_kv", "attn_comp_kv"):
+                    assert call(L, cache(**{name: FAKE + off}, **kw), heads=heads) == -1, (name, off)
+                assert chunk(L, cache(**kw), rows=FAKE + off, heads=heads) == -1
+            assert call(L, cache(**kw), topk=FAKE + 2, heads=heads) == -1
+            assert call(L, cache(seq_pos=FAKE + 2, **kw), heads=heads) == -1
+
+
+def test_attention_on_the_cuda_cores_wants_whole_elements(L):
+    for kw, es, heads in ((dict(dtype=lib.DS4A_F32), 4, 64), (dict(), 2, 8), (dict(head_dim=128), 2, 64)):
+        for call in (decode, chunk):
+            for name in ("q", "out"):
+                assert call(L, cache(**kw), nbytes=8, heads=heads, **{name: FAKE + es}) == -8
+                assert call(L, cache(**kw), heads=heads, **{name: FAKE + es // 2}) == -1
+            for name in ("raw_kv", "attn_comp_kv"):
+                assert call(L, cache(**{name: FAKE + es}, **kw), nbytes=8, heads=heads) == -8
+                assert call(L, cache(**{name: FAKE + es // 2}, **kw), heads=heads) == -1
+            assert call(L, cache(**kw), ws=FAKE + 8, heads=heads) == -1
+    # a row of the window that ds4a_norm_rope may write need not suit the attention
+    assert L.ds4a_norm_rope(ctypes.byref(cache(raw_kv=FAKE + 2)), 0, FAKE, None, 0, 0, None, None, FAKE,
+                            512, None, None, FAKE, 0, None) == 0
+    assert decode(L, cache(raw_kv=FAKE + 2)) == -1
+
+
+def test_other_calls_check_alignment(L):
+    def topk(c, q=FAKE, w=FAKE, out=FAKE, ws=FAKE, nbytes=BIG, heads=64):
+        return L.ds4a_index_topk(ctypes.byref(c), 9, 1, q, w, heads, 512, out, ws, nbytes, None)
+
+    assert topk(cache(), q=FAKE + 2, w=FAKE + 2, nbytes=8) == -8         # (any element's place will do)
+    assert topk(cache(), q=FAKE + 1) == -1 and topk(cache(), w=FAKE + 1) == -1
+    assert topk(cache(), out=FAKE + 2) == -1 and topk(cache(), ws=FAKE + 8) == -1
+    assert topk(cache(index_comp_kv=FAKE + 8)) == -1
+    assert topk(cache(index_comp_kv=FAKE + 2), heads=8, nbytes=8) == -8
+    assert topk(cache(index_comp_kv=FAKE + 1), heads=8) == -1
+    assert topk(cache(dtype=lib.DS4A_F32), q=FAKE + 2) == -1
+
+    def app(c, **kw):
+        args = [kw.get(f"a{i}", FAKE) for i in range(9)]
+        return L.ds4a_compress_append(ctypes.byref(c), 10, 1, *args, None, None)
+
+    for i in range(9):
+        assert app(cache(), **{f"a{i}": FAKE + 1}) == -1, i
+    assert app(cache(attn_state_kv=FAKE + 4)) == -1 and app(cache(attn_state_score=FAKE + 4)) == -1
+    assert app(cache(raw_kv=FAKE + 1)) == -1
+
+    fp4 = cache(qat=lib.FP4_ROWS)
+    for fn in (L.ds4a_pack_rows, L.ds4a_unpack_rows):
+        assert fn(ctypes.byref(fp4), 3, FAKE, FAKE + 2, None) == -1
+        assert fn(ctypes.byref(fp4), 3, FAKE + 1, FAKE, None) == -1
+
+    def norm(**kw):
+        a = dict(pos=FAKE, q=FAKE, gq=FAKE, qo=2 * FAKE, kv=FAKE, gk=FAKE, kvo=None, slots=FAKE)
+        a.update(kw)
+        return L.ds4a_norm_rope(ctypes.byref(cache()), 0, a["pos"], a["q"], 64 * 512, 64, a["gq"], a["qo"],
+                                a["kv"], 512, a["gk"], a["kvo"], a["slots"], 0, None)
+
+    assert norm() == 0                                   # (no tokens: nothing to do)
+    assert norm(pos=FAKE + 2) == -1 and norm(slots=FAKE + 2) == -1
+    for name in ("q", "gq", "qo", "kv", "gk"):
+        assert norm(**{name: FAKE + 1}) == -1, name
+        assert norm(**{name: FAKE + 2}) == 0, name
+    assert norm(kvo=FAKE + 1, slots=None) == -1
+
+    def tables(ctx=FAKE, new=FAKE, pool=(), step=()):
+        p = lib.BlockPoolC(**{**dict(rows=4, max_blocks=8, n_blocks=16, table=FAKE, held=FAKE,
+                                     free_list=FAKE, state=FAKE), **dict(pool)})
+        s = lib.StepTablesC(**{**dict(max_tokens=4), **dict(step)})
+        return L.ds4a_block_tables(ctypes.byref(p), ctx, new, 0, ctypes.byref(s), None)
+
+    assert tables() == -2                                # past the pointers (no window)
+    assert tables(ctx=FAKE + 2) == -1 and tables(new=FAKE + 1) == -1
+    for name in ("table", "held", "free_list", "state"):
+        assert tables(pool={name: FAKE + 2}) == -1, name
+    for name in ("seq_pos", "cu_len", "tok_seq", "tok_pos", "raw_slot", "comp_slot4", "comp_slot128"):
+        assert tables(step={name: FAKE + 2}) == -1, name
