@@ -438,9 +438,9 @@ cudaError_t launch_attention_t(const AttnArgs &a, cudaStream_t s) {
   const Plan pl = make_plan(a.ratio, a.batch, a.T, a.n_heads, a.head_dim, a.cap_raw,
                             a.comp_cap, a.top_k, a.fp4);
   const size_t smem = smem_bytes(pl, a.head_dim);
-  static DeviceSmem smem_set[2];
+  static RaisedLimit smem_set[2];
   auto *kernel = a.fp4 ? attn_kernel<T, true> : attn_kernel<T, false>;
-  cudaError_t e = ensure_smem(kernel, smem, smem_set[a.fp4].here());
+  cudaError_t e = ensure_smem(kernel, smem, smem_set[a.fp4]);
   if (e != cudaSuccess) return e;
   // (the first 256 bytes: the error word of the workspace; this path has no
   // device waits and leaves it alone)

@@ -1911,9 +1911,9 @@ cudaError_t launch_attention_tc(const AttnArgs &a, uint32_t rows_max, int *err, 
                        : attn_tc_kernel<false, false, false, kH>;
   P.n_heads = a.n_heads;
   P.hg = (a.n_heads + nh - 1) / nh;
-  static DeviceSmem smem_set[2][4];
+  static RaisedLimit smem_set[2][4];
   cudaError_t e = ensure_smem(a.T == 1 ? k_dec : k_pf, smem,
-                              smem_set[a.T == 1][fp4 ? 2 + (nh == kH) : paged].here());
+                              smem_set[a.T == 1][fp4 ? 2 + (nh == kH) : paged]);
   if (e != cudaSuccess) return e;
   CUtensorMap tq;
   if (fp4) {   // Q as [n_q][H][512]: boxes of one CTA's heads, zeros past the last head

@@ -863,8 +863,8 @@ cudaError_t launch_index_exact(const IndexArgs &a, cudaStream_t s) {
   note_launches(1);
   const uint32_t Hp = round_up8(a.n_heads);
   const size_t smem = ((size_t)a.dim * Hp + Hp + (size_t)kRowsPerBlock * (a.dim + 1)) * 4;
-  static int smem_set = 0;
-  cudaError_t e = ensure_smem(index_score_exact_kernel<T>, smem, &smem_set);
+  static RaisedLimit smem_set;
+  cudaError_t e = ensure_smem(index_score_exact_kernel<T>, smem, smem_set);
   if (e != cudaSuccess) return e;
   const uint32_t vis_max = min((a.pos0 + a.T) / 4, a.n_comp);
   if (vis_max > a.top_k) {
@@ -929,24 +929,23 @@ cudaError_t launch_index_tc(const IndexArgs &a, cudaStream_t s) {
   const uint32_t G = select_groups(nq);
   if (G == 1) {
     const size_t smem = SelCfg<256>::smem(a.comp_cap);
-    static int smem_set = 0;
-    cudaError_t e = ensure_smem(topk_select_tc_kernel<256>, smem, &smem_set);
+    static RaisedLimit smem_set;
+    cudaError_t e = ensure_smem(topk_select_tc_kernel<256>, smem, smem_set);
     if (e != cudaSuccess) return e;
     // four blocks per SM: the largest shared-memory carveout
-    static int carve = 0;
-    if (!carve) {
-      e = cudaFuncSetAttribute(topk_select_tc_kernel<256>,
-                               cudaFuncAttributePreferredSharedMemoryCarveout,
-                               cudaSharedmemCarveoutMaxShared);
-      if (e != cudaSuccess) return e;
-      carve = 1;
-    }
+    static RaisedLimit carve;
+    e = raise_here(carve, 1, [](size_t) {
+      return cudaFuncSetAttribute(topk_select_tc_kernel<256>,
+                                  cudaFuncAttributePreferredSharedMemoryCarveout,
+                                  cudaSharedmemCarveoutMaxShared);
+    });
+    if (e != cudaSuccess) return e;
     e = launch_pdl(topk_select_tc_kernel<256>, dim3(nq), dim3(256), smem, s, a, w, (float)cb, G);
     if (e != cudaSuccess) return e;
   } else {
     const size_t smem = SelCfg<1024>::smem(a.comp_cap);
-    static int smem_set = 0;
-    cudaError_t e = ensure_smem(topk_select_tc_kernel<1024>, smem, &smem_set);
+    static RaisedLimit smem_set;
+    cudaError_t e = ensure_smem(topk_select_tc_kernel<1024>, smem, smem_set);
     if (e != cudaSuccess) return e;
     // the G blocks of a query form a cluster (their candidates go to the
     // first block's shared memory)

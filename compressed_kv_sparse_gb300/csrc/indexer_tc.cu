@@ -503,8 +503,8 @@ cudaError_t launch_qg(const IndexTcArgs &a, cudaStream_t s) {
   P.map = a.map;
   P.seq_pos = a.seq_pos;
   if (P.total_items == 0) return cudaSuccess;
-  static int smem_set = 0;
-  e = ensure_smem(index_score_tc_kernel<QG>, C::kSmem, &smem_set);
+  static RaisedLimit smem_set;
+  e = ensure_smem(index_score_tc_kernel<QG>, C::kSmem, smem_set);
   if (e != cudaSuccess) return e;
   // one group per CTA range when that costs no more tiles per CTA than the
   // contiguous split (a CTA that changes query reloads its heads and flushes

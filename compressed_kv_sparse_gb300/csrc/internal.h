@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include "ds4a.h"
+#include "limit.h"
 
 namespace ds4a {
 
@@ -16,25 +17,24 @@ void note_launches(uint32_t n);
 // Records a CUDA error for ds4a_last_error and passes it through.
 cudaError_t note_error(cudaError_t e);
 
-// Raise a kernel's dynamic shared memory limit to `bytes` (no-op below 48 KiB
-// or when already raised that far).
-template <typename F>
-cudaError_t ensure_smem(F *func, size_t bytes, int *done) {
-  if (bytes <= 48 * 1024 || (size_t)*done >= bytes) return cudaSuccess;
-  cudaError_t e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (e == cudaSuccess) *done = (int)bytes;
-  return e;
+// Raises `limit` on the current device to `bytes` by set(bytes) where it is below.
+template <typename Set>
+cudaError_t raise_here(RaisedLimit &limit, size_t bytes, Set set) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= RaisedLimit::kDevices) return cudaErrorInvalidDevice;
+  return limit.raise(dev, bytes, set);
 }
 
-// A kernel's ensure_smem record per device (the limit is set on the current one).
-struct DeviceSmem {
-  int done[64] = {};
-  int *here() {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
-    return done + dev;
-  }
-};
+// Raises a kernel's dynamic shared memory limit to `bytes` (nothing to do up to 48 KiB).
+template <typename F>
+cudaError_t ensure_smem(F *func, size_t bytes, RaisedLimit &limit) {
+  if (bytes <= 48 * 1024) return cudaSuccess;
+  return raise_here(limit, bytes, [&](size_t b) {
+    return cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)b);
+  });
+}
 
 // Launch with programmatic stream serialization (see pdl_wait in common.cuh).
 template <typename... KArgs, typename... Args>

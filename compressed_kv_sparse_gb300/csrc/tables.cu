@@ -280,10 +280,10 @@ cudaError_t launch_nt(TablesArgs a, cudaStream_t s) {
   a.shift = 0;   // rows per thread: 2^shift
   while (((uint64_t)NT << a.shift) < a.rows) ++a.shift;
   const size_t smem = (size_t)(a.rows + (a.rows >> a.shift) + 1) * kRowWords * sizeof(uint32_t);
-  static DeviceSmem smem_set;
+  static RaisedLimit smem_set;
   auto *k = block_tables_kernel<NT, TPT>;
   // (the limit without the attribute counts the static arrays too)
-  cudaError_t e = ensure_smem(k, smem + 1024, smem_set.here());
+  cudaError_t e = ensure_smem(k, smem + 1024, smem_set);
   if (e != cudaSuccess) return e;
   e = launch_pdl(k, dim3((uint32_t)g), dim3(NT), smem, s, a);
   if (e != cudaSuccess) return e;
