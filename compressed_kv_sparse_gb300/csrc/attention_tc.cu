@@ -1710,6 +1710,9 @@ int max_active_clusters(uint32_t C, size_t smem) {
       return -1;
     }
   }
+  // (the size may be asked for before the first launch; the limit is every launch's)
+  (void)cudaFuncSetAttribute(attn_tc_kernel<true, false, false, kNhDec>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
