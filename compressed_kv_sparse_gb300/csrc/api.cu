@@ -33,21 +33,28 @@ bool aligned(uint32_t align, std::initializer_list<const void *> ptrs) {
 }
 uint32_t elem_bytes(const ds4a_layer_cache *c) { return c->dtype == DS4A_BF16 ? 2u : 4u; }
 
-ds4a_status check_cache(const ds4a_layer_cache *c) {
+// The sizes of a cache alone.
+ds4a_status check_sizes(const ds4a_layer_cache *c) {
   if (!c) return DS4A_ERR_ARG;
   if (c->dtype != DS4A_F32 && c->dtype != DS4A_BF16) return DS4A_ERR_DTYPE;
   if (c->ratio != 0 && c->ratio != 4 && c->ratio != 128) return DS4A_ERR_ARG;
   if (c->batch == 0 || c->head_dim == 0 || c->head_dim > 1024 || c->head_dim % 4) return DS4A_ERR_SHAPE;
   if (c->n_rot > c->head_dim || c->n_rot % 2) return DS4A_ERR_SHAPE;
   if (c->cap_raw == 0 || c->cap_raw > 1024) return DS4A_ERR_SHAPE;
-  if (!c->raw_kv || !c->rope_cos || !c->rope_sin || c->rope_max_pos == 0) return DS4A_ERR_ARG;
-  if (c->ratio) {
-    if (!c->attn_comp_kv || !c->attn_state_kv || !c->attn_state_score) return DS4A_ERR_ARG;
-    if (c->comp_cap == 0) return DS4A_ERR_CAPACITY;
-  }
+  if (c->ratio && c->comp_cap == 0) return DS4A_ERR_CAPACITY;
   if (c->ratio == 4) {
     if (c->index_dim == 0 || c->index_dim > 256 || c->index_dim % 4) return DS4A_ERR_SHAPE;
     if (c->index_rot > c->index_dim || c->index_rot % 2) return DS4A_ERR_SHAPE;
+  }
+  return DS4A_OK;
+}
+
+ds4a_status check_cache(const ds4a_layer_cache *c) {
+  const ds4a_status st = check_sizes(c);
+  if (st) return st;
+  if (!c->raw_kv || !c->rope_cos || !c->rope_sin || c->rope_max_pos == 0) return DS4A_ERR_ARG;
+  if (c->ratio && (!c->attn_comp_kv || !c->attn_state_kv || !c->attn_state_score)) return DS4A_ERR_ARG;
+  if (c->ratio == 4) {
     if (!c->index_comp_kv || !c->index_state_kv || !c->index_state_score) return DS4A_ERR_ARG;
     if (!c->index_norm || !c->index_norm_max) return DS4A_ERR_ARG;
     if (!c->index_rope_cos || !c->index_rope_sin) return DS4A_ERR_ARG;
@@ -295,7 +302,8 @@ ds4a_status ds4a_compress_append_lanes(ds4a_layer_cache *c, uint32_t pos0, uint3
 
 size_t ds4a_workspace_bytes(int call, const ds4a_layer_cache *c, uint32_t T, uint32_t n_heads,
                             uint32_t top_k) {
-  if (!c) return 0;
+  // sizes that every call refuses need nothing (and would divide by zero below)
+  if (check_sizes(c) != DS4A_OK || T == 0 || n_heads == 0 || n_heads > 128) return 0;
   const bool fp4 = (c->qat & DS4A_FP4_ROWS) != 0;
   switch (call) {
     case DS4A_CALL_INDEX_TOPK:

@@ -598,7 +598,8 @@ ds4a_status ds4a_set_decode_cluster(uint32_t C);
 uint32_t ds4a_decode_cluster_size(const ds4a_layer_cache *cache, uint32_t n_heads,
                                   uint32_t top_k);
 
-/* Workspace bytes a call needs for these sizes (0: none). */
+/* Workspace bytes a call needs for these sizes (0: none, or sizes that no call takes; the
+ * cache's pointers are not looked at). */
 size_t ds4a_workspace_bytes(int call, const ds4a_layer_cache *cache, uint32_t T,
                             uint32_t n_heads, uint32_t top_k);
 

@@ -121,3 +121,44 @@ def test_other_calls_check_alignment(L):
         assert tables(pool={name: FAKE + 2}) == -1, name
     for name in ("seq_pos", "cu_len", "tok_seq", "tok_pos", "raw_slot", "comp_slot4", "comp_slot128"):
         assert tables(step={name: FAKE + 2}) == -1, name
+
+
+SIZES = """
+import ctypes, sys
+sys.path[:0] = ['.', 'tests']
+from compressed_kv_sparse_gb300 import lib
+from test_abi_cpu import _fake_cache
+L = lib.load()
+calls = (lib.CALL_INDEX_TOPK, lib.CALL_ATTN_DECODE, lib.CALL_ATTN_PREFILL)
+
+
+def ask(c, T=3, H=64, k=512):
+    return [L.ds4a_workspace_bytes(w, ctypes.byref(c), T, H, k) for w in calls]
+
+
+for qat in (0, lib.FP4_ROWS):
+    for dtype in (0, 1):
+        for ratio in (4, 128):
+            def cache(**kw):
+                c = _fake_cache(ratio=ratio, dtype=dtype)
+                c.qat = qat
+                for n, v in kw.items():
+                    setattr(c, n, v)
+                return c
+            assert all(ask(cache())), (qat, dtype, ratio)
+            assert ask(cache(raw_kv=None, attn_comp_kv=None, rope_cos=None)) == ask(cache())
+            for kw in (dict(T=0), dict(H=0), dict(H=129)):
+                assert ask(cache(), **kw) == [0, 0, 0], kw
+            for kw in (dict(head_dim=0), dict(head_dim=2000), dict(head_dim=6), dict(batch=0), dict(dtype=9),
+                       dict(cap_raw=0), dict(comp_cap=0), dict(ratio=7)):
+                assert ask(cache(**kw)) == [0, 0, 0], kw
+print('sizes done')
+"""
+
+
+def test_workspace_bytes_of_sizes_that_no_call_takes(L):
+    """In a process of its own, which a division by zero would end."""
+    import subprocess
+    import sys
+    r = subprocess.run([sys.executable, "-c", SIZES], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and "sizes done" in r.stdout, (r.returncode, r.stderr[-2000:])
