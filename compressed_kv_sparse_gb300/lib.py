@@ -33,6 +33,10 @@ class Ds4aError(RuntimeError):
         self.status = status
 
 
+class ArgumentError(ValueError, AssertionError):
+    """A tensor of another type, size, layout or device than the call reads."""
+
+
 class LayerCacheC(ctypes.Structure):
     _fields_ = [(n, ctypes.c_uint32) for n in
                 ("ratio", "head_dim", "n_rot", "index_dim", "index_rot", "batch", "cap_raw",
@@ -148,19 +152,40 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     return lib
 
 
-def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
+def _refuse(t: torch.Tensor, dev: int):
+    if not t.is_contiguous():
+        raise ArgumentError("tensors passed to the library must be contiguous")
+    raise ArgumentError(f"a tensor on {t.device}, where the call's are on "
+                        + (f"cuda:{dev}" if dev >= 0 else "the CPU"))
+
+
+def _ptr(t: Optional[torch.Tensor], dev: int) -> Optional[int]:
+    """Address of a contiguous tensor on device `dev` (-1: the CPU)."""
     if t is None:
         return None
-    assert t.is_contiguous(), "tensors passed to the library must be contiguous"
+    if t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, dev)
     return t.data_ptr()
 
 
-def _stream(stream) -> Optional[int]:
-    if stream is None:
-        if torch.cuda.is_initialized():   # (the current stream without building its object)
-            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
-        stream = torch.cuda.current_stream()
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+def _need(ok: bool, what: str):
+    if not ok:
+        raise ArgumentError(what)
+
+
+def _stream(stream, dev: int) -> Optional[int]:
+    """The stream of a call whose tensors are on device `dev`, the current one."""
+    if dev < 0:
+        raise ArgumentError("the call's tensors are not on a GPU")
+    if torch._C._cuda_getDevice() != dev:
+        raise ArgumentError(f"the call's tensors are on cuda:{dev}, which is not the current device")
+    if stream is None:       # (the current stream without building its object)
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if not hasattr(stream, "cuda_stream"):
+        return stream
+    if stream.device_index != dev:
+        raise ArgumentError(f"a stream of cuda:{stream.device_index}, the call's tensors are on cuda:{dev}")
+    return stream.cuda_stream
 
 
 def _check(status: int, call: str):
@@ -173,6 +198,7 @@ _tables: Dict[tuple, tuple] = {}
 
 def rope_table(base: float, n_rot: int, n_pos: int, device) -> tuple:
     """Device cos / sin tables [n_pos][n_rot/2] built by ds4a_rope_table."""
+    device = torch.empty(0, device=device).device   # (with its index)
     key = (float(base), int(n_rot), int(n_pos), str(device))
     if key not in _tables:
         lib = load()
@@ -206,14 +232,17 @@ class LayerCache:
         self.block_table, self.n_blocks = block_table, n_blocks
         paged = block_table is not None
         if paged:
-            assert block_table.dtype == torch.int32 and block_table.shape[0] == batch
-            assert comp_cap == block_table.shape[1] * (256 // ratio)
+            _need(block_table.dtype == torch.int32 and block_table.shape[0] == batch,
+                  "block_table: [batch][max_blocks] int32")
+            _need(comp_cap == block_table.shape[1] * (256 // ratio),
+                  "comp_cap: every row of max_blocks blocks")
         rpb = 256 // ratio if ratio else 0
         self.fp4_rows = bool(qat & FP4_ROWS)   # attn_comp_kv: 4-bit rows, as bytes
         # comp rows: [B][comp_cap][w] or a pool [n_blocks][rows per block][w]
         rows = (lambda w, r, dt=td: z(n_blocks, r, w, dt=dt)) if paged else \
                (lambda w, r, dt=td: z(batch, comp_cap, w, dt=dt))
         self.raw_kv = z(batch, cap_raw, head_dim)
+        self.dev = dev = self.raw_kv.get_device()   # (-1: the CPU)
         self.attn_comp_kv = self.attn_state_kv = self.attn_state_score = None
         self.index_comp_kv = self.index_state_kv = self.index_state_score = None
         self.index_norm = self.index_norm_max = None
@@ -242,22 +271,25 @@ class LayerCache:
             ratio=ratio, head_dim=head_dim, n_rot=n_rot, index_dim=index_dim,
             index_rot=index_rot, batch=batch, cap_raw=cap_raw, comp_cap=comp_cap,
             dtype=DS4A_BF16 if dtype == "bf16" else DS4A_F32, n_tokens=0,
-            raw_kv=_ptr(self.raw_kv), attn_comp_kv=_ptr(self.attn_comp_kv),
-            attn_state_kv=_ptr(self.attn_state_kv), attn_state_score=_ptr(self.attn_state_score),
-            index_comp_kv=_ptr(self.index_comp_kv), index_state_kv=_ptr(self.index_state_kv),
-            index_state_score=_ptr(self.index_state_score), index_norm=_ptr(self.index_norm),
-            index_norm_max=_ptr(self.index_norm_max), rope_cos=_ptr(self.rope_cos),
-            rope_sin=_ptr(self.rope_sin), index_rope_cos=_ptr(self.index_rope_cos),
-            index_rope_sin=_ptr(self.index_rope_sin), rope_max_pos=rope_max_pos, qat=qat,
-            block_table=_ptr(block_table), max_blocks=block_table.shape[1] if paged else 0,
+            raw_kv=_ptr(self.raw_kv, dev), attn_comp_kv=_ptr(self.attn_comp_kv, dev),
+            attn_state_kv=_ptr(self.attn_state_kv, dev), attn_state_score=_ptr(self.attn_state_score, dev),
+            index_comp_kv=_ptr(self.index_comp_kv, dev), index_state_kv=_ptr(self.index_state_kv, dev),
+            index_state_score=_ptr(self.index_state_score, dev), index_norm=_ptr(self.index_norm, dev),
+            index_norm_max=_ptr(self.index_norm_max, dev), rope_cos=_ptr(self.rope_cos, dev),
+            rope_sin=_ptr(self.rope_sin, dev), index_rope_cos=_ptr(self.index_rope_cos, dev),
+            index_rope_sin=_ptr(self.index_rope_sin, dev), rope_max_pos=rope_max_pos, qat=qat,
+            block_table=_ptr(block_table, dev), max_blocks=block_table.shape[1] if paged else 0,
             n_blocks=n_blocks if paged else 0)
+        self._ref = ctypes.byref(self.c)
 
     def set_seq_pos(self, seq_pos: Optional[torch.Tensor]):
         """Ragged decode: [B] uint32/int32 device positions of this step's
         tokens (None: every sequence at the call's position). The tensor must
         stay alive while calls use it."""
+        _need(seq_pos is None or (seq_pos.dtype in (torch.int32, torch.uint32)
+                                  and seq_pos.numel() == self.batch), "seq_pos: [batch] int32 or uint32")
+        self.c.seq_pos = _ptr(seq_pos, self.dev)
         self.seq_pos = seq_pos
-        self.c.seq_pos = _ptr(seq_pos)
 
     def logical(self, name: str) -> torch.Tensor:
         """[B][comp_cap][...] view of compressed rows / row norms (a gather
@@ -290,7 +322,7 @@ class LayerCache:
         self.c.n_tokens = v
 
     def ref(self):
-        return ctypes.byref(self.c)
+        return self._ref
 
     def load_state(self, hist: Dict[str, torch.Tensor], n_tokens: int):
         """Copy a cache snapshot (same layout as the tensors here) in, set
@@ -326,21 +358,23 @@ class LayerCache:
 
 
 def ds4a_cache_reset(cache: LayerCache, stream=None):
-    _check(load().ds4a_cache_reset(cache.ref(), _stream(stream)), "ds4a_cache_reset")
+    _check(load().ds4a_cache_reset(cache.ref(), _stream(stream, cache.dev)), "ds4a_cache_reset")
 
 
 def ds4a_index_norms(cache: LayerCache, stream=None):
-    _check(load().ds4a_index_norms(cache.ref(), _stream(stream)), "ds4a_index_norms")
+    _check(load().ds4a_index_norms(cache.ref(), _stream(stream, cache.dev)), "ds4a_index_norms")
+
+
+_APPEND = ("raw_kv_in", "attn_cand", "attn_score", "ape_attn", "gamma_attn", "idx_cand", "idx_score",
+           "ape_idx", "gamma_idx")
 
 
 def ds4a_compress_append(cache: LayerCache, pos0: int, T: int, inp: Dict[str, torch.Tensor],
                          raw_chunk_out: Optional[torch.Tensor] = None, stream=None):
-    g = inp.get
+    dev = cache.dev
     _check(load().ds4a_compress_append(
-        cache.ref(), pos0, T, _ptr(g("raw_kv_in")), _ptr(g("attn_cand")), _ptr(g("attn_score")),
-        _ptr(g("ape_attn")), _ptr(g("gamma_attn")), _ptr(g("idx_cand")), _ptr(g("idx_score")),
-        _ptr(g("ape_idx")), _ptr(g("gamma_idx")), _ptr(raw_chunk_out), _stream(stream)),
-        "ds4a_compress_append")
+        cache.ref(), pos0, T, *[_ptr(inp.get(n), dev) for n in _APPEND], _ptr(raw_chunk_out, dev),
+        _stream(stream, dev)), "ds4a_compress_append")
 
 
 LANE_RAW, LANE_ATTN, LANE_INDEX = 1, 2, 4   # DS4A_LANE_*
@@ -350,19 +384,18 @@ def ds4a_compress_append_lanes(cache: LayerCache, pos0: int, T: int, lanes: int,
                                inp: Dict[str, torch.Tensor],
                                raw_chunk_out: Optional[torch.Tensor] = None, stream=None):
     """The parts `lanes` of an append; n_tokens is left for the caller to set."""
-    g = inp.get
+    dev = cache.dev
     _check(load().ds4a_compress_append_lanes(
-        cache.ref(), pos0, T, lanes, _ptr(g("raw_kv_in")), _ptr(g("attn_cand")),
-        _ptr(g("attn_score")), _ptr(g("ape_attn")), _ptr(g("gamma_attn")), _ptr(g("idx_cand")),
-        _ptr(g("idx_score")), _ptr(g("ape_idx")), _ptr(g("gamma_idx")), _ptr(raw_chunk_out),
-        _stream(stream)), "ds4a_compress_append_lanes")
+        cache.ref(), pos0, T, lanes, *[_ptr(inp.get(n), dev) for n in _APPEND],
+        _ptr(raw_chunk_out, dev), _stream(stream, dev)), "ds4a_compress_append_lanes")
 
 
 def ds4a_index_topk(cache: LayerCache, pos0: int, T: int, q_idx: torch.Tensor, w: torch.Tensor,
                     n_heads: int, top_k: int, topk: torch.Tensor, ws: torch.Tensor, stream=None):
-    _check(load().ds4a_index_topk(cache.ref(), pos0, T, _ptr(q_idx), _ptr(w), n_heads, top_k,
-                                  _ptr(topk), _ptr(ws), ws.numel() * ws.element_size(),
-                                  _stream(stream)), "ds4a_index_topk")
+    dev = cache.dev
+    _check(load().ds4a_index_topk(cache.ref(), pos0, T, _ptr(q_idx, dev), _ptr(w, dev), n_heads, top_k,
+                                  _ptr(topk, dev), _ptr(ws, dev), _nbytes(ws), _stream(stream, dev)),
+           "ds4a_index_topk")
 
 
 def row_bytes(head_dim: int, n_rot: int, dtype: str) -> int:
@@ -376,27 +409,26 @@ def row_bytes(head_dim: int, n_rot: int, dtype: str) -> int:
 _I32 = torch.int32
 
 
-def _rows_match(cache: LayerCache, rows: torch.Tensor, slots) -> int:
-    n = rows.size(0)
-    assert rows.dtype is cache.torch_dtype and rows.size(1) == cache.head_dim
-    assert slots is None or (slots.dtype is _I32 and slots.numel() == n)
-    return n
+def _rows_call(name: str, cache: LayerCache, rows: torch.Tensor, slots, stream):
+    n, dev = rows.size(0), cache.dev
+    if not (rows.dtype is cache.torch_dtype and rows.size(1) == cache.head_dim):
+        raise ArgumentError("rows: [n][head_dim]")
+    if not (slots is None or (slots.dtype is _I32 and slots.numel() == n)):
+        raise ArgumentError("slots: [n] int32")
+    _check(getattr(_lib or load(), name)(cache.ref(), n, _ptr(rows, dev), _ptr(slots, dev),
+                                         _stream(stream, dev) if n else None), name)
 
 
 def ds4a_pack_rows(cache: LayerCache, rows: torch.Tensor, slots: Optional[torch.Tensor] = None,
                    stream=None):
     """rows [n][D] into the 4-bit rows `slots` (None: 0 .. n - 1) of the cache's pool."""
-    n = _rows_match(cache, rows, slots)
-    _check(load().ds4a_pack_rows(cache.ref(), n, _ptr(rows), _ptr(slots),
-                                 _stream(stream)), "ds4a_pack_rows")
+    _rows_call("ds4a_pack_rows", cache, rows, slots, stream)
 
 
 def ds4a_unpack_rows(cache: LayerCache, rows: torch.Tensor, slots: Optional[torch.Tensor] = None,
                      stream=None):
     """The values of 4-bit rows `slots` (None: 0 .. n - 1) into rows [n][D]."""
-    n = _rows_match(cache, rows, slots)
-    _check(load().ds4a_unpack_rows(cache.ref(), n, _ptr(rows), _ptr(slots),
-                                   _stream(stream)), "ds4a_unpack_rows")
+    _rows_call("ds4a_unpack_rows", cache, rows, slots, stream)
 
 
 NORM_ROTATE_Q = 1   # DS4A_NORM_ROTATE_Q
@@ -412,28 +444,35 @@ def ds4a_norm_rope(cache: LayerCache, pos: torch.Tensor, *, q: Optional[torch.Te
     are contiguous. kv goes to kv_out [n][D] or, kv_out None, to rows `slots` of
     the raw window."""
     n, H, D, dt, q_stride, kv_stride = pos.numel(), 0, cache.head_dim, cache.torch_dtype, 0, 0
-    assert pos.dtype is _I32 and (slots is None or (slots.dtype is _I32 and slots.numel() == n))
+    dev = cache.dev
+    # (the checks of this call and the next two in line: they are a good part of a small call)
+    if not (pos.dtype is _I32 and (slots is None or (slots.dtype is _I32 and slots.numel() == n))):
+        raise ArgumentError("pos and slots: [n] int32")
     if q is not None:
         (N, H, W), (q_stride, s1, s2) = q.shape, q.stride()
-        assert q.dtype is dt and N == n and W == D and s2 == 1 and (H == 1 or s1 == D)
-        assert q_out is None or (q_out.dtype is dt and q_out.numel() == n * H * D)
-        assert gamma_q is None or (gamma_q.dtype is dt and gamma_q.numel() == D)
+        if not (q.dtype is dt and N == n and W == D and s2 == 1 and (H == 1 or s1 == D)
+                and q.get_device() == dev):
+            raise ArgumentError("q: [n][heads][head_dim] with whole tokens, on the cache's device")
+        if not ((q_out is None or (q_out.dtype is dt and q_out.numel() == n * H * D))
+                and (gamma_q is None or (gamma_q.dtype is dt and gamma_q.numel() == D))):
+            raise ArgumentError("q_out: like q; gamma_q: [head_dim]")
     if kv is not None:
         kv_stride, s1 = kv.stride()
-        assert kv.dtype is dt and kv.shape == (n, D) and s1 == 1
-        assert kv_out is None or (kv_out.dtype is dt and kv_out.numel() == n * D)
-        assert gamma_kv is None or (gamma_kv.dtype is dt and gamma_kv.numel() == D)
+        if not (kv.dtype is dt and kv.size(0) == n and kv.size(1) == D and s1 == 1
+                and kv.get_device() == dev):
+            raise ArgumentError("kv: [n][head_dim] with whole tokens, on the cache's device")
+        if not ((kv_out is None or (kv_out.dtype is dt and kv_out.numel() == n * D))
+                and (gamma_kv is None or (gamma_kv.dtype is dt and gamma_kv.numel() == D))):
+            raise ArgumentError("kv_out: like kv; gamma_kv: [head_dim]")
     if n == 1:   # (one token: its stride is whatever the slice left)
         q_stride, kv_stride = H * D, D
     if n == 0:   # (empty tensors have no address)
         return
-    _check(load().ds4a_norm_rope(
-        cache.ref(), n, _ptr(pos), None if q is None else q.data_ptr(),
-        q_stride, H, _ptr(gamma_q),
-        _ptr(q_out), None if kv is None else kv.data_ptr(),
-        kv_stride, _ptr(gamma_kv),
-        _ptr(kv_out), _ptr(slots), NORM_ROTATE_Q if rot_q else 0, _stream(stream)),
-        "ds4a_norm_rope")
+    _check((_lib or load()).ds4a_norm_rope(
+        cache.ref(), n, _ptr(pos, dev), None if q is None else q.data_ptr(), q_stride, H,
+        _ptr(gamma_q, dev), _ptr(q_out, dev), None if kv is None else kv.data_ptr(), kv_stride,
+        _ptr(gamma_kv, dev), _ptr(kv_out, dev), _ptr(slots, dev), NORM_ROTATE_Q if rot_q else 0,
+        _stream(stream, dev)), "ds4a_norm_rope")
 
 
 class BlockPool:
@@ -446,9 +485,10 @@ class BlockPool:
         self.held = torch.zeros(rows, **i32)
         self.free_list = torch.arange(n_blocks, **i32)
         self.state = torch.tensor([0, n_blocks, 0, 0], **i32)
+        self.dev = dev = self.state.get_device()
         self.c = BlockPoolC(rows=rows, max_blocks=max_blocks, n_blocks=n_blocks,
-                            table=_ptr(self.table), held=_ptr(self.held),
-                            free_list=_ptr(self.free_list), state=_ptr(self.state))
+                            table=_ptr(self.table, dev), held=_ptr(self.held, dev),
+                            free_list=_ptr(self.free_list, dev), state=_ptr(self.state, dev))
 
 
 class StepTables:
@@ -461,18 +501,22 @@ class StepTables:
         self.cu_len = torch.zeros(rows + 1, **i32)
         tok = torch.full((5, max_tokens), -1, **i32)
         self.tok_seq, self.tok_pos, self.raw_slot, self.comp_slot4, self.comp_slot128 = tok
+        self.dev = self.seq_pos.get_device()
         self.c = StepTablesC(max_tokens=max_tokens, **{
-            n: _ptr(getattr(self, n)) for n in ("seq_pos", "cu_len", "tok_seq", "tok_pos",
-                                                "raw_slot", "comp_slot4", "comp_slot128")})
+            n: _ptr(getattr(self, n), self.dev) for n in ("seq_pos", "cu_len", "tok_seq", "tok_pos",
+                                                          "raw_slot", "comp_slot4", "comp_slot128")})
 
 
 def ds4a_block_tables(pool: BlockPool, ctx_len: torch.Tensor, new_len: torch.Tensor, cap_raw: int,
                       step: StepTables, stream=None):
     """Blocks for rows of ctx_len [B] tokens (the last new_len [B] of them new), int32."""
-    assert ctx_len.dtype is _I32 and new_len.dtype is _I32
-    assert ctx_len.numel() == pool.rows == new_len.numel() == step.rows
-    _check(load().ds4a_block_tables(ctypes.byref(pool.c), _ptr(ctx_len), _ptr(new_len), cap_raw,
-                                    ctypes.byref(step.c), _stream(stream)), "ds4a_block_tables")
+    dev = pool.dev
+    if not (ctx_len.dtype is _I32 and new_len.dtype is _I32
+            and ctx_len.numel() == pool.rows == new_len.numel() == step.rows and step.dev == dev):
+        raise ArgumentError("ctx_len, new_len: [rows] int32; a step of as many rows on the pool's device")
+    _check((_lib or load()).ds4a_block_tables(
+        ctypes.byref(pool.c), _ptr(ctx_len, dev), _ptr(new_len, dev), cap_raw, ctypes.byref(step.c),
+        _stream(stream, dev)), "ds4a_block_tables")
 
 
 STATIC_SCRATCH_BYTES = 8 << 20
@@ -482,17 +526,19 @@ def ds4a_index_topk_noalloc(cache: LayerCache, pos0: int, T: int, q_idx: torch.T
                             w: torch.Tensor, n_heads: int, top_k: int, topk: torch.Tensor,
                             stream=None):
     """ds4a_index_topk with the library's static scratch instead of a workspace."""
-    _check(load().ds4a_index_topk_noalloc(cache.ref(), pos0, T, _ptr(q_idx), _ptr(w), n_heads,
-                                          top_k, _ptr(topk), _stream(stream)),
+    dev = cache.dev
+    _check(load().ds4a_index_topk_noalloc(cache.ref(), pos0, T, _ptr(q_idx, dev), _ptr(w, dev), n_heads,
+                                          top_k, _ptr(topk, dev), _stream(stream, dev)),
            "ds4a_index_topk_noalloc")
 
 
 def ds4a_sparse_attn_decode(cache: LayerCache, pos: int, q: torch.Tensor, n_heads: int,
                             topk: Optional[torch.Tensor], top_k: int, scale: float,
                             out: torch.Tensor, ws: Optional[torch.Tensor], stream=None):
-    nb = 0 if ws is None else ws.numel() * ws.element_size()
-    _check(load().ds4a_sparse_attn_decode(cache.ref(), pos, _ptr(q), n_heads, _ptr(topk), top_k,
-                                          scale, _ptr(out), _ptr(ws), nb, _stream(stream)),
+    dev = cache.dev
+    _check(load().ds4a_sparse_attn_decode(cache.ref(), pos, _ptr(q, dev), n_heads, _ptr(topk, dev), top_k,
+                                          scale, _ptr(out, dev), _ptr(ws, dev), _nbytes(ws),
+                                          _stream(stream, dev)),
            "ds4a_sparse_attn_decode")
 
 
@@ -500,10 +546,11 @@ def ds4a_sparse_attn_prefill_chunk(cache: LayerCache, pos0: int, T: int, q: torc
                                    n_heads: int, raw_chunk: torch.Tensor,
                                    topk: Optional[torch.Tensor], top_k: int, scale: float,
                                    out: torch.Tensor, ws: Optional[torch.Tensor], stream=None):
-    nb = 0 if ws is None else ws.numel() * ws.element_size()
-    _check(load().ds4a_sparse_attn_prefill_chunk(cache.ref(), pos0, T, _ptr(q), n_heads,
-                                                 _ptr(raw_chunk), _ptr(topk), top_k, scale,
-                                                 _ptr(out), _ptr(ws), nb, _stream(stream)),
+    dev = cache.dev
+    _check(load().ds4a_sparse_attn_prefill_chunk(cache.ref(), pos0, T, _ptr(q, dev), n_heads,
+                                                 _ptr(raw_chunk, dev), _ptr(topk, dev), top_k, scale,
+                                                 _ptr(out, dev), _ptr(ws, dev), _nbytes(ws),
+                                                 _stream(stream, dev)),
            "ds4a_sparse_attn_prefill_chunk")
 
 
@@ -542,7 +589,7 @@ def ds4a_workspace_status(ws: torch.Tensor) -> int:
     Synchronises nothing itself: call after the calls' stream is synchronised.
     Returns the count; the status (DS4A_OK / DS4A_ERR_TIMEOUT) follows from it."""
     n = ctypes.c_uint32(0)
-    st = load().ds4a_workspace_status(_ptr(ws), _nbytes(ws), ctypes.byref(n))
+    st = load().ds4a_workspace_status(_ptr(ws, ws.get_device()), _nbytes(ws), ctypes.byref(n))
     if st not in (0, -7):
         _check(st, "ds4a_workspace_status")
     assert (st == -7) == (n.value != 0)
@@ -550,7 +597,8 @@ def ds4a_workspace_status(ws: torch.Tensor) -> int:
 
 
 def ds4a_workspace_clear_status(ws: torch.Tensor, stream=None):
-    _check(load().ds4a_workspace_clear_status(_ptr(ws), _nbytes(ws), _stream(stream)),
+    dev = ws.get_device()
+    _check(load().ds4a_workspace_clear_status(_ptr(ws, dev), _nbytes(ws), _stream(stream, dev)),
            "ds4a_workspace_clear_status")
 
 
@@ -564,7 +612,8 @@ def ds4a_noalloc_status() -> int:
 
 
 def ds4a_wait_selftest(ws: torch.Tensor, limit_us: int, stream=None):
-    _check(load().ds4a_wait_selftest(_ptr(ws), _nbytes(ws), limit_us, _stream(stream)),
+    dev = ws.get_device()
+    _check(load().ds4a_wait_selftest(_ptr(ws, dev), _nbytes(ws), limit_us, _stream(stream, dev)),
            "ds4a_wait_selftest")
 
 
