@@ -65,7 +65,7 @@
 // - Any number of heads: groups of 64 (32 in decode of small batches), the last one
 //   part-filled with zero queries that are not stored.
 // Measured (one GB300): a tile takes 5.7 thousand cycles, of which 2.9 PV and 1.5 the
-// rest of S^T; reads and writes of shared memory alone are 4.2 (S^T 192 KiB, PV 192,
+// rest of S^T; reads and writes of shared memory alone are 4.35 (S^T 192 KiB, PV 192,
 // the tile's conversion 128, P and L 32, at 128 bytes a cycle), which is what bounds it;
 // a query of a chunk costs another 4 thousand for its change of Q and O. 4096 queries of
 // 640 rows x 64 heads: 460 us (bf16 rows 645), 0.39 of the burst bf16 rate; c128a decode,
@@ -436,10 +436,8 @@ __device__ __forceinline__ bool merge_heads(const TcAttnParams &P, Smem &S, uint
   return true;
 }
 
-// One query row of the tile from its 4-bit form (rec: this lane's 32-byte record,
-// tail: its 16 bytes of rotated dims) into 64-dim blocks kb0, kb0 + 1 of the tile, as
-// 16-byte chunk `at` of each. sl, sh: the scale bytes of blocks 0 .. 3 and 4 .. 6.
-// E2M1 times 2^-126 (fp4_pair_raw) becomes the bf16 value by one exact product with
+// The eight dims of code word w, a lane's word of 64-dim block KB, as the 16-byte chunk of
+// the bf16 tile. sl, sh: the scale bytes of the lane's blocks 0 .. 3 and 4 .. 6. E2M1 times 2^-126 (fp4_pair_raw) becomes the bf16 value by one exact product with
 // 2^(k + 126), a bf16 number while k <= 1 (byte <= 128: largest magnitude up to 12);
 // `wide`: the row has a larger scale and takes two products.
 template <uint32_t KB>
