@@ -432,7 +432,7 @@ static ds4a_status attn_common(const ds4a_layer_cache *c, uint32_t pos0, uint32_
   a.seq_pos = c->seq_pos;
   a.fp4 = (c->qat & DS4A_FP4_ROWS) != 0;
   a.q_rotated = (c->qat & DS4A_Q_ROTATED) != 0;
-  a.q_ready = (c->qat & DS4A_Q_READY) != 0;
+  a.q_ready = (c->qat & DS4A_Q_READY) != 0 && !raw_chunk;   // (decode calls alone)
   return cuda_status(launch_attention(a, s));
 }
 
