@@ -109,6 +109,13 @@ uint32_t comp_rows(const ds4a_layer_cache *c, uint32_t n_tokens) {
   return c->ratio ? n_tokens / c->ratio : 0;
 }
 
+// n_tokens may be the caller's own: the rows that it says there are lie inside the cache, and
+// the positions below `end` inside the rotation tables.
+ds4a_status check_filled(const ds4a_layer_cache *c, uint64_t end) {
+  if (c->ratio && comp_rows(c, c->n_tokens) > c->comp_cap) return DS4A_ERR_CAPACITY;
+  return end > c->rope_max_pos ? DS4A_ERR_CAPACITY : DS4A_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -191,6 +198,8 @@ ds4a_status ds4a_index_norms(ds4a_layer_cache *c, ds4a_stream_t stream) {
   ds4a_status st = check_cache(c);
   if (st) return st;
   if (c->ratio != 4) return DS4A_ERR_ARG;
+  st = check_filled(c, 0);
+  if (st) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   st = cuda_status(cudaMemsetAsync(c->index_norm_max, 0, sizeof(uint32_t) * c->batch, s));
   if (st) return st;
@@ -333,6 +342,8 @@ ds4a_status index_topk_check(const ds4a_layer_cache *c, uint32_t pos0, uint32_t 
   if (T == 0 || n_heads == 0 || n_heads > 128 || top_k == 0 || top_k > 2048) return DS4A_ERR_SHAPE;
   if (!q_idx || !w || !topk) return DS4A_ERR_ARG;
   if ((uint64_t)pos0 + T > c->n_tokens) return DS4A_ERR_POSITION;
+  st = check_filled(c, (uint64_t)pos0 + T);
+  if (st) return st;
   // (the tensor-core scorer reads keys by TMA)
   const bool tc = c->dtype == DS4A_BF16 && index_tc_supported(n_heads, c->index_dim);
   if (!aligned(tc ? 16 : elem_bytes(c), {c->index_comp_kv}) || !aligned(elem_bytes(c), {q_idx, w}) ||
@@ -391,6 +402,8 @@ static ds4a_status attn_common(const ds4a_layer_cache *c, uint32_t pos0, uint32_
   if (!q || !out) return DS4A_ERR_ARG;
   if (!std::isfinite(scale)) return DS4A_ERR_ARG;
   if (c->ratio == 4 && (!topk || top_k == 0 || top_k > 2048)) return DS4A_ERR_ARG;
+  const ds4a_status filled = check_filled(c, (uint64_t)pos0 + T);
+  if (filled) return filled;
   // The tensor-core kernels copy rows and queries 16 bytes at a time and store the output in
   // 4- and 8-byte words.
   const bool tc = attn_tc_supported(c->dtype, n_heads, c->head_dim, c->n_rot,

@@ -437,7 +437,8 @@ __device__ __forceinline__ bool merge_heads(const TcAttnParams &P, Smem &S, uint
 }
 
 // The eight dims of code word w, a lane's word of 64-dim block KB, as the 16-byte chunk of
-// the bf16 tile. sl, sh: the scale bytes of the lane's blocks 0 .. 3 and 4 .. 6. E2M1 times 2^-126 (fp4_pair_raw) becomes the bf16 value by one exact product with
+// the bf16 tile. sl, sh: the scale bytes of the lane's blocks 0 .. 3 and 4 .. 6. E2M1
+// times 2^-126 (fp4_pair_raw) becomes the bf16 value by one exact product with
 // 2^(k + 126), a bf16 number while k <= 1 (byte <= 128: largest magnitude up to 12);
 // `wide`: the row has a larger scale and takes two products.
 template <uint32_t KB>

@@ -30,7 +30,9 @@
  *  - All sequences of a batch are at the same position. ds4a_layer_cache.n_tokens
  *    is the host-side count of tokens appended so far; ds4a_compress_append
  *    requires pos0 == n_tokens and advances it, the other calls require the
- *    tokens they read to have been appended (DS4A_ERR_POSITION otherwise).
+ *    tokens they read to have been appended (DS4A_ERR_POSITION otherwise). A
+ *    count of the caller's own that the compressed rows (comp_cap) or the
+ *    rotation tables (rope_max_pos) have no room for is DS4A_ERR_CAPACITY.
  *  - Row-major layouts, innermost dimension last. Element type of rows,
  *    inputs and outputs is ds4a_layer_cache.dtype (fp32 or bf16); the
  *    compressor state is always fp32.
@@ -254,7 +256,7 @@ ds4a_status ds4a_cache_reset(ds4a_layer_cache *cache, ds4a_stream_t stream);
  * imported cache). The pages have no counterpart: the norms serve the
  * certified top-k only. Asynchronous on `stream`.
  * Errors: DS4A_ERR_ARG (not ratio 4, or a cache field missing),
- * DS4A_ERR_CUDA.
+ * DS4A_ERR_CAPACITY, DS4A_ERR_CUDA.
  */
 ds4a_status ds4a_index_norms(ds4a_layer_cache *cache, ds4a_stream_t stream);
 

@@ -162,3 +162,25 @@ def test_workspace_bytes_of_sizes_that_no_call_takes(L):
     import sys
     r = subprocess.run([sys.executable, "-c", SIZES], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0 and "sizes done" in r.stdout, (r.returncode, r.stderr[-2000:])
+
+
+def test_a_count_of_tokens_that_the_cache_has_no_room_for(L):
+    """n_tokens set by the caller (ds4a_norm_rope and the append by lanes leave it to them)."""
+    def topk(c, nbytes=8):
+        return L.ds4a_index_topk(ctypes.byref(c), c.n_tokens - 1, 1, FAKE, FAKE, 64, 512, FAKE, FAKE, nbytes,
+                                 None)
+
+    small = lambda call: (lambda c: call(c) if call is topk else call(L, c, nbytes=8))  # noqa: E731
+    for call in map(small, (decode, chunk, topk)):
+        full = cache(n_tokens=64 + 3)                    # 16 rows of 4 tokens, and some
+        assert call(full) == -8                          # past the checks: too small a workspace
+        assert call(cache(n_tokens=64 + 4)) == -3        # a row more than comp_cap
+        assert call(cache(n_tokens=60, rope_max_pos=60)) == -8
+        assert call(cache(n_tokens=60, rope_max_pos=59)) == -3
+    for call in map(small, (decode, chunk)):
+        assert call(cache(ratio=128, n_tokens=17 * 128, rope_max_pos=1 << 20)) == -3
+        assert call(cache(ratio=128, n_tokens=17 * 128 - 1, rope_max_pos=1 << 20)) == -8
+    for call in (decode, chunk):                         # the raw window alone
+        assert call(L, cache(ratio=0, n_tokens=1000), nbytes=8) == -8
+        assert call(L, cache(ratio=0, n_tokens=1001), nbytes=8) == -3
+    assert L.ds4a_index_norms(ctypes.byref(cache(n_tokens=64 + 4)), None) == -3
