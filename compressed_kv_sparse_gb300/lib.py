@@ -6,6 +6,7 @@ library is missing, ``load()`` raises.
 """
 from __future__ import annotations
 
+import copy
 import ctypes
 import math
 import os
@@ -290,6 +291,25 @@ class LayerCache:
                                   and seq_pos.numel() == self.batch), "seq_pos: [batch] int32 or uint32")
         self.c.seq_pos = _ptr(seq_pos, self.dev)
         self.seq_pos = seq_pos
+
+    def rows(self, b0: int, b1: int) -> "LayerCache":
+        """Sequences b0 .. b1 - 1 as a cache of their own on the same memory, with its own
+        n_tokens: what runs together of a step whose sequences have different numbers of new
+        tokens (positions are seq_pos's as it was set before)."""
+        _need(0 <= b0 < b1 <= self.batch, f"sequences {b0} .. {b1 - 1} of {self.batch}")
+        v = copy.copy(self)
+        v.c, v.batch = LayerCacheC.from_buffer_copy(self.c), b1 - b0
+        names = ["raw_kv", "attn_state_kv", "attn_state_score", "index_state_kv", "index_state_score",
+                 "index_norm_max", "block_table", "seq_pos"]
+        if self.block_table is None:
+            names += ["attn_comp_kv", "index_comp_kv", "index_norm"]
+        for n in names:
+            t = getattr(self, n, None)
+            if t is not None:
+                setattr(v, n, t[b0:b1])
+                setattr(v.c, n, _ptr(t[b0:b1], self.dev))
+        v.c.batch, v._ref = v.batch, ctypes.byref(v.c)
+        return v
 
     def logical(self, name: str) -> torch.Tensor:
         """[B][comp_cap][...] view of compressed rows / row norms (a gather

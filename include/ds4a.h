@@ -42,7 +42,8 @@
  *    of 512 dims with a 64-dim tail (64 heads, or 4-bit rows), index_comp_kv of
  *    an indexer of 64 heads x 128 dims; attn_state_kv and attn_state_score on 8
  *    bytes for 512 and 1024 dims. DS4A_ERR_ARG otherwise.
- *  - Order within a step: append -> index_topk (ratio 4) -> attention.
+ *  - Order within a step: append -> index_topk (ratio 4) -> attention. Calls that
+ *    may run at once (two streams, two captured graphs) need a workspace each.
  */
 #ifndef DS4A_H
 #define DS4A_H
@@ -466,6 +467,17 @@ ds4a_status ds4a_norm_rope(ds4a_layer_cache *cache, uint32_t n, const int32_t *p
  *  comp_slot4, comp_slot128  the row of a ratio-4 / ratio-128 pool that the token
  *              completes (block * 64 + .., block * 2 + ..), -1 when it completes none
  *  Entries behind the last token are -1.
+ *
+ * A step whose rows have different numbers of new tokens: ds4a_norm_rope takes the
+ * packed tokens, whichever rows they are of; append, top-k and attention take one T.
+ * Order the rows so that those with as many new tokens stand together, and make these
+ * calls for every such run of rows b0 .. b1 - 1 with a ds4a_layer_cache of batch
+ * b1 - b0 whose per-sequence arrays (raw_kv, the states, index_norm_max, block_table,
+ * seq_pos) start at row b0; the paged pools are shared. Rows with one new token take
+ * the norms' K = V rows by raw_slot (decode; it numbers the rows of the whole cache,
+ * which this call is then given), rows with more by kv_out (raw_chunk of the chunk
+ * call, which still reads the window as it was). Such calls touch nothing of
+ * each other's and may run at once, a workspace each.
  *
  * ds4a_block_tables: row b is to hold ctx_len[b] tokens (0: the row is free) of
  * which the last min(new_len[b], ctx_len[b]) are new. It takes blocks from the

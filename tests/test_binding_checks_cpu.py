@@ -120,3 +120,27 @@ print('refused', n)
 """
     r = subprocess.run([sys.executable, "-O", "-c", code], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0 and "refused 5" in r.stdout, (r.stdout, r.stderr[-2000:])
+
+
+@pytest.mark.parametrize("paged", [False, True])
+def test_rows_of_a_cache(L, paged):
+    """Sequences of a cache as a cache of their own: the same memory, its own count."""
+    kw = dict(block_table=torch.arange(8, **I32).view(4, 2), n_blocks=9) if paged else {}
+    c = cache(ratio=4, batch=4, comp_cap=128, index_dim=128, index_rot=64, **kw)
+    c.set_seq_pos(torch.arange(4, **I32))
+    c.n_tokens = 12
+    v = c.rows(1, 3)
+    assert v.batch == v.c.batch == 2 and c.c.batch == 4 and v.n_tokens == 12
+    v.n_tokens = 13
+    assert c.n_tokens == 12 and v.ref()._obj.n_tokens == 13 and c.ref()._obj.n_tokens == 12
+    per = ["raw_kv", "attn_state_kv", "attn_state_score", "index_state_kv", "index_state_score",
+           "index_norm_max", "seq_pos"]
+    pool = ["attn_comp_kv", "index_comp_kv", "index_norm"]
+    for n in per + (["block_table"] if paged else pool):
+        assert getattr(v.c, n) == getattr(c, n)[1:].data_ptr() and getattr(v, n).shape[0] == 2, n
+    for n in (pool if paged else []) + ["rope_cos", "rope_sin", "index_rope_cos"]:
+        assert getattr(v.c, n) == getattr(c, n).data_ptr(), n
+    assert v.slots(2).tolist() == (c.slots(2)[1:3].tolist() if paged else [[0, 1], [128, 129]])
+    for bad in ((0, 0), (2, 1), (0, 5), (-1, 2)):
+        with pytest.raises(lib.ArgumentError):
+            c.rows(*bad)
