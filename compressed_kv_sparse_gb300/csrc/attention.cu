@@ -114,9 +114,10 @@ __global__ void __launch_bounds__(kThreads)
   pdl_wait();
   pdl_trigger();
 
-  const uint32_t qi = blockIdx.z, b = qi / a.T, t = qi % a.T;
+  // (one grid dimension: the others end at 65,535, and queries may be more)
+  const uint32_t split = blockIdx.x % pl.n_splits, h0 = blockIdx.x / pl.n_splits % pl.n_hg * HG;
+  const uint32_t qi = blockIdx.x / (pl.n_splits * pl.n_hg), b = qi / a.T, t = qi % a.T;
   const uint32_t p = seq_base(a.seq_pos, a.pos0, b) + t;
-  const uint32_t h0 = blockIdx.y * HG, split = blockIdx.x;
   const uint32_t n_w = min(p + 1, a.cap_raw);
   const int32_t *tk = a.topk ? a.topk + (size_t)qi * a.top_k : nullptr;
 
@@ -361,7 +362,7 @@ constexpr uint32_t kMergeBatch = 8;
 template <typename T>
 __global__ void attn_merge_kernel(AttnArgs a, Plan pl, const float *part) {
   pdl_wait();
-  const uint32_t h = blockIdx.x, qi = blockIdx.y, t = qi % a.T;
+  const uint32_t h = blockIdx.x % a.n_heads, qi = blockIdx.x / a.n_heads, t = qi % a.T;
   const uint32_t p = seq_base(a.seq_pos, a.pos0, qi / a.T) + t;
   const uint32_t D = a.head_dim, H = a.n_heads, ns = pl.n_splits, n_nope = D - a.n_rot;
   const size_t nq = (size_t)a.batch * a.T;
@@ -445,13 +446,15 @@ cudaError_t launch_attention_t(const AttnArgs &a, cudaStream_t s) {
   // (the first 256 bytes: the error word of the workspace; this path has no
   // device waits and leaves it alone)
   float *part = a.ws ? reinterpret_cast<float *>(static_cast<uint8_t *>(a.ws) + 256) : nullptr;
-  dim3 grid(pl.n_splits, pl.n_hg, a.batch * a.T);
-  e = launch_pdl(kernel, grid, dim3(kThreads), smem, s, a, pl, part);
+  const uint64_t nq = (uint64_t)a.batch * a.T;
+  if (nq * pl.n_splits * pl.n_hg > 0x7fffffffu || nq * a.n_heads > 0x7fffffffu)
+    return cudaErrorInvalidConfiguration;
+  e = launch_pdl(kernel, dim3((uint32_t)nq * pl.n_splits * pl.n_hg), dim3(kThreads), smem, s, a, pl, part);
   if (e != cudaSuccess) return e;
   note_launches(1);
   if (pl.n_splits > 1) {
     const float *sums = part;
-    e = launch_pdl(attn_merge_kernel<T>, dim3(a.n_heads, a.batch * a.T), dim3(128), 0, s, a, pl, sums);
+    e = launch_pdl(attn_merge_kernel<T>, dim3((uint32_t)nq * a.n_heads), dim3(128), 0, s, a, pl, sums);
     if (e != cudaSuccess) return e;
     note_launches(1);
   }

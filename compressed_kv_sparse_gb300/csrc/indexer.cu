@@ -281,12 +281,13 @@ __global__ void index_qrot_kernel(IndexArgs a, float *qrot, int *err) {
 
 template <typename T>
 __global__ void __launch_bounds__(kRowsPerBlock)
-    index_score_exact_kernel(IndexArgs a, const float *qrot, float *scores) {
+    index_score_exact_kernel(IndexArgs a, const float *qrot, float *scores, uint32_t n_tiles) {
   extern __shared__ float4 smem4[];
-  const uint32_t qi = blockIdx.y, b = qi / a.T, t = qi % a.T;
+  // (one grid dimension: queries may be more than 65,535)
+  const uint32_t qi = blockIdx.x / n_tiles, b = qi / a.T, t = qi % a.T;
   const uint32_t p = seq_base(a.seq_pos, a.pos0, b) + t;
   const uint32_t vis = min((p + 1) / 4, a.n_comp);
-  const uint32_t row0 = blockIdx.x * kRowsPerBlock;
+  const uint32_t row0 = blockIdx.x % n_tiles * kRowsPerBlock;
   if (vis <= a.top_k || row0 >= vis) return;
   const uint32_t Hi = a.n_heads, Di = a.dim, Hp = round_up8(Hi), ks_stride = Di + 1;
   float *qs = reinterpret_cast<float *>(smem4);  // [Di][Hp]
@@ -868,8 +869,10 @@ cudaError_t launch_index_exact(const IndexArgs &a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const uint32_t vis_max = min((a.pos0 + a.T) / 4, a.n_comp);
   if (vis_max > a.top_k) {
-    dim3 grid((vis_max + kRowsPerBlock - 1) / kRowsPerBlock, nq);
-    index_score_exact_kernel<T><<<grid, kRowsPerBlock, smem, s>>>(a, w.qrot, w.scores);
+    const uint32_t n_tiles = (vis_max + kRowsPerBlock - 1) / kRowsPerBlock;
+    if ((uint64_t)n_tiles * nq > 0x7fffffffu) return cudaErrorInvalidConfiguration;
+    index_score_exact_kernel<T>
+        <<<n_tiles * nq, kRowsPerBlock, smem, s>>>(a, w.qrot, w.scores, n_tiles);
     note_launches(1);
   }
   topk_select_kernel<<<nq, kSelectThreads, 0, s>>>(a, w.scores);
