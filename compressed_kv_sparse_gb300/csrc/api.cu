@@ -59,6 +59,15 @@ ds4a_status check_cache(const ds4a_layer_cache *c) {
     if (!c->index_norm || !c->index_norm_max) return DS4A_ERR_ARG;
     if (!c->index_rope_cos || !c->index_rope_sin) return DS4A_ERR_ARG;
   }
+  // (what single kernels read in wider words is checked with their calls)
+  if (!aligned(elem_bytes(c), {c->raw_kv, c->ratio ? c->attn_comp_kv : nullptr,
+                               c->ratio == 4 ? c->index_comp_kv : nullptr}) ||
+      !aligned(4, {c->rope_cos, c->rope_sin, c->seq_pos, c->block_table}))
+    return DS4A_ERR_ARG;
+  if (c->ratio && !aligned(4, {c->attn_state_kv, c->attn_state_score})) return DS4A_ERR_ARG;
+  if (c->ratio == 4 && !aligned(4, {c->index_state_kv, c->index_state_score, c->index_norm,
+                                    c->index_norm_max, c->index_rope_cos, c->index_rope_sin}))
+    return DS4A_ERR_ARG;
   if (c->block_table) {
     if (c->ratio == 0 || c->max_blocks == 0 || c->n_blocks == 0) return DS4A_ERR_ARG;
     if ((uint64_t)c->max_blocks * (256u / c->ratio) != c->comp_cap) return DS4A_ERR_SHAPE;
@@ -232,11 +241,11 @@ ds4a_status append_parts(ds4a_layer_cache *c, uint32_t pos0, uint32_t T, uint32_
   if (la && (!attn_cand || !attn_score || !ape_attn || !gamma_attn)) return DS4A_ERR_ARG;
   if (li && (!idx_cand || !idx_score || !ape_idx || !gamma_idx)) return DS4A_ERR_ARG;
   // (the step kernel of 512- and 1024-wide rows reads the state as pairs)
-  if (la && !aligned(c->head_dim == 512 || c->head_dim == 1024 ? 8 : 4,
-                     {c->attn_state_kv, c->attn_state_score}))
+  if (la && (c->head_dim == 512 || c->head_dim == 1024) &&
+      !aligned(8, {c->attn_state_kv, c->attn_state_score}))
     return DS4A_ERR_ARG;
-  if (!aligned(elem_bytes(c), {raw_kv_in, raw_chunk_out, c->raw_kv, attn_cand, attn_score, ape_attn,
-                               gamma_attn, idx_cand, idx_score, ape_idx, gamma_idx}))
+  if (!aligned(elem_bytes(c), {raw_kv_in, raw_chunk_out, attn_cand, attn_score, ape_attn, gamma_attn,
+                               idx_cand, idx_score, ape_idx, gamma_idx}))
     return DS4A_ERR_ARG;
 
   AppendArgs a;
@@ -346,8 +355,8 @@ ds4a_status index_topk_check(const ds4a_layer_cache *c, uint32_t pos0, uint32_t 
   if (st) return st;
   // (the tensor-core scorer reads keys by TMA)
   const bool tc = c->dtype == DS4A_BF16 && index_tc_supported(n_heads, c->index_dim);
-  if (!aligned(tc ? 16 : elem_bytes(c), {c->index_comp_kv}) || !aligned(elem_bytes(c), {q_idx, w}) ||
-      !aligned(4, {topk, c->index_norm, c->index_norm_max, c->seq_pos, c->block_table}))
+  if ((tc && !aligned(16, {c->index_comp_kv})) || !aligned(elem_bytes(c), {q_idx, w}) ||
+      !aligned(4, {topk}))
     return DS4A_ERR_ARG;
   const uint32_t Hp = (n_heads + 7u) & ~7u;
   if (((size_t)c->index_dim * Hp + Hp + 128 * (size_t)(c->index_dim + 1)) * 4 > 227 * 1024)
@@ -410,7 +419,7 @@ static ds4a_status attn_common(const ds4a_layer_cache *c, uint32_t pos0, uint32_
                                     (c->qat & DS4A_FP4_ROWS) != 0);
   if (!aligned(tc ? 16 : elem_bytes(c),
                {q, out, raw_chunk, c->raw_kv, c->ratio ? c->attn_comp_kv : nullptr}) ||
-      !aligned(4, {c->ratio == 4 ? topk : nullptr, c->seq_pos, c->block_table}))
+      !aligned(4, {c->ratio == 4 ? topk : nullptr}))
     return DS4A_ERR_ARG;
   const size_t need = attn_ws_bytes(c->dtype, c->ratio, c->batch, T, n_heads, c->head_dim,
                                     c->n_rot, c->cap_raw, c->comp_cap, c->ratio == 4 ? top_k : 0,
@@ -545,7 +554,7 @@ ds4a_status ds4a_norm_rope(ds4a_layer_cache *c, uint32_t n, const int32_t *pos, 
     if (kv == kv_out && kv_stride != c->head_dim) return DS4A_ERR_ARG;
     if (!kv_out) n_dst = (uint64_t)c->batch * c->cap_raw;
     if (n_dst > 0x7fffffffu) return DS4A_ERR_SHAPE;
-    if (!aligned(es, {kv, kv_out, gamma_kv, c->raw_kv})) return DS4A_ERR_ARG;
+    if (!aligned(es, {kv, kv_out, gamma_kv})) return DS4A_ERR_ARG;
   }
   if (n == 0) return DS4A_OK;
   NormRopeArgs a;

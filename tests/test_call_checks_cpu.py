@@ -184,3 +184,16 @@ def test_a_count_of_tokens_that_the_cache_has_no_room_for(L):
         assert call(L, cache(ratio=0, n_tokens=1000), nbytes=8) == -8
         assert call(L, cache(ratio=0, n_tokens=1001), nbytes=8) == -3
     assert L.ds4a_index_norms(ctypes.byref(cache(n_tokens=64 + 4)), None) == -3
+
+
+def test_every_array_of_a_cache_starts_on_an_element(L):
+    for name in ("attn_state_kv", "attn_state_score", "index_state_kv", "index_state_score", "index_norm",
+                 "index_norm_max", "rope_cos", "rope_sin", "index_rope_cos", "index_rope_sin", "seq_pos"):
+        for off in (1, 2):
+            assert L.ds4a_cache_reset(ctypes.byref(cache(**{name: FAKE + off})), None) == -1, name
+    for name in ("raw_kv", "attn_comp_kv", "index_comp_kv"):
+        assert append(L, cache(**{name: FAKE + 2})) == -4, name          # (bf16: past the cache's checks)
+        assert append(L, cache(**{name: FAKE + 1})) == -1, name
+        assert append(L, cache(dtype=lib.DS4A_F32, **{name: FAKE + 2})) == -1, name
+    # arrays that a layer does not have are not looked at
+    assert append(L, cache(ratio=128, index_comp_kv=FAKE + 1, index_norm=FAKE + 1)) == -4
