@@ -68,8 +68,9 @@
 // rest of S^T; reads and writes of shared memory alone are 4.35 (S^T 192 KiB, PV 192,
 // the tile's conversion 128, P and L 32, at 128 bytes a cycle), which is what bounds it;
 // a query of a chunk costs another 4 thousand for its change of Q and O. 4096 queries of
-// 640 rows x 64 heads: 460 us (bf16 rows 645), 0.39 of the burst bf16 rate; c128a decode,
-// 32 sequences of 4,224 rows: 37 us (87); c4a decode, 8 sequences: 12.5 us (12.4).
+// 640 rows x 64 heads: 457 us (bf16 rows 650), 0.40 of the burst bf16 rate; c128a decode,
+// 32 sequences of 4,224 rows: 37 us (88); c4a decode, 8 sequences: 12.5 us (13.8), with
+// q_ready 12.2 (13.1).
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -243,9 +244,10 @@ static __device__ __noinline__ uint32_t list_stop(const int32_t *tk, uint32_t n,
 // place of a list a row of a tile where as many rows are visible (the list is then full, or has
 // holes), without reading it before the first gather: entries that are no visible row are masked
 // one by one, those behind the list's end once the loaders have looked for it, while the first
-// rows are on their way (c4a, 8 sequences: 13.0 us; with the list read by every role before the
-// first gather 13.8, without any look for its end 12.6). Where fewer rows are visible than the
-// list has places, it is read for its length. n_list: the length of a ratio-4 list where it is
+// rows are on their way (c4a, 8 sequences, side by side with early queries: 13.0 us; with the
+// list read by every role before the first gather 13.8, without any look for its end 12.6).
+// Where fewer rows are visible than the list has places, it is read for its length (500
+// visible positions: 14.4 us, 3,000: 13.8). n_list: the length of a ratio-4 list where it is
 // known (4-bit rows).
 template <bool SCAN>
 __device__ __forceinline__ QueryGeo query_geo(const TcAttnParams &P, uint32_t qi, uint32_t t0,
@@ -532,8 +534,8 @@ __global__ void __launch_bounds__(Warps<FP4>::THREADS, 1)
   auto item_q = [&](uint32_t it) { return FP4 || dec ? it / HG : it; };
   auto item_h = [&](uint32_t it) { return FP4 || dec ? (it % HG) * NH : 0u; };   // first head
   // The wait for the previous launch: in a chunk here; in decode behind the block's own
-  // preparations or, with q_ready, in the loaders behind the first query's Q load (c4a, 8
-  // sequences, alone: 13.0 and 13.8 us; here for every call 14.3).
+  // preparations (c4a over bf16 rows, 8 sequences: 13.8 us; here for every call 14.3) or,
+  // with q_ready, in the loaders behind the first query's Q load (13.1).
   const bool ready = DEC && P.q_ready != 0;
   if (!DEC) pdl_wait();
   // (this launch's view of the error word: see ErrWord)

@@ -6,8 +6,8 @@
 // One warp owns one row (a head of a token, or the token's K = V row): the row
 // stays in registers between the sum of squares and the scaled, rotated store, so
 // each element is read once and written once. Bound by HBM at a chunk's size (4096
-// tokens of 64 heads x 512 in bf16: 92 us, 0.88 of the measured copy rate), by the
-// launch and two dependent look-ups at a decode step's (8 tokens: 3.1 us).
+// tokens of 64 heads x 512 in bf16: 91 us, 0.89 of the measured copy rate), by the
+// launch and two dependent look-ups at a decode step's (8 tokens: 2.7 us).
 #include "common.cuh"
 
 namespace ds4a {
@@ -64,8 +64,8 @@ __device__ __forceinline__ void store_e(T *p, const float *v) {
 // NV: chunks of E elements per lane (D <= 32 E NV). LAST: the rotated tail is whole
 // chunks of each lane's last one (512 dims with a 64-dim tail, for instance): a lane then
 // keeps its coefficients in registers for all rows of a token (looked up pair by pair
-// for every row: 160 us). Three blocks of 80 registers and three rows ahead measured
-// 92 us, four of 64 and two rows 94, five of 48 and two rows 146.
+// for every row: 160 us). Three blocks of 80 registers and three rows ahead measured,
+// side by side, 92 us, four of 64 and two rows 94, five of 48 and two rows 146.
 template <typename T, int E, int NV, bool LAST>
 __global__ void __launch_bounds__(kThreads, NV <= 2 ? 3 : 1) norm_rope_kernel(NormArgs a) {
   constexpr int PF = NV <= 2 ? 3 : NV <= 4 ? 2 : 1;

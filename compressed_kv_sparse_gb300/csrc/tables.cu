@@ -12,8 +12,8 @@
 // read (held, the free list's head and count) is advanced by the block that
 // arrives last at a ticket, after every block has taken its copy; none waits.
 // Bound by the launch and a chain of latencies (8 decoding rows: 3.3 us), then by what
-// each block does for all rows (2,048 rows with 239,593 tokens: 7.8 us); by the stores of
-// five words per token beyond some 10^6 tokens.
+// each block does for all rows (2,048 rows with 239,593 tokens: 7.3 us, 11.8 where 47,533
+// blocks change hands); by the stores of five words per token beyond some 10^6 tokens.
 #include "common.cuh"
 
 namespace ds4a {
@@ -294,11 +294,12 @@ cudaError_t launch_nt(TablesArgs a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_block_tables(TablesArgs a, cudaStream_t s) {
-  // Few rows and tokens: one small block, which needs no ticket (8 decoding rows 3.2 us
-  // against 3.7 in large ones, 24 rows 4.5 in three small ones against 4.3). Otherwise up
-  // to one block of 1,024 threads per SM, which shares the sums over all rows among more
-  // threads (200 rows with 27,145 tokens: 5.6 us, in blocks of 256 threads 6.2; 2,048
-  // rows with 239,593: 7.7 against 9.9; 8,192 decoding: 9.0 against 18.8).
+  // Few rows and tokens: one small block, which needs no ticket (side by side, some
+  // 0.4 us above today's figures: 8 decoding rows 3.3 us against 3.7 in large ones, 24 rows
+  // 4.5 in three small ones against 4.3). Otherwise up to one block of 1,024 threads per
+  // SM, which shares the sums over all rows among more threads (200 rows with 27,145
+  // tokens: 5.6 us, in blocks of 256 threads 6.2; 2,048 rows with 239,593: 7.7 against 9.9;
+  // 8,192 decoding: 9.0 against 18.8).
   return a.rows <= 16 && a.max_tokens <= 512 ? launch_nt<256, 2>(a, s) : launch_nt<1024, 1>(a, s);
 }
 
