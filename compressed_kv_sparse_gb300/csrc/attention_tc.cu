@@ -246,8 +246,8 @@ static __device__ __noinline__ uint32_t list_stop(const int32_t *tk, uint32_t n,
 // one by one, those behind the list's end once the loaders have looked for it, while the first
 // rows are on their way (c4a, 8 sequences, side by side with early queries: 13.0 us; with the
 // list read by every role before the first gather 13.8, without any look for its end 12.6).
-// Where fewer rows are visible than the list has places, it is read for its length (500
-// visible positions: 14.4 us, 3,000: 13.8). n_list: the length of a ratio-4 list where it is
+// Where fewer rows are visible than the list has places, it is read for its length (at
+// position 500: 14.4 us, at 3,000 13.8). n_list: the length of a ratio-4 list where it is
 // known (4-bit rows).
 template <bool SCAN>
 __device__ __forceinline__ QueryGeo query_geo(const TcAttnParams &P, uint32_t qi, uint32_t t0,
