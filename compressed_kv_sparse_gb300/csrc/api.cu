@@ -4,7 +4,6 @@
 #include <atomic>
 #include <cmath>
 #include <cstring>
-#include <initializer_list>
 
 #include "fp4rows.cuh"
 #include "internal.h"
@@ -25,12 +24,6 @@ namespace {
 
 uint32_t window_of(uint32_t ratio) { return ratio == 4 ? 8u : ratio == 128 ? 128u : 0u; }
 
-// The pointers (NULL: not there) start on multiples of `align` bytes.
-bool aligned(uint32_t align, std::initializer_list<const void *> ptrs) {
-  uintptr_t all = 0;
-  for (const void *p : ptrs) all |= reinterpret_cast<uintptr_t>(p);
-  return all % align == 0;
-}
 uint32_t elem_bytes(const ds4a_layer_cache *c) { return c->dtype == DS4A_BF16 ? 2u : 4u; }
 
 // The sizes of a cache alone.

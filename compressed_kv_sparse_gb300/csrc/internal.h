@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "ds4a.h"
 #include "limit.h"
 
@@ -16,6 +18,13 @@ void note_launches(uint32_t n);
 
 // Records a CUDA error for ds4a_last_error and passes it through.
 cudaError_t note_error(cudaError_t e);
+
+// The pointers (NULL: not there) start on multiples of `align` bytes.
+inline bool aligned(uint32_t align, std::initializer_list<const void *> ptrs) {
+  uintptr_t all = 0;
+  for (const void *p : ptrs) all |= reinterpret_cast<uintptr_t>(p);
+  return all % align == 0;
+}
 
 // Raises `limit` on the current device to `bytes` by set(bytes) where it is below.
 template <typename Set>
@@ -233,6 +242,48 @@ struct TablesArgs {
   uint32_t search, shift;   // (set by the launch)
 };
 cudaError_t launch_block_tables(TablesArgs a, cudaStream_t s);
+
+struct RopeArgs {
+  int dtype, kv_dtype;
+  uint32_t n, n_heads, n_kv, head_dim, rot_at, n_rot, max_pos, half, inverse;
+  const void *x, *k, *v;          // NULL: none
+  uint64_t x_stride, k_stride, v_stride, y_stride;
+  void *y, *k_pool, *v_pool;
+  const float *k_scale, *v_scale, *cos, *sin;
+  const int32_t *pos, *seq, *table;   // seq NULL: no cache
+  uint32_t batch, max_blocks, n_blocks;
+};
+cudaError_t launch_rope(const RopeArgs &a, cudaStream_t s);
+
+// Attention over a paged cache of keys and values.
+struct PagedArgs {
+  int dtype, kv_dtype;
+  uint32_t head_dim, n_kv, batch, max_blocks, n_blocks, max_new, n_heads, window;
+  float scale;
+  const void *q, *k, *v;
+  uint64_t q_stride;
+  const float *k_scale, *v_scale;
+  const int32_t *table;
+  const uint32_t *seq_pos, *cu_len;
+  void *out;
+  float *lse;
+  void *ws;
+};
+size_t paged_attn_ws_bytes(const PagedArgs &a);
+cudaError_t launch_paged_attn(const PagedArgs &a, cudaStream_t s);
+
+struct VerifyArgs {
+  int dtype;
+  uint32_t batch, max_drafts, vocab;
+  const uint32_t *cu_len, *seq_pos;
+  const int32_t *drafts;
+  const void *target, *draft_probs;
+  uint64_t target_stride;
+  const float *u_accept, *u_sample;
+  int32_t *tokens;
+  uint32_t *n_out, *ctx_out;
+};
+cudaError_t launch_verify(const VerifyArgs &a, cudaStream_t s);
 
 cudaError_t launch_state_reset(float *kv, float *score, size_t n, cudaStream_t s);
 cudaError_t launch_index_norms(int dtype, const void *rows, const RowMap &map, uint32_t dim,

@@ -17,7 +17,7 @@ import torch
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libds4a.so")
 
-DS4A_F32, DS4A_BF16 = 0, 1
+DS4A_F32, DS4A_BF16, DS4A_E4M3 = 0, 1, 2
 CALL_APPEND, CALL_INDEX_TOPK, CALL_ATTN_DECODE, CALL_ATTN_PREFILL = 0, 1, 2, 3
 STATUS = {0: "ok", -1: "invalid argument", -2: "unsupported or inconsistent shape",
           -3: "capacity exceeded", -4: "position does not match the cache",
@@ -74,6 +74,19 @@ class StepTablesC(ctypes.Structure):
                                        "comp_slot4", "comp_slot128")]
 
 
+class RopeSpecC(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_uint32) for n in ("rot_at", "n_rot", "max_pos", "flags")] + [
+        ("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p)]
+
+
+class KvCacheC(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_uint32) for n in
+                ("head_dim", "n_kv_heads", "batch", "max_blocks", "n_blocks")] + [
+        ("dtype", ctypes.c_int32), ("kv_dtype", ctypes.c_int32)] + [
+        (n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale", "block_table", "seq_pos")] + [
+        ("rope", RopeSpecC)]
+
+
 EXPORTS = {
     "ds4a_cache_reset": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),
     "ds4a_index_norms": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),
@@ -108,6 +121,23 @@ EXPORTS = {
                                       ctypes.c_void_p, ctypes.c_uint32, ctypes.c_void_p]),
     "ds4a_block_tables": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                          ctypes.c_uint32, ctypes.c_void_p, ctypes.c_void_p]),
+    "ds4a_rope_table_scaled": (ctypes.c_int, [ctypes.c_int] + [ctypes.c_double] * 6 + [ctypes.c_uint32] * 2
+                               + [ctypes.c_void_p] * 2),
+    "ds4a_rope": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_uint32, ctypes.c_void_p,
+                                 ctypes.c_void_p, ctypes.c_uint64, ctypes.c_uint32, ctypes.c_uint32,
+                                 ctypes.c_void_p, ctypes.c_uint64, ctypes.c_void_p]),
+    "ds4a_kv_append": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_uint32, ctypes.c_void_p, ctypes.c_void_p,
+                                      ctypes.c_void_p, ctypes.c_uint64, ctypes.c_void_p, ctypes.c_uint64,
+                                      ctypes.c_void_p, ctypes.c_uint64, ctypes.c_uint32, ctypes.c_void_p,
+                                      ctypes.c_void_p]),
+    "ds4a_paged_attn_decode": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_uint32,
+                                              ctypes.c_void_p, ctypes.c_uint64, ctypes.c_uint32,
+                                              ctypes.c_uint32, ctypes.c_float, ctypes.c_void_p,
+                                              ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
+                                              ctypes.c_void_p]),
+    "ds4a_paged_attn_ws_bytes": (ctypes.c_size_t, [ctypes.c_void_p, ctypes.c_uint32, ctypes.c_uint32]),
+    "ds4a_verify_drafts": (ctypes.c_int, [ctypes.c_int] + [ctypes.c_uint32] * 3 + [ctypes.c_void_p] * 4
+                           + [ctypes.c_uint64] + [ctypes.c_void_p] * 7),
     "ds4a_index_topk_noalloc": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_uint32, ctypes.c_uint32,
                                                ctypes.c_void_p, ctypes.c_void_p, ctypes.c_uint32,
                                                ctypes.c_uint32, ctypes.c_void_p, ctypes.c_void_p]),
@@ -537,6 +567,188 @@ def ds4a_block_tables(pool: BlockPool, ctx_len: torch.Tensor, new_len: torch.Ten
     _check((_lib or load()).ds4a_block_tables(
         ctypes.byref(pool.c), _ptr(ctx_len, dev), _ptr(new_len, dev), cap_raw, ctypes.byref(step.c),
         _stream(stream, dev)), "ds4a_block_tables")
+
+
+ROPE_HALF, ROPE_INVERSE = 1, 2   # DS4A_ROPE_*
+SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}   # DS4A_SCALE_*
+_DTYPE = {"f32": DS4A_F32, "bf16": DS4A_BF16, "e4m3": DS4A_E4M3}
+_TORCH = {"f32": torch.float32, "bf16": torch.bfloat16, "e4m3": torch.float8_e4m3fn}
+_TORCH_DTYPE = {torch.float32: DS4A_F32, torch.bfloat16: DS4A_BF16}
+
+
+class Rope:
+    """Rotary positions of a head's dims rot_at .. rot_at + n_rot - 1 (ds4a_rope_spec) and their
+    tables: pairs of neighbours, or of halves (half); scaling "none", "linear", "ntk" or "yarn"
+    (ds4a_rope_table_scaled). Tables of the same numbers are shared."""
+
+    def __init__(self, *, n_rot: int, max_pos: int, base: float, rot_at: int = 0, half: bool = False,
+                 scaling: str = "none", factor: float = 1.0, orig_len: float = 0.0, beta_fast: float = 32.0,
+                 beta_slow: float = 1.0, magnitude: float = 0.0, device="cuda"):
+        _need(scaling in SCALINGS, f"scaling: one of {', '.join(SCALINGS)}")
+        device = torch.empty(0, device=device).device   # (with its index)
+        nums = (float(base), float(factor), float(orig_len), float(beta_fast), float(beta_slow), float(magnitude))
+        key = (scaling, nums, int(n_rot), int(max_pos), str(device))
+        if key not in _tables:
+            c = torch.empty((max_pos, n_rot // 2), dtype=torch.float32)
+            s = torch.empty((max_pos, n_rot // 2), dtype=torch.float32)
+            _check(load().ds4a_rope_table_scaled(SCALINGS[scaling], *nums, n_rot, max_pos, c.data_ptr(),
+                                                 s.data_ptr()), "ds4a_rope_table_scaled")
+            _tables[key] = (c.to(device), s.to(device))
+        self.cos, self.sin = _tables[key]
+        self.n_rot, self.max_pos, self.rot_at, self.half = n_rot, max_pos, rot_at, half
+        self.dev = dev = self.cos.get_device()
+        self.c = RopeSpecC(rot_at=rot_at, n_rot=n_rot, max_pos=max_pos, flags=ROPE_HALF if half else 0,
+                           cos=_ptr(self.cos, dev), sin=_ptr(self.sin, dev))
+        self._back = RopeSpecC.from_buffer_copy(self.c)
+        self._back.flags |= ROPE_INVERSE
+        self._refs = ctypes.byref(self.c), ctypes.byref(self._back)
+
+
+def _heads(t: torch.Tensor, n: int, heads: int, dim: int, dt: torch.dtype, dev: int, what: str) -> int:
+    """Elements from token to token of t [n][heads][dim], whole tokens that may be strided."""
+    s = t.stride()
+    if not (t.dtype is dt and t.shape == (n, heads, dim) and (dim == 1 or s[2] == 1)
+            and (heads == 1 or s[1] == dim) and t.get_device() == dev):
+        raise ArgumentError(f"{what}: [{n}][{heads}][{dim}] of {dt} with whole tokens, on the call's device")
+    return s[0] if n > 1 else heads * dim
+
+
+def ds4a_rope(rope: Rope, pos: torch.Tensor, x: torch.Tensor, y: torch.Tensor, inverse: bool = False, stream=None):
+    """Heads x [n][H][D] rotated at pos [n] int32 into y (which may be x). The tokens of both may be
+    strided; inverse: rotated back (also the gradient of the rotation)."""
+    dev, n = rope.dev, pos.numel()
+    _need(pos.dtype is _I32 and x.dim() == 3 and x.dtype in _TORCH_DTYPE, "pos: [n] int32; x: [n][heads][dim]")
+    H, D, dt = x.size(1), x.size(2), x.dtype
+    xs, ys = _heads(x, n, H, D, dt, dev, "x"), _heads(y, n, H, D, dt, dev, "y")
+    if n == 0:
+        return
+    _check((_lib or load()).ds4a_rope(rope._refs[1 if inverse else 0], _TORCH_DTYPE[dt], n, _ptr(pos, dev),
+                                      x.data_ptr(), xs, H, D, y.data_ptr(), ys, _stream(stream, dev)),
+           "ds4a_rope")
+
+
+class KvCache:
+    """A paged cache of keys and values (ds4a_kv_cache): pools k, v [n_blocks][K][256][D], made
+    here unless given, blocks by block_table [B][max_blocks] int32 (a BlockPool's table, for
+    instance). kv_dtype "e4m3": 8-bit floats with a scale per head, k_scale and v_scale [K] fp32."""
+
+    def __init__(self, *, head_dim: int, n_kv_heads: int, batch: int, block_table: torch.Tensor, n_blocks: int,
+                 dtype: str = "bf16", kv_dtype: Optional[str] = None, k_scale: Optional[torch.Tensor] = None,
+                 v_scale: Optional[torch.Tensor] = None, rope: Optional[Rope] = None,
+                 k: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = None, device="cuda"):
+        kv_dtype = kv_dtype or dtype
+        _need(dtype in ("f32", "bf16") and kv_dtype in (dtype, "e4m3"), "dtype: f32 or bf16; kv_dtype: dtype or e4m3")
+        self.head_dim, self.n_kv_heads, self.batch, self.n_blocks = head_dim, n_kv_heads, batch, n_blocks
+        self.dtype, self.kv_dtype, self.torch_dtype, kt = dtype, kv_dtype, _TORCH[dtype], _TORCH[kv_dtype]
+        _need(block_table.dtype is _I32 and block_table.dim() == 2 and block_table.shape[0] == batch,
+              "block_table: [batch][max_blocks] int32")
+        shape = (n_blocks, n_kv_heads, 256, head_dim)
+        # (zeros by their bytes: 8-bit floats have no fill everywhere)
+        zeros = lambda: torch.zeros(shape, dtype=torch.uint8 if kv_dtype == "e4m3" else kt, device=device).view(kt)  # noqa: E731
+        self.k, self.v = zeros() if k is None else k, zeros() if v is None else v
+        _need(all(t.dtype is kt and tuple(t.shape) == shape for t in (self.k, self.v)),
+              f"k, v: [n_blocks][n_kv_heads][256][head_dim] of {kt}")
+        self.dev = dev = self.k.get_device()
+        _need((k_scale is not None) == (v_scale is not None) == (kv_dtype == "e4m3"), "scales: with e4m3 only")
+        _need(all(s is None or (s.dtype is torch.float32 and s.numel() == n_kv_heads) for s in (k_scale, v_scale)),
+              "k_scale, v_scale: [n_kv_heads] fp32")
+        _need(rope is None or rope.dev == dev, "the rotation's tables are on another device")
+        self.block_table, self.k_scale, self.v_scale, self.rope, self.seq_pos = block_table, k_scale, v_scale, rope, None
+        self.c = KvCacheC(head_dim=head_dim, n_kv_heads=n_kv_heads, batch=batch, max_blocks=block_table.shape[1],
+                          n_blocks=n_blocks, dtype=_DTYPE[dtype], kv_dtype=_DTYPE[kv_dtype], k=_ptr(self.k, dev),
+                          v=_ptr(self.v, dev), k_scale=_ptr(k_scale, dev), v_scale=_ptr(v_scale, dev),
+                          block_table=_ptr(block_table, dev), rope=rope.c if rope else RopeSpecC())
+        self._ref = ctypes.byref(self.c)
+
+    def set_seq_pos(self, seq_pos: torch.Tensor):
+        """[B] int32 or uint32: the position of each sequence's first new token (StepTables.seq_pos).
+        The tensor must stay alive while calls use it."""
+        _need(seq_pos.dtype in (torch.int32, torch.uint32) and seq_pos.numel() == self.batch,
+              "seq_pos: [batch] int32 or uint32")
+        self.c.seq_pos = _ptr(seq_pos, self.dev)
+        self.seq_pos = seq_pos
+
+    def attn_workspace_bytes(self, n_heads: int, max_new: int = 1) -> int:
+        n = load().ds4a_paged_attn_ws_bytes(self._ref, max_new, n_heads)
+        if n == 0:
+            raise Ds4aError(-2, "ds4a_paged_attn_ws_bytes")
+        return n
+
+
+def ds4a_kv_append(cache: KvCache, tok_seq: torch.Tensor, tok_pos: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                   q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None, stream=None):
+    """Keys k (rotated) and values v [n][K][D] of the packed new tokens (StepTables.tok_seq and
+    tok_pos) into the cache; q [n][H][D] rotated into q_out (which may be q). Tokens of q, k and v
+    may be strided (slices of one projection's output)."""
+    dev, n, K, D, dt = cache.dev, tok_seq.numel(), cache.n_kv_heads, cache.head_dim, cache.torch_dtype
+    if not (tok_seq.dtype is _I32 and tok_pos.dtype is _I32 and tok_pos.numel() == n):
+        raise ArgumentError("tok_seq, tok_pos: [n] int32")
+    ks, vs, qs, H = _heads(k, n, K, D, dt, dev, "k"), _heads(v, n, K, D, dt, dev, "v"), 0, 0
+    _need((q is None) == (q_out is None), "q and q_out: both or neither")
+    if q is not None:
+        _need(q.dim() == 3, "q: [n][heads][head_dim]")
+        H = q.size(1)
+        qs = _heads(q, n, H, D, dt, dev, "q")
+        if not (q_out.dtype is dt and q_out.numel() == n * H * D):
+            raise ArgumentError("q_out: [n][heads][head_dim], like q")
+    if n == 0:
+        return
+    _check((_lib or load()).ds4a_kv_append(
+        cache._ref, n, _ptr(tok_seq, dev), _ptr(tok_pos, dev), k.data_ptr(), ks, v.data_ptr(), vs,
+        None if q is None else q.data_ptr(), qs, H, _ptr(q_out, dev), _stream(stream, dev)), "ds4a_kv_append")
+
+
+def ds4a_paged_attn_decode(cache: KvCache, q: torch.Tensor, out: torch.Tensor, ws: torch.Tensor, *, max_new: int = 1,
+                           cu_len: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None, window: int = 0,
+                           scale: Optional[float] = None, stream=None):
+    """Attention of q [tokens][H][D] (rotated; tokens may be strided) over the cache into out
+    [tokens][H][D]. cu_len [B + 1] int32 or uint32 (StepTables.cu_len): the tokens of each sequence,
+    at most max_new; None: max_new each. lse [tokens][H] fp32: the logarithms of the sums. window: 0 or
+    the last positions that a token sees; scale: 1 / sqrt(D) by default."""
+    dev, D = cache.dev, cache.head_dim
+    _need(q.dim() == 3, "q: [tokens][heads][head_dim]")
+    n, H = q.size(0), q.size(1)
+    qs = _heads(q, n, H, D, cache.torch_dtype, dev, "q")
+    if not (out.dtype is cache.torch_dtype and out.numel() == n * H * D):
+        raise ArgumentError("out: [tokens][heads][head_dim], like q")
+    if not ((lse is None or (lse.dtype is torch.float32 and lse.numel() == n * H))
+            and (cu_len is None or (cu_len.dtype in (_I32, torch.uint32) and cu_len.numel() == cache.batch + 1))):
+        raise ArgumentError("lse: [tokens][heads] fp32; cu_len: [batch + 1] int32 or uint32")
+    _need(cu_len is not None or n == cache.batch * max_new, "q: max_new tokens for each sequence without cu_len")
+    if n == 0:   # (empty tensors have no address)
+        return
+    _check((_lib or load()).ds4a_paged_attn_decode(
+        cache._ref, _ptr(cu_len, dev), max_new, q.data_ptr(), qs, H, window,
+        1.0 / math.sqrt(D) if scale is None else scale, _ptr(out, dev), _ptr(lse, dev), _ptr(ws, dev), _nbytes(ws),
+        _stream(stream, dev)), "ds4a_paged_attn_decode")
+
+
+def ds4a_verify_drafts(target: torch.Tensor, drafts: torch.Tensor, u_accept: torch.Tensor, u_sample: torch.Tensor,
+                       tokens: torch.Tensor, n_out: torch.Tensor, *, draft_probs: Optional[torch.Tensor] = None,
+                       cu_len: Optional[torch.Tensor] = None, seq_pos: Optional[torch.Tensor] = None,
+                       ctx_out: Optional[torch.Tensor] = None, stream=None):
+    """Which of drafts [B][N] int32 stand against the target's probabilities [tokens][V] (rows may be
+    strided), into tokens [B][N + 1] and n_out [B] int32; ctx_out [B]: what each sequence then holds, from
+    seq_pos [B]. draft_probs [B][N][V] or None (greedy drafts); cu_len as in ds4a_paged_attn_decode."""
+    dev = target.get_device()
+    _need(target.dim() == 2 and drafts.dim() == 2 and target.dtype in _TORCH_DTYPE, "target: [tokens][vocab]; drafts: [batch][N]")
+    (B, N), V = drafts.shape, target.size(1)
+    rows, ints = target.size(0), (_I32, torch.uint32)
+    if not ((V == 1 or target.stride(1) == 1) and drafts.dtype is _I32 and u_accept.dtype is torch.float32
+            and u_sample.dtype is torch.float32 and u_accept.numel() == B * N and u_sample.numel() == B
+            and tokens.dtype is _I32 and tokens.numel() == B * (N + 1)):
+        raise ArgumentError("target: whole rows; drafts [B][N], tokens [B][N + 1] int32; u_accept [B][N], u_sample [B] fp32")
+    if not (draft_probs is None or (draft_probs.dtype is target.dtype and draft_probs.numel() == B * N * V)):
+        raise ArgumentError("draft_probs: [batch][N][vocab] of the target's type")
+    for t, m in ((n_out, B), (seq_pos, B), (ctx_out, B), (cu_len, B + 1)):
+        if not (t is None or (t.dtype in ints and t.numel() == m)):
+            raise ArgumentError("n_out, seq_pos, ctx_out: [batch], cu_len: [batch + 1], int32 or uint32")
+    _need(cu_len is not None or rows == B * (N + 1), "target: N + 1 rows for each sequence without cu_len")
+    _check((_lib or load()).ds4a_verify_drafts(
+        _TORCH_DTYPE[target.dtype], B, N, V, _ptr(cu_len, dev), _ptr(seq_pos, dev), _ptr(drafts, dev),
+        target.data_ptr(), target.stride(0) if rows > 1 else V, _ptr(draft_probs, dev), _ptr(u_accept, dev),
+        _ptr(u_sample, dev), _ptr(tokens, dev), _ptr(n_out, dev), _ptr(ctx_out, dev), _stream(stream, dev)),
+        "ds4a_verify_drafts")
 
 
 STATIC_SCRATCH_BYTES = 8 << 20

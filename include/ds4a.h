@@ -16,6 +16,13 @@
  *   ds4a_norm_rope                query-head and K = V norms, rotation, insert
  *   ds4a_pack_rows / _unpack_rows compressed rows to and from 4 bits
  *
+ * and for layers, or a drafting model, with a key and a value per head in the same blocks:
+ *
+ *   ds4a_rope                     rotary positions of whole tokens' heads
+ *   ds4a_kv_append                keys and values into the paged cache
+ *   ds4a_paged_attn_decode        attention of a step's new tokens over it
+ *   ds4a_verify_drafts            which drafted tokens stand
+ *
  * Sources ("page §n" below): "【#3】ds4.c を読み解く" (qiita, DwarfStar series
  * part 3) and "vLLM DeepSeek V4 サポート: 効率的な長文コンテキスト注意機構"
  * (section "DeepSeek V4 アテンションアーキテクチャ").
@@ -69,7 +76,8 @@ typedef enum {
   DS4A_ERR_WORKSPACE = -8  /* workspace missing or smaller than required */
 } ds4a_status;
 
-typedef enum { DS4A_F32 = 0, DS4A_BF16 = 1 } ds4a_dtype;
+/* (DS4A_E4M3: ds4a_kv_cache.kv_dtype alone) */
+typedef enum { DS4A_F32 = 0, DS4A_BF16 = 1, DS4A_E4M3 = 2 } ds4a_dtype;
 
 /*
  * One layer's cache for `batch` sequences (page §2, ds4_layer_cache).
@@ -509,6 +517,184 @@ typedef struct {
 ds4a_status ds4a_block_tables(const ds4a_block_pool *pool, const uint32_t *ctx_len,
                               const uint32_t *new_len, uint32_t cap_raw,
                               const ds4a_step_tables *step, ds4a_stream_t stream);
+
+/*
+ * ---- layers that keep a key and a value per head ---------------------------
+ *
+ * Beside compressed layers a stack, or the small model that drafts tokens for it, may have
+ * layers with plain grouped-query attention. Their keys and values live in the same
+ * 256-position blocks (ds4a_block_tables gives table, positions and packed tokens; several
+ * caches share one table). The pages have no counterpart: the formulas are stated here.
+ *
+ * Rotary positions (ds4a_rope_spec): of a head's D dims the n_rot ones from rot_at on are
+ * n_rot / 2 pairs. Pair i is (rot_at + 2 i, rot_at + 2 i + 1), or with DS4A_ROPE_HALF
+ * (rot_at + i, rot_at + n_rot / 2 + i). At position p, with c = cos[p][i], s = sin[p][i]:
+ *   (x0, x1) -> (x0 c - x1 s, x0 s + x1 c)
+ * in fp32, each product and sum rounded once (no fused multiply-add), the result rounded to
+ * the type. DS4A_ROPE_INVERSE takes -s for s: the rotation back, which is also the gradient's.
+ *  rot_at, n_rot  even, rot_at + n_rot <= D; n_rot 0: nothing is rotated (cos, sin may be NULL)
+ *  max_pos        rows of the tables
+ *  cos, sin       [max_pos][n_rot / 2] fp32 DEVICE
+ */
+#define DS4A_ROPE_HALF 1u
+#define DS4A_ROPE_INVERSE 2u
+typedef struct {
+  uint32_t rot_at, n_rot, max_pos, flags;
+  const float *cos, *sin;
+} ds4a_rope_spec;
+
+/*
+ * Host helper: tables for contexts longer than the trained ones, into HOST arrays
+ * [n_pos][n_rot / 2], angles in fp64, rounded once. kind:
+ *  DS4A_SCALE_NONE    theta_i = base^(-2 i / n_rot)
+ *  DS4A_SCALE_LINEAR  theta_i / factor
+ *  DS4A_SCALE_NTK     theta_i of the base times factor^(n_rot / (n_rot - 2)); n_rot > 2
+ *  DS4A_SCALE_YARN    theta_i (g_i + (1 - g_i) / factor): g_i falls linearly from 1 to 0
+ *    between pairs low = max(floor(at(beta_fast)), 0) and high = min(ceil(at(beta_slow)),
+ *    n_rot / 2 - 1), at(turns) = n_rot ln(orig_len / (2 pi turns)) / (2 ln base) being the
+ *    pair that turns so often over orig_len positions (a distance below 0.001 counts as
+ *    that). Cosines and sines are multiplied by magnitude; 0 stands for 0.1 ln(factor) + 1.
+ *    (Peng et al., "YaRN: Efficient Context Window Extension of Large Language Models".)
+ * factor >= 1, base > 1. Errors: DS4A_ERR_ARG.
+ */
+enum { DS4A_SCALE_NONE = 0, DS4A_SCALE_LINEAR = 1, DS4A_SCALE_NTK = 2, DS4A_SCALE_YARN = 3 };
+ds4a_status ds4a_rope_table_scaled(int kind, double base, double factor, double orig_len,
+                                   double beta_fast, double beta_slow, double magnitude,
+                                   uint32_t n_rot, uint32_t n_pos, float *cos_out, float *sin_out);
+
+/*
+ * Rotates the heads of n tokens.
+ *  dtype   of x and y (DS4A_F32 or DS4A_BF16)
+ *  pos     [n] int32 DEVICE; a token whose position is negative or >= max_pos is skipped (y
+ *          stays as it was)
+ *  x, y    [n][n_heads][D], x_stride and y_stride elements from token to token (>= n_heads *
+ *          D; a token's heads are contiguous). Dims that are not rotated are copied. y may be
+ *          x with equal strides; it overlaps x in no other way.
+ *  n_heads 1 .. 1024, D even, <= 512
+ * n = 0 does nothing. Errors: DS4A_ERR_ARG (a missing or misaligned pointer, flags, in place
+ * with other strides), DS4A_ERR_SHAPE, DS4A_ERR_DTYPE, DS4A_ERR_CUDA.
+ */
+ds4a_status ds4a_rope(const ds4a_rope_spec *rope, int dtype, uint32_t n, const int32_t *pos,
+                      const void *x, uint64_t x_stride, uint32_t n_heads, uint32_t head_dim,
+                      void *y, uint64_t y_stride, ds4a_stream_t stream);
+
+/*
+ * A paged cache of keys and values.
+ *  head_dim     D of keys, values and queries; even, <= 256
+ *  n_kv_heads   K, <= 128
+ *  batch        B, at most DS4A_MAX_TABLE_ROWS
+ *  max_blocks, n_blocks, block_table  as in ds4a_layer_cache: [B][max_blocks] int32 DEVICE,
+ *               entry (b, j) the block of positions 256 j .. of sequence b. An entry outside
+ *               [0, n_blocks) is not written to, and its keys take no part in the attention.
+ *               max_blocks <= 2^23, n_blocks * K * 256 < 2^31.
+ *  dtype        of queries, new rows and outputs: DS4A_F32 or DS4A_BF16
+ *  kv_dtype     of the cache: dtype, or DS4A_E4M3 (8-bit floats: sign, 4 exponent and 3
+ *               mantissa bits, largest 448, no infinities)
+ *  k, v         DEVICE pools [n_blocks][K][256][D], on 16 bytes
+ *  k_scale, v_scale  [K] fp32 DEVICE, with DS4A_E4M3 only: a stored code stands for its value
+ *               times the head's scale (positive)
+ *  seq_pos      [B] uint32 DEVICE: position of each sequence's first new token in this step
+ *               (attention only; ds4a_step_tables.seq_pos)
+ *  rope         rotation of keys and queries at the append (n_rot 0: none); no
+ *               DS4A_ROPE_INVERSE
+ */
+typedef struct {
+  uint32_t head_dim, n_kv_heads, batch, max_blocks, n_blocks;
+  int32_t dtype, kv_dtype;
+  void *k, *v;
+  const float *k_scale, *v_scale;
+  const int32_t *block_table;
+  const uint32_t *seq_pos;
+  ds4a_rope_spec rope;
+} ds4a_kv_cache;
+
+/*
+ * Appends the keys (rotated) and values of n packed new tokens, and rotates their queries in
+ * the same pass.
+ *  tok_seq, tok_pos  [n] int32 DEVICE (ds4a_step_tables): a token whose sequence is not in
+ *               [0, B) or whose position is negative, >= rope.max_pos (where rope.n_rot > 0)
+ *               or >= 256 max_blocks is skipped; one whose block is not there leaves its key
+ *               and value out. (sequence, position) must be distinct: of two tokens for one
+ *               place either one, or a mix of both, remains.
+ *  k, v         [n][K][D] (dtype), k_stride and v_stride elements from token to token
+ *  q            [n][n_heads][D], q_stride elements; NULL: no queries (then n_heads 0)
+ *  q_out        [n][n_heads][D], contiguous; may be q itself when q_stride == n_heads * D
+ * With DS4A_E4M3 a value x becomes the code nearest x * (1 / scale), the reciprocal rounded to
+ * fp32, ties to the even code, values beyond 448 held to 448, NaN kept.
+ * n = 0 does nothing. Errors: DS4A_ERR_ARG, DS4A_ERR_SHAPE, DS4A_ERR_DTYPE, DS4A_ERR_CUDA.
+ */
+ds4a_status ds4a_kv_append(const ds4a_kv_cache *cache, uint32_t n, const int32_t *tok_seq,
+                           const int32_t *tok_pos, const void *k, uint64_t k_stride,
+                           const void *v, uint64_t v_stride, const void *q, uint64_t q_stride,
+                           uint32_t n_heads, void *q_out, ds4a_stream_t stream);
+
+/*
+ * Attention of the new tokens of a decode step (one per sequence, or one and its drafts)
+ * over the paged cache, which holds their own rows already.
+ *  cu_len    [B + 1] uint32 DEVICE (ds4a_step_tables): sequence b's tokens are the packed ones
+ *            cu_len[b] .. cu_len[b + 1] - 1; NULL: max_new each. Of more than max_new the
+ *            first max_new are computed, the others' outputs stay as they were.
+ *  max_new   the most new tokens of a sequence, 1 .. 256
+ *  q         [tokens][n_heads][D] (dtype), rotated, q_stride elements from token to token
+ *  n_heads   H, a multiple of K, <= 1024: query head h reads key head h / (H / K)
+ *  window    0: every position up to the token's own; W: the last W of them, its own included
+ *  scale     of the products, before the softmax
+ *  out       [tokens][H][D] (dtype), contiguous
+ *  lse       [tokens][H] fp32, NULL: not wanted: the natural logarithm of the softmax's sum
+ *            (for joining with attention over other keys)
+ *  ws        ds4a_paged_attn_ws_bytes bytes on 16; its first 4 bytes count timed-out device
+ *            waits (ds4a_workspace_status). Calls that may run at once need one each.
+ * Token t of sequence b is at p = seq_pos[b] + t and sees keys max(0, p - W + 1) .. p of blocks
+ * that are there. One that sees none gets zeros, and -infinity as lse. What lies in unseen
+ * rows of a block (never written, NaN) changes nothing. A NaN in a seen key or value gives
+ * NaN, an infinity NaN or an infinity. Sums and statistics are fp32; the result does not depend on
+ * timing. It may differ in the last bits with the number of SMs and of sequences in the call.
+ * Errors: DS4A_ERR_ARG, DS4A_ERR_SHAPE, DS4A_ERR_DTYPE, DS4A_ERR_WORKSPACE, DS4A_ERR_CUDA.
+ * ds4a_paged_attn_ws_bytes: 0 for sizes that no call takes; with the device of the call
+ * current.
+ */
+ds4a_status ds4a_paged_attn_decode(const ds4a_kv_cache *cache, const uint32_t *cu_len,
+                                   uint32_t max_new, const void *q, uint64_t q_stride,
+                                   uint32_t n_heads, uint32_t window, float scale, void *out,
+                                   float *lse, void *ws, size_t ws_bytes, ds4a_stream_t stream);
+size_t ds4a_paged_attn_ws_bytes(const ds4a_kv_cache *cache, uint32_t max_new, uint32_t n_heads);
+
+/*
+ * Which drafted tokens stand, and the token that follows them (Leviathan et al., "Fast
+ * Inference from Transformers via Speculative Decoding"): every emitted token is distributed
+ * as the target's.
+ *  dtype       of target and draft_probs (DS4A_F32 or DS4A_BF16)
+ *  batch       B, at most DS4A_MAX_TABLE_ROWS; max_drafts N, 1 .. 255; vocab V, <= 2^20
+ *  cu_len      [B + 1] uint32 DEVICE, the step's new tokens: sequence b's last accepted token
+ *              and its m = cu_len[b + 1] - cu_len[b] - 1 drafts (at most N are looked at); no new
+ *              token: the sequence is free. NULL: N drafts each.
+ *  seq_pos     [B] position of the first of them; NULL without ctx_out
+ *  drafts      [B][N] int32: the drafted tokens. One outside [0, V) falls.
+ *  target      [tokens][V]: row cu_len[b] + i are the probabilities after i drafts of b;
+ *              target_stride elements from row to row
+ *  draft_probs [B][N][V] contiguous: what draft i was drawn from; NULL: the drafts were not
+ *              drawn (greedy): probability 1 for the drafted token
+ *  u_accept    [B][N], u_sample [B] fp32: random numbers in [0, 1)
+ *  tokens      [B][N + 1] int32 out: the a drafts that stand, the new token, then -1
+ *  n_out       [B] uint32 out: a + 1; 0 for a free sequence
+ *  ctx_out     [B] uint32 out or NULL: seq_pos[b] + a + 1, what the sequence holds of the
+ *              cache that stays valid (the next ctx_len of ds4a_block_tables without its new
+ *              tokens); seq_pos[b] for a free sequence
+ * Drafts stand while u_accept q(x) < p(x), compared exactly. The new token is drawn from
+ * w = max(p - q, 0) of the first one that fell (p with the drafted token at 0 where draft_probs
+ * is NULL), or from p where all stand: the lowest token whose running sum of w exceeds
+ * u_sample times the sum. For these sums p and q are each rounded to a multiple of 2^-s, s = 62 -
+ * ceil(log2 V) (45 for 131,072 tokens), and added as whole numbers, so the order of sums changes
+ * nothing; probabilities above 1 count as 1, negative ones and NaN as 0. A w that is zero everywhere
+ * gives way to p, and a p that is zero everywhere to token V - 1.
+ * Errors: DS4A_ERR_ARG, DS4A_ERR_SHAPE, DS4A_ERR_DTYPE, DS4A_ERR_CUDA.
+ */
+ds4a_status ds4a_verify_drafts(int dtype, uint32_t batch, uint32_t max_drafts, uint32_t vocab,
+                               const uint32_t *cu_len, const uint32_t *seq_pos,
+                               const int32_t *drafts, const void *target,
+                               uint64_t target_stride, const void *draft_probs,
+                               const float *u_accept, const float *u_sample, int32_t *tokens,
+                               uint32_t *n_out, uint32_t *ctx_out, ds4a_stream_t stream);
 
 /*
  * ds4a_index_topk for callers that cannot allocate device memory (the pages
