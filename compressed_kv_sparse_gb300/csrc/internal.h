@@ -98,9 +98,11 @@ ds4a_status index_topk_check(const ds4a_layer_cache *c, uint32_t pos0, uint32_t 
                              const void *q_idx, const void *w, uint32_t n_heads, uint32_t top_k,
                              const int32_t *topk);
 
-// TMA tensor map over bf16 data with 128-byte swizzle (tmap.cu).
+// TMA tensor maps over bf16 and 8-bit data with 128-byte swizzle (tmap.cu).
 cudaError_t make_tmap_bf16(CUtensorMap *map, const void *base, int rank, const uint64_t *dims,
                            const uint64_t *strides_bytes, const uint32_t *box);
+cudaError_t make_tmap_u8(CUtensorMap *map, const void *base, int rank, const uint64_t *dims,
+                         const uint64_t *strides_bytes, const uint32_t *box);
 int num_sms();
 
 // One compressor lane (attention or indexer) of a layer.
@@ -271,6 +273,10 @@ struct PagedArgs {
 };
 size_t paged_attn_ws_bytes(const PagedArgs &a);
 cudaError_t launch_paged_attn(const PagedArgs &a, cudaStream_t s);
+// On the tensor cores (paged_attn_tc.cu): bf16 layers whose rows TMA can copy.
+bool paged_attn_tc_takes(const PagedArgs &a);
+size_t paged_attn_tc_ws_bytes(const PagedArgs &a);
+cudaError_t launch_paged_attn_tc(const PagedArgs &a, cudaStream_t s);
 
 struct VerifyArgs {
   int dtype;

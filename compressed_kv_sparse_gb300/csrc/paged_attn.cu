@@ -1,4 +1,5 @@
-// Attention of a step's new tokens over a paged cache of keys and values, on the CUDA cores.
+// Attention of a step's new tokens over a paged cache of keys and values, on the CUDA cores: the
+// exact path of fp32 layers and the one for sizes that the tensor-core kernel does not take.
 //
 // Rows (a sequence's tokens x the query heads of one key head) in groups of up to 16, keys in
 // tiles of 64: a block scores a tile (a thread per key and quarter of the rows), updates each
@@ -7,7 +8,7 @@
 // leaves its sums with their maximum, and a second launch joins them in order.
 #include <cuda_fp8.h>
 
-#include "common.cuh"
+#include "paged.cuh"
 
 namespace ds4a {
 
@@ -21,25 +22,6 @@ struct Params {
   uint32_t G, groups, splits;   // query heads per key head, row groups, shares of the keys
   float *part;                  // [batch * max_new * H][splits][D], then (max, sum) of each
 };
-
-struct Item {
-  uint32_t first, cnt, pos0;   // packed tokens, position of the first
-  uint32_t lo, hi;             // keys that some token may see
-};
-
-// The tokens of sequence b and the keys they see.
-__device__ __forceinline__ Item item_of(const PagedArgs &a, uint32_t b) {
-  Item it;
-  it.first = a.cu_len ? __ldg(a.cu_len + b) : b * a.max_new;
-  const uint32_t n = a.cu_len ? __ldg(a.cu_len + b + 1) - it.first : a.max_new;
-  it.cnt = n < 0x80000000u ? min(n, a.max_new) : 0u;
-  it.pos0 = __ldg(a.seq_pos + b);
-  const uint64_t end = (uint64_t)it.pos0 + it.cnt, room = (uint64_t)a.max_blocks * 256u;
-  it.hi = (uint32_t)(end < room ? end : room);
-  it.lo = a.window && it.pos0 + 1 > a.window ? it.pos0 + 1 - a.window : 0u;
-  if (it.lo > it.hi) it.lo = it.hi;
-  return it;
-}
 
 template <typename T>
 __device__ __forceinline__ float ld_kv(const T *p, size_t i) {
@@ -62,7 +44,7 @@ __global__ void __launch_bounds__(kThreads) paged_attn_kernel(Params P) {
   pdl_trigger();
   const uint32_t split = blockIdx.x, kh = blockIdx.y / P.groups, rg = blockIdx.y % P.groups, b = blockIdx.z;
   const uint32_t t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  const Item it = item_of(a, b);
+  const PagedItem it = paged_item(a, b);
   const uint32_t r0 = rg * kRows, all = it.cnt * P.G;
   if (r0 >= all) return;
   const uint32_t nr = min(kRows, all - r0);
@@ -174,7 +156,7 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(Params P) {
   pdl_trigger();
   const PagedArgs &a = P.a;
   const uint32_t D = a.head_dim, H = a.n_heads, h = blockIdx.x, tk = blockIdx.y, b = blockIdx.z;
-  const Item it = item_of(a, b);
+  const PagedItem it = paged_item(a, b);
   if (tk >= it.cnt) return;
   const size_t row = ((size_t)b * a.max_new + tk) * H + h, rows = (size_t)a.batch * a.max_new * H;
   const float *ml = P.part + rows * P.splits * D + 2 * row * P.splits;
@@ -235,11 +217,13 @@ cudaError_t launch_t(const PagedArgs &a, cudaStream_t s) {
 }  // namespace
 
 size_t paged_attn_ws_bytes(const PagedArgs &a) {
+  if (paged_attn_tc_takes(a)) return kWsHead + paged_attn_tc_ws_bytes(a);
   const uint32_t S = splits_of(a);
   return kWsHead + (S > 1 ? (size_t)a.batch * a.max_new * a.n_heads * S * (a.head_dim + 2) * 4 : 0);
 }
 
 cudaError_t launch_paged_attn(const PagedArgs &a, cudaStream_t s) {
+  if (paged_attn_tc_takes(a)) return launch_paged_attn_tc(a, s);
   if (a.kv_dtype == DS4A_E4M3)
     return a.dtype == DS4A_BF16 ? launch_t<__nv_bfloat16, __nv_fp8_storage_t>(a, s)
                                 : launch_t<float, __nv_fp8_storage_t>(a, s);

@@ -29,10 +29,10 @@ EncodeTiledFn encode_fn() {
 
 }  // namespace
 
-// bf16 tensor map, 128-byte swizzle, zero fill out of bounds. dims[0] is the
+// Tensor map, 128-byte swizzle, zero fill out of bounds. dims[0] is the
 // innermost extent; strides_bytes[i] is the stride of dimension i + 1.
-cudaError_t make_tmap_bf16(CUtensorMap *map, const void *base, int rank, const uint64_t *dims,
-                           const uint64_t *strides_bytes, const uint32_t *box) {
+static cudaError_t make_tmap(CUtensorMapDataType type, CUtensorMap *map, const void *base, int rank,
+                             const uint64_t *dims, const uint64_t *strides_bytes, const uint32_t *box) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return cudaErrorNotSupported;
   if (reinterpret_cast<uintptr_t>(base) % 16) return cudaErrorMisalignedAddress;
@@ -47,10 +47,20 @@ cudaError_t make_tmap_bf16(CUtensorMap *map, const void *base, int rank, const u
       if (st[i] % 16) return cudaErrorInvalidValue;
     }
   }
-  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void *>(base),
+  CUresult r = fn(map, type, (cuuint32_t)rank, const_cast<void *>(base),
                   d, st, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t make_tmap_bf16(CUtensorMap *map, const void *base, int rank, const uint64_t *dims,
+                           const uint64_t *strides_bytes, const uint32_t *box) {
+  return make_tmap(CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, map, base, rank, dims, strides_bytes, box);
+}
+
+cudaError_t make_tmap_u8(CUtensorMap *map, const void *base, int rank, const uint64_t *dims,
+                         const uint64_t *strides_bytes, const uint32_t *box) {
+  return make_tmap(CU_TENSOR_MAP_DATA_TYPE_UINT8, map, base, rank, dims, strides_bytes, box);
 }
 
 int num_sms() {

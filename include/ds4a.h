@@ -647,8 +647,10 @@ ds4a_status ds4a_kv_append(const ds4a_kv_cache *cache, uint32_t n, const int32_t
  * Token t of sequence b is at p = seq_pos[b] + t and sees keys max(0, p - W + 1) .. p of blocks
  * that are there. One that sees none gets zeros, and -infinity as lse. What lies in unseen
  * rows of a block (never written, NaN) changes nothing. A NaN in a seen key or value gives
- * NaN, an infinity NaN or an infinity. Sums and statistics are fp32; the result does not depend on
+ * NaN; an infinity there is not looked after. Sums and statistics are fp32; the result does not depend on
  * timing. It may differ in the last bits with the number of SMs and of sequences in the call.
+ * Runs on the tensor cores for bf16 layers (D a multiple of 8; of 16 with DS4A_E4M3), on the
+ * CUDA cores otherwise.
  * Errors: DS4A_ERR_ARG, DS4A_ERR_SHAPE, DS4A_ERR_DTYPE, DS4A_ERR_WORKSPACE, DS4A_ERR_CUDA.
  * ds4a_paged_attn_ws_bytes: 0 for sizes that no call takes; with the device of the call
  * current.
