@@ -34,9 +34,9 @@
 namespace ds4a {
 namespace {
 
-constexpr uint32_t kTile = 128, kThreads = 256, kBox = kTile * 128;   // keys; bytes of a 128-byte column
+constexpr uint32_t kTile = 128, kBox = kTile * 128;   // keys; bytes of a 128-byte column
 constexpr uint32_t kSegs = 4, kMaxSlots = 16;
-constexpr uint32_t kSmemMost = 227 * 1024, kFixed = 8192;
+constexpr uint32_t kSmemSm = 228 * 1024, kSmemBlock = 1024;   // shared memory of an SM; reserved per block
 constexpr float kNoRef = 3e38f;   // -reference of a row that has seen no key
 
 struct Segment {
@@ -44,23 +44,27 @@ struct Segment {
   uint32_t first, pos0;            // packed index and position of the sequence's first token
   uint32_t tile0, nt;              // tiles (of 128 positions); nt 0: no more segments
   uint32_t whole;                  // bit 0: its first tile is here, bit 1: its last
+  uint32_t blocks;                 // blocks behind this one that hold some of it
 };
 
-// What a block left of the segments that it does not hold whole: [0] the one that began before,
-// [1] the one that goes on.
+// What a block left of a segment that goes on in the next `blocks` ones (0: no such segment).
 struct Part {
-  uint32_t valid, last, b, kh, r0, nr, first, pad;
+  uint32_t blocks, kh, r0, nr, first, pad[3];
 };
 
 struct Params {
   PagedArgs a;
   uint32_t G;           // query heads per key head
   uint32_t nbox, nmb;   // 128-byte columns of a key's row; blocks of 128 dims of the output
-  uint32_t n_slots, n_q;
+  uint32_t ubox;        // columns of a unit, what is loaded at once: a tile's keys or values of 128 dims
+  uint32_t n_slots, n_q, n_p;   // units, query tiles and weight tiles held
+  uint32_t g_mul;       // 2^32 / G + 1 (rows are below 2^18), 0: G is 1
   uint32_t q_vec;       // queries start on 16 bytes
   float c2;             // scale * log2(e)
-  Part *parts;          // [blocks][2]
-  float *sums;          // [blocks][2][RP][D], then (reference, sum) [blocks][2][RP][2]
+  Part *parts;          // [blocks]
+  // [blocks][2][RP][D], then (reference, sum) [blocks][2][RP][2]: of what began before a block, and of
+  // what goes on behind it
+  float *sums;
   int *err;
 };
 
@@ -68,44 +72,52 @@ template <int RP, bool F8>
 struct Cfg {
   static constexpr uint32_t kQRows = F8 ? 2 * RP : (RP < 16 ? 16 : RP);   // rows of the Q operand
   static constexpr uint32_t kPBytes = kTile * 2 * RP * (F8 ? 1 : 2);
+  // softmax warps: four, which take a quarter of the keys each, or two such sets with every other
+  // eight rows each
+  static constexpr uint32_t kSets = RP >= 32 ? 2 : 1, kWarps = 4 * kSets, kThreads = 128 + 32 * kWarps;
+  static constexpr int kRows = RP / kSets;
+  // few rows: two blocks a SM, so that one computes while the other starts, ends or waits
+  static constexpr uint32_t kPerSm = RP <= 16 ? 2 : 1;
   static constexpr float kOff = F8 ? 5.f : 0.f;     // weights are 2^(s - m + kOff)
   static constexpr float kTop = F8 ? 8.75f : 8.f;   // ... and at most 2^kTop (448 for 8 bits)
 };
 
+template <int RP>
 struct Shared {
   uint64_t full[kMaxSlots], empty[kMaxSlots];
   uint64_t seg_full[kSegs], seg_empty[kSegs];
   uint64_t q_full[2], q_empty[2], s_full[2], s_empty[2];
-  uint64_t p_full, pv_done, o_free, group, drain;
+  uint64_t p_full[2], pv_done[2], o_free, drain;
   uint32_t tmem;
   uint32_t start_b;
-  uint64_t start_off, start_n;
-  uint64_t scan[kThreads / 32];
-  uint32_t over[3], bad;
+  uint32_t shares;
+  uint64_t start_off, start_n, total, end;   // of the list of tiles: see below
+  uint64_t scan[12];
+  uint32_t bad;
   Segment seg[kSegs];
-  alignas(16) float qs[kSegs][64];   // factor of each row's scores (8-bit queries)
-  alignas(16) float negm[64];        // -reference of each row
-  alignas(16) float fac[64];
-  alignas(16) float wmax[4][64];
+  alignas(16) float qs[kSegs][RP];   // factor of each row's scores (8-bit queries)
+  alignas(16) float negm[RP];        // -reference of each row
+  alignas(16) float fac[RP];
+  alignas(16) float wmax[4][RP];
+  uint32_t row_out[RP];              // packed token * H + head of each row
 };
-static_assert(sizeof(Shared) <= kFixed - 1024, "fixed shared memory");
 
-// Products with 8-bit operands, both E4M3, fp32 sums.
-__device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+// Products with 8-bit operands, both E4M3, fp32 sums; from code that the whole warp runs.
+__device__ __forceinline__ void mma_e4m3_elect(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                               uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, e;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc)
       : "memory");
 }
 
-// Descriptor of an operand without swizzle, MN-major: 16 bytes along N by 8 along K are 128
-// contiguous bytes; k_step bytes to the next 8 along K, mn_step to the next 16 bytes along N.
-__device__ __forceinline__ uint64_t sdesc_plain_mn(uint32_t addr, uint32_t k_step, uint32_t mn_step) {
-  return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(k_step >> 4) << 16) | ((uint64_t)(mn_step >> 4) << 32) |
-         ((uint64_t)1 << 46);
-}
+// High half of the descriptor of an operand without swizzle, MN-major: 16 bytes along N by 8 along
+// K are 128 contiguous bytes; `mn_step` bytes to the next 16 bytes along N. (The low half's leading byte
+// offset is the step to the next 8 along K.)
+__host__ __device__ constexpr uint32_t desc_hi_plain(uint32_t mn_step) { return (mn_step >> 4) | (1u << 14); }
 
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
@@ -125,21 +137,102 @@ __device__ __forceinline__ float2 unpack_e4m3(uint16_t u) {
   return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(u, __NV_E4M3)));
 }
 
-// Largest value of the warp, a NaN if there is one (as FMA makes them).
-__device__ __forceinline__ float warp_max_nan(float v) {
-  const uint32_t u = __float_as_uint(v);
-  const uint32_t k = redux_max_u32((u & 0x80000000u) ? ~u : u | 0x80000000u);
-  return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
+// Reductions of R values over the warp, all at once: lane 32 / R * r ends up with value r (each step
+// halves the values that a lane holds).
+template <int R, typename Op>
+__device__ __forceinline__ float warp_reduce_rows(float (&v)[R], uint32_t lane, Op op) {
+  uint32_t o = 16;
+#pragma unroll
+  for (int n = R; n > 1; n >>= 1, o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < n / 2; ++i) {
+      const float keep = up ? v[i + n / 2] : v[i], give = up ? v[i] : v[i + n / 2];
+      v[i] = op(keep, __shfl_xor_sync(0xffffffffu, give, o));
+    }
+  }
+  for (; o; o >>= 1) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
+  return v[0];
+}
+// The larger of two, a NaN if either is one.
+__device__ __forceinline__ float max_nan(float a, float b) { return a > b || a != a ? a : b; }
+
+// The waits of the chain from scores to output: a test, which a thread that issues products needs (a
+// blocking wait would hold it until those in flight have drained), then blocking tries; the time is looked
+// at when those have failed for long.
+__device__ __forceinline__ bool wait_chain(uint64_t *bar, uint32_t parity, ErrWord err) {
+  if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
+  bool ok = false;
+  for (uint32_t i = 0; i < 64 && !ok; ++i) ok = mbar_try_wait(bar, parity);
+  if (__all_sync(0xffffffffu, ok)) return true;
+  return __all_sync(0xffffffffu, mbar_wait_long(smem_u32(bar), parity, err.p, err.base));
 }
 
-// One arrival and one bounded wait for each of the softmax's four warps.
-__device__ __forceinline__ bool warps_sync(uint64_t *bar, uint32_t &phase, uint32_t lane, ErrWord err) {
+// Two fp32 operations at once, each rounded as the single one.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 c, a, b, c;\n\tmov.b64 {%0, %1}, c;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+// The share that place x - 1 of a list of `total` is in: the largest c with total c / shares < x.
+__device__ __forceinline__ uint32_t last_share(uint64_t x, uint32_t shares, uint64_t total) {
+  const uint64_t n = x * shares - 1;
+  return (n | total) >> 32 ? (uint32_t)(n / total) : (uint32_t)n / (uint32_t)total;
+}
+// a b / c, mostly in 32 bits.
+__device__ __forceinline__ uint64_t mul_div(uint64_t a, uint32_t b, uint64_t c) {
+  const uint64_t n = a * b;
+  return (n | c) >> 32 ? n / c : (uint32_t)n / (uint32_t)c;
+}
+
+// One arrival of a warp.
+__device__ __forceinline__ void warps_arrive(uint64_t *bar, uint32_t lane) {
   __syncwarp();
   if (lane == 0) mbar_arrive(bar);
-  const bool ok = mbar_wait_warp(bar, phase, err);
-  phase ^= 1;
-  return ok;
 }
+
+// Hardware barrier of the softmax's `count` threads; the second tells whether any of them says so. (An mbarrier
+// costs some 300 clocks to the waiting side, this 50. It cannot run out, so these warps enter a segment
+// together or not at all and go through it whatever their other waits say.)
+__device__ __forceinline__ void group_bar(uint32_t count) { named_bar_sync(1, count); }
+__device__ __forceinline__ bool group_any(bool mine, uint32_t count) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, 1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"((uint32_t)mine), "r"(count)
+      : "memory");
+  return any != 0;
+}
+
+// n / G
+__device__ __forceinline__ uint32_t by_group(const Params &P, uint32_t n) { return P.g_mul ? __umulhi(n, P.g_mul) : n; }
 
 __device__ __forceinline__ uint32_t tiles_of(const PagedItem &it) {
   if (it.cnt == 0) return 0;
@@ -151,17 +244,18 @@ __device__ __forceinline__ uint32_t phys_of(const PagedArgs &a, uint32_t b, uint
   return j < a.max_blocks ? (uint32_t)__ldg(a.table + (size_t)b * a.max_blocks + j) : 0xffffffffu;
 }
 
-// Physical block of a tile, from 32 entries at a time in the warp's lanes.
+// Physical block of a tile, from 32 entries at a time in the warp's lanes. look() before at(), apart so
+// that the load overlaps a wait.
 struct BlockList {
   uint32_t base, mine;
   __device__ __forceinline__ void start() { base = 0xffffffffu; }
-  __device__ __forceinline__ uint32_t at(const PagedArgs &a, uint32_t b, uint32_t j, uint32_t lane) {
+  __device__ __forceinline__ void look(const PagedArgs &a, uint32_t b, uint32_t j, uint32_t lane) {
     if (base == 0xffffffffu || j - base >= 32) {
       base = j;
       mine = phys_of(a, b, j + lane);
     }
-    return __shfl_sync(0xffffffffu, mine, j - base);
   }
+  __device__ __forceinline__ uint32_t at(uint32_t j) { return __shfl_sync(0xffffffffu, mine, j - base); }
 };
 
 // Place of V(j) in the order of a segment's loads, K0 K1 V0 K2 V1 .. V(nt - 1).
@@ -180,9 +274,9 @@ struct Ring {   // slot and parity of the loads, counted from the block's first
 // A value row of an unseen key, or the NaNs and infinities of one that only some rows see, made zeros in
 // shared memory: 0 times them would be a NaN. Returns whether there were any of the latter.
 template <bool F8>
-__device__ __noinline__ bool clean_row(uint32_t row, uint32_t nbox, bool all) {
+__device__ __noinline__ bool clean_row(uint32_t row, uint32_t ubox, bool all) {
   bool found = false;
-  for (uint32_t x = 0; x < nbox; ++x)
+  for (uint32_t x = 0; x < ubox; ++x)
     for (uint32_t c = 0; c < 8; ++c) {
       const uint32_t at = row + x * kBox + 16 * c;
       uint32_t v[4] = {0, 0, 0, 0};
@@ -245,15 +339,16 @@ __device__ __noinline__ float taken_out(const PagedArgs &a, const Segment &sg, u
 }
 
 template <int RP, bool F8>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<RP, F8>::kThreads, Cfg<RP, F8>::kPerSm)
     paged_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, Params P) {
   using C = Cfg<RP, F8>;
+  constexpr uint32_t kThreads = C::kThreads;
   extern __shared__ uint8_t raw[];
   uint8_t *smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   const PagedArgs &a = P.a;
-  const uint32_t slot_bytes = P.nbox * kBox, q_bytes = C::kQRows * P.nbox * 128u;
+  const uint32_t slot_bytes = P.ubox * kBox, q_bytes = C::kQRows * P.nbox * 128u;
   uint8_t *s_slot = smem, *s_q = s_slot + P.n_slots * slot_bytes, *s_p = s_q + P.n_q * q_bytes;
-  Shared &S = *reinterpret_cast<Shared *>(s_p + C::kPBytes);
+  Shared<RP> &S = *reinterpret_cast<Shared<RP> *>(s_p + P.n_p * C::kPBytes);
   const uint32_t t = threadIdx.x, lane = t & 31, warp = t >> 5, D = a.head_dim;
   const uint32_t o_cols = P.nmb * 2 * RP;   // output sums, then two score tiles
   const uint32_t cols = o_cols + 2 * C::kQRows;
@@ -261,20 +356,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (t == 0) {
     for (uint32_t i = 0; i < P.n_slots; ++i) mbar_init(&S.full[i], 1), mbar_init(&S.empty[i], 1);
-    for (uint32_t i = 0; i < kSegs; ++i) mbar_init(&S.seg_full[i], 1), mbar_init(&S.seg_empty[i], 7);
+    for (uint32_t i = 0; i < kSegs; ++i) mbar_init(&S.seg_full[i], 1), mbar_init(&S.seg_empty[i], 3 + C::kWarps);
     for (uint32_t i = 0; i < 2; ++i) {
       mbar_init(&S.q_full[i], 1);
       mbar_init(&S.q_empty[i], 1);
       mbar_init(&S.s_full[i], 1);
-      mbar_init(&S.s_empty[i], 4);
+      mbar_init(&S.s_empty[i], C::kWarps);
+      mbar_init(&S.p_full[i], C::kWarps);
+      mbar_init(&S.pv_done[i], 1);
     }
-    mbar_init(&S.p_full, 4);
-    mbar_init(&S.pv_done, 1);
-    mbar_init(&S.o_free, 4);
-    mbar_init(&S.group, 4);
+    mbar_init(&S.o_free, C::kWarps);
     mbar_init(&S.drain, 1);
     S.start_n = 0;
-    S.over[0] = S.over[1] = S.over[2] = S.bad = 0;
+    S.bad = 0;
     fence_mbar_init();
     prefetch_tmap(&map_k);
     prefetch_tmap(&map_v);
@@ -288,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t per = (a.batch + kThreads - 1) / kThreads, b0 = min(a.batch, t * per), b1 = min(a.batch, b0 + per);
     auto weight = [&](uint32_t b) {
       const PagedItem it = paged_item(a, b);
-      return (uint64_t)tiles_of(it) * a.n_kv * ((it.cnt * P.G + RP - 1) / RP);
+      return (uint64_t)tiles_of(it) * a.n_kv * ((it.cnt * P.G + RP - 1) / RP);   // (RP: a power of two)
     };
     uint64_t own = 0;
     for (uint32_t b = b0; b < b1; ++b) own += weight(b);
@@ -308,8 +402,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       total += S.scan[w];
     }
     // (no more shares than tiles, so that the parts of a segment are in neighbouring blocks)
-    const uint64_t shares = min((uint64_t)gridDim.x, total), c = blockIdx.x;
-    const uint64_t from = c < shares ? total * c / shares : total, to = c < shares ? total * (c + 1) / shares : total;
+    const uint32_t shares = (uint32_t)min((uint64_t)gridDim.x, total), c = blockIdx.x;
+    const uint64_t from = c < shares ? mul_div(total, c, shares) : total;
+    const uint64_t to = c < shares ? mul_div(total, c + 1, shares) : total;
     if (from < to && before <= from && from < before + own) {   // (one thread, or none)
       uint64_t off = from - before;
       uint32_t b = b0;
@@ -322,6 +417,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       S.start_off = off;
       S.start_n = to - from;
     }
+    if (t == 0) {
+      S.total = total;
+      S.shares = shares;
+      S.end = to;
+    }
     __syncthreads();
   }
   const uint32_t tmem = S.tmem;
@@ -333,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t issued = 0;
     bool ok = true;
     for (uint32_t s = 0; ok; ++s) {
-      if (!mbar_wait_warp(&S.seg_full[s % kSegs], (s / kSegs) & 1, err)) break;
+      if (!wait_chain(&S.seg_full[s % kSegs], (s / kSegs) & 1, err)) break;
       const Segment sg = S.seg[s % kSegs];
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.seg_empty[s % kSegs]);
@@ -346,20 +446,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (uint32_t e = 0; e < 2 * sg.nt; ++e) {
         const bool is_v = e + 1 == 2 * sg.nt || (e && !(e & 1));
         const uint32_t j = e + 1 == 2 * sg.nt ? sg.nt - 1 : is_v ? e / 2 - 1 : (e + 1) / 2, tile = sg.tile0 + j;
-        uint32_t phys = is_v ? vl.at(a, sg.b, tile / 2, lane) : kl.at(a, sg.b, tile / 2, lane);
+        BlockList &bl = is_v ? vl : kl;
+        bl.look(a, sg.b, tile / 2, lane);
+        uint32_t phys = bl.at(tile / 2);
         if (phys >= a.n_blocks) phys = 0;   // (its keys are masked)
-        ok = mbar_wait_warp(&S.empty[ring.slot], ring.phase ^ 1, err);
-        if (!ok) break;
-        if (lane == 0) {
-          uint64_t *bar = &S.full[ring.slot];
-          uint8_t *dst = s_slot + ring.slot * slot_bytes;
-          mbar_arrive_expect_tx(bar, slot_bytes);
-          const int y = (int)((phys * a.n_kv + sg.kh) * 256u + (tile & 1) * kTile);
-          for (uint32_t x = 0; x < P.nbox; ++x)
-            tma_load_2d_hint(dst + x * kBox, is_v ? &map_v : &map_k, bar, (int)(x * (F8 ? 128 : 64)), y, policy);
+        const int y = (int)((phys * a.n_kv + sg.kh) * 256u + (tile & 1) * kTile);
+        for (uint32_t m = 0; m < P.nmb; ++m) {
+          ok = mbar_wait_sleep(&S.empty[ring.slot], ring.phase ^ 1, err);
+          if (!ok) break;
+          if (lane == 0) {
+            uint64_t *bar = &S.full[ring.slot];
+            uint8_t *dst = s_slot + ring.slot * slot_bytes;
+            mbar_arrive_expect_tx(bar, slot_bytes);
+            for (uint32_t x = 0; x < P.ubox; ++x)   // (columns behind the row are filled with zeros)
+              tma_load_2d_hint(dst + x * kBox, is_v ? &map_v : &map_k, bar,
+                               (int)((m * P.ubox + x) * (F8 ? 128 : 64)), y, policy);
+          }
+          ++issued;
+          ring.next(P.n_slots);
         }
-        ++issued;
-        ring.next(P.n_slots);
+        if (!ok) break;
       }
     }
     // every load of this block lands before it can end (bounded)
@@ -372,94 +478,98 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
-    // ---------------- MMA
-    if (lane == 0) {
-      constexpr uint32_t kFmt = F8 ? (1u << 4) : (1u << 4) | (1u << 7) | (1u << 10);
-      constexpr uint32_t id_s = kFmt | ((C::kQRows >> 3) << 17) | ((128u >> 4) << 24);
-      constexpr uint32_t id_o = kFmt | ((2u * RP >> 3) << 17) | ((128u >> 4) << 24) | kIdescMajorA_MN | kIdescMajorB_MN;
-      const uint32_t slot0 = smem_u32(s_slot), q0 = smem_u32(s_q), p0 = smem_u32(s_p);
-      const uint32_t t_o = tmem, t_s = tmem + o_cols;
-      Ring ring{0, 0};
-      uint32_t sc = 0, pv = 0;   // score tiles issued, output products issued
-      bool ok = true;
-      uint32_t qb = 0;
-      auto scores = [&]() {
-        const uint32_t sb = sc & 1;
-        if (!mbar_wait(&S.s_empty[sb], ((sc >> 1) & 1) ^ 1, err) || !mbar_wait(&S.full[ring.slot], ring.phase, err))
-          return false;
+    // ---------------- MMA (the whole warp runs this; one thread issues)
+    constexpr uint32_t kFmt = F8 ? (1u << 4) : (1u << 4) | (1u << 7) | (1u << 10);
+    constexpr uint32_t id_s = kFmt | ((C::kQRows >> 3) << 17) | ((128u >> 4) << 24);
+    constexpr uint32_t id_o = kFmt | ((2u * RP >> 3) << 17) | ((128u >> 4) << 24) | kIdescMajorA_MN | kIdescMajorB_MN;
+    const uint32_t slot0 = uniform(desc_lo(smem_u32(s_slot))), unit = uniform(slot_bytes >> 4);
+    const uint32_t q0 = uniform(desc_lo(smem_u32(s_q)) | desc_lbo(16)), p0 = uniform(desc_lo(smem_u32(s_p)) | desc_lbo(128));
+    const uint32_t t_o = uniform(tmem), t_s = uniform(tmem + o_cols);
+    // (128 dims: one column of 8-bit codes, two of bf16; a lone one is read twice: half of the lanes
+    // is then not used)
+    const uint32_t v_lbo = uniform(P.ubox == 2 ? desc_lbo(kBox) : 0u);
+    Ring ring{0, 0};
+    uint32_t sc = 0, pv = 0, qb = 0;   // score tiles issued, output products issued
+    bool ok = true;
+    auto scores = [&]() {
+      const uint32_t sb = sc & 1, d = t_s + sb * C::kQRows;
+      if (!wait_chain(&S.s_empty[sb], ((sc >> 1) & 1) ^ 1, err)) return false;
+      for (uint32_t m = 0; m < P.nmb; ++m) {
+        if (!wait_chain(&S.full[ring.slot], ring.phase, err)) return false;
         tc_fence_after();
-        for (uint32_t x = 0; x < P.nbox; ++x) {
-          const uint32_t ka = slot0 + ring.slot * slot_bytes + x * kBox, qa = q0 + qb * q_bytes + x * C::kQRows * 128u;
+        for (uint32_t x = 0; x < P.ubox && m * P.ubox + x < P.nbox; ++x) {
+          const uint32_t ka = (slot0 | desc_lbo(16)) + ring.slot * unit + x * (kBox >> 4);
+          const uint32_t qa = q0 + (qb * q_bytes >> 4) + (m * P.ubox + x) * C::kQRows * 8u;
 #pragma unroll
           for (uint32_t k = 0; k < 4; ++k) {
-            const uint64_t ad = sdesc_sw128(ka + 32 * k), bd = sdesc_sw128(qa + 32 * k);
+            const uint64_t ad = desc_at(ka + 2 * k, kDescHiK), bd = desc_at(qa + 2 * k, kDescHiK);
             if (F8)
-              mma_e4m3(t_s + sb * C::kQRows, ad, bd, id_s, x | k);
+              mma_e4m3_elect(d, ad, bd, id_s, m | x | k);
             else
-              mma_bf16(t_s + sb * C::kQRows, ad, bd, id_s, x | k);
+              mma_bf16_elect(d, ad, bd, id_s, m | x | k);
           }
         }
-        mma_commit(&S.empty[ring.slot]);
-        mma_commit(&S.s_full[sb]);
+        mma_commit_elect(&S.empty[ring.slot]);
         ring.next(P.n_slots);
-        ++sc;
-        return true;
-      };
-      for (uint32_t s = 0; ok; ++s) {
-        if (!(ok = mbar_wait(&S.seg_full[s % kSegs], (s / kSegs) & 1, err))) break;
-        const uint32_t nt = S.seg[s % kSegs].nt;
-        mbar_arrive(&S.seg_empty[s % kSegs]);
-        if (nt == 0) break;
-        qb = s % P.n_q;
-        if (!(ok = mbar_wait(&S.q_full[qb], (s / P.n_q) & 1, err))) break;
-        if (!(ok = scores())) break;
-        if (nt == 1) mma_commit(&S.q_empty[qb]);
-        for (uint32_t j = 0; j < nt; ++j) {
-          if (j + 1 < nt) {
-            if (!(ok = scores())) break;
-            if (j + 2 == nt) mma_commit(&S.q_empty[qb]);
-          }
-          if (!(ok = mbar_wait(&S.full[ring.slot], ring.phase, err))) break;
-          if (j == 0 && s && !(ok = mbar_wait(&S.o_free, (s - 1) & 1, err))) break;
-          if (!(ok = mbar_wait(&S.p_full, pv & 1, err))) break;
-          tc_fence_after();
-          for (uint32_t m = 0; m < P.nmb; ++m) {
-            // 128 dims: one column of 8-bit codes, two of bf16 (a lone one is read twice: the
-            // second half of the lanes is not used)
-            const uint32_t x0 = F8 ? m : 2 * m, va = slot0 + ring.slot * slot_bytes + x0 * kBox;
-            const uint32_t lbo = !F8 && x0 + 1 < P.nbox ? kBox : 0u;
-#pragma unroll
-            for (uint32_t k = 0; k < (F8 ? 4u : 8u); ++k) {
-              const uint64_t ad = sdesc_sw128_mn(va + k * (F8 ? 4096u : 2048u), lbo, 1024);
-              const uint64_t bd = sdesc_plain_mn(p0 + k * (F8 ? 512u : 256u), 128, 2048);
-              if (F8)
-                mma_e4m3(t_o + m * 2 * RP, ad, bd, id_o, j | k);
-              else
-                mma_bf16(t_o + m * 2 * RP, ad, bd, id_o, j | k);
-            }
-          }
-          mma_commit(&S.empty[ring.slot]);
-          mma_commit(&S.pv_done);
-          ring.next(P.n_slots);
-          ++pv;
-        }
       }
-      if (!ok) {   // let the products in flight end (bounded)
-        mma_commit(&S.drain);
-        const uint64_t t0 = global_ns();
-        while (!mbar_try_wait(&S.drain, 0) && global_ns() - t0 < kWaitLimitNs) {
+      mma_commit_elect(&S.s_full[sb]);
+      ++sc;
+      return true;
+    };
+    for (uint32_t s = 0; ok; ++s) {
+      if (!(ok = wait_chain(&S.seg_full[s % kSegs], (s / kSegs) & 1, err))) break;
+      const uint32_t nt = uniform(S.seg[s % kSegs].nt);
+      warps_arrive(&S.seg_empty[s % kSegs], lane);
+      if (nt == 0) break;
+      qb = P.n_q == 2 ? s & 1 : 0u;
+      if (!(ok = wait_chain(&S.q_full[qb], (P.n_q == 2 ? s >> 1 : s) & 1, err))) break;
+      if (!(ok = scores())) break;
+      if (nt == 1) mma_commit_elect(&S.q_empty[qb]);
+      for (uint32_t j = 0; ok && j < nt; ++j) {
+        if (j + 1 < nt) {
+          if (!(ok = scores())) break;
+          if (j + 2 == nt) mma_commit_elect(&S.q_empty[qb]);
         }
+        if (j == 0 && s && !(ok = wait_chain(&S.o_free, (s - 1) & 1, err))) break;
+        const uint32_t pb = P.n_p == 2 ? pv & 1 : 0u, use = P.n_p == 2 ? pv >> 1 : pv;
+        if (!(ok = wait_chain(&S.p_full[pb], use & 1, err))) break;
+        for (uint32_t m = 0; m < P.nmb; ++m) {
+          if (!(ok = wait_chain(&S.full[ring.slot], ring.phase, err))) break;
+          tc_fence_after();
+          const uint32_t va = (slot0 | v_lbo) + ring.slot * unit, pa = p0 + (pb * C::kPBytes >> 4);
+#pragma unroll
+          for (uint32_t k = 0; k < (F8 ? 4u : 8u); ++k) {
+            const uint64_t ad = desc_at(va + k * ((F8 ? 4096u : 2048u) >> 4), kDescHiK);
+            const uint64_t bd = desc_at(pa + k * ((F8 ? 512u : 256u) >> 4), desc_hi_plain(2048));
+            if (F8)
+              mma_e4m3_elect(t_o + m * 2 * RP, ad, bd, id_o, j | k);
+            else
+              mma_bf16_elect(t_o + m * 2 * RP, ad, bd, id_o, j | k);
+          }
+          mma_commit_elect(&S.empty[ring.slot]);
+          ring.next(P.n_slots);
+        }
+        if (!ok) break;
+        mma_commit_elect(&S.pv_done[pb]);
+        ++pv;
+      }
+    }
+    if (!ok) {   // let the products in flight end (bounded)
+      mma_commit_elect(&S.drain);
+      const uint64_t t0 = global_ns();
+      while (!mbar_try_wait(&S.drain, 0) && global_ns() - t0 < kWaitLimitNs) {
       }
     }
     __syncwarp();
   } else if (warp == 2) {
     // ---------------- the segments: sequences 32 at a time, a lane each
-    uint32_t b = S.start_b, base = 0xffffffffu, s = 0;
+    uint32_t b = S.start_b, base = b, s = 0;
     uint64_t off = S.start_off, left = S.start_n;
     PagedItem mine = {};
+    if (left && b + lane < a.batch) mine = paged_item(a, b + lane);
     bool ok = true;
     while (left && b < a.batch) {
-      if (base == 0xffffffffu || b - base >= 32) {
+      if (b - base >= 32) {
         base = b;
         mine = PagedItem{};
         if (b + lane < a.batch) mine = paged_item(a, b + lane);
@@ -471,35 +581,47 @@ __global__ void __launch_bounds__(kThreads, 1)
       it.pos0 = __shfl_sync(0xffffffffu, mine.pos0, src);
       it.lo = __shfl_sync(0xffffffffu, mine.lo, src);
       it.hi = __shfl_sync(0xffffffffu, mine.hi, src);
-      const uint32_t tiles = tiles_of(it), groups = (it.cnt * P.G + RP - 1) / RP, items = a.n_kv * groups;
+      const uint32_t tiles = tiles_of(it), groups = (it.cnt * P.G + RP - 1) / RP;
       if (tiles) {
-        uint32_t i = (uint32_t)(off / tiles), t0 = (uint32_t)(off % tiles);
-        for (; i < items && left; ++i, t0 = 0) {
+        uint32_t kh = 0, rg = 0, t0 = 0;
+        if (off) {
+          const uint32_t i = (uint32_t)mul_div(off, 1, tiles);
+          t0 = (uint32_t)(off - (uint64_t)i * tiles);
+          kh = i / groups;
+          rg = i % groups;
+        }
+        for (; kh < a.n_kv && left; t0 = 0) {
           const uint32_t nt = (uint32_t)min((uint64_t)(tiles - t0), left);
-          if (!(ok = mbar_wait_warp(&S.seg_empty[s % kSegs], ((s / kSegs) & 1) ^ 1, err))) break;
+          if (!(ok = mbar_wait_sleep(&S.seg_empty[s % kSegs], ((s / kSegs) & 1) ^ 1, err))) break;
           if (lane == 0) {
             Segment &sg = S.seg[s % kSegs];
             sg.b = b;
-            sg.kh = i / groups;
-            sg.r0 = (i % groups) * RP;
+            sg.kh = kh;
+            sg.r0 = rg * RP;
             sg.nr = min((uint32_t)RP, it.cnt * P.G - sg.r0);
             sg.first = it.first;
             sg.pos0 = it.pos0;
             sg.tile0 = it.lo / kTile + t0;
             sg.nt = nt;
-            sg.whole = (t0 == 0 ? 1u : 0u) | (t0 + nt == tiles ? 2u : 0u);
+            const uint32_t rest = tiles - t0 - nt;   // (its other tiles follow the block's share)
+            sg.whole = (t0 == 0 ? 1u : 0u) | (rest == 0 ? 2u : 0u);
+            sg.blocks = rest ? last_share(S.end + rest, S.shares, S.total) - blockIdx.x : 0u;
             mbar_arrive(&S.seg_full[s % kSegs]);
           }
           __syncwarp();
           left -= nt;
           ++s;
+          if (++rg == groups) {
+            rg = 0;
+            ++kh;
+          }
         }
         if (!ok) break;
       }
       off = 0;
       ++b;
     }
-    if (ok && mbar_wait_warp(&S.seg_empty[s % kSegs], ((s / kSegs) & 1) ^ 1, err) && lane == 0) {
+    if (ok && mbar_wait_sleep(&S.seg_empty[s % kSegs], ((s / kSegs) & 1) ^ 1, err) && lane == 0) {
       S.seg[s % kSegs].nt = 0;
       mbar_arrive(&S.seg_full[s % kSegs]);
     }
@@ -508,22 +630,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------- queries of a segment, as the second operand of the scores
     const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q);
     for (uint32_t s = 0;; ++s) {
-      if (!mbar_wait_warp(&S.seg_full[s % kSegs], (s / kSegs) & 1, err)) break;
+      if (!wait_chain(&S.seg_full[s % kSegs], (s / kSegs) & 1, err)) break;
       const Segment sg = S.seg[s % kSegs];
-      const uint32_t qb = s % P.n_q;
+      const uint32_t qb = P.n_q == 2 ? s & 1 : 0u;
       if (sg.nt == 0) {
         __syncwarp();
         if (lane == 0) mbar_arrive(&S.seg_empty[s % kSegs]);
         break;
       }
-      if (!mbar_wait_warp(&S.q_empty[qb], ((s / P.n_q) & 1) ^ 1, err)) break;
+      if (!mbar_wait_sleep(&S.q_empty[qb], ((P.n_q == 2 ? s >> 1 : s) & 1) ^ 1, err)) break;
       uint8_t *dst = s_q + qb * q_bytes;
-      // 8 elements of a row (zeros outside)
-      auto load8 = [&](uint32_t r, uint32_t d) {
+      // 8 elements of a row, its token and query head given (zeros outside)
+      auto load8 = [&](uint32_t r, uint32_t tok, uint32_t g, uint32_t d) {
         uint4 v = make_uint4(0, 0, 0, 0);
         if (r < sg.nr && d < D) {
-          const uint32_t row = sg.r0 + r;
-          const __nv_bfloat16 *p = q + (sg.first + row / P.G) * a.q_stride + (size_t)(sg.kh * P.G + row % P.G) * D + d;
+          const __nv_bfloat16 *p = q + (sg.first + tok) * a.q_stride + (size_t)(sg.kh * P.G + g) * D + d;
           if (P.q_vec) {
             v = __ldg(reinterpret_cast<const uint4 *>(p));
           } else {
@@ -536,29 +657,51 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return v;
       };
+      const uint32_t tok_r0 = by_group(P, sg.r0), g_r0 = sg.r0 - tok_r0 * P.G;
+      // a lane's rows are `step` apart
+      auto advance = [&](uint32_t &tok, uint32_t &g, uint32_t step) {
+        for (g += step; g >= P.G; g -= P.G) ++tok;
+      };
       auto place = [&](uint32_t r, uint32_t c) {   // 16-byte piece c of row r
         return dst + (c / 8) * C::kQRows * 128u + r * 128u + (((c & 7) ^ (r & 7)) << 4);
       };
       if constexpr (!F8) {
-        const uint32_t pieces = P.nbox * 8, n = C::kQRows * pieces;   // (a multiple of 128)
-        for (uint32_t i0 = lane; i0 < n; i0 += 128) {
-          uint4 v[4];
+        const uint32_t pieces = P.nbox * 8, rpp = 32 / pieces, sub = lane / pieces, c = lane % pieces;
+        uint32_t tok = tok_r0, g = g_r0;
+        advance(tok, g, sub);
+        if (sub < rpp) {
+          for (uint32_t r0 = sub; r0 < C::kQRows; r0 += 8 * rpp) {
+            uint4 v[8];
 #pragma unroll
-          for (int u = 0; u < 4; ++u) v[u] = load8((i0 + 32 * u) / pieces, (i0 + 32 * u) % pieces * 8);
+            for (int u = 0; u < 8; ++u) {
+              v[u] = load8(r0 + u * rpp, tok, g, 8 * c);
+              advance(tok, g, rpp);
+            }
 #pragma unroll
-          for (int u = 0; u < 4; ++u)
-            *reinterpret_cast<uint4 *>(place((i0 + 32 * u) / pieces, (i0 + 32 * u) % pieces)) = v[u];
+            for (int u = 0; u < 8; ++u)
+              if (r0 + u * rpp < C::kQRows) *reinterpret_cast<uint4 *>(place(r0 + u * rpp, c)) = v[u];
+          }
         }
       } else {
         // half a warp per row, 16 elements a lane: q 2^k = hi + lo / 16, k so that the largest
         // entry is in [128, 256)
         const uint32_t c = lane & 15;
         const float ks = __ldg(a.k_scale + sg.kh) * P.c2;
-#pragma unroll 4
-        for (uint32_t r = lane >> 4; r < RP; r += 2) {
-          uint32_t w[8];
-          *reinterpret_cast<uint4 *>(w) = load8(r, 16 * c);
-          *reinterpret_cast<uint4 *>(w + 4) = load8(r, 16 * c + 8);
+        uint32_t tok = tok_r0, g = g_r0;
+        advance(tok, g, lane >> 4);
+        for (uint32_t r1 = lane >> 4; r1 < RP; r1 += 8) {
+        uint4 in[4][2];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          in[u][0] = load8(r1 + 2 * u, tok, g, 16 * c);
+          in[u][1] = load8(r1 + 2 * u, tok, g, 16 * c + 8);
+          advance(tok, g, 2);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const uint32_t r = r1 + 2 * u;
+          const uint32_t w[8] = {in[u][0].x, in[u][0].y, in[u][0].z, in[u][0].w,
+                                 in[u][1].x, in[u][1].y, in[u][1].z, in[u][1].w};
           uint32_t top = 0;
 #pragma unroll
           for (int i = 0; i < 8; ++i) top = max(top, max(w[i] & 0x7fffu, w[i] >> 16 & 0x7fffu));
@@ -590,6 +733,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (c == 0) S.qs[s % kSegs][r] = down * ks;
         }
+        }
       }
       fence_proxy_async();
       __syncwarp();
@@ -599,215 +743,216 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    // ---------------- softmax and output: a thread per key, then per dim
-    const uint32_t quarter = warp & 3, me = quarter * 32 + lane;
+    // ---------------- softmax and output: a thread per key (then per dim) and kRows rows
+    constexpr int R = C::kRows;
+    const uint32_t quarter = warp & 3, me = quarter * 32 + lane, half = (warp - 4) / 4;
     const uint32_t t_lane = (quarter * 32) << 16, t_o = tmem + t_lane, t_s = tmem + o_cols + t_lane;
-    uint32_t sc = 0, pv = 0, ph = 0, tick = 0, base = 0;   // base: loads of the segments before
-    Part left[2] = {};
-    bool ok = true;
-    for (uint32_t s = 0; ok; ++s) {
-      if (!mbar_wait_warp(&S.seg_full[s % kSegs], (s / kSegs) & 1, err)) break;
+    // the group's rows in eights: this set's i-th eight start at row8(i); element r of its arrays is
+    // row row8(r / 8) + r % 8
+    constexpr int E = R / 8;
+    auto row8 = [&](uint32_t i) { return (C::kSets * i + half) * 8; };
+    constexpr uint32_t kGroup = C::kWarps * 32;
+    uint32_t sc = 0, pv = 0, base = 0;   // score tiles, weight tiles, loads of the segments before
+    Part part = {};
+    bool ok = true;   // (false: a wait has run out; no more are made, and the results are void)
+    // a row's score in units of log2 is x c2; that of a key that it does not see is -infinity
+    const float c2 = F8 ? 1.f : P.c2, unseen = c2 > 0.f ? -INFINITY : INFINITY;
+    auto p_buf = [&](uint32_t n) { return P.n_p == 2 ? n & 1 : 0u; };
+    auto p_use = [&](uint32_t n) { return P.n_p == 2 ? n >> 1 : n; };
+    // the output product n is done
+    auto pv_wait = [&](uint32_t n) { ok = ok && wait_chain(&S.pv_done[p_buf(n)], p_use(n) & 1, err); };
+    for (uint32_t s = 0;; ++s) {
+      ok = ok && wait_chain(&S.seg_full[s % kSegs], (s / kSegs) & 1, err);
+      if (group_any(!ok, kGroup)) break;
       const Segment sg = S.seg[s % kSegs];
       if (sg.nt == 0) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&S.seg_empty[s % kSegs]);
+        warps_arrive(&S.seg_empty[s % kSegs], lane);
         break;
       }
-      const uint32_t p_first = sg.pos0 + sg.r0 / P.G, p_last = sg.pos0 + (sg.r0 + sg.nr - 1) / P.G;
-      float l[RP];
+      const uint32_t tok_a = by_group(P, sg.r0);
+      const uint32_t p_first = sg.pos0 + tok_a, p_last = sg.pos0 + by_group(P, sg.r0 + sg.nr - 1);
+      if (half == 0 && me < RP) {
+        const uint32_t tok = by_group(P, sg.r0 + me);
+        S.row_out[me] = (sg.first + tok) * a.n_heads + sg.kh * P.G + sg.r0 + me - tok * P.G;
+      }
+      float l[R], nm[R];   // sums of this thread's keys, -references
 #pragma unroll
-      for (int r = 0; r < RP; ++r) l[r] = 0.f;
+      for (int r = 0; r < R; ++r) l[r] = 0.f;
       BlockList bl;
       bl.start();
-      for (uint32_t j = 0; j < sg.nt; ++j) {
+      for (uint32_t j = 0; j < sg.nt; ++j, ++pv, ++sc) {
         const uint32_t tile = sg.tile0 + j, key0 = tile * kTile, key = key0 + me, sb = sc & 1;
-        const bool held = bl.at(a, sg.b, tile / 2, lane) < a.n_blocks;
-        // ---- scores, in units of log2
-        if (!(ok = mbar_wait_warp(&S.s_full[sb], (sc >> 1) & 1, err))) break;
+        bl.look(a, sg.b, tile / 2, lane);
+        ok = ok && wait_chain(&S.s_full[sb], (sc >> 1) & 1, err);
         tc_fence_after();
-        float x[RP];
-        {
-          uint32_t v[RP];
-          if constexpr (RP == 64) {
-            uint32_t(&v0)[32] = *reinterpret_cast<uint32_t(*)[32]>(v);
-            uint32_t(&v1)[32] = *reinterpret_cast<uint32_t(*)[32]>(v + 32);
-            tmem_ld(t_s + sb * C::kQRows, v0);
-            tmem_ld(t_s + sb * C::kQRows + 32, v1);
-          } else {
-            tmem_ld(t_s + sb * C::kQRows, v);
-          }
+        const bool held = bl.at(tile / 2) < a.n_blocks;
+        const bool plain = held && key0 + kTile - 1 <= p_first && (!a.window || p_last - key0 < a.window);
+        // (eights behind the last row are left out: nothing reads their columns)
+        float x[R];   // scores
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          uint32_t v[8], w[8];
+          if (e && row8(e) >= sg.nr) break;
+          tmem_ld8(t_s + sb * C::kQRows + row8(e), v);
+          if (F8) tmem_ld8(t_s + sb * C::kQRows + RP + row8(e), w);
           tmem_ld_wait();
 #pragma unroll
-          for (int r = 0; r < RP; ++r) x[r] = __uint_as_float(v[r]);
-          if constexpr (F8) {
-            if constexpr (RP == 64) {
-              uint32_t(&v0)[32] = *reinterpret_cast<uint32_t(*)[32]>(v);
-              uint32_t(&v1)[32] = *reinterpret_cast<uint32_t(*)[32]>(v + 32);
-              tmem_ld(t_s + sb * C::kQRows + RP, v0);
-              tmem_ld(t_s + sb * C::kQRows + RP + 32, v1);
-            } else {
-              tmem_ld(t_s + sb * C::kQRows + RP, v);
+          for (int i = 0; i < 8; i += 2) {
+            float2 u = make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+            if (F8) {   // (in units of log2)
+              u = fma2(make_float2(__uint_as_float(w[i]), __uint_as_float(w[i + 1])), make_float2(0.0625f, 0.0625f), u);
+              u = mul2(u, *reinterpret_cast<const float2 *>(&S.qs[s % kSegs][row8(e) + i]));
             }
-            tmem_ld_wait();
-            const float *qs = S.qs[s % kSegs];
-#pragma unroll
-            for (int r = 0; r < RP; ++r) x[r] = fmaf(__uint_as_float(v[r]), 0.0625f, x[r]) * qs[r];
-          } else {
-#pragma unroll
-            for (int r = 0; r < RP; ++r) x[r] *= P.c2;
+            x[8 * e + i] = u.x;
+            x[8 * e + i + 1] = u.y;
           }
         }
         tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&S.s_empty[sb]);
-        ++sc;
-        // ---- unseen keys
-        const bool plain = held && key0 + kTile - 1 <= p_first && (!a.window || p_last - key0 < a.window);
-        bool all = true, any = true;
-        if (!plain) {
-          all = held && key <= p_first && (!a.window || p_last - key < a.window);
-          any = held && key <= p_last && !(a.window && key < p_first && p_first - key >= a.window);
-          uint32_t tok = sg.r0 / P.G, g = sg.r0 % P.G;
+        warps_arrive(&S.s_empty[sb], lane);
+        if (!plain) {   // unseen keys
 #pragma unroll
-          for (int r = 0; r < RP; ++r) {
-            const uint32_t p = sg.pos0 + tok;
-            if (!held || key > p || (a.window && p - key >= a.window)) x[r] = -INFINITY;
-            if (++g == P.G) {
-              g = 0;
-              ++tok;
+          for (int e = 0; e < E; ++e) {
+            if (e && row8(e) >= sg.nr) break;
+            const uint32_t tok = by_group(P, sg.r0 + row8(e));
+            uint32_t p = sg.pos0 + tok, g = sg.r0 + row8(e) - tok * P.G;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              if (!held || key > p || (a.window && p - key >= a.window)) x[8 * e + i] = unseen;
+              if (++g == P.G) {
+                g = 0;
+                ++p;
+              }
             }
           }
         }
-        // ---- the reference moves where a weight would be too large
-        bool mine = j == 0;
+        bool over = j == 0;   // a weight passes the margin
         if (j) {
+          float top = -INFINITY;
 #pragma unroll
-          for (int r = 0; r < RP; ++r) mine |= x[r] + S.negm[r] > C::kTop;
-        }
-        if (__any_sync(0xffffffffu, mine) && lane == 0) S.over[tick] = 1;
-        if (!(ok = warps_sync(&S.group, ph, lane, err))) break;
-        const bool over = *(volatile uint32_t *)&S.over[tick] != 0;
-        // (the place of the tile after next: last read before this barrier, set behind the next one)
-        tick = tick == 2 ? 0 : tick + 1;
-        if (me == 0) S.over[tick == 2 ? 0 : tick + 1] = 0;
-        if (j) {   // the products before read the sums' old scale and P
-          if (!(ok = mbar_wait_warp(&S.pv_done, pv & 1, err))) break;
-          ++pv;
-        }
-        if (over) {
+          for (int e = 0; e < E; ++e) {
+            if (e && row8(e) >= sg.nr) break;
 #pragma unroll
-          for (int r = 0; r < RP; ++r) {
-            const float m = warp_max_nan(x[r]);
-            if (lane == (r & 31)) S.wmax[quarter][r] = m;
+            for (int r = 8 * e; r < 8 * e + 8; r += 2) {
+              const float2 y = fma2(make_float2(x[r], x[r + 1]), make_float2(c2, c2), make_float2(nm[r], nm[r + 1]));
+              top = fmaxf(top, fmaxf(y.x, y.y));
+            }
           }
-          if (!(ok = warps_sync(&S.group, ph, lane, err))) break;
-          if (me < RP) {
+          over = group_any(top > C::kTop, kGroup);
+        }
+        if (over) {   // new references, sums so far brought to them
+          {
+            float m[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) m[r] = x[r] * c2;
+            const float top = warp_reduce_rows(m, lane, [](float u, float v) { return max_nan(u, v); });
+            const uint32_t r = lane / (32 / R);
+            if (lane % (32 / R) == 0) S.wmax[quarter][row8(r / 8) + r % 8] = top;
+          }
+          group_bar(kGroup);
+          if (half == 0 && me < RP) {
             float m = S.wmax[0][me];
 #pragma unroll
-            for (int w = 1; w < 4; ++w) {
-              const float y = S.wmax[w][me];
-              m = y > m || y != y ? y : m;
-            }
-            const float was = j ? S.negm[me] : kNoRef, now = m == -INFINITY ? was : fminf(was, C::kOff - m);
-            const float now_ = m != m ? m : now;   // (fminf drops a NaN)
-            S.fac[me] = ex2_approx(now_ - was);
-            S.negm[me] = now_;
+            for (int i = 1; i < 4; ++i) m = max_nan(m, S.wmax[i][me]);
+            const float was = j ? S.negm[me] : kNoRef, least = m == -INFINITY ? was : fminf(was, C::kOff - m);
+            const float now = m != m ? m : least;   // (fminf drops a NaN)
+            S.fac[me] = ex2_approx(now - was);
+            S.negm[me] = now;
           }
-          if (!(ok = warps_sync(&S.group, ph, lane, err))) break;
+          group_bar(kGroup);
 #pragma unroll
-          for (int r = 0; r < RP; ++r) l[r] *= S.fac[r];
+          for (int r = 0; r < R; ++r) nm[r] = S.negm[row8(r / 8) + r % 8];
           if (j) {
-            tc_fence_after();
-            for (uint32_t c = 0; c < o_cols; c += 8) {
-              uint32_t v[8];
-              tmem_ld8(t_o + c, v);
-              tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 8; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * S.fac[(c + i) % RP]);
-              tmem_st8(t_o + c, v);
-            }
+            for (int r = 0; r < R; ++r) l[r] *= S.fac[row8(r / 8) + r % 8];
+            pv_wait(pv - 1);
+            tc_fence_after();
+#pragma unroll 1
+            for (uint32_t c = 0; c < o_cols; c += RP)   // (hi and lo of each 128 dims)
+#pragma unroll 1
+              for (uint32_t e = 0; e < (uint32_t)E; ++e) {
+                uint32_t v[8];
+                tmem_ld8(t_o + c + row8(e), v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * S.fac[row8(e) + i]);
+                tmem_st8(t_o + c + row8(e), v);
+              }
             tmem_st_wait();
           }
         }
         // ---- weights, in two parts each
-        uint8_t *dst = s_p + (me / 8) * 128 + (me % 8) * 16;
-        if constexpr (!F8) {
+        if (pv >= P.n_p) pv_wait(pv - P.n_p);   // (the product before has read this place)
+        uint8_t *dst = s_p + p_buf(pv) * C::kPBytes + (me / 8) * 128 + (me % 8) * 16;
 #pragma unroll
-          for (int r0 = 0; r0 < RP; r0 += 8) {
-            uint32_t hi[4], lo[4];
+        for (int e = 0; e < E; ++e) {
+          if (e && row8(e) >= sg.nr) break;
+          uint32_t hi[4], lo[4];   // (8 bits: 16 of them, in two words each)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int r = r0 + 2 * i;
-              const float w0 = ex2_approx(x[r] + S.negm[r]), w1 = ex2_approx(x[r + 1] + S.negm[r + 1]);
-              l[r] += w0;
-              l[r + 1] += w1;
-              hi[i] = pack_bf16(w0, w1);
-              lo[i] = pack_bf16(w0 - __uint_as_float(hi[i] << 16), w1 - __uint_as_float(hi[i] & 0xffff0000u));
+          for (int i = 0; i < 4; ++i) {
+            const int r = 8 * e + 2 * i;
+            const float2 y = fma2(make_float2(x[r], x[r + 1]), make_float2(c2, c2), make_float2(nm[r], nm[r + 1]));
+            const float2 w = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+            const float2 sum = add2(make_float2(l[r], l[r + 1]), w);
+            l[r] = sum.x;
+            l[r + 1] = sum.y;
+            float2 h;
+            if (F8) {
+              hi[i] = pack_e4m3(w.x, w.y);
+              h = unpack_e4m3((uint16_t)hi[i]);
+            } else {   // (cut off rather than rounded)
+              const uint32_t b0 = __float_as_uint(w.x), b1 = __float_as_uint(w.y);
+              hi[i] = __byte_perm(b0, b1, 0x7632);
+              h = make_float2(__uint_as_float(b0 & 0xffff0000u), __uint_as_float(b1 & 0xffff0000u));
             }
-            *reinterpret_cast<uint4 *>(dst + r0 / 8 * 2048) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4 *>(dst + (RP + r0) / 8 * 2048) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            float2 rest = add2(w, make_float2(-h.x, -h.y));
+            if (F8) rest = mul2(rest, make_float2(16.f, 16.f));
+            lo[i] = F8 ? pack_e4m3(rest.x, rest.y) : pack_bf16(rest.x, rest.y);
           }
-        } else {
-          uint32_t hi[RP / 4], lo[RP / 4];
-#pragma unroll
-          for (int i = 0; i < RP / 4; ++i) {
-            float w[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int r = 4 * i + k;
-              w[k] = ex2_approx(x[r] + S.negm[r]);
-              l[r] += w[k];
-            }
-            const uint16_t h0 = pack_e4m3(w[0], w[1]), h1 = pack_e4m3(w[2], w[3]);
-            const float2 f0 = unpack_e4m3(h0), f1 = unpack_e4m3(h1);
-            hi[i] = h0 | (uint32_t)h1 << 16;
-            lo[i] = pack_e4m3((w[0] - f0.x) * 16.f, (w[1] - f0.y) * 16.f) |
-                    (uint32_t)pack_e4m3((w[2] - f1.x) * 16.f, (w[3] - f1.y) * 16.f) << 16;
-          }
-          if constexpr (RP == 8) {
-            *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], lo[0], lo[1]);
+          if constexpr (!F8) {
+            *reinterpret_cast<uint4 *>(dst + row8(e) / 8 * 2048) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4 *>(dst + (RP + row8(e)) / 8 * 2048) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
           } else {
-#pragma unroll
-            for (int g = 0; g < RP / 16; ++g) {
-              *reinterpret_cast<uint4 *>(dst + g * 2048) = make_uint4(hi[4 * g], hi[4 * g + 1], hi[4 * g + 2], hi[4 * g + 3]);
-              *reinterpret_cast<uint4 *>(dst + (RP / 16 + g) * 2048) =
-                  make_uint4(lo[4 * g], lo[4 * g + 1], lo[4 * g + 2], lo[4 * g + 3]);
+            const uint2 h2 = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+            const uint2 l2 = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+            if constexpr (RP == 8) {
+              *reinterpret_cast<uint4 *>(dst) = make_uint4(h2.x, h2.y, l2.x, l2.y);
+            } else {   // (16 rows to 16 bytes)
+              *reinterpret_cast<uint2 *>(dst + row8(e) / 16 * 2048 + row8(e) % 16) = h2;
+              *reinterpret_cast<uint2 *>(dst + (RP + row8(e)) / 16 * 2048 + row8(e) % 16) = l2;
             }
           }
         }
-        if (!plain) {
+        if (!plain && half == 0) {
+          const bool all = held && key <= p_first && (!a.window || p_last - key < a.window);
+          const bool any = held && key <= p_last && !(a.window && key < p_first && p_first - key >= a.window);
           // (the values are there: a slot is refilled only behind the products that this arrival starts)
-          const uint32_t k = base + place_v(j, sg.nt), slot = k % P.n_slots;
-          if (!(ok = mbar_wait_warp(&S.full[slot], (k / P.n_slots) & 1, err))) break;
-          if (!all && clean_row<F8>(smem_u32(s_slot + slot * slot_bytes) + me * 128, P.nbox, !any)) S.bad = 1;
+          for (uint32_t m = 0; m < P.nmb; ++m) {
+            const uint32_t k = (base + place_v(j, sg.nt)) * P.nmb + m, slot = k % P.n_slots;
+            ok = ok && wait_chain(&S.full[slot], (k / P.n_slots) & 1, err);
+            if (!all && clean_row<F8>(smem_u32(s_slot + slot * slot_bytes) + me * 128, P.ubox, !any)) S.bad = 1;
+            __syncwarp();
+          }
         }
         fence_proxy_async();
         tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&S.p_full);
+        warps_arrive(&S.p_full[p_buf(pv)], lane);
       }
-      if (!ok) break;
       base += 2 * sg.nt;
       // ---- the segment's end: sums over the keys, then the output, a thread per dim
-#pragma unroll
-      for (int r = 0; r < RP; ++r) {
-        const float sum = warp_sum(l[r]);
-        if (lane == (r & 31)) S.wmax[quarter][r] = sum;
+      {
+        const float sum = warp_reduce_rows(l, lane, [](float u, float v) { return u + v; });
+        const uint32_t r = lane / (32 / R);
+        if (lane % (32 / R) == 0) S.wmax[quarter][row8(r / 8) + r % 8] = sum;
       }
-      if (!(ok = mbar_wait_warp(&S.pv_done, pv & 1, err))) break;
-      ++pv;
-      tc_fence_after();
-      if (!(ok = warps_sync(&S.group, ph, lane, err))) break;
+      group_bar(kGroup);
       const bool whole = sg.whole == 3, bad = *(volatile uint32_t *)&S.bad != 0;
       const uint32_t side = sg.whole & 1;   // (a part: 0 began in an earlier block, 1 goes on in the next)
       float *sums = P.sums + ((size_t)blockIdx.x * 2 + side) * RP * D;
-      if (me < sg.nr) {
+      if (half == 0 && me < sg.nr) {
         const float sum = S.wmax[0][me] + S.wmax[1][me] + S.wmax[2][me] + S.wmax[3][me];
         if (whole) {
-          const uint32_t row = sg.r0 + me;
           if (a.lse)
-            a.lse[(size_t)(sg.first + row / P.G) * a.n_heads + sg.kh * P.G + row % P.G] =
-                sum == 0.f ? -INFINITY : (log2f(sum) - S.negm[me]) * 0.6931471805599453f;
+            a.lse[S.row_out[me]] = sum == 0.f ? -INFINITY : (log2f(sum) - S.negm[me]) * 0.6931471805599453f;
         } else {
           float *ml = P.sums + (size_t)gridDim.x * 2 * RP * D + (((size_t)blockIdx.x * 2 + side) * RP + me) * 2;
           ml[0] = -S.negm[me];
@@ -815,44 +960,54 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         S.fac[me] = sum == 0.f ? 0.f : (F8 ? __ldg(a.v_scale + sg.kh) : 1.f) / sum;
       }
-      if (!(ok = warps_sync(&S.group, ph, lane, err))) break;
+      pv_wait(pv - 1);
+      tc_fence_after();
+      group_bar(kGroup);
+#pragma unroll 1
       for (uint32_t m = 0; m < P.nmb; ++m) {
         const uint32_t d = m * 128 + me;
-#pragma unroll
-        for (int r0 = 0; r0 < RP; r0 += 8) {
-          uint32_t h[8], w[8];
-          tmem_ld8(t_o + m * 2 * RP + r0, h);
-          tmem_ld8(t_o + m * 2 * RP + RP + r0, w);
+#pragma unroll 1
+        for (uint32_t e = 0; e < (uint32_t)E && row8(e) < sg.nr; ++e) {
+          const uint32_t r0 = row8(e), nr = sg.nr - r0;
+          uint32_t hi[8], lo[8];
+          tmem_ld8(t_o + m * 2 * RP + r0, hi);
+          tmem_ld8(t_o + m * 2 * RP + RP + r0, lo);
           tmem_ld_wait();
+          float o[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint32_t r = r0 + i, row = sg.r0 + r;
-            if (r >= sg.nr || d >= D) break;
-            float o = F8 ? fmaf(__uint_as_float(w[i]), 0.0625f, __uint_as_float(h[i]))
-                         : __uint_as_float(h[i]) + __uint_as_float(w[i]);
-            if (bad) o += taken_out<F8>(a, sg, sg.pos0 + row / P.G, p_first, p_last, d);
-            if (whole)
-              static_cast<__nv_bfloat16 *>(a.out)[((size_t)(sg.first + row / P.G) * a.n_heads + sg.kh * P.G + row % P.G) * D + d] =
-                  __float2bfloat16_rn(o * S.fac[r]);
-            else
-              sums[(size_t)r * D + d] = o;
+          for (int i = 0; i < 8; ++i)
+            o[i] = F8 ? fmaf(__uint_as_float(lo[i]), 0.0625f, __uint_as_float(hi[i]))
+                      : __uint_as_float(hi[i]) + __uint_as_float(lo[i]);
+          if (bad && d < D)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (i < nr) o[i] += taken_out<F8>(a, sg, sg.pos0 + by_group(P, sg.r0 + r0 + i), p_first, p_last, d);
+          if (d < D) {
+            if (whole) {
+              __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + d;
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (i < nr) out[(size_t)S.row_out[r0 + i] * D] = __float2bfloat16_rn(o[i] * S.fac[r0 + i]);
+            } else {
+              float *out = sums + (size_t)r0 * D + d;
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (i < nr) out[(size_t)i * D] = o[i];
+            }
           }
           __syncwarp();
         }
       }
-      if (!whole) left[side] = Part{1u, sg.whole >> 1, sg.b, sg.kh, sg.r0, sg.nr, sg.first, 0u};
+      if (!whole && side) part = Part{sg.blocks, sg.kh, sg.r0, sg.nr, sg.first, {0u, 0u, 0u}};
       tc_fence_before();
-      if (!(ok = warps_sync(&S.group, ph, lane, err))) break;   // (the shared sums are free)
-      if (me == 0) S.bad = 0;
+      group_bar(kGroup);   // (the shared sums are free)
+      if (half == 0 && me == 0) S.bad = 0;
       if (lane == 0) {
         mbar_arrive(&S.o_free);
         mbar_arrive(&S.seg_empty[s % kSegs]);
       }
     }
-    if (me == 0) {
-      P.parts[blockIdx.x * 2] = left[0];
-      P.parts[blockIdx.x * 2 + 1] = left[1];
-    }
+    if (half == 0 && me == 0) P.parts[blockIdx.x] = part;
   }
   tc_fence_before();
   __syncthreads();
@@ -862,45 +1017,64 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the parts of what begins in block blockIdx.x and goes on: rows blockIdx.y, + gridDim.y, ..
-// each as the sum of its parts brought to the largest reference, in the order of the blocks.
+// Joins the parts of what begins in block blockIdx.x and goes on behind it: rows blockIdx.y, +
+// gridDim.y, .. each as the sum of its parts brought to the largest reference, in the order of the
+// blocks. Every warp works out the weights of the parts for itself, 32 at a time, a lane each; the first
+// parts are loaded before it is known how many there are.
+constexpr uint32_t kAhead = 8;
 template <int RP, bool F8>
 __global__ void __launch_bounds__(256) paged_join_tc_kernel(Params P, uint32_t blocks) {
+  const PagedArgs &a = P.a;
+  const uint32_t c0 = blockIdx.x, D = a.head_dim, d = threadIdx.x, lane = d & 31;
+  const float2 *ml = reinterpret_cast<const float2 *>(P.sums + (size_t)blocks * 2 * RP * D);
+  // piece i: block c0 + i, what goes on (i = 0) or what began before
+  auto at = [&](uint32_t i, uint32_t r) { return ((size_t)(c0 + i) * 2 + (i ? 0u : 1u)) * RP + r; };
+  auto there = [&](uint32_t i) { return c0 + i < blocks; };
   pdl_wait();
   pdl_trigger();
-  const PagedArgs &a = P.a;
-  const uint32_t c0 = blockIdx.x, D = a.head_dim;
-  const Part part = P.parts[2 * c0 + 1];
-  if (!part.valid) return;
-  uint32_t n = 1;
-  for (; c0 + n < blocks; ++n)
-    if (P.parts[2 * (c0 + n)].last) break;
-  if (c0 + n >= blocks) return;
-  const float *ml = P.sums + (size_t)blocks * 2 * RP * D;
-  // piece i: block c0 + i, its second half (i = 0) or its first
-  auto at = [&](uint32_t i, uint32_t r) { return ((size_t)(c0 + i) * 2 + (i ? 0u : 1u)) * RP + r; };
-  for (uint32_t r = blockIdx.y; r < part.nr; r += gridDim.y) {
-    float m = -kNoRef;
-    bool nan = false;
-    for (uint32_t i = threadIdx.x & 31; i <= n; i += 32) {
-      const float x = ml[at(i, r) * 2];
-      nan |= x != x;
-      m = fmaxf(m, x);
+  uint32_t r = blockIdx.y;
+  const Part part = P.parts[c0];
+  float2 mine = there(lane) ? ml[at(lane, r)] : make_float2(0.f, 0.f);
+  float v[kAhead];
+#pragma unroll
+  for (uint32_t u = 0; u < kAhead; ++u) v[u] = d < D && there(u) ? P.sums[at(u, r) * D + d] : 0.f;
+  const uint32_t n = part.blocks + 1;   // pieces
+  if (n == 1 || c0 + n > blocks) return;
+  while (r < part.nr) {
+    // the largest reference (a NaN if there is one)
+    float m = lane < n ? mine.x : -kNoRef;
+    for (uint32_t i = lane + 32; i < n; i += 32) m = max_nan(m, ml[at(i, r)].x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float l = 0.f, acc = 0.f;
+    for (uint32_t i0 = 0; i0 < n; i0 += 32) {
+      const float2 x = i0 == 0 ? mine : i0 + lane < n ? ml[at(i0 + lane, r)] : make_float2(0.f, 0.f);
+      const float w = i0 + lane >= n || x.x <= -kNoRef ? 0.f : ex2_approx(x.x - m);
+      if (w != 0.f) l = fmaf(x.y, w, l);   // (a lane without a part holds anything)
+      for (uint32_t i = i0; i < min(n, i0 + 32); i += kAhead) {
+        if (i) {
+#pragma unroll
+          for (uint32_t u = 0; u < kAhead; ++u) v[u] = d < D && i + u < n ? P.sums[at(i + u, r) * D + d] : 0.f;
+        }
+#pragma unroll
+        for (uint32_t u = 0; u < kAhead; ++u) {
+          const float f = __shfl_sync(0xffffffffu, w, (i - i0 + u) & 31);
+          if (i + u < n && f != 0.f) acc = fmaf(v[u], f, acc);
+        }
+      }
     }
-    m = __any_sync(0xffffffffu, nan) ? NAN : warp_max(m);
-    float l = 0.f, o = 0.f;
-    const uint32_t d = threadIdx.x;
-    for (uint32_t i = 0; i <= n; ++i) {
-      const size_t k = at(i, r);
-      const float w = ml[2 * k] <= -kNoRef ? 0.f : ex2_approx(ml[2 * k] - m);
-      l = fmaf(ml[2 * k + 1], w, l);
-      if (d < D && (w != 0.f)) o = fmaf(P.sums[k * D + d], w, o);
-    }
-    const uint32_t row = part.r0 + r;
-    const size_t out = (size_t)(part.first + row / P.G) * a.n_heads + part.kh * P.G + row % P.G;
+    l = warp_sum(l);
+    const uint32_t row = part.r0 + r, tok = by_group(P, row);
+    const uint32_t out = (part.first + tok) * a.n_heads + part.kh * P.G + row - tok * P.G;
     const float scale = l == 0.f ? 0.f : (F8 ? __ldg(a.v_scale + part.kh) : 1.f) / l;
-    if (d < D) static_cast<__nv_bfloat16 *>(a.out)[out * D + d] = __float2bfloat16_rn(o * scale);
+    if (d < D) static_cast<__nv_bfloat16 *>(a.out)[(size_t)out * D + d] = __float2bfloat16_rn(acc * scale);
     if (a.lse && d == 0) a.lse[out] = l == 0.f ? -INFINITY : (log2f(l) + m) * 0.6931471805599453f;
+    r += gridDim.y;
+    if (r < part.nr) {
+      mine = there(lane) ? ml[at(lane, r)] : make_float2(0.f, 0.f);
+#pragma unroll
+      for (uint32_t u = 0; u < kAhead; ++u) v[u] = d < D && there(u) ? P.sums[at(u, r) * D + d] : 0.f;
+    }
   }
 }
 
@@ -910,7 +1084,7 @@ uint32_t rows_of(const PagedArgs &a) {
   return r <= 8 ? 8 : r <= 16 ? 16 : r <= 32 ? 32 : 64;
 }
 
-// Blocks: one a SM, or one a tile where there can be no more tiles.
+// Blocks: one or two a SM (Cfg::kPerSm), or one a tile where there can be no more tiles.
 uint32_t blocks_of(const PagedArgs &a) {
   const uint32_t rp = rows_of(a), groups = (a.max_new * (a.n_heads / a.n_kv) + rp - 1) / rp;
   uint64_t tiles = 2ull * a.max_blocks;
@@ -918,7 +1092,7 @@ uint32_t blocks_of(const PagedArgs &a) {
     const uint64_t w = ((uint64_t)a.window + a.max_new) / kTile + 2;
     tiles = w < tiles ? w : tiles;
   }
-  const uint64_t most = tiles * a.batch * a.n_kv * groups, sms = (uint64_t)num_sms();
+  const uint64_t most = tiles * a.batch * a.n_kv * groups, sms = (uint64_t)num_sms() * (rp <= 16 ? 2 : 1);
   return (uint32_t)(most < sms ? most : sms);
 }
 
@@ -944,25 +1118,29 @@ cudaError_t launch_rp(const PagedArgs &a, cudaStream_t s) {
   P.nmb = (a.head_dim + 127) / 128;
   P.q_vec = aligned(16, {a.q}) && a.q_stride % 8 == 0;
   P.c2 = a.scale * 1.4426950408889634f;
-  const uint32_t blocks = blocks_of(a), slot = P.nbox * kBox, q = C::kQRows * P.nbox * 128u;
+  if (fabsf(P.c2) < 0x1p-126f) P.c2 = 0x1p-126f;   // (0 times the -infinity of an unseen key is a NaN)
+  P.ubox = F8 || P.nbox == 1 ? 1 : 2;
+  P.g_mul = P.G > 1 ? (uint32_t)((1ull << 32) / P.G) + 1u : 0u;
+  const uint32_t blocks = blocks_of(a), slot = P.ubox * kBox, q = C::kQRows * P.nbox * 128u;
   uint8_t *ws = static_cast<uint8_t *>(a.ws);
   P.err = reinterpret_cast<int *>(ws);
   P.parts = reinterpret_cast<Part *>(ws + 256);
-  P.sums = reinterpret_cast<float *>(ws + 256 + (size_t)num_sms() * 2 * sizeof(Part));
-  const uint32_t room = kSmemMost - kFixed - C::kPBytes;
-  P.n_q = (room - 2 * q) / slot >= 3 ? 2 : 1;
-  P.n_slots = (room - P.n_q * q) / slot;
+  P.sums = reinterpret_cast<float *>(ws + 256 + (size_t)blocks * sizeof(Part));
+  // two query and two weight tiles where four units fit beside them
+  const uint32_t room = kSmemSm / C::kPerSm - kSmemBlock - 1024 - (uint32_t)sizeof(Shared<RP>);
+  P.n_q = P.n_p = room >= 2 * (q + C::kPBytes) + 4 * slot ? 2 : 1;
+  P.n_slots = (room - P.n_q * (q + C::kPBytes)) / slot;
   if (P.n_slots > kMaxSlots) P.n_slots = kMaxSlots;
-  const size_t smem = 1024 + (size_t)P.n_slots * slot + P.n_q * q + C::kPBytes + sizeof(Shared);
+  const size_t smem = 1024 + (size_t)P.n_slots * slot + P.n_q * (q + C::kPBytes) + sizeof(Shared<RP>);
   static RaisedLimit smem_set;
   auto *k = paged_attn_tc_kernel<RP, F8>;
   e = ensure_smem(k, smem, smem_set);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(k, dim3(blocks), dim3(kThreads), smem, s, mk, mv, P);
+  e = launch_pdl(k, dim3(blocks), dim3(C::kThreads), smem, s, mk, mv, P);
   if (e != cudaSuccess) return e;
   note_launches(1);
   if (blocks > 1) {   // (a lone block holds every segment whole)
-    e = launch_pdl(paged_join_tc_kernel<RP, F8>, dim3(blocks, 8), dim3(256), 0, s, P, blocks);
+    e = launch_pdl(paged_join_tc_kernel<RP, F8>, dim3(blocks - 1, 8), dim3((a.head_dim + 31) / 32 * 32), 0, s, P, blocks);
     if (e != cudaSuccess) return e;
     note_launches(1);
   }
@@ -976,7 +1154,7 @@ bool paged_attn_tc_takes(const PagedArgs &a) {
 }
 
 size_t paged_attn_tc_ws_bytes(const PagedArgs &a) {
-  return (size_t)num_sms() * 2 * (sizeof(Part) + (size_t)rows_of(a) * (a.head_dim + 2) * 4);
+  return (size_t)blocks_of(a) * (sizeof(Part) + 2 * (size_t)rows_of(a) * (a.head_dim + 2) * 4);
 }
 
 cudaError_t launch_paged_attn_tc(const PagedArgs &a, cudaStream_t s) {
