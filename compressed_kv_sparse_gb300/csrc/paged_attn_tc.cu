@@ -24,7 +24,8 @@
 // does not hold whole is left as sums with their reference, and a second launch joins
 // the parts in order. Bound by HBM: every visible key and value is read once.
 //
-// Warps: 0 TMA, 1 MMA, 2 the block's list of segments, 3 queries, 4 .. 7 softmax and output.
+// Warps: 0 TMA, 1 MMA, 2 the block's list of segments, 3 queries, 4 .. 7 (4 .. 11)
+// softmax and output.
 // Every wait is bounded (tc.cuh).
 #include <cuda_fp8.h>
 
@@ -75,6 +76,9 @@ struct Cfg {
   // softmax warps: four, which take a quarter of the keys each, or two such sets with every other
   // eight rows each
   static constexpr uint32_t kSets = RP >= 32 ? 2 : 1, kWarps = 4 * kSets, kThreads = 128 + 32 * kWarps;
+  // What a segment costs beside its tiles, in tiles, for even shares: measured, one tile takes
+  // 1.6 us (bf16, D 128) and 0.8 us (8 bits).
+  static constexpr uint32_t kStart = RP <= 16 ? 1 : F8 ? 6 : 3;
   static constexpr int kRows = RP / kSets;
   // few rows: two blocks a SM, so that one computes while the other starts, ends or waits
   static constexpr uint32_t kPerSm = RP <= 16 ? 2 : 1;
@@ -377,12 +381,14 @@ __global__ void __launch_bounds__(Cfg<RP, F8>::kThreads, Cfg<RP, F8>::kPerSm)
   pdl_wait();
   pdl_trigger();
   const ErrWord err{P.err, *(volatile int *)P.err};
-  // ---- the block's share of the list of tiles: each thread counts some sequences'
+  // ---- the block's share of the list: kStart places for each segment, then its tiles; each thread
+  // counts some sequences'
   {
     const uint32_t per = (a.batch + kThreads - 1) / kThreads, b0 = min(a.batch, t * per), b1 = min(a.batch, b0 + per);
     auto weight = [&](uint32_t b) {
       const PagedItem it = paged_item(a, b);
-      return (uint64_t)tiles_of(it) * a.n_kv * ((it.cnt * P.G + RP - 1) / RP);   // (RP: a power of two)
+      const uint32_t tiles = tiles_of(it);
+      return (uint64_t)(tiles ? tiles + C::kStart : 0u) * a.n_kv * ((it.cnt * P.G + RP - 1) / RP);
     };
     uint64_t own = 0;
     for (uint32_t b = b0; b < b1; ++b) own += weight(b);
@@ -583,15 +589,19 @@ __global__ void __launch_bounds__(Cfg<RP, F8>::kThreads, Cfg<RP, F8>::kPerSm)
       it.hi = __shfl_sync(0xffffffffu, mine.hi, src);
       const uint32_t tiles = tiles_of(it), groups = (it.cnt * P.G + RP - 1) / RP;
       if (tiles) {
-        uint32_t kh = 0, rg = 0, t0 = 0;
+        const uint32_t places = tiles + C::kStart;
+        uint32_t kh = 0, rg = 0, o = 0;   // o: the first place of the segment here
         if (off) {
-          const uint32_t i = (uint32_t)mul_div(off, 1, tiles);
-          t0 = (uint32_t)(off - (uint64_t)i * tiles);
+          const uint32_t i = (uint32_t)mul_div(off, 1, places);
+          o = (uint32_t)(off - (uint64_t)i * places);
           kh = i / groups;
           rg = i % groups;
         }
-        for (; kh < a.n_kv && left; t0 = 0) {
-          const uint32_t nt = (uint32_t)min((uint64_t)(tiles - t0), left);
+        for (; kh < a.n_kv && left; o = 0) {
+          const uint32_t n = (uint32_t)min((uint64_t)(places - o), left), e = o + n;
+          const uint32_t t0 = o > C::kStart ? o - C::kStart : 0u, nt = e > C::kStart ? e - C::kStart - t0 : 0u;
+          left -= n;
+          if (nt == 0) break;   // (the share ends before the segment's first tile)
           if (!(ok = mbar_wait_sleep(&S.seg_empty[s % kSegs], ((s / kSegs) & 1) ^ 1, err))) break;
           if (lane == 0) {
             Segment &sg = S.seg[s % kSegs];
@@ -609,7 +619,6 @@ __global__ void __launch_bounds__(Cfg<RP, F8>::kThreads, Cfg<RP, F8>::kPerSm)
             mbar_arrive(&S.seg_full[s % kSegs]);
           }
           __syncwarp();
-          left -= nt;
           ++s;
           if (++rg == groups) {
             rg = 0;
@@ -640,6 +649,8 @@ __global__ void __launch_bounds__(Cfg<RP, F8>::kThreads, Cfg<RP, F8>::kPerSm)
       }
       if (!mbar_wait_sleep(&S.q_empty[qb], ((P.n_q == 2 ? s >> 1 : s) & 1) ^ 1, err)) break;
       uint8_t *dst = s_q + qb * q_bytes;
+      // (rows of eights that nothing reads are left as they are)
+      const uint32_t most = max(16u, (sg.nr + 7) & ~7u), rows = F8 ? min(most, (uint32_t)RP) : min(most, C::kQRows);
       // 8 elements of a row, its token and query head given (zeros outside)
       auto load8 = [&](uint32_t r, uint32_t tok, uint32_t g, uint32_t d) {
         uint4 v = make_uint4(0, 0, 0, 0);
@@ -670,7 +681,7 @@ __global__ void __launch_bounds__(Cfg<RP, F8>::kThreads, Cfg<RP, F8>::kPerSm)
         uint32_t tok = tok_r0, g = g_r0;
         advance(tok, g, sub);
         if (sub < rpp) {
-          for (uint32_t r0 = sub; r0 < C::kQRows; r0 += 8 * rpp) {
+          for (uint32_t r0 = sub; r0 < rows; r0 += 8 * rpp) {
             uint4 v[8];
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
@@ -679,29 +690,36 @@ __global__ void __launch_bounds__(Cfg<RP, F8>::kThreads, Cfg<RP, F8>::kPerSm)
             }
 #pragma unroll
             for (int u = 0; u < 8; ++u)
-              if (r0 + u * rpp < C::kQRows) *reinterpret_cast<uint4 *>(place(r0 + u * rpp, c)) = v[u];
+              if (r0 + u * rpp < rows) *reinterpret_cast<uint4 *>(place(r0 + u * rpp, c)) = v[u];
           }
         }
       } else {
         // half a warp per row, 16 elements a lane: q 2^k = hi + lo / 16, k so that the largest
-        // entry is in [128, 256)
+        // entry is in [128, 256); four rows ahead
+        constexpr uint32_t kDeep = 4;
         const uint32_t c = lane & 15;
         const float ks = __ldg(a.k_scale + sg.kh) * P.c2;
-        uint32_t tok = tok_r0, g = g_r0;
-        advance(tok, g, lane >> 4);
-        for (uint32_t r1 = lane >> 4; r1 < RP; r1 += 8) {
-        uint4 in[4][2];
+        uint32_t tok = tok_r0, g = g_r0, r1 = lane >> 4;
+        advance(tok, g, r1);
+        uint4 in[kDeep][2];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (uint32_t u = 0; u < kDeep; ++u) {
           in[u][0] = load8(r1 + 2 * u, tok, g, 16 * c);
           in[u][1] = load8(r1 + 2 * u, tok, g, 16 * c + 8);
           advance(tok, g, 2);
         }
+        for (uint32_t r2 = 0; r2 < rows; r2 += 2, r1 += 2) {   // (both halves go on together)
+          const uint32_t r = r1;
+          const uint32_t w[8] = {in[0][0].x, in[0][0].y, in[0][0].z, in[0][0].w,
+                                 in[0][1].x, in[0][1].y, in[0][1].z, in[0][1].w};
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const uint32_t r = r1 + 2 * u;
-          const uint32_t w[8] = {in[u][0].x, in[u][0].y, in[u][0].z, in[u][0].w,
-                                 in[u][1].x, in[u][1].y, in[u][1].z, in[u][1].w};
+          for (uint32_t u = 0; u + 1 < kDeep; ++u) {
+            in[u][0] = in[u + 1][0];
+            in[u][1] = in[u + 1][1];
+          }
+          in[kDeep - 1][0] = load8(r + 2 * kDeep, tok, g, 16 * c);
+          in[kDeep - 1][1] = load8(r + 2 * kDeep, tok, g, 16 * c + 8);
+          advance(tok, g, 2);
           uint32_t top = 0;
 #pragma unroll
           for (int i = 0; i < 8; ++i) top = max(top, max(w[i] & 0x7fffu, w[i] >> 16 & 0x7fffu));
@@ -714,25 +732,23 @@ __global__ void __launch_bounds__(Cfg<RP, F8>::kThreads, Cfg<RP, F8>::kPerSm)
           uint32_t hi[4], lo[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            float x[4];
+            float2 x[2];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              x[2 * k] = __uint_as_float(w[2 * i + k] << 16) * up;
-              x[2 * k + 1] = __uint_as_float(w[2 * i + k] & 0xffff0000u) * up;
-            }
-            const uint16_t h0 = pack_e4m3(x[0], x[1]), h1 = pack_e4m3(x[2], x[3]);
+            for (int k = 0; k < 2; ++k)
+              x[k] = mul2(make_float2(__uint_as_float(w[2 * i + k] << 16), __uint_as_float(w[2 * i + k] & 0xffff0000u)),
+                          make_float2(up, up));
+            const uint16_t h0 = pack_e4m3(x[0].x, x[0].y), h1 = pack_e4m3(x[1].x, x[1].y);
             const float2 f0 = unpack_e4m3(h0), f1 = unpack_e4m3(h1);
-            const uint16_t l0 = pack_e4m3((x[0] - f0.x) * 16.f, (x[1] - f0.y) * 16.f);
-            const uint16_t l1 = pack_e4m3((x[2] - f1.x) * 16.f, (x[3] - f1.y) * 16.f);
+            const float2 r0 = mul2(add2(x[0], make_float2(-f0.x, -f0.y)), make_float2(16.f, 16.f));
+            const float2 s0 = mul2(add2(x[1], make_float2(-f1.x, -f1.y)), make_float2(16.f, 16.f));
             hi[i] = h0 | (uint32_t)h1 << 16;
-            lo[i] = l0 | (uint32_t)l1 << 16;
+            lo[i] = pack_e4m3(r0.x, r0.y) | (uint32_t)pack_e4m3(s0.x, s0.y) << 16;
           }
           if (c < P.nbox * 8) {
             *reinterpret_cast<uint4 *>(place(r, c)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
             *reinterpret_cast<uint4 *>(place(RP + r, c)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
           }
           if (c == 0) S.qs[s % kSegs][r] = down * ks;
-        }
         }
       }
       fence_proxy_async();
