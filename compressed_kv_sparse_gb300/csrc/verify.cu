@@ -3,14 +3,16 @@
 //
 // Draft i stands while u_i q_i(x_i) < p_i(x_i). The token behind the last that stands is drawn
 // from w = max(p - q, 0) of the one that fell, or from p, by the first running sum above u
-// times the total. p and q are taken as whole multiples of 2^-s (s = 62 - ceil(log2 V)), so
-// the sums are whole numbers: any order gives the same ones, and blocks and warps may share a row.
+// times the total. p and q are taken as whole multiples of 2^-s (s = 45, less beyond 131,072 tokens),
+// so the sums are whole numbers: any order gives the same ones, and blocks and warps may share a row.
 //
 // A cluster of blocks per sequence. Every block tests the drafts for itself (a warp, a draft
-// per lane), sums its share of the row (each warp consecutive tokens), and reads
-// the others' sums through distributed shared memory; the warp in whose part the sum passes
-// the threshold reads its part again (it is in the caches) and finds the token.
+// per lane), sums its share of the row (each warp consecutive chunks of 512 tokens, whose sums it
+// keeps), and reads the others' sums through distributed shared memory; the warp in whose part
+// the sum passes the threshold finds the chunk, reads it again (it is in the caches) and finds the token.
 // Bound by HBM for many sequences: a row of p, and one of q where a draft fell, read once.
+#include <type_traits>
+
 #include "common.cuh"
 #include "tc.cuh"
 
@@ -18,16 +20,29 @@ namespace ds4a {
 namespace {
 
 constexpr uint32_t kThreads = 256, kWarps = kThreads / 32;
+constexpr uint32_t kChunk = 512;   // tokens that a warp adds at once
 
 struct Params {
   VerifyArgs a;
   uint32_t shift;    // s
-  uint32_t part;     // tokens per block (a multiple of 128 * kWarps)
+  uint32_t part;     // tokens per block (a multiple of a chunk per warp)
 };
 
-// Whole multiples of 2^-s of a probability; above 1: 1, negative and NaN: 0.
-__device__ __forceinline__ uint64_t fixed(float p, float scale) {
-  return __float2ull_rn(fminf(fmaxf(p, 0.f), 1.f) * scale);
+// A probability (above 1: 1, negative and NaN: 0) as the whole number of 2^-s nearest to it, in two parts, hi
+// 2^(s - 23) + lo: hi its nearest multiple of 2^-23, lo what is left of it. Adding 1, or 1.5 * 2^23 to a
+// number below 2^22, rounds to whole steps that stand in the low bits; the conversion instructions take
+// 16 clocks a warp. bits() of hi and lo carry constants, which differences drop.
+struct Parts {
+  uint32_t hi, lo;
+};
+constexpr uint32_t kHi0 = 0x3f800000u, kLo0 = 0x4b400000u;   // the bits of 1 and of 1.5 * 2^23
+__device__ __forceinline__ Parts parts_of(float p, float scale) {   // p in [0, 1]
+  const float t = p + 1.f, rest = p - (t - 1.f);
+  return Parts{__float_as_uint(t), __float_as_uint(fmaf(rest, scale, 12582912.f))};
+}
+// a - b in units of 2^-s.
+__device__ __forceinline__ int64_t difference(Parts a, Parts b, uint32_t hi_unit) {
+  return (int64_t)(int32_t)(a.hi - b.hi) * (int32_t)hi_unit + (int32_t)(a.lo - b.lo);
 }
 
 template <typename T, bool VEC>
@@ -52,17 +67,13 @@ __device__ __forceinline__ void load4(float (&v)[4], const T *row, uint32_t i, u
 }
 
 // Weights of tokens i .. i + 3: p - q where positive, p without q; drop: this token's is 0.
-template <typename T, bool VEC>
 __device__ __forceinline__ void weights(uint64_t (&w)[4], const float (&p)[4], const float (&q)[4], bool has_q,
-                                        uint32_t i, uint32_t drop, float scale) {
+                                        uint32_t i, uint32_t drop, float scale, uint32_t hi_unit) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    uint64_t x = fixed(p[k], scale);
-    if (has_q) {
-      const uint64_t y = fixed(q[k], scale);
-      x = x > y ? x - y : 0ull;
-    }
-    w[k] = i + k == drop ? 0ull : x;
+    const float x = __saturatef(p[k]);
+    const Parts y = has_q ? parts_of(fminf(x, __saturatef(q[k])), scale) : Parts{kHi0, kLo0};
+    w[k] = i + k == drop ? 0ull : (uint64_t)difference(parts_of(x, scale), y, hi_unit);
   }
 }
 
@@ -78,8 +89,12 @@ __device__ __forceinline__ uint64_t ld_cluster_u64(uint32_t addr) {
   return v;
 }
 
+// (Four blocks a SM hide the loads: 256 sequences of 131,072 tokens, three quarters with a draft that fell,
+// take 43 us, with three blocks 55, two 121; with the next chunks on their way in registers or shared
+// memory, which leave room for two or three blocks, 54 to 60.)
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads) verify_kernel(Params P) {
+__global__ void __launch_bounds__(kThreads, 4) verify_kernel(Params P) {
+  extern __shared__ uint64_t s_chunks[];   // [warp][chunks of a warp]
   __shared__ uint64_t s_sum[2];         // this block's sum, of each of two attempts
   __shared__ uint64_t s_warp[kWarps];
   __shared__ uint32_t s_acc;
@@ -135,28 +150,57 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(Params P) {
   const T *p_row = static_cast<const T *>(a.target) + (c0 + acc) * a.target_stride;
   const T *q_row = static_cast<const T *>(a.draft_probs) + ((size_t)b * N + acc) * V;
   const float scale = __uint_as_float((P.shift + 127u) << 23);
+  const uint32_t hi_unit = 1u << (P.shift - 23);
   const uint32_t wpart = P.part / kWarps, w0 = rank * P.part + warp * wpart, w1 = min(V, w0 + wpart);
   for (uint32_t attempt = 0; attempt < 2; ++attempt) {
     // (attempt 1: no weight was above zero; p alone)
     const bool has_q = fell && a.draft_probs && !attempt;
     const uint32_t drop = fell && !a.draft_probs && !attempt ? (uint32_t)__ldg(a.drafts + (size_t)b * N + acc)
                                                              : 0xffffffffu;
+    // (a chunk's 16 tokens of a lane: i0 + 128 u + 4 lane + k)
+    uint64_t *mine = s_chunks + warp * (wpart / kChunk);
     uint64_t sum = 0;
-    for (uint32_t i0 = w0; i0 < w1; i0 += 512) {
-      float p[4][4], q[4][4];
+    auto add = [&](auto hq, uint32_t i0, const float (&p)[4][4], const float (&q)[4][4]) {
+      // (sums of 16 parts stay in 32 bits)
+      uint32_t hi = 0;
+      int32_t lo = 0;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        load4<T, VEC>(p[u], p_row, i0 + 128 * u + 4 * lane, w1);
-        if (has_q) load4<T, VEC>(q[u], q_row, i0 + 128 * u + 4 * lane, w1);
-      }
+      for (int u = 0; u < 4; ++u)
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        uint64_t w[4];
-        weights<T, VEC>(w, p[u], q[u], has_q, i0 + 128 * u + 4 * lane, drop, scale);
-        sum += w[0] + w[1] + w[2] + w[3];
+        for (int k = 0; k < 4; ++k) {
+          const float x = __saturatef(p[u][k]);
+          const Parts f = parts_of(x, scale);
+          if constexpr (decltype(hq)::value) {
+            const Parts g = parts_of(fminf(x, __saturatef(q[u][k])), scale);   // (where q is larger: p - p)
+            hi += f.hi - g.hi;
+            lo += (int32_t)(f.lo - g.lo);
+          } else {
+            hi += f.hi - kHi0;
+            lo += (int32_t)(f.lo - kLo0);
+          }
+        }
+      uint64_t c = (uint64_t)hi * hi_unit + (int64_t)lo;
+      c = warp_sum64(c);
+      if (drop - i0 < kChunk && drop < w1)
+        c -= (uint64_t)difference(parts_of(__saturatef(ld_f32(p_row, drop)), scale), Parts{kHi0, kLo0}, hi_unit);
+      if (lane == 0) mine[(i0 - w0) / kChunk] = c;
+      sum += c;
+    };
+    auto pass = [&](auto hq) {
+      for (uint32_t i0 = w0; i0 < w1; i0 += kChunk) {
+        float p[4][4], q[4][4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          load4<T, VEC>(p[u], p_row, i0 + 128 * u + 4 * lane, w1);
+          if (hq.value) load4<T, VEC>(q[u], q_row, i0 + 128 * u + 4 * lane, w1);
+        }
+        add(hq, i0, p, q);
       }
-    }
-    sum = warp_sum64(sum);
+    };
+    if (has_q)
+      pass(std::true_type{});
+    else
+      pass(std::false_type{});
     if (lane == 0) s_warp[warp] = sum;
     __syncthreads();
     uint64_t before = 0, own = 0;
@@ -181,30 +225,29 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(Params P) {
     const float u = fminf(fmaxf(__ldg(a.u_sample + b), 0.f), 0x1.fffffep-1f);
     const uint64_t thr = (uint64_t)((double)u * (double)total);   // below total
     if (before <= thr && thr < before + sum) {   // this warp's part (the whole warp)
+      __syncwarp();
       uint64_t run = before;
-      for (uint32_t i0 = w0; i0 < w1; i0 += 128) {
-        const uint32_t i = i0 + 4 * lane;
+      uint32_t i0 = w0;
+      for (uint32_t n = 0; run + mine[n] <= thr; ++n, i0 += kChunk) run += mine[n];   // (it is there)
+#pragma unroll 1
+      for (uint32_t i = i0 + 4 * lane;; i += 128) {   // (it is in one of the four)
         float p[4], q[4];
         uint64_t w[4];
         load4<T, VEC>(p, p_row, i, w1);
         if (has_q) load4<T, VEC>(q, q_row, i, w1);
-        weights<T, VEC>(w, p, q, has_q, i, drop, scale);
-        const uint64_t mine = w[0] + w[1] + w[2] + w[3];
-        uint64_t inc = mine;
+        weights(w, p, q, has_q, i, drop, scale, hi_unit);
+        const uint64_t four = (w[0] + w[1]) + (w[2] + w[3]);
+        uint64_t inc = four;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const uint64_t y = __shfl_up_sync(0xffffffffu, inc, o);
           if (lane >= (uint32_t)o) inc += y;
         }
         const uint32_t hit = __ballot_sync(0xffffffffu, run + inc > thr);
-        if (hit) {
-          if (lane == (uint32_t)__ffs(hit) - 1) {
-            uint64_t r = run + inc - mine;
-            uint32_t k = 0;
-            for (; k < 3; ++k) {
-              r += w[k];
-              if (r > thr) break;
-            }
+        if (hit || i - 4 * lane + 128 >= w1) {
+          if (hit && lane == (uint32_t)__ffs(hit) - 1) {
+            const uint64_t a0 = run + inc - four + w[0], a1 = a0 + w[1], a2 = a1 + w[2];
+            const uint32_t k = a0 > thr ? 0u : a1 > thr ? 1u : a2 > thr ? 2u : 3u;
             a.tokens[(size_t)b * (N + 1) + acc] = (int32_t)(i + k);
           }
           break;
@@ -222,13 +265,18 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(Params P) {
 cudaError_t launch_verify(const VerifyArgs &a, cudaStream_t s) {
   Params P;
   P.a = a;
-  P.shift = 62;
+  P.shift = 45;   // (V times 2^s stays below 2^62, a rest below 2^-24 times 2^s below 2^22)
   while ((1ull << (62 - P.shift)) < a.vocab) --P.shift;
-  constexpr uint32_t kCluster = 8, kStep = 128 * kWarps;
-  P.part = ((a.vocab + kCluster - 1) / kCluster + kStep - 1) / kStep * kStep;
   const uintptr_t all = reinterpret_cast<uintptr_t>(a.target) | reinterpret_cast<uintptr_t>(a.draft_probs);
   const uint32_t es = a.dtype == DS4A_BF16 ? 2 : 4;
   const bool vec = all % (4 * es) == 0 && a.vocab % 4 == 0 && a.target_stride % 4 == 0;
+  // up to eight blocks a sequence while no more than four a SM come of it, which run at once (eight
+  // for every one of 256 sequences: 46 us, two 43)
+  uint32_t cluster = 8;
+  while (cluster > 1 && (uint64_t)a.batch * cluster > 4ull * num_sms()) cluster /= 2;
+  constexpr uint32_t kStep = kChunk * kWarps;
+  P.part = ((a.vocab + cluster - 1) / cluster + kStep - 1) / kStep * kStep;
+  const size_t smem = P.part / kChunk * sizeof(uint64_t);   // (at most 16 KiB)
   auto *k = a.dtype == DS4A_BF16 ? (vec ? verify_kernel<__nv_bfloat16, true> : verify_kernel<__nv_bfloat16, false>)
                                  : (vec ? verify_kernel<float, true> : verify_kernel<float, false>);
   cudaLaunchConfig_t cfg = {};
@@ -236,11 +284,12 @@ cudaError_t launch_verify(const VerifyArgs &a, cudaStream_t s) {
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = kCluster;
+  at[1].val.clusterDim.x = cluster;
   at[1].val.clusterDim.y = 1;
   at[1].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(kCluster, a.batch);
+  cfg.gridDim = dim3(cluster, a.batch);
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = at;
   cfg.numAttrs = 2;

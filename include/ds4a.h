@@ -685,8 +685,8 @@ size_t ds4a_paged_attn_ws_bytes(const ds4a_kv_cache *cache, uint32_t max_new, ui
  * Drafts stand while u_accept q(x) < p(x), compared exactly. The new token is drawn from
  * w = max(p - q, 0) of the first one that fell (p with the drafted token at 0 where draft_probs
  * is NULL), or from p where all stand: the lowest token whose running sum of w exceeds
- * u_sample times the sum. For these sums p and q are each rounded to a multiple of 2^-s, s = 62 -
- * ceil(log2 V) (45 for 131,072 tokens), and added as whole numbers, so the order of sums changes
+ * u_sample times the sum. For these sums p and q are each rounded to a multiple of 2^-s, s = 45 (62 -
+ * ceil(log2 V) beyond 131,072 tokens), and added as whole numbers, so the order of sums changes
  * nothing; probabilities above 1 count as 1, negative ones and NaN as 0. A w that is zero everywhere
  * gives way to p, and a p that is zero everywhere to token V - 1.
  * Errors: DS4A_ERR_ARG, DS4A_ERR_SHAPE, DS4A_ERR_DTYPE, DS4A_ERR_CUDA.

@@ -142,7 +142,7 @@ def verify(target, drafts, draft_probs, u_accept, u_sample, cnt):
     """One sequence: target [cnt][V], drafts [N], draft_probs [N][V] or None, u_accept [N]. Returns the
     tokens it emits."""
     V = target.shape[1]
-    shift = 62 - max(0, (V - 1).bit_length())
+    shift = min(45, 62 - max(0, (V - 1).bit_length()))
     m = min(cnt - 1, len(drafts))
     a = 0
     while a < m:
