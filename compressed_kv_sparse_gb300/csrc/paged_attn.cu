@@ -1,25 +1,34 @@
 // Attention of a step's new tokens over a paged cache of keys and values, on the CUDA cores: the
 // exact path of fp32 layers and the one for sizes that the tensor-core kernel does not take.
 //
-// Rows (a sequence's tokens x the query heads of one key head) in groups of up to 16, keys in
-// tiles of 64: a block scores a tile (a thread per key and quarter of the rows), updates each
-// row's running maximum and sum (a warp per row), and adds the weighted values (a thread
-// per dim). A sequence's tiles are shared among several blocks where there are few rows; each
-// leaves its sums with their maximum, and a second launch joins them in order.
+// Rows (a sequence's tokens x the query heads of one key head) in groups of 8 or 16, keys in tiles of
+// 32 or 64, the next tile on its way while one is worked on. A block scores a tile (a thread per
+// key and part of the dims, all rows), updates each row's running maximum and sum (a warp
+// per row) and adds the weighted values (a warp per eighth of the keys, a lane per four dims, all
+// rows), so that a key or value is read from shared memory once for all rows. A sequence's
+// tiles are shared among several blocks where there are few rows; each leaves its sums
+// with their maximum, and a second launch joins them in order.
+// Bound by HBM up to 8 rows, beyond by the fp32 units and shared memory.
 #include <cuda_fp8.h>
 
 #include "paged.cuh"
+#include "tc.cuh"
 
 namespace ds4a {
 
 namespace {
 
-constexpr uint32_t kThreads = 256, kTile = 64, kRows = 16;
+constexpr uint32_t kThreads = 256, kWarps = kThreads / 32;
+// Keys of a tile: 32 and two or three blocks a SM for 8 rows (8 x 8,000 tokens of 8 heads of 128 dims: 159 us,
+// 64 keys 251); 64 for 16 rows (3 x 1,024 tokens, 10 rows of 80 dims: 13.7 us, 32 keys 15.5).
+__host__ __device__ constexpr uint32_t tile_of(uint32_t R) { return R == 8 ? 32 : 64; }
 constexpr uint32_t kWsHead = 256;   // the status word's line
+constexpr uint32_t kSmemMost = 227 * 1024;
 
 struct Params {
   PagedArgs a;
   uint32_t G, groups, splits;   // query heads per key head, row groups, shares of the keys
+  uint32_t stages;              // key and value tiles in shared memory
   float *part;                  // [batch * max_new * H][splits][D], then (max, sum) of each
 };
 
@@ -31,79 +40,142 @@ __device__ __forceinline__ float ld_kv(const __nv_fp8_storage_t *p, size_t i) {
   return __half2float(__half(__nv_cvt_fp8_to_halfraw(p[i], __NV_E4M3)));
 }
 
-template <typename T, typename KV>
+// Floats of shared memory: queries, key tiles, value tiles, partial scores, weights, max, sum, factor.
+__host__ __device__ constexpr uint32_t smem_floats(uint32_t D4, uint32_t R, uint32_t stages) {
+  const uint32_t kTile = tile_of(R), kParts = kThreads / kTile;
+  return R * 4 * D4 + stages * kTile * (4 * D4 + 4) + stages * kTile * 4 * D4 + kParts * R * kTile + kTile * (R + 4) + 3 * R;
+}
+
+// R: rows of a group. DV: fours of dims per lane (D <= 128 DV).
+template <typename T, typename KV, int R, int DV>
 __global__ void __launch_bounds__(kThreads) paged_attn_kernel(Params P) {
-  extern __shared__ float sm[];
+  constexpr uint32_t kTile = tile_of(R), kParts = kThreads / kTile;
+  extern __shared__ __align__(16) float sm[];
   const PagedArgs &a = P.a;
-  const uint32_t D = a.head_dim, DP = D + 1, H = a.n_heads, K = a.n_kv;
-  float *s_k = sm;                        // [64][D + 1]
-  float *s_q = s_k + kTile * DP;          // [16][D]
-  float *s_p = s_q + kRows * D;           // [16][64]
-  float *s_m = s_p + kRows * kTile, *s_l = s_m + kRows, *s_c = s_l + kRows;   // max, sum, factor
+  const uint32_t D = a.head_dim, D4 = (D + 3) / 4, VS = 4 * D4, KS = VS + 4, PS = R + 4, H = a.n_heads, K = a.n_kv;
+  float *s_q = sm;                                      // [R][VS]
+  float *s_k = s_q + R * VS;                            // [stage][kTile][KS]
+  float *s_v = s_k + P.stages * kTile * KS;             // [stage][kTile][VS]
+  float *s_s = s_v + P.stages * kTile * VS;             // [part][R][kTile]
+  float *s_p = s_s + kParts * R * kTile;                     // [kTile][PS]
+  float *s_m = s_p + kTile * PS, *s_l = s_m + R, *s_c = s_l + R;
   pdl_wait();
   pdl_trigger();
   const uint32_t split = blockIdx.x, kh = blockIdx.y / P.groups, rg = blockIdx.y % P.groups, b = blockIdx.z;
   const uint32_t t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const PagedItem it = paged_item(a, b);
-  const uint32_t r0 = rg * kRows, all = it.cnt * P.G;
+  const uint32_t r0 = rg * R, all = it.cnt * P.G;
   if (r0 >= all) return;
-  const uint32_t nr = min(kRows, all - r0);
+  const uint32_t nr = min((uint32_t)R, all - r0);
+  auto token = [&](uint32_t r) { return (r0 + r) / P.G; };
+  auto head = [&](uint32_t r) { return kh * P.G + (r0 + r) % P.G; };
+  // the keys that some row of the group sees, and those that all of them do
+  const uint32_t p_first = it.pos0 + token(0), p_last = it.pos0 + token(nr - 1);
+  const uint32_t k_lo = a.window && p_first + 1 > a.window ? p_first + 1 - a.window : 0u, k_hi = min(p_last + 1, it.hi);
   const uint32_t t_lo = it.lo / kTile, t_hi = (it.hi + kTile - 1) / kTile, nt = t_hi > t_lo ? t_hi - t_lo : 0u;
   const uint32_t t0 = t_lo + (uint32_t)((uint64_t)nt * split / P.splits);
   const uint32_t t1 = t_lo + (uint32_t)((uint64_t)nt * (split + 1) / P.splits);
   const float ks = a.k_scale ? __ldg(a.k_scale + kh) : 1.f, vs = a.v_scale ? __ldg(a.v_scale + kh) : 1.f;
-  auto token = [&](uint32_t r) { return (r0 + r) / P.G; };
-  auto head = [&](uint32_t r) { return kh * P.G + (r0 + r) % P.G; };
-  for (uint32_t i = t; i < nr * D; i += kThreads) {
-    const uint32_t r = i / D, d = i % D;
-    s_q[i] = ld_f32(static_cast<const T *>(a.q) + (it.first + token(r)) * a.q_stride, (size_t)head(r) * D + d) * (a.scale * ks);
+  const bool async = sizeof(KV) == 4 && D % 4 == 0;   // (rows start on 16 bytes)
+  // a tile's keys and values; rows that the group does not see are zeros (they may hold NaNs)
+  auto load = [&](uint32_t stage, uint32_t tile) {
+    const uint32_t phys = (uint32_t)__ldg(a.table + (size_t)b * a.max_blocks + tile / (256 / kTile));
+    const bool held = phys < a.n_blocks;
+    const size_t base = (((size_t)(held ? phys : 0u) * K + kh) * 256u + tile % (256 / kTile) * kTile) * D;
+    const KV *kp = static_cast<const KV *>(a.k) + base, *vp = static_cast<const KV *>(a.v) + base;
+    float *dk = s_k + stage * kTile * KS, *dv = s_v + stage * kTile * VS;
+#pragma unroll 4
+    for (uint32_t r = warp; r < kTile; r += kWarps) {
+      const uint32_t key = tile * kTile + r;
+      const bool seen = held && key >= k_lo && key < k_hi;
+      if (async) {
+#pragma unroll
+        for (int i = 0; i < DV; ++i) {
+          const uint32_t c = lane + 32 * i;
+          if (c < D4) {
+            cp_async16(dk + r * KS + 4 * c, kp + (size_t)r * D + 4 * c, seen ? 16u : 0u);
+            cp_async16(dv + r * VS + 4 * c, vp + (size_t)r * D + 4 * c, seen ? 16u : 0u);
+          }
+        }
+      } else {
+        for (uint32_t c = lane; c < VS; c += 32) {
+          const bool in = seen && c < D;
+          dk[r * KS + c] = in ? ld_kv(kp, (size_t)r * D + c) : 0.f;
+          dv[r * VS + c] = in ? ld_kv(vp, (size_t)r * D + c) : 0.f;
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  if (t0 < t1) load(0, t0);
+  for (uint32_t i = t; i < R * VS; i += kThreads) {
+    const uint32_t r = i / VS, d = i % VS;
+    s_q[i] = r < nr && d < D
+                 ? ld_f32(static_cast<const T *>(a.q) + (it.first + token(r)) * a.q_stride, (size_t)head(r) * D + d) * (a.scale * ks)
+                 : 0.f;
   }
-  if (t < kRows) {
+  if (t < R) {
     s_m[t] = -INFINITY;
     s_l[t] = 0.f;
   }
-  float acc[kRows];
+  float4 acc[R][DV];
 #pragma unroll
-  for (uint32_t i = 0; i < kRows; ++i) acc[i] = 0.f;
-  // values: thread -> dim d, rows sub, sub + subs, ..
-  const uint32_t subs = kThreads / D, sub = t / D, d = t % D;   // (D <= 256)
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int i = 0; i < DV; ++i) acc[r][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  const uint32_t key = t % kTile, part = t / kTile, dq = (D4 + kParts - 1) / kParts;
   for (uint32_t tile = t0; tile < t1; ++tile) {
-    const uint32_t blk = tile / (256 / kTile);
-    const uint32_t phys = (uint32_t)__ldg(a.table + (size_t)b * a.max_blocks + blk);
-    if (phys >= a.n_blocks) continue;   // (the whole block)
-    const size_t base = (((size_t)phys * K + kh) * 256u + tile % (256 / kTile) * kTile) * D;
-    const KV *kp = static_cast<const KV *>(a.k) + base, *vp = static_cast<const KV *>(a.v) + base;
-    __syncthreads();
-    for (uint32_t i = t; i < kTile * D; i += kThreads) s_k[i / D * DP + i % D] = ld_kv(kp, i);
-    __syncthreads();
-    {
-      const uint32_t key = t % kTile, q4 = t / kTile, pos = tile * kTile + key;
-      float s[kRows / 4] = {0.f, 0.f, 0.f, 0.f};
-      for (uint32_t e = 0; e < D; ++e) {
-        const float x = s_k[key * DP + e];
-#pragma unroll
-        for (uint32_t i = 0; i < kRows / 4; ++i)
-          if (q4 + 4 * i < nr) s[i] = fmaf(x, s_q[(q4 + 4 * i) * D + e], s[i]);
-      }
-#pragma unroll
-      for (uint32_t i = 0; i < kRows / 4; ++i) {
-        const uint32_t r = q4 + 4 * i;
-        if (r >= nr) break;
-        const uint32_t p = it.pos0 + token(r);
-        const bool seen = pos <= p && pos < it.hi && (!a.window || p - pos < a.window);
-        s_p[r * kTile + key] = seen ? s[i] : -INFINITY;
-      }
+    const uint32_t stage = P.stages == 2 ? (tile - t0) & 1 : 0u;
+    if (P.stages == 2 && tile + 1 < t1) {
+      load(stage ^ 1, tile + 1);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+    } else {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
     __syncthreads();
-    for (uint32_t r = warp; r < nr; r += kThreads / 32) {
-      const float x0 = s_p[r * kTile + lane], x1 = s_p[r * kTile + 32 + lane], m0 = s_m[r];
-      const float m1 = fmaxf(m0, warp_max(fmaxf(x0, x1)));
+    {   // scores of one key over a part of the dims
+      const float *kr = s_k + (stage * kTile + key) * KS;
+      float s[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) s[r] = 0.f;
+      const uint32_t d1 = min(D4, (part + 1) * dq);
+      for (uint32_t d = part * dq; d < d1; ++d) {
+        const float4 x = *reinterpret_cast<const float4 *>(kr + 4 * d);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const float4 y = *reinterpret_cast<const float4 *>(s_q + r * VS + 4 * d);
+          s[r] = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, s[r]))));
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) s_s[(part * R + r) * kTile + key] = s[r];
+    }
+    __syncthreads();
+    const uint32_t blk_ok = (uint32_t)__ldg(a.table + (size_t)b * a.max_blocks + tile / (256 / kTile));
+    const bool held = blk_ok < a.n_blocks;
+    for (uint32_t r = warp; r < R; r += kWarps) {
+      const uint32_t p = it.pos0 + token(min(r, nr - 1));
+      float x[kTile / 32], top = -INFINITY;   // (lanes per key)
+#pragma unroll
+      for (uint32_t i = 0; i < kTile / 32; ++i) {
+        const uint32_t k = lane + 32 * i, pos = tile * kTile + k;
+        x[i] = 0.f;
+#pragma unroll
+        for (uint32_t q = 0; q < kParts; ++q) x[i] += s_s[(q * R + r) * kTile + k];
+        if (!held || pos > p || pos >= it.hi || (a.window && p - pos >= a.window)) x[i] = -INFINITY;
+        top = fmaxf(top, x[i]);
+      }
+      const float m0 = s_m[r], m1 = fmaxf(m0, warp_max(top));
       // (nothing seen yet: no weights; a NaN stays one)
-      const float e0 = x0 == -INFINITY ? 0.f : expf(x0 - m1), e1 = x1 == -INFINITY ? 0.f : expf(x1 - m1);
       const float c = m0 == -INFINITY ? 0.f : expf(m0 - m1);
-      const float sum = warp_sum(e0 + e1);
-      s_p[r * kTile + lane] = e0;
-      s_p[r * kTile + 32 + lane] = e1;
+      float sum = 0.f;
+#pragma unroll
+      for (uint32_t i = 0; i < kTile / 32; ++i) {
+        const float e = x[i] == -INFINITY ? 0.f : expf(x[i] - m1);
+        s_p[(lane + 32 * i) * PS + r] = e;
+        sum += e;
+      }
+      sum = warp_sum(sum);
       if (lane == 0) {
         s_m[r] = m1;
         s_l[r] = s_l[r] * c + sum;
@@ -111,114 +183,179 @@ __global__ void __launch_bounds__(kThreads) paged_attn_kernel(Params P) {
       }
     }
     __syncthreads();
-    if (sub < subs) {
+    // a warp's eighth of the keys, four dims a lane (twice beyond 128)
+    const bool plain = tile * kTile + kTile - 1 <= p_first && (!a.window || p_last - tile * kTile < a.window);
 #pragma unroll
-      for (uint32_t i = 0; i < kRows; ++i)
-        if (sub + i * subs < nr) acc[i] *= s_c[sub + i * subs];
-      for (uint32_t key = 0; key < kTile; ++key) {
-        const float v = ld_kv(vp, (size_t)key * D + d);
+    for (int r = 0; r < R; ++r) {
+      const float c = s_c[r];
 #pragma unroll
-        for (uint32_t i = 0; i < kRows; ++i) {
-          if (sub + i * subs >= nr) break;
-          const float p = s_p[(sub + i * subs) * kTile + key];
-          if (p != 0.f) acc[i] = fmaf(p, v, acc[i]);   // (an unseen row may hold a NaN)
+      for (int i = 0; i < DV; ++i) {
+        acc[r][i].x *= c;
+        acc[r][i].y *= c;
+        acc[r][i].z *= c;
+        acc[r][i].w *= c;
+      }
+    }
+    const float *vt = s_v + stage * kTile * VS;
+    for (uint32_t k = warp; k < kTile; k += kWarps) {
+      float pr[R];
+#pragma unroll
+      for (int r = 0; r < R; r += 4) {
+        const float4 f = *reinterpret_cast<const float4 *>(s_p + k * PS + r);
+        pr[r] = f.x, pr[r + 1] = f.y, pr[r + 2] = f.z, pr[r + 3] = f.w;
+      }
+#pragma unroll
+      for (int i = 0; i < DV; ++i) {
+        const uint32_t c = lane + 32 * i;
+        const float4 v = c < D4 ? *reinterpret_cast<const float4 *>(vt + k * VS + 4 * c) : make_float4(0.f, 0.f, 0.f, 0.f);
+        // (a key that only some rows see may hold a NaN)
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+          if (plain || pr[r] != 0.f) {
+            acc[r][i].x = fmaf(pr[r], v.x, acc[r][i].x);
+            acc[r][i].y = fmaf(pr[r], v.y, acc[r][i].y);
+            acc[r][i].z = fmaf(pr[r], v.z, acc[r][i].z);
+            acc[r][i].w = fmaf(pr[r], v.w, acc[r][i].w);
+          }
+      }
+    }
+    __syncthreads();   // the tile and the weights are free
+    if (P.stages == 1 && tile + 1 < t1) load(0, tile + 1);
+  }
+  __syncthreads();
+  // ---- the warps' sums, added in order through shared memory: [warp][VS] a row at a time
+  float *red = s_k;
+  for (uint32_t r = 0; r < nr; ++r) {
+#pragma unroll
+    for (int q = 0; q < R; ++q)   // (registers are not indexed)
+      if ((uint32_t)q == r)
+#pragma unroll
+        for (int i = 0; i < DV; ++i)
+          if (lane + 32 * i < D4) *reinterpret_cast<float4 *>(red + warp * VS + 4 * (lane + 32 * i)) = acc[q][i];
+    __syncthreads();
+    const float m = s_m[r], l = s_l[r];
+    for (uint32_t d = t; d < D; d += kThreads) {
+      float o = 0.f;
+#pragma unroll
+      for (uint32_t w = 0; w < kWarps; ++w) o += red[w * VS + d];
+      if (P.splits == 1) {
+        const size_t row = (size_t)(it.first + token(r)) * H + head(r);
+        st_elem(static_cast<T *>(a.out), row * D + d, l == 0.f ? 0.f : o / l * vs);
+        if (a.lse && d == 0) a.lse[row] = l == 0.f ? -INFINITY : m + logf(l);
+      } else {
+        const size_t row = ((size_t)b * a.max_new + token(r)) * H + head(r), at = row * P.splits + split;
+        P.part[at * D + d] = o;
+        if (d == 0) {
+          float *ml = P.part + (size_t)a.batch * a.max_new * H * P.splits * D + 2 * at;
+          ml[0] = m;
+          ml[1] = l;
         }
       }
     }
-  }
-  __syncthreads();
-  if (sub >= subs) return;
-#pragma unroll
-  for (uint32_t i = 0; i < kRows; ++i) {
-    const uint32_t r = sub + i * subs;
-    if (r >= nr) break;
-    const float m = s_m[r], l = s_l[r];
-    if (P.splits == 1) {
-      const size_t row = (size_t)(it.first + token(r)) * H + head(r);
-      st_elem(static_cast<T *>(a.out), row * D + d, l == 0.f ? 0.f : acc[i] / l * vs);
-      if (a.lse && d == 0) a.lse[row] = l == 0.f ? -INFINITY : m + logf(l);
-    } else {
-      const size_t row = ((size_t)b * a.max_new + token(r)) * H + head(r), at = row * P.splits + split;
-      P.part[at * D + d] = acc[i];
-      if (d == 0) {
-        float *ml = P.part + (size_t)a.batch * a.max_new * H * P.splits * D + 2 * at;
-        ml[0] = m;
-        ml[1] = l;
-      }
-    }
+    __syncthreads();
   }
 }
 
-// A block per row: the shares' sums brought to their common maximum and added in order.
+// A block per row: the shares' sums brought to their common maximum and added in order. Every
+// warp works out the shares' weights for itself, 32 at a time, a lane each.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) paged_join_kernel(Params P) {
   pdl_wait();
   pdl_trigger();
   const PagedArgs &a = P.a;
-  const uint32_t D = a.head_dim, H = a.n_heads, h = blockIdx.x, tk = blockIdx.y, b = blockIdx.z;
+  const uint32_t D = a.head_dim, H = a.n_heads, h = blockIdx.x, tk = blockIdx.y, b = blockIdx.z, S = P.splits;
+  const uint32_t d = threadIdx.x, lane = d & 31;
   const PagedItem it = paged_item(a, b);
   if (tk >= it.cnt) return;
   const size_t row = ((size_t)b * a.max_new + tk) * H + h, rows = (size_t)a.batch * a.max_new * H;
-  const float *ml = P.part + rows * P.splits * D + 2 * row * P.splits;
+  const float *ml = P.part + rows * S * D + 2 * row * S, *part = P.part + row * S * D;
   float m = -INFINITY, l = 0.f, acc = 0.f;
   bool nan = false;   // (fmaxf drops one)
-  for (uint32_t s = 0; s < P.splits; ++s) m = fmaxf(m, ml[2 * s]), nan |= isnan(ml[2 * s + 1]);
-  if (nan) m = NAN;
-  const uint32_t d = threadIdx.x;
-  for (uint32_t s = 0; s < P.splits; ++s) {
-    if (ml[2 * s + 1] == 0.f) continue;
-    const float c = expf(ml[2 * s] - m);
-    l = fmaf(ml[2 * s + 1], c, l);
-    if (d < D) acc = fmaf(P.part[(row * P.splits + s) * D + d], c, acc);
+  for (uint32_t s = lane; s < S; s += 32) m = fmaxf(m, ml[2 * s]), nan |= isnan(ml[2 * s + 1]);
+  m = __any_sync(0xffffffffu, nan) ? NAN : warp_max(m);
+  for (uint32_t s0 = 0; s0 < S; s0 += 32) {
+    const float ls = s0 + lane < S ? ml[2 * (s0 + lane) + 1] : 0.f;
+    const float w = ls == 0.f ? 0.f : expf(ml[2 * (s0 + lane)] - m);
+    l = fmaf(ls, w, l);
+    for (uint32_t s = s0; s < min(S, s0 + 32); s += 8) {
+      float v[8];
+#pragma unroll
+      for (uint32_t u = 0; u < 8; ++u) v[u] = d < D && s + u < S ? part[(size_t)(s + u) * D + d] : 0.f;
+#pragma unroll
+      for (uint32_t u = 0; u < 8; ++u) {
+        const float f = __shfl_sync(0xffffffffu, w, (s - s0 + u) & 31);
+        if (s + u < S && f != 0.f) acc = fmaf(v[u], f, acc);
+      }
+    }
   }
+  l = warp_sum(l);
   const float vs = a.v_scale ? __ldg(a.v_scale + h / P.G) : 1.f;
   const size_t out = (size_t)(it.first + tk) * H + h;
   if (d < D) st_elem(static_cast<T *>(a.out), out * D + d, l == 0.f ? 0.f : acc / l * vs);
   if (a.lse && d == 0) a.lse[out] = l == 0.f ? -INFINITY : m + logf(l);
 }
 
-// Shares of a sequence's keys: enough blocks for two a SM, 256 keys each at least.
-uint32_t splits_of(const PagedArgs &a) {
-  const uint32_t G = a.n_heads / a.n_kv, groups = (a.max_new * G + kRows - 1) / kRows;
-  const uint64_t blocks = (uint64_t)a.batch * a.n_kv * groups, want = (uint64_t)num_sms() * 2;
-  uint64_t s = (want + blocks - 1) / blocks, most = a.max_blocks;
-  if (a.window) {
-    const uint64_t w = ((uint64_t)a.window + a.max_new) / 256 + 1;
-    most = w < most ? w : most;
-  }
-  if (s > most) s = most;
-  return s < 1 ? 1u : (uint32_t)s;
+uint32_t group_rows(const PagedArgs &a) { return a.max_new * (a.n_heads / a.n_kv) <= 8 ? 8u : 16u; }
+
+uint64_t blocks_unsplit(const PagedArgs &a) {
+  const uint32_t G = a.n_heads / a.n_kv, R = group_rows(a);
+  return (uint64_t)a.batch * a.n_kv * ((a.max_new * G + R - 1) / R);
 }
 
-template <typename T, typename KV>
-cudaError_t launch_t(const PagedArgs &a, cudaStream_t s) {
+// The most shares of a sequence's keys: three blocks a SM (two for 16 rows), and a tile each. (A workspace is for any window.)
+uint32_t splits_most(const PagedArgs &a, uint64_t tiles) {
+  const uint64_t blocks = blocks_unsplit(a), s = ((group_rows(a) == 8 ? 3ull : 2ull) * num_sms() + blocks - 1) / blocks;
+  return (uint32_t)(s < tiles ? s : tiles);
+}
+
+// Shares: as many, or two tiles each where that still makes a block a SM.
+uint32_t splits_of(const PagedArgs &a) {
+  const uint32_t tile = tile_of(group_rows(a));
+  uint64_t tiles = 256ull / tile * a.max_blocks;
+  if (a.window) {
+    const uint64_t w = ((uint64_t)a.window + a.max_new) / tile + 2;
+    tiles = w < tiles ? w : tiles;
+  }
+  const uint32_t s = splits_most(a, tiles);
+  return s * 2ull > tiles && blocks_unsplit(a) * tiles > 2ull * num_sms() ? (uint32_t)((tiles + 1) / 2) : s;
+}
+
+template <typename T, typename KV, int R, int DV>
+cudaError_t launch_r(const PagedArgs &a, cudaStream_t s) {
   Params P;
   P.a = a;
   P.G = a.n_heads / a.n_kv;
-  P.groups = (a.max_new * P.G + kRows - 1) / kRows;
+  P.groups = (a.max_new * P.G + R - 1) / R;
   P.splits = splits_of(a);
   P.part = reinterpret_cast<float *>(static_cast<uint8_t *>(a.ws) + kWsHead);
-  const size_t smem = ((size_t)kTile * (a.head_dim + 1) + kRows * a.head_dim + kRows * kTile + 3 * kRows) * 4;
+  const uint32_t D4 = (a.head_dim + 3) / 4;
+  P.stages = smem_floats(D4, R, 2) * 4 <= kSmemMost ? 2 : 1;
+  const size_t smem = smem_floats(D4, R, P.stages) * 4;
   static RaisedLimit smem_set;
-  auto *k = paged_attn_kernel<T, KV>;
+  auto *k = paged_attn_kernel<T, KV, R, DV>;
   cudaError_t e = ensure_smem(k, smem, smem_set);
   if (e != cudaSuccess) return e;
   e = launch_pdl(k, dim3(P.splits, a.n_kv * P.groups, a.batch), dim3(kThreads), smem, s, P);
   if (e != cudaSuccess) return e;
   note_launches(1);
   if (P.splits > 1) {
-    e = launch_pdl(paged_join_kernel<T>, dim3(a.n_heads, a.max_new, a.batch), dim3(kThreads), 0, s, P);
+    e = launch_pdl(paged_join_kernel<T>, dim3(a.n_heads, a.max_new, a.batch), dim3((a.head_dim + 31) / 32 * 32), 0, s, P);
     if (e != cudaSuccess) return e;
     note_launches(1);
   }
   return cudaGetLastError();
+}
+template <typename T, typename KV>
+cudaError_t launch_t(const PagedArgs &a, cudaStream_t s) {
+  if (group_rows(a) == 8) return a.head_dim <= 128 ? launch_r<T, KV, 8, 1>(a, s) : launch_r<T, KV, 8, 2>(a, s);
+  return a.head_dim <= 128 ? launch_r<T, KV, 16, 1>(a, s) : launch_r<T, KV, 16, 2>(a, s);
 }
 
 }  // namespace
 
 size_t paged_attn_ws_bytes(const PagedArgs &a) {
   if (paged_attn_tc_takes(a)) return kWsHead + paged_attn_tc_ws_bytes(a);
-  const uint32_t S = splits_of(a);
+  const uint32_t S = splits_most(a, 256ull / tile_of(group_rows(a)) * a.max_blocks);
   return kWsHead + (S > 1 ? (size_t)a.batch * a.max_new * a.n_heads * S * (a.head_dim + 2) * 4 : 0);
 }
 
