@@ -38,6 +38,7 @@ namespace {
 constexpr uint32_t kTile = 128, kBox = kTile * 128;   // keys; bytes of a 128-byte column
 constexpr uint32_t kSegs = 4, kMaxSlots = 16;
 constexpr uint32_t kSmemSm = 228 * 1024, kSmemBlock = 1024;   // shared memory of an SM; reserved per block
+constexpr uint32_t kLeast = 2;    // places of a share at least: fewer parts to join
 constexpr float kNoRef = 3e38f;   // -reference of a row that has seen no key
 
 struct Segment {
@@ -407,8 +408,7 @@ __global__ void __launch_bounds__(Cfg<RP, F8>::kThreads, Cfg<RP, F8>::kPerSm)
       if (w < warp) before += S.scan[w];
       total += S.scan[w];
     }
-    // (no more shares than tiles, so that the parts of a segment are in neighbouring blocks)
-    const uint32_t shares = (uint32_t)min((uint64_t)gridDim.x, total), c = blockIdx.x;
+    const uint32_t shares = (uint32_t)min((uint64_t)gridDim.x, (total + kLeast - 1) / kLeast), c = blockIdx.x;
     const uint64_t from = c < shares ? mul_div(total, c, shares) : total;
     const uint64_t to = c < shares ? mul_div(total, c + 1, shares) : total;
     if (from < to && before <= from && from < before + own) {   // (one thread, or none)
@@ -1033,49 +1033,47 @@ __global__ void __launch_bounds__(Cfg<RP, F8>::kThreads, Cfg<RP, F8>::kPerSm)
   }
 }
 
-// Joins the parts of what begins in block blockIdx.x and goes on behind it: rows blockIdx.y, +
-// gridDim.y, .. each as the sum of its parts brought to the largest reference, in the order of the
-// blocks. Every warp works out the weights of the parts for itself, 32 at a time, a lane each; the first
-// parts are loaded before it is known how many there are.
-constexpr uint32_t kAhead = 8;
+// Joins the parts of what begins in block blockIdx.x and goes on behind it, each row as the sum of its
+// parts brought to the largest reference, in the order of the blocks. A block takes as many rows at
+// once as it has threads for. Every warp works out the weights of the parts for itself, 32 at a time, a lane each.
+constexpr uint32_t kJoinThreads = 512;
 template <int RP, bool F8>
-__global__ void __launch_bounds__(256) paged_join_tc_kernel(Params P, uint32_t blocks) {
+__global__ void __launch_bounds__(kJoinThreads) paged_join_tc_kernel(Params P, uint32_t blocks) {
   const PagedArgs &a = P.a;
-  const uint32_t c0 = blockIdx.x, D = a.head_dim, d = threadIdx.x, lane = d & 31;
+  const uint32_t c0 = blockIdx.x, D = a.head_dim, wide = (D + 31) & ~31u, at_once = kJoinThreads / wide;
+  const uint32_t d = threadIdx.x % wide, sub = threadIdx.x / wide, lane = threadIdx.x & 31;
   const float2 *ml = reinterpret_cast<const float2 *>(P.sums + (size_t)blocks * 2 * RP * D);
   // piece i: block c0 + i, what goes on (i = 0) or what began before
   auto at = [&](uint32_t i, uint32_t r) { return ((size_t)(c0 + i) * 2 + (i ? 0u : 1u)) * RP + r; };
-  auto there = [&](uint32_t i) { return c0 + i < blocks; };
   pdl_wait();
   pdl_trigger();
-  uint32_t r = blockIdx.y;
   const Part part = P.parts[c0];
-  float2 mine = there(lane) ? ml[at(lane, r)] : make_float2(0.f, 0.f);
-  float v[kAhead];
-#pragma unroll
-  for (uint32_t u = 0; u < kAhead; ++u) v[u] = d < D && there(u) ? P.sums[at(u, r) * D + d] : 0.f;
   const uint32_t n = part.blocks + 1;   // pieces
-  if (n == 1 || c0 + n > blocks) return;
-  while (r < part.nr) {
+  if (n == 1 || c0 + n > blocks || sub >= at_once) return;
+  for (uint32_t r = blockIdx.y * at_once + sub; r < part.nr; r += gridDim.y * at_once) {
+    const float2 mine = lane < n ? ml[at(lane, r)] : make_float2(-kNoRef, 0.f);
+    float v[8];
+#pragma unroll
+    for (uint32_t u = 0; u < 8; ++u) v[u] = d < D && u < n ? P.sums[at(u, r) * D + d] : 0.f;
     // the largest reference (a NaN if there is one)
-    float m = lane < n ? mine.x : -kNoRef;
+    float m = mine.x;
     for (uint32_t i = lane + 32; i < n; i += 32) m = max_nan(m, ml[at(i, r)].x);
 #pragma unroll
     for (int o = 16; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     float l = 0.f, acc = 0.f;
     for (uint32_t i0 = 0; i0 < n; i0 += 32) {
-      const float2 x = i0 == 0 ? mine : i0 + lane < n ? ml[at(i0 + lane, r)] : make_float2(0.f, 0.f);
-      const float w = i0 + lane >= n || x.x <= -kNoRef ? 0.f : ex2_approx(x.x - m);
-      if (w != 0.f) l = fmaf(x.y, w, l);   // (a lane without a part holds anything)
-      for (uint32_t i = i0; i < min(n, i0 + 32); i += kAhead) {
-        if (i) {
+      const float2 x = i0 == 0 ? mine : i0 + lane < n ? ml[at(i0 + lane, r)] : make_float2(-kNoRef, 0.f);
+      const float w = x.x <= -kNoRef ? 0.f : ex2_approx(x.x - m);
+      l = fmaf(x.y, w, l);
+      for (uint32_t i = i0; i < min(n, i0 + 32); i += 8) {
+        float next[8];   // (the next eight on their way)
 #pragma unroll
-          for (uint32_t u = 0; u < kAhead; ++u) v[u] = d < D && i + u < n ? P.sums[at(i + u, r) * D + d] : 0.f;
-        }
+        for (uint32_t u = 0; u < 8; ++u) next[u] = d < D && i + 8 + u < n ? P.sums[at(i + 8 + u, r) * D + d] : 0.f;
 #pragma unroll
-        for (uint32_t u = 0; u < kAhead; ++u) {
+        for (uint32_t u = 0; u < 8; ++u) {
           const float f = __shfl_sync(0xffffffffu, w, (i - i0 + u) & 31);
           if (i + u < n && f != 0.f) acc = fmaf(v[u], f, acc);
+          v[u] = next[u];
         }
       }
     }
@@ -1085,12 +1083,6 @@ __global__ void __launch_bounds__(256) paged_join_tc_kernel(Params P, uint32_t b
     const float scale = l == 0.f ? 0.f : (F8 ? __ldg(a.v_scale + part.kh) : 1.f) / l;
     if (d < D) static_cast<__nv_bfloat16 *>(a.out)[(size_t)out * D + d] = __float2bfloat16_rn(acc * scale);
     if (a.lse && d == 0) a.lse[out] = l == 0.f ? -INFINITY : (log2f(l) + m) * 0.6931471805599453f;
-    r += gridDim.y;
-    if (r < part.nr) {
-      mine = there(lane) ? ml[at(lane, r)] : make_float2(0.f, 0.f);
-#pragma unroll
-      for (uint32_t u = 0; u < kAhead; ++u) v[u] = d < D && there(u) ? P.sums[at(u, r) * D + d] : 0.f;
-    }
   }
 }
 
@@ -1156,7 +1148,7 @@ cudaError_t launch_rp(const PagedArgs &a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   note_launches(1);
   if (blocks > 1) {   // (a lone block holds every segment whole)
-    e = launch_pdl(paged_join_tc_kernel<RP, F8>, dim3(blocks - 1, 8), dim3((a.head_dim + 31) / 32 * 32), 0, s, P, blocks);
+    e = launch_pdl(paged_join_tc_kernel<RP, F8>, dim3(blocks - 1, RP / 4), dim3(kJoinThreads), 0, s, P, blocks);
     if (e != cudaSuccess) return e;
     note_launches(1);
   }

@@ -38,49 +38,60 @@ struct RopeKernelArgs {
   uint32_t tok_par, row_par, slice;
 };
 
+// E elements of a row in one access of 2 to 16 bytes.
+template <int BYTES>
+struct Word {};
+template <>
+struct Word<16> {
+  using type = uint4;
+};
+template <>
+struct Word<8> {
+  using type = uint2;
+};
+template <>
+struct Word<4> {
+  using type = uint32_t;
+};
+template <>
+struct Word<2> {
+  using type = uint16_t;
+};
+template <>
+struct Word<1> {
+  using type = uint8_t;
+};
 template <typename T, int E>
-struct Vec {
-  alignas(E * sizeof(T) == 16 ? 16 : sizeof(T)) T x[E];
-  __device__ __forceinline__ void load(const T *p) {
-    if (E * sizeof(T) == 16) {
-      *reinterpret_cast<uint4 *>(x) = *reinterpret_cast<const uint4 *>(p);
-    } else {
-#pragma unroll
-      for (int i = 0; i < E; ++i) x[i] = p[i];
-    }
-  }
+struct alignas(E * sizeof(T)) Vec {
+  using W = typename Word<E * sizeof(T)>::type;
+  T x[E];
+  __device__ __forceinline__ void load(const T *p) { *reinterpret_cast<W *>(x) = *reinterpret_cast<const W *>(p); }
 };
 template <typename T, int E>
 __device__ __forceinline__ void put(T *p, const float (&v)[E]) {
+  using W = typename Word<E * sizeof(T)>::type;
   Vec<T, E> o;
 #pragma unroll
   for (int i = 0; i < E; ++i) st_elem(o.x, i, v[i]);
-  if (E * sizeof(T) == 16) {
-    *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<const uint4 *>(o.x);
-  } else {
-#pragma unroll
-    for (int i = 0; i < E; ++i) p[i] = o.x[i];
-  }
+  *reinterpret_cast<W *>(p) = *reinterpret_cast<const W *>(o.x);
 }
 // E codes of values already multiplied by the scale's reciprocal.
 template <int E>
 __device__ __forceinline__ void put_e4m3(uint8_t *p, const float (&v)[E]) {
+  using W = typename Word<E>::type;
+  alignas(E) uint8_t c[E];
   if (E == 1) {
-    *p = (uint8_t)__nv_cvt_float_to_fp8(v[0], __NV_SATFINITE, __NV_E4M3);
+    c[0] = (uint8_t)__nv_cvt_float_to_fp8(v[0], __NV_SATFINITE, __NV_E4M3);
   } else {
-    uint16_t h[E / 2 ? E / 2 : 1];
 #pragma unroll
     for (int i = 0; i + 1 < E; i += 2)
-      h[i / 2] = __nv_cvt_float2_to_fp8x2(make_float2(v[i], v[i + 1 < E ? i + 1 : i]), __NV_SATFINITE, __NV_E4M3);
-    if (E == 8)
-      *reinterpret_cast<uint2 *>(p) = make_uint2(h[0] | (uint32_t)h[E > 2 ? 1 : 0] << 16,
-                                                 h[E > 4 ? 2 : 0] | (uint32_t)h[E > 6 ? 3 : 0] << 16);
-    else
-      *reinterpret_cast<uint32_t *>(p) = h[0] | (uint32_t)h[E > 2 ? 1 : 0] << 16;
+      *reinterpret_cast<uint16_t *>(c + i) =
+          __nv_cvt_float2_to_fp8x2(make_float2(v[i], v[i + 1 < E ? i + 1 : i]), __NV_SATFINITE, __NV_E4M3);
   }
+  *reinterpret_cast<W *>(p) = *reinterpret_cast<const W *>(c);
 }
 
-// E: elements of a chunk (16 bytes; 1 where rows or the rotated part do not start on
+// E: elements of a chunk (16 bytes, fewer where rows or the rotated part do not start on
 // 16 bytes). F8: the cache holds 8-bit floats. U: rows in flight per thread.
 template <typename T, bool F8, int E, int U>
 __global__ void __launch_bounds__(kThreads, 2) rope_kernel(RopeKernelArgs a) {
@@ -269,8 +280,8 @@ cudaError_t launch_rows(RopeKernelArgs a, cudaStream_t s) {
     all |= reinterpret_cast<uintptr_t>(a.src[1]) | reinterpret_cast<uintptr_t>(a.src[2]);
     sizes |= a.stride[1] | a.stride[2];
   }
-  const bool vec = all % 16 == 0 && sizes % EV == 0;
-  const uint32_t e = vec ? EV : 1;
+  uint32_t e = EV;   // the widest chunk that divides all
+  while (e > 1 && (all % (e * sizeof(T)) || sizes % e)) e /= 2;
   const uint32_t nr = a.half ? a.n_rot / (2 * e) : 0;
   // (D - n_rot chunks that no half pairs, two to a thread)
   const uint32_t rest = (a.half ? a.D - a.n_rot : a.D) / e;
@@ -294,13 +305,15 @@ cudaError_t launch_rows(RopeKernelArgs a, cudaStream_t s) {
         a.row_par = rp;
         a.tok_par = tp;
       }
-      if (rp == 1) break;
     }
     a.slice = a.rows;
   }
   const uint32_t toks = (a.n + a.tok_par - 1) / a.tok_par;
   const dim3 grid(toks < sms * 4 ? toks : sms * 4, (a.rows + a.slice - 1) / a.slice);
-  auto *k = vec ? rope_kernel<T, F8, EV, 4> : rope_kernel<T, F8, 1, 4>;
+  auto *k = e == 8   ? rope_kernel<T, F8, EV, 4>
+            : e == 4 ? rope_kernel<T, F8, 4, 4>
+            : e == 2 ? rope_kernel<T, F8, 2, 4>
+                     : rope_kernel<T, F8, 1, 4>;
   const cudaError_t err = launch_pdl(k, grid, dim3(kThreads), 0, s, a);
   if (err != cudaSuccess) return err;
   note_launches(1);

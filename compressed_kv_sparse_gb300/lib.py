@@ -574,6 +574,7 @@ SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}   # DS4A_SCALE_*
 _DTYPE = {"f32": DS4A_F32, "bf16": DS4A_BF16, "e4m3": DS4A_E4M3}
 _TORCH = {"f32": torch.float32, "bf16": torch.bfloat16, "e4m3": torch.float8_e4m3fn}
 _TORCH_DTYPE = {torch.float32: DS4A_F32, torch.bfloat16: DS4A_BF16}
+_INTS = (torch.int32, torch.uint32)
 
 
 class Rope:
@@ -606,25 +607,32 @@ class Rope:
 
 def _heads(t: torch.Tensor, n: int, heads: int, dim: int, dt: torch.dtype, dev: int, what: str) -> int:
     """Elements from token to token of t [n][heads][dim], whole tokens that may be strided."""
-    s = t.stride()
-    if not (t.dtype is dt and t.shape == (n, heads, dim) and (dim == 1 or s[2] == 1)
-            and (heads == 1 or s[1] == dim) and t.get_device() == dev):
+    s0, s1, s2 = t.stride()
+    if not (t.dtype is dt and t.shape == (n, heads, dim) and (s2 == 1 or dim == 1)
+            and (s1 == dim or heads == 1) and t.get_device() == dev):
         raise ArgumentError(f"{what}: [{n}][{heads}][{dim}] of {dt} with whole tokens, on the call's device")
-    return s[0] if n > 1 else heads * dim
+    return s0 if n > 1 else heads * dim   # (one token: its stride is whatever the slice left)
 
 
 def ds4a_rope(rope: Rope, pos: torch.Tensor, x: torch.Tensor, y: torch.Tensor, inverse: bool = False, stream=None):
     """Heads x [n][H][D] rotated at pos [n] int32 into y (which may be x). The tokens of both may be
     strided; inverse: rotated back (also the gradient of the rotation)."""
     dev, n = rope.dev, pos.numel()
-    _need(pos.dtype is _I32 and x.dim() == 3 and x.dtype in _TORCH_DTYPE, "pos: [n] int32; x: [n][heads][dim]")
-    H, D, dt = x.size(1), x.size(2), x.dtype
-    xs, ys = _heads(x, n, H, D, dt, dev, "x"), _heads(y, n, H, D, dt, dev, "y")
+    # (the checks of these calls in line: they are a good part of a small call)
+    if not (pos.dtype is _I32 and x.dim() == 3 and y.dim() == 3):
+        raise ArgumentError("pos: [n] int32; x, y: [n][heads][dim]")
+    _, H, D = x.shape
+    dt = _TORCH_DTYPE.get(x.dtype)
+    if dt is None:
+        raise ArgumentError("x: fp32 or bf16")
+    xs = _heads(x, n, H, D, x.dtype, dev, "x")
+    ys = xs if y is x else _heads(y, n, H, D, x.dtype, dev, "y")
     if n == 0:
         return
-    _check((_lib or load()).ds4a_rope(rope._refs[1 if inverse else 0], _TORCH_DTYPE[dt], n, _ptr(pos, dev),
-                                      x.data_ptr(), xs, H, D, y.data_ptr(), ys, _stream(stream, dev)),
-           "ds4a_rope")
+    st = (_lib or load()).ds4a_rope(rope._refs[1 if inverse else 0], dt, n, _ptr(pos, dev), x.data_ptr(), xs, H, D,
+                                    y.data_ptr(), ys, _stream(stream, dev))
+    if st:
+        raise Ds4aError(st, "ds4a_rope")
 
 
 class KvCache:
@@ -683,10 +691,10 @@ def ds4a_kv_append(cache: KvCache, tok_seq: torch.Tensor, tok_pos: torch.Tensor,
     dev, n, K, D, dt = cache.dev, tok_seq.numel(), cache.n_kv_heads, cache.head_dim, cache.torch_dtype
     if not (tok_seq.dtype is _I32 and tok_pos.dtype is _I32 and tok_pos.numel() == n):
         raise ArgumentError("tok_seq, tok_pos: [n] int32")
+    if not (k.dim() == 3 and v.dim() == 3 and (q is None or q.dim() == 3) and (q is None) == (q_out is None)):
+        raise ArgumentError("k, v: [n][n_kv_heads][head_dim]; q: [n][heads][head_dim] with q_out, or neither")
     ks, vs, qs, H = _heads(k, n, K, D, dt, dev, "k"), _heads(v, n, K, D, dt, dev, "v"), 0, 0
-    _need((q is None) == (q_out is None), "q and q_out: both or neither")
     if q is not None:
-        _need(q.dim() == 3, "q: [n][heads][head_dim]")
         H = q.size(1)
         qs = _heads(q, n, H, D, dt, dev, "q")
         if not (q_out.dtype is dt and q_out.numel() == n * H * D):
@@ -730,25 +738,29 @@ def ds4a_verify_drafts(target: torch.Tensor, drafts: torch.Tensor, u_accept: tor
     """Which of drafts [B][N] int32 stand against the target's probabilities [tokens][V] (rows may be
     strided), into tokens [B][N + 1] and n_out [B] int32; ctx_out [B]: what each sequence then holds, from
     seq_pos [B]. draft_probs [B][N][V] or None (greedy drafts); cu_len as in ds4a_paged_attn_decode."""
-    dev = target.get_device()
-    _need(target.dim() == 2 and drafts.dim() == 2 and target.dtype in _TORCH_DTYPE, "target: [tokens][vocab]; drafts: [batch][N]")
-    (B, N), V = drafts.shape, target.size(1)
-    rows, ints = target.size(0), (_I32, torch.uint32)
-    if not ((V == 1 or target.stride(1) == 1) and drafts.dtype is _I32 and u_accept.dtype is torch.float32
-            and u_sample.dtype is torch.float32 and u_accept.numel() == B * N and u_sample.numel() == B
-            and tokens.dtype is _I32 and tokens.numel() == B * (N + 1)):
+    dev, dt, f32 = target.get_device(), _TORCH_DTYPE.get(target.dtype), torch.float32
+    if not (target.dim() == 2 and drafts.dim() == 2 and dt is not None):
+        raise ArgumentError("target: [tokens][vocab] fp32 or bf16; drafts: [batch][N]")
+    (B, N), (rows, V), (s0, s1) = drafts.shape, target.shape, target.stride()
+    if not ((s1 == 1 or V == 1) and drafts.dtype is _I32 and u_accept.dtype is f32 and u_sample.dtype is f32
+            and u_accept.numel() == B * N and u_sample.numel() == B and tokens.dtype is _I32
+            and tokens.numel() == B * (N + 1)):
         raise ArgumentError("target: whole rows; drafts [B][N], tokens [B][N + 1] int32; u_accept [B][N], u_sample [B] fp32")
     if not (draft_probs is None or (draft_probs.dtype is target.dtype and draft_probs.numel() == B * N * V)):
         raise ArgumentError("draft_probs: [batch][N][vocab] of the target's type")
-    for t, m in ((n_out, B), (seq_pos, B), (ctx_out, B), (cu_len, B + 1)):
-        if not (t is None or (t.dtype in ints and t.numel() == m)):
-            raise ArgumentError("n_out, seq_pos, ctx_out: [batch], cu_len: [batch + 1], int32 or uint32")
-    _need(cu_len is not None or rows == B * (N + 1), "target: N + 1 rows for each sequence without cu_len")
-    _check((_lib or load()).ds4a_verify_drafts(
-        _TORCH_DTYPE[target.dtype], B, N, V, _ptr(cu_len, dev), _ptr(seq_pos, dev), _ptr(drafts, dev),
-        target.data_ptr(), target.stride(0) if rows > 1 else V, _ptr(draft_probs, dev), _ptr(u_accept, dev),
-        _ptr(u_sample, dev), _ptr(tokens, dev), _ptr(n_out, dev), _ptr(ctx_out, dev), _stream(stream, dev)),
-        "ds4a_verify_drafts")
+    if not (n_out.dtype in _INTS and n_out.numel() == B
+            and (seq_pos is None or (seq_pos.dtype in _INTS and seq_pos.numel() == B))
+            and (ctx_out is None or (ctx_out.dtype in _INTS and ctx_out.numel() == B))
+            and (cu_len is None or (cu_len.dtype in _INTS and cu_len.numel() == B + 1))):
+        raise ArgumentError("n_out, seq_pos, ctx_out: [batch], cu_len: [batch + 1], int32 or uint32")
+    if cu_len is None and rows != B * (N + 1):
+        raise ArgumentError("target: N + 1 rows for each sequence without cu_len")
+    st = (_lib or load()).ds4a_verify_drafts(
+        dt, B, N, V, _ptr(cu_len, dev), _ptr(seq_pos, dev), _ptr(drafts, dev), target.data_ptr(), s0 if rows > 1 else V,
+        _ptr(draft_probs, dev), _ptr(u_accept, dev), _ptr(u_sample, dev), _ptr(tokens, dev), _ptr(n_out, dev),
+        _ptr(ctx_out, dev), _stream(stream, dev))
+    if st:
+        raise Ds4aError(st, "ds4a_verify_drafts")
 
 
 STATIC_SCRATCH_BYTES = 8 << 20
