@@ -64,6 +64,37 @@ def test_attention(old, new, H, K, D, window, dtype, kvd):
 
 
 @pytest.mark.parametrize("kvd", ["bf16", "e4m3"])
+@pytest.mark.parametrize("D", [16, 64, 80, 112, 128, 176, 192, 240, 256])
+@pytest.mark.parametrize("T,G", [(1, 3), (2, 7), (4, 8), (5, 8), (7, 16)])
+def test_every_row_count_and_width(T, G, D, kvd):
+    """Each number of rows a block takes, on each width of keys and values."""
+    step = Step(lib_(), T * G + D, [200, 31, 3], [T, max(1, T - 2), T], 2 * G, 2, D, "bf16", kvd)
+    c, cu = step.on_gpu()
+    check(step, *run(step, c, cu), 1 / np.sqrt(D))
+
+
+@pytest.mark.parametrize("dtype,kvd", [("bf16", "bf16"), ("bf16", "e4m3"), ("f32", "f32")])
+@pytest.mark.parametrize("scale", [0.0, -0.3, 2.0])
+def test_scales_and_a_window_wider_than_the_context(dtype, kvd, scale):
+    step = Step(lib_(), 21, [290, 7], [2, 1], 8, 2, 64, dtype, kvd, window=5000)
+    c, cu = step.on_gpu()
+    check(step, *run(step, c, cu, scale=scale), scale)
+
+
+@pytest.mark.parametrize("dtype,kvd", [("bf16", "bf16"), ("bf16", "e4m3"), ("f32", "f32")])
+def test_many_sequences_some_of_them_free(dtype, kvd):
+    """More sequences than blocks, most of them short; free rows in between and at the ends."""
+    rng = np.random.default_rng(5)
+    B = 700
+    old, new = rng.integers(0, 40, B), rng.integers(0, 3, B)
+    old[350], new[350], new[:3], new[-40:] = 1500, 2, 0, 0
+    old[new == 0] = 0
+    step = Step(lib_(), 22, list(old), list(new), 4, 2, 32, dtype, kvd)
+    c, cu = step.on_gpu()
+    check(step, *run(step, c, cu), 1 / np.sqrt(32))
+
+
+@pytest.mark.parametrize("kvd", ["bf16", "e4m3"])
 @pytest.mark.parametrize("B", [1, 40])
 def test_long_and_many(B, kvd):
     """One sequence shared among all SMs, and a ragged batch that several share."""
