@@ -39,6 +39,7 @@ constexpr uint32_t kTile = 128, kBox = kTile * 128;   // keys; bytes of a 128-by
 constexpr uint32_t kSegs = 4, kMaxSlots = 16;
 constexpr uint32_t kSmemSm = 228 * 1024, kSmemBlock = 1024;   // shared memory of an SM; reserved per block
 constexpr uint32_t kLeast = 2;    // places of a share at least: fewer parts to join
+constexpr uint32_t kWholeTiles = 4;   // the most tiles of a sequence that is not divided
 constexpr float kNoRef = 3e38f;   // -reference of a row that has seen no key
 
 struct Segment {
@@ -62,6 +63,7 @@ struct Params {
   uint32_t n_slots, n_q, n_p;   // units, query tiles and weight tiles held
   uint32_t g_mul;       // 2^32 / G + 1 (rows are below 2^18), 0: G is 1
   uint32_t q_vec;       // queries start on 16 bytes
+  uint32_t whole;       // segments are not divided: no parts, a place each
   float c2;             // scale * log2(e)
   Part *parts;          // [blocks]
   // [blocks][2][RP][D], then (reference, sum) [blocks][2][RP][2]: of what began before a block, and of
@@ -277,38 +279,51 @@ struct Ring {   // slot and parity of the loads, counted from the block's first
 };
 
 // A value row of an unseen key, or the NaNs and infinities of one that only some rows see, made zeros in
-// shared memory: 0 times them would be a NaN. Returns whether there were any of the latter.
+// shared memory: 0 times them would be a NaN. Returns whether there were any of the latter. (Lanes start a
+// piece of 16 bytes apart, so that eight of them cover all banks.)
 template <bool F8>
-__device__ __noinline__ bool clean_row(uint32_t row, uint32_t ubox, bool all) {
+__device__ __noinline__ bool clean_row(uint32_t row, uint32_t ubox, bool all, uint32_t lane) {
   bool found = false;
-  for (uint32_t x = 0; x < ubox; ++x)
-    for (uint32_t c = 0; c < 8; ++c) {
-      const uint32_t at = row + x * kBox + 16 * c;
-      uint32_t v[4] = {0, 0, 0, 0};
-      if (!all) {
+  for (uint32_t x = 0; x < ubox; ++x, row += kBox) {
+    if (all) {
+#pragma unroll
+      for (uint32_t c = 0; c < 8; ++c)
+        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(row + 16 * ((c + lane) & 7)), "r"(0u) : "memory");
+      continue;
+    }
+#pragma unroll 1
+    for (uint32_t c = 0; c < 8; c += 4) {
+      uint32_t v[4][4];
+#pragma unroll
+      for (uint32_t u = 0; u < 4; ++u)
         asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                     : "r"(at));
-        bool here = false;
+                     : "=r"(v[u][0]), "=r"(v[u][1]), "=r"(v[u][2]), "=r"(v[u][3])
+                     : "r"(row + 16 * ((c + u + lane) & 7)));
+      bool here = false;
+#pragma unroll
+      for (uint32_t u = 0; u < 4; ++u)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           uint32_t keep = 0;
           if (F8) {
 #pragma unroll
-            for (int k = 0; k < 32; k += 8) keep |= (v[i] >> k & 0x7fu) == 0x7fu ? 0u : 0xffu << k;
+            for (int k = 0; k < 32; k += 8) keep |= (v[u][i] >> k & 0x7fu) == 0x7fu ? 0u : 0xffu << k;
           } else {
 #pragma unroll
-            for (int k = 0; k < 32; k += 16) keep |= (v[i] >> k & 0x7f80u) == 0x7f80u ? 0u : 0xffffu << k;
+            for (int k = 0; k < 32; k += 16) keep |= (v[u][i] >> k & 0x7f80u) == 0x7f80u ? 0u : 0xffffu << k;
           }
           here |= keep != 0xffffffffu;
-          v[i] &= keep;
+          v[u][i] &= keep;
         }
-        if (!here) continue;
-        found = true;
-      }
-      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
-                   : "memory");
+      if (!here) continue;
+      found = true;
+#pragma unroll
+      for (uint32_t u = 0; u < 4; ++u)
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(row + 16 * ((c + u + lane) & 7)), "r"(v[u][0]),
+                     "r"(v[u][1]), "r"(v[u][2]), "r"(v[u][3])
+                     : "memory");
     }
+  }
   return found;
 }
 
@@ -389,7 +404,7 @@ __global__ void __launch_bounds__(Cfg<RP, F8>::kThreads, Cfg<RP, F8>::kPerSm)
     auto weight = [&](uint32_t b) {
       const PagedItem it = paged_item(a, b);
       const uint32_t tiles = tiles_of(it);
-      return (uint64_t)(tiles ? tiles + C::kStart : 0u) * a.n_kv * ((it.cnt * P.G + RP - 1) / RP);
+      return (uint64_t)(tiles ? P.whole ? 1u : tiles + C::kStart : 0u) * a.n_kv * ((it.cnt * P.G + RP - 1) / RP);
     };
     uint64_t own = 0;
     for (uint32_t b = b0; b < b1; ++b) own += weight(b);
@@ -408,7 +423,8 @@ __global__ void __launch_bounds__(Cfg<RP, F8>::kThreads, Cfg<RP, F8>::kPerSm)
       if (w < warp) before += S.scan[w];
       total += S.scan[w];
     }
-    const uint32_t shares = (uint32_t)min((uint64_t)gridDim.x, (total + kLeast - 1) / kLeast), c = blockIdx.x;
+    const uint32_t least = P.whole ? 1u : kLeast;
+    const uint32_t shares = (uint32_t)min((uint64_t)gridDim.x, (total + least - 1) / least), c = blockIdx.x;
     const uint64_t from = c < shares ? mul_div(total, c, shares) : total;
     const uint64_t to = c < shares ? mul_div(total, c + 1, shares) : total;
     if (from < to && before <= from && from < before + own) {   // (one thread, or none)
@@ -589,7 +605,7 @@ __global__ void __launch_bounds__(Cfg<RP, F8>::kThreads, Cfg<RP, F8>::kPerSm)
       it.hi = __shfl_sync(0xffffffffu, mine.hi, src);
       const uint32_t tiles = tiles_of(it), groups = (it.cnt * P.G + RP - 1) / RP;
       if (tiles) {
-        const uint32_t places = tiles + C::kStart;
+        const uint32_t places = P.whole ? 1u : tiles + C::kStart;
         uint32_t kh = 0, rg = 0, o = 0;   // o: the first place of the segment here
         if (off) {
           const uint32_t i = (uint32_t)mul_div(off, 1, places);
@@ -599,7 +615,8 @@ __global__ void __launch_bounds__(Cfg<RP, F8>::kThreads, Cfg<RP, F8>::kPerSm)
         }
         for (; kh < a.n_kv && left; o = 0) {
           const uint32_t n = (uint32_t)min((uint64_t)(places - o), left), e = o + n;
-          const uint32_t t0 = o > C::kStart ? o - C::kStart : 0u, nt = e > C::kStart ? e - C::kStart - t0 : 0u;
+          const uint32_t t0 = o > C::kStart ? o - C::kStart : 0u;
+          const uint32_t nt = P.whole ? tiles : e > C::kStart ? e - C::kStart - t0 : 0u;
           left -= n;
           if (nt == 0) break;   // (the share ends before the segment's first tile)
           if (!(ok = mbar_wait_sleep(&S.seg_empty[s % kSegs], ((s / kSegs) & 1) ^ 1, err))) break;
@@ -680,7 +697,17 @@ __global__ void __launch_bounds__(Cfg<RP, F8>::kThreads, Cfg<RP, F8>::kPerSm)
         const uint32_t pieces = P.nbox * 8, rpp = 32 / pieces, sub = lane / pieces, c = lane % pieces;
         uint32_t tok = tok_r0, g = g_r0;
         advance(tok, g, sub);
-        if (sub < rpp) {
+        if (P.q_vec) {   // (all of them on their way at once)
+          const size_t wrap = a.q_stride - (size_t)P.G * D;   // from behind a token's heads to the next token's
+          const __nv_bfloat16 *p = q + (sg.first + tok) * a.q_stride + (size_t)(sg.kh * P.G + g) * D + 8 * c;
+          for (uint32_t r = sub; sub < rpp && r < rows; r += rpp) {
+            const bool in = r < sg.nr && 8 * c < D;
+            cp_async16(place(r, c), in ? p : q, in ? 16u : 0u);
+            p += rpp * D;
+            for (g += rpp; g >= P.G; g -= P.G) p += wrap;
+          }
+          asm volatile("cp.async.wait_all;" ::: "memory");
+        } else if (sub < rpp) {
           for (uint32_t r0 = sub; r0 < rows; r0 += 8 * rpp) {
             uint4 v[8];
 #pragma unroll
@@ -945,7 +972,7 @@ __global__ void __launch_bounds__(Cfg<RP, F8>::kThreads, Cfg<RP, F8>::kPerSm)
           for (uint32_t m = 0; m < P.nmb; ++m) {
             const uint32_t k = (base + place_v(j, sg.nt)) * P.nmb + m, slot = k % P.n_slots;
             ok = ok && wait_chain(&S.full[slot], (k / P.n_slots) & 1, err);
-            if (!all && clean_row<F8>(smem_u32(s_slot + slot * slot_bytes) + me * 128, P.ubox, !any)) S.bad = 1;
+            if (!all && clean_row<F8>(smem_u32(s_slot + slot * slot_bytes) + me * 128, P.ubox, !any, lane)) S.bad = 1;
             __syncwarp();
           }
         }
@@ -1092,14 +1119,17 @@ uint32_t rows_of(const PagedArgs &a) {
   return r <= 8 ? 8 : r <= 16 ? 16 : r <= 32 ? 32 : 64;
 }
 
+// The most tiles that a sequence can have.
+uint64_t most_tiles(const PagedArgs &a) {
+  const uint64_t all = 2ull * a.max_blocks, w = ((uint64_t)a.window + a.max_new) / kTile + 2;
+  return a.window && w < all ? w : all;
+}
+
 // Blocks: one or two a SM (Cfg::kPerSm), or one a tile where there can be no more tiles.
 uint32_t blocks_of(const PagedArgs &a) {
   const uint32_t rp = rows_of(a), groups = (a.max_new * (a.n_heads / a.n_kv) + rp - 1) / rp;
-  uint64_t tiles = 2ull * a.max_blocks;
-  if (a.window) {
-    const uint64_t w = ((uint64_t)a.window + a.max_new) / kTile + 2;
-    tiles = w < tiles ? w : tiles;
-  }
+  uint64_t tiles = most_tiles(a);
+  if (tiles <= kWholeTiles) tiles = 1;
   const uint64_t most = tiles * a.batch * a.n_kv * groups, sms = (uint64_t)num_sms() * (rp <= 16 ? 2 : 1);
   return (uint32_t)(most < sms ? most : sms);
 }
@@ -1127,6 +1157,7 @@ cudaError_t launch_rp(const PagedArgs &a, cudaStream_t s) {
   P.q_vec = aligned(16, {a.q}) && a.q_stride % 8 == 0;
   P.c2 = a.scale * 1.4426950408889634f;
   if (fabsf(P.c2) < 0x1p-126f) P.c2 = 0x1p-126f;   // (0 times the -infinity of an unseen key is a NaN)
+  P.whole = most_tiles(a) <= kWholeTiles;
   P.ubox = F8 || P.nbox == 1 ? 1 : 2;
   P.g_mul = P.G > 1 ? (uint32_t)((1ull << 32) / P.G) + 1u : 0u;
   const uint32_t blocks = blocks_of(a), slot = P.ubox * kBox, q = C::kQRows * P.nbox * 128u;
@@ -1147,8 +1178,10 @@ cudaError_t launch_rp(const PagedArgs &a, cudaStream_t s) {
   e = launch_pdl(k, dim3(blocks), dim3(C::kThreads), smem, s, mk, mv, P);
   if (e != cudaSuccess) return e;
   note_launches(1);
-  if (blocks > 1) {   // (a lone block holds every segment whole)
-    e = launch_pdl(paged_join_tc_kernel<RP, F8>, dim3(blocks - 1, RP < 32 ? RP / 2 : 16), dim3(kJoinThreads), 0, s, P, blocks);
+  if (blocks > 1 && !P.whole) {   // (a lone block holds every segment whole)
+    const uint32_t at_once = kJoinThreads / ((a.head_dim + 31) / 32 * 32), most = RP < 32 ? RP : 32;
+    e = launch_pdl(paged_join_tc_kernel<RP, F8>, dim3(blocks - 1, (most + at_once - 1) / at_once), dim3(kJoinThreads), 0, s,
+                   P, blocks);
     if (e != cudaSuccess) return e;
     note_launches(1);
   }
