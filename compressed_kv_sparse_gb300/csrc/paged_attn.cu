@@ -22,8 +22,10 @@ constexpr uint32_t kThreads = 256, kWarps = kThreads / 32;
 // Keys of a tile: 32 and two or three blocks a SM for 8 rows (8 x 8,000 tokens of 8 heads of 128 dims: 159 us,
 // 64 keys 251); 64 for 16 rows (3 x 1,024 tokens, 10 rows of 80 dims: 13.7 us, 32 keys 15.5).
 __host__ __device__ constexpr uint32_t tile_of(uint32_t R) { return R == 8 ? 32 : 64; }
+// Blocks that an SM's registers have room for (16 rows of 256 dims take 249 a thread).
+__host__ __device__ constexpr uint32_t blocks_per_sm(int R, int DV) { return R == 16 && DV == 2 ? 1 : 2; }
 constexpr uint32_t kWsHead = 256;   // the status word's line
-constexpr uint32_t kSmemMost = 227 * 1024;
+constexpr uint32_t kSmemMost = 227 * 1024, kSmemSm = 228 * 1024, kSmemBlock = 1024;
 
 struct Params {
   PagedArgs a;
@@ -48,7 +50,7 @@ __host__ __device__ constexpr uint32_t smem_floats(uint32_t D4, uint32_t R, uint
 
 // R: rows of a group. DV: fours of dims per lane (D <= 128 DV).
 template <typename T, typename KV, int R, int DV>
-__global__ void __launch_bounds__(kThreads) paged_attn_kernel(Params P) {
+__global__ void __launch_bounds__(kThreads, blocks_per_sm(R, DV)) paged_attn_kernel(Params P) {
   constexpr uint32_t kTile = tile_of(R), kParts = kThreads / kTile;
   extern __shared__ __align__(16) float sm[];
   const PagedArgs &a = P.a;
@@ -223,36 +225,34 @@ __global__ void __launch_bounds__(kThreads) paged_attn_kernel(Params P) {
     if (P.stages == 1 && tile + 1 < t1) load(0, tile + 1);
   }
   __syncthreads();
-  // ---- the warps' sums, added in order through shared memory: [warp][VS] a row at a time
+  // ---- the warps' sums, added in order through shared memory: [warp][R][VS] in the tiles' place
   float *red = s_k;
-  for (uint32_t r = 0; r < nr; ++r) {
 #pragma unroll
-    for (int q = 0; q < R; ++q)   // (registers are not indexed)
-      if ((uint32_t)q == r)
+  for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int i = 0; i < DV; ++i)
-          if (lane + 32 * i < D4) *reinterpret_cast<float4 *>(red + warp * VS + 4 * (lane + 32 * i)) = acc[q][i];
-    __syncthreads();
+    for (int i = 0; i < DV; ++i)
+      if (lane + 32 * i < D4) *reinterpret_cast<float4 *>(red + (warp * R + r) * VS + 4 * (lane + 32 * i)) = acc[r][i];
+  __syncthreads();
+  for (uint32_t i = t; i < nr * VS; i += kThreads) {
+    const uint32_t r = i / VS, d = i % VS;
+    if (d >= D) continue;
     const float m = s_m[r], l = s_l[r];
-    for (uint32_t d = t; d < D; d += kThreads) {
-      float o = 0.f;
+    float o = 0.f;
 #pragma unroll
-      for (uint32_t w = 0; w < kWarps; ++w) o += red[w * VS + d];
-      if (P.splits == 1) {
-        const size_t row = (size_t)(it.first + token(r)) * H + head(r);
-        st_elem(static_cast<T *>(a.out), row * D + d, l == 0.f ? 0.f : o / l * vs);
-        if (a.lse && d == 0) a.lse[row] = l == 0.f ? -INFINITY : m + logf(l);
-      } else {
-        const size_t row = ((size_t)b * a.max_new + token(r)) * H + head(r), at = row * P.splits + split;
-        P.part[at * D + d] = o;
-        if (d == 0) {
-          float *ml = P.part + (size_t)a.batch * a.max_new * H * P.splits * D + 2 * at;
-          ml[0] = m;
-          ml[1] = l;
-        }
+    for (uint32_t w = 0; w < kWarps; ++w) o += red[w * R * VS + i];
+    if (P.splits == 1) {
+      const size_t row = (size_t)(it.first + token(r)) * H + head(r);
+      st_elem(static_cast<T *>(a.out), row * D + d, l == 0.f ? 0.f : o / l * vs);
+      if (a.lse && d == 0) a.lse[row] = l == 0.f ? -INFINITY : m + logf(l);
+    } else {
+      const size_t row = ((size_t)b * a.max_new + token(r)) * H + head(r), at = row * P.splits + split;
+      P.part[at * D + d] = o;
+      if (d == 0) {
+        float *ml = P.part + (size_t)a.batch * a.max_new * H * P.splits * D + 2 * at;
+        ml[0] = m;
+        ml[1] = l;
       }
     }
-    __syncthreads();
   }
 }
 
@@ -302,22 +302,33 @@ uint64_t blocks_unsplit(const PagedArgs &a) {
   return (uint64_t)a.batch * a.n_kv * ((a.max_new * G + R - 1) / R);
 }
 
-// The most shares of a sequence's keys: three blocks a SM (two for 16 rows), and a tile each. (A workspace is for any window.)
-uint32_t splits_most(const PagedArgs &a, uint64_t tiles) {
-  const uint64_t blocks = blocks_unsplit(a), s = ((group_rows(a) == 8 ? 3ull : 2ull) * num_sms() + blocks - 1) / blocks;
-  return (uint32_t)(s < tiles ? s : tiles);
+// Shares of a sequence of `tiles` tiles at most: as many as fill the SMs (three blocks each, two for 16 rows),
+// and up to eight blocks a SM where eight tiles are left to each, so that short sequences' SMs go on with
+// long ones' shares (8 ragged sequences of 5,104 with 8 new tokens: 140 us with the former alone, 78); beyond 32 the
+// join takes more than it saves (a sequence of 8,000 tokens, 8 heads of 64 dims: 57 shares 31 us, 32 26).
+uint32_t splits_for(const PagedArgs &a, uint64_t tiles) {
+  const uint64_t blocks = blocks_unsplit(a), sms = (uint64_t)num_sms();
+  const uint64_t fill = ((group_rows(a) == 8 ? 3 : 2) * sms + blocks - 1) / blocks;
+  uint64_t more = 8 * sms / blocks;
+  if (more > tiles / 8) more = tiles / 8;
+  uint64_t s = fill > more ? fill : more;
+  if (s > 32 && 32 * blocks >= sms) s = 32;
+  if (s > tiles) s = tiles;
+  // (two tiles each where that still makes a block a SM)
+  return (uint32_t)(s * 2 > tiles && blocks * tiles > 2 * sms ? (tiles + 1) / 2 : s);
 }
 
-// Shares: as many, or two tiles each where that still makes a block a SM.
-uint32_t splits_of(const PagedArgs &a) {
+// The most tiles of a sequence.
+uint64_t most_tiles(const PagedArgs &a) {
   const uint32_t tile = tile_of(group_rows(a));
-  uint64_t tiles = 256ull / tile * a.max_blocks;
-  if (a.window) {
-    const uint64_t w = ((uint64_t)a.window + a.max_new) / tile + 2;
-    tiles = w < tiles ? w : tiles;
-  }
-  const uint32_t s = splits_most(a, tiles);
-  return s * 2ull > tiles && blocks_unsplit(a) * tiles > 2ull * num_sms() ? (uint32_t)((tiles + 1) / 2) : s;
+  const uint64_t all = 256ull / tile * a.max_blocks, w = ((uint64_t)a.window + a.max_new) / tile + 2;
+  return a.window && w < all ? w : all;
+}
+
+// What a workspace has room for, whatever the window: at most as many shares as the SMs take.
+uint32_t splits_most(const PagedArgs &a) {
+  const uint64_t blocks = blocks_unsplit(a), s = (8ull * num_sms() + blocks - 1) / blocks, tiles = 256ull / tile_of(group_rows(a)) * a.max_blocks;
+  return (uint32_t)(s < tiles ? s : tiles);
 }
 
 template <typename T, typename KV, int R, int DV>
@@ -326,10 +337,14 @@ cudaError_t launch_r(const PagedArgs &a, cudaStream_t s) {
   P.a = a;
   P.G = a.n_heads / a.n_kv;
   P.groups = (a.max_new * P.G + R - 1) / R;
-  P.splits = splits_of(a);
+  P.splits = splits_for(a, most_tiles(a));
   P.part = reinterpret_cast<float *>(static_cast<uint8_t *>(a.ws) + kWsHead);
   const uint32_t D4 = (a.head_dim + 3) / 4;
-  P.stages = smem_floats(D4, R, 2) * 4 <= kSmemMost ? 2 : 1;
+  // the next tile on its way, unless that leaves one block a SM and without it there are two (4 sequences of
+  // 7,000, 48 rows of 128 dims: 112 us with one, 103 with two)
+  auto per_sm = [&](uint32_t stages) { return kSmemSm / (smem_floats(D4, R, stages) * 4 + kSmemBlock); };
+  P.stages = per_sm(2) >= 2 || per_sm(1) < 2 || blocks_per_sm(R, DV) < 2 ? 2 : 1;
+  if (P.stages == 2 && smem_floats(D4, R, 2) * 4 > kSmemMost) P.stages = 1;
   const size_t smem = smem_floats(D4, R, P.stages) * 4;
   static RaisedLimit smem_set;
   auto *k = paged_attn_kernel<T, KV, R, DV>;
@@ -355,7 +370,7 @@ cudaError_t launch_t(const PagedArgs &a, cudaStream_t s) {
 
 size_t paged_attn_ws_bytes(const PagedArgs &a) {
   if (paged_attn_tc_takes(a)) return kWsHead + paged_attn_tc_ws_bytes(a);
-  const uint32_t S = splits_most(a, 256ull / tile_of(group_rows(a)) * a.max_blocks);
+  const uint32_t S = splits_most(a);
   return kWsHead + (S > 1 ? (size_t)a.batch * a.max_new * a.n_heads * S * (a.head_dim + 2) * 4 : 0);
 }
 

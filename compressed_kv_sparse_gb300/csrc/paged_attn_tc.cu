@@ -668,85 +668,54 @@ __global__ void __launch_bounds__(Cfg<RP, F8>::kThreads, Cfg<RP, F8>::kPerSm)
       uint8_t *dst = s_q + qb * q_bytes;
       // (rows of eights that nothing reads are left as they are)
       const uint32_t most = max(16u, (sg.nr + 7) & ~7u), rows = F8 ? min(most, (uint32_t)RP) : min(most, C::kQRows);
-      // 8 elements of a row, its token and query head given (zeros outside)
-      auto load8 = [&](uint32_t r, uint32_t tok, uint32_t g, uint32_t d) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (r < sg.nr && d < D) {
-          const __nv_bfloat16 *p = q + (sg.first + tok) * a.q_stride + (size_t)(sg.kh * P.G + g) * D + d;
-          if (P.q_vec) {
-            v = __ldg(reinterpret_cast<const uint4 *>(p));
-          } else {
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              w[i] = (uint32_t)__bfloat16_as_ushort(p[2 * i]) | (uint32_t)__bfloat16_as_ushort(p[2 * i + 1]) << 16;
-            v = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        }
-        return v;
-      };
       const uint32_t tok_r0 = by_group(P, sg.r0), g_r0 = sg.r0 - tok_r0 * P.G;
-      // a lane's rows are `step` apart
-      auto advance = [&](uint32_t &tok, uint32_t &g, uint32_t step) {
-        for (g += step; g >= P.G; g -= P.G) ++tok;
-      };
-      auto place = [&](uint32_t r, uint32_t c) {   // 16-byte piece c of row r
+      // 16-byte piece c of row r of the operand. 8-bit rows (hi r, lo RP + r) hold the bf16 row first: a column's
+      // sixteen pieces in the places of its hi and lo.
+      auto place = [&](uint32_t r, uint32_t c) {
         return dst + (c / 8) * C::kQRows * 128u + r * 128u + (((c & 7) ^ (r & 7)) << 4);
       };
-      if constexpr (!F8) {
-        const uint32_t pieces = P.nbox * 8, rpp = 32 / pieces, sub = lane / pieces, c = lane % pieces;
-        uint32_t tok = tok_r0, g = g_r0;
-        advance(tok, g, sub);
-        if (P.q_vec) {   // (all of them on their way at once)
-          const size_t wrap = a.q_stride - (size_t)P.G * D;   // from behind a token's heads to the next token's
-          const __nv_bfloat16 *p = q + (sg.first + tok) * a.q_stride + (size_t)(sg.kh * P.G + g) * D + 8 * c;
-          for (uint32_t r = sub; sub < rpp && r < rows; r += rpp) {
-            const bool in = r < sg.nr && 8 * c < D;
-            cp_async16(place(r, c), in ? p : q, in ? 16u : 0u);
-            p += rpp * D;
-            for (g += rpp; g >= P.G; g -= P.G) p += wrap;
-          }
-          asm volatile("cp.async.wait_all;" ::: "memory");
-        } else if (sub < rpp) {
-          for (uint32_t r0 = sub; r0 < rows; r0 += 8 * rpp) {
-            uint4 v[8];
+      auto raw_place = [&](uint32_t r, uint32_t c) {
+        return F8 ? place(c & 8 ? RP + r : r, (c >> 4) * 8 + (c & 7)) : place(r, c);
+      };
+      {
+        const uint32_t pieces = P.nbox * (F8 ? 16 : 8), rpp = 32 / pieces, sub = lane / pieces, c = lane % pieces;
+        const size_t wrap = a.q_stride - (size_t)P.G * D;   // from behind a token's heads to the next token's
+        uint32_t g = g_r0;
+        const __nv_bfloat16 *p = q + (sg.first + tok_r0) * a.q_stride + (size_t)(sg.kh * P.G + g) * D + 8 * c;
+        auto advance = [&](uint32_t step) {   // a lane's rows are `step` apart
+          p += step * D;
+          for (g += step; g >= P.G; g -= P.G) p += wrap;
+        };
+        advance(sub);
+        for (uint32_t r = sub; sub < rpp && r < rows; r += rpp, advance(rpp)) {
+          const bool in = r < sg.nr && 8 * c < D;   // (zeros outside)
+          if (P.q_vec) {   // (all rows on their way at once)
+            cp_async16(raw_place(r, c), in ? p : q, in ? 16u : 0u);
+          } else {
+            uint32_t w[4] = {0, 0, 0, 0};
+            if (in)
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-              v[u] = load8(r0 + u * rpp, tok, g, 8 * c);
-              advance(tok, g, rpp);
-            }
-#pragma unroll
-            for (int u = 0; u < 8; ++u)
-              if (r0 + u * rpp < rows) *reinterpret_cast<uint4 *>(place(r0 + u * rpp, c)) = v[u];
+              for (int i = 0; i < 4; ++i)
+                w[i] = (uint32_t)__bfloat16_as_ushort(p[2 * i]) | (uint32_t)__bfloat16_as_ushort(p[2 * i + 1]) << 16;
+            *reinterpret_cast<uint4 *>(raw_place(r, c)) = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
-      } else {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+      }
+      if constexpr (F8) {
         // half a warp per row, 16 elements a lane: q 2^k = hi + lo / 16, k so that the largest
-        // entry is in [128, 256); four rows ahead
-        constexpr uint32_t kDeep = 4;
+        // entry is in [128, 256)
         const uint32_t c = lane & 15;
+        const bool in = c < P.nbox * 8;
         const float ks = __ldg(a.k_scale + sg.kh) * P.c2;
-        uint32_t tok = tok_r0, g = g_r0, r1 = lane >> 4;
-        advance(tok, g, r1);
-        uint4 in[kDeep][2];
-#pragma unroll
-        for (uint32_t u = 0; u < kDeep; ++u) {
-          in[u][0] = load8(r1 + 2 * u, tok, g, 16 * c);
-          in[u][1] = load8(r1 + 2 * u, tok, g, 16 * c + 8);
-          advance(tok, g, 2);
-        }
-        for (uint32_t r2 = 0; r2 < rows; r2 += 2, r1 += 2) {   // (both halves go on together)
-          const uint32_t r = r1;
-          const uint32_t w[8] = {in[0][0].x, in[0][0].y, in[0][0].z, in[0][0].w,
-                                 in[0][1].x, in[0][1].y, in[0][1].z, in[0][1].w};
-#pragma unroll
-          for (uint32_t u = 0; u + 1 < kDeep; ++u) {
-            in[u][0] = in[u + 1][0];
-            in[u][1] = in[u + 1][1];
+        __syncwarp();
+        for (uint32_t r = lane >> 4; r < rows; r += 2) {   // (both halves go on together)
+          uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
+          if (in) {
+            x0 = *reinterpret_cast<const uint4 *>(raw_place(r, 2 * c));
+            x1 = *reinterpret_cast<const uint4 *>(raw_place(r, 2 * c + 1));
           }
-          in[kDeep - 1][0] = load8(r + 2 * kDeep, tok, g, 16 * c);
-          in[kDeep - 1][1] = load8(r + 2 * kDeep, tok, g, 16 * c + 8);
-          advance(tok, g, 2);
+          const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
           uint32_t top = 0;
 #pragma unroll
           for (int i = 0; i < 8; ++i) top = max(top, max(w[i] & 0x7fffu, w[i] >> 16 & 0x7fffu));
@@ -771,7 +740,8 @@ __global__ void __launch_bounds__(Cfg<RP, F8>::kThreads, Cfg<RP, F8>::kPerSm)
             hi[i] = h0 | (uint32_t)h1 << 16;
             lo[i] = pack_e4m3(r0.x, r0.y) | (uint32_t)pack_e4m3(s0.x, s0.y) << 16;
           }
-          if (c < P.nbox * 8) {
+          __syncwarp();   // (the row is in registers)
+          if (in) {
             *reinterpret_cast<uint4 *>(place(r, c)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
             *reinterpret_cast<uint4 *>(place(RP + r, c)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
           }
