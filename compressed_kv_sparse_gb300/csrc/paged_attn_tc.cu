@@ -1031,14 +1031,16 @@ __global__ void __launch_bounds__(Cfg<RP, F8>::kThreads, Cfg<RP, F8>::kPerSm)
 }
 
 // Joins the parts of what begins in block blockIdx.x and goes on behind it, each row as the sum of its
-// parts brought to the largest reference, in the order of the blocks. A block takes as many rows at
-// once as it has threads for (512 threads, or fewer blocks of more rows: 0.5 to 3 us more). Every warp works out the weights of the parts for itself, 32 at a time, a lane each.
-constexpr uint32_t kJoinThreads = 256;
-template <int RP, bool F8>
+// parts brought to the largest reference, always in the same order. Two rows at once, four warps
+// each: a warp takes every fourth part, 32 parts on their way at once, and works out the
+// weights of all parts for itself, a lane each.
+constexpr uint32_t kJoinRows = 2, kJoinWarps = 4, kJoinThreads = 32 * kJoinWarps * kJoinRows;
+template <int RP, bool F8, int DV>   // (D <= 128 DV)
 __global__ void __launch_bounds__(kJoinThreads) paged_join_tc_kernel(Params P, uint32_t blocks) {
+  __shared__ float4 s_acc[kJoinRows][kJoinWarps][32 * DV];
   const PagedArgs &a = P.a;
-  const uint32_t c0 = blockIdx.x, D = a.head_dim, wide = (D + 31) & ~31u, at_once = kJoinThreads / wide;
-  const uint32_t d = threadIdx.x % wide, sub = threadIdx.x / wide, lane = threadIdx.x & 31;
+  const uint32_t c0 = blockIdx.x, D = a.head_dim, D4 = D / 4;
+  const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x / 32 % kJoinWarps, sub = threadIdx.x / (32 * kJoinWarps);
   const float2 *ml = reinterpret_cast<const float2 *>(P.sums + (size_t)blocks * 2 * RP * D);
   // piece i: block c0 + i, what goes on (i = 0) or what began before
   auto at = [&](uint32_t i, uint32_t r) { return ((size_t)(c0 + i) * 2 + (i ? 0u : 1u)) * RP + r; };
@@ -1046,40 +1048,69 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_tc_kernel(Params P, u
   pdl_trigger();
   const Part part = P.parts[c0];
   const uint32_t n = part.blocks + 1;   // pieces
-  if (n == 1 || c0 + n > blocks || sub >= at_once) return;
-  for (uint32_t r = blockIdx.y * at_once + sub; r < part.nr; r += gridDim.y * at_once) {
-    const float2 mine = lane < n ? ml[at(lane, r)] : make_float2(-kNoRef, 0.f);
-    float v[8];
+  if (n == 1 || c0 + n > blocks) return;
+  for (uint32_t r0 = blockIdx.y * kJoinRows; r0 < part.nr; r0 += gridDim.y * kJoinRows) {
+    const uint32_t r = min(r0 + sub, part.nr - 1);   // (the last one twice)
+    float2 mine = lane < n ? ml[at(lane, r)] : make_float2(-kNoRef, 0.f);
+    float4 v[8][DV];
+    auto fetch = [&](uint32_t i0) {
 #pragma unroll
-    for (uint32_t u = 0; u < 8; ++u) v[u] = d < D && u < n ? P.sums[at(u, r) * D + d] : 0.f;
+      for (uint32_t u = 0; u < 8; ++u) {
+        const uint32_t i = i0 + warp + kJoinWarps * u;
+#pragma unroll
+        for (uint32_t k = 0; k < DV; ++k)
+          if (i < n && lane + 32 * k < D4) v[u][k] = reinterpret_cast<const float4 *>(P.sums + at(i, r) * D)[lane + 32 * k];
+      }
+    };
+    fetch(0);
     // the largest reference (a NaN if there is one)
     float m = mine.x;
     for (uint32_t i = lane + 32; i < n; i += 32) m = max_nan(m, ml[at(i, r)].x);
 #pragma unroll
     for (int o = 16; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float l = 0.f, acc = 0.f;
+    float l = 0.f;
+    float4 acc[DV];
+#pragma unroll
+    for (int k = 0; k < DV; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
     for (uint32_t i0 = 0; i0 < n; i0 += 32) {
-      const float2 x = i0 == 0 ? mine : i0 + lane < n ? ml[at(i0 + lane, r)] : make_float2(-kNoRef, 0.f);
-      const float w = x.x <= -kNoRef ? 0.f : ex2_approx(x.x - m);
-      l = fmaf(x.y, w, l);
-      for (uint32_t i = i0; i < min(n, i0 + 32); i += 8) {
-        float next[8];   // (the next eight on their way)
+      if (i0) {
+        mine = i0 + lane < n ? ml[at(i0 + lane, r)] : make_float2(-kNoRef, 0.f);
+        fetch(i0);
+      }
+      const float w = mine.x <= -kNoRef ? 0.f : ex2_approx(mine.x - m);
+      l = fmaf(mine.y, w, l);
 #pragma unroll
-        for (uint32_t u = 0; u < 8; ++u) next[u] = d < D && i + 8 + u < n ? P.sums[at(i + 8 + u, r) * D + d] : 0.f;
+      for (uint32_t u = 0; u < 8; ++u) {
+        const uint32_t i = warp + kJoinWarps * u;
+        const float f = __shfl_sync(0xffffffffu, w, i);
+        if (i0 + i < n && f != 0.f)
 #pragma unroll
-        for (uint32_t u = 0; u < 8; ++u) {
-          const float f = __shfl_sync(0xffffffffu, w, (i - i0 + u) & 31);
-          if (i + u < n && f != 0.f) acc = fmaf(v[u], f, acc);
-          v[u] = next[u];
-        }
+          for (int k = 0; k < DV; ++k) {
+            acc[k].x = fmaf(v[u][k].x, f, acc[k].x);
+            acc[k].y = fmaf(v[u][k].y, f, acc[k].y);
+            acc[k].z = fmaf(v[u][k].z, f, acc[k].z);
+            acc[k].w = fmaf(v[u][k].w, f, acc[k].w);
+          }
       }
     }
+#pragma unroll
+    for (int k = 0; k < DV; ++k) s_acc[sub][warp][lane + 32 * k] = acc[k];
+    __syncthreads();
     l = warp_sum(l);
     const uint32_t row = part.r0 + r, tok = by_group(P, row);
     const uint32_t out = (part.first + tok) * a.n_heads + part.kh * P.G + row - tok * P.G;
     const float scale = l == 0.f ? 0.f : (F8 ? __ldg(a.v_scale + part.kh) : 1.f) / l;
-    if (d < D) static_cast<__nv_bfloat16 *>(a.out)[(size_t)out * D + d] = __float2bfloat16_rn(acc * scale);
-    if (a.lse && d == 0) a.lse[out] = l == 0.f ? -INFINITY : (log2f(l) + m) * 0.6931471805599453f;
+    if (r0 + sub < part.nr) {
+      const float *sums = reinterpret_cast<const float *>(s_acc[sub]);
+      for (uint32_t d = warp * 32 + lane; d < D; d += 32 * kJoinWarps) {
+        float o = 0.f;
+#pragma unroll
+        for (uint32_t w = 0; w < kJoinWarps; ++w) o += sums[w * 128 * DV + d];
+        static_cast<__nv_bfloat16 *>(a.out)[(size_t)out * D + d] = __float2bfloat16_rn(o * scale);
+      }
+      if (a.lse && warp == 0 && lane == 0) a.lse[out] = l == 0.f ? -INFINITY : (log2f(l) + m) * 0.6931471805599453f;
+    }
+    __syncthreads();   // (the sums are free)
   }
 }
 
@@ -1149,9 +1180,8 @@ cudaError_t launch_rp(const PagedArgs &a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   note_launches(1);
   if (blocks > 1 && !P.whole) {   // (a lone block holds every segment whole)
-    const uint32_t at_once = kJoinThreads / ((a.head_dim + 31) / 32 * 32), most = RP < 32 ? RP : 32;
-    e = launch_pdl(paged_join_tc_kernel<RP, F8>, dim3(blocks - 1, (most + at_once - 1) / at_once), dim3(kJoinThreads), 0, s,
-                   P, blocks);
+    auto *join = a.head_dim <= 128 ? paged_join_tc_kernel<RP, F8, 1> : paged_join_tc_kernel<RP, F8, 2>;
+    e = launch_pdl(join, dim3(blocks - 1, (RP < 32 ? RP : 32) / kJoinRows), dim3(kJoinThreads), 0, s, P, blocks);
     if (e != cudaSuccess) return e;
     note_launches(1);
   }
