@@ -8,7 +8,9 @@
 // rows), so that a key or value is read from shared memory once for all rows. A sequence's
 // tiles are shared among several blocks where there are few rows; each leaves its sums
 // with their maximum, and a second launch joins them in order.
-// Bound by HBM up to 8 rows, beyond by the fp32 units and shared memory.
+// Up to 8 rows half bound by HBM (8 sequences of 8,000 fp32 tokens, 8 heads of 128 dims, one row each 155 us, 3.4
+// TB/s; 8 rows 164), beyond by the fp32 units and shared memory (128 rows 1,504 us, 22 TFLOP/s); short calls by two
+// launches and a tile's steps (3 of a 1,024-token window 11.9 us).
 #include <cuda_fp8.h>
 
 #include "paged.cuh"
@@ -19,10 +21,11 @@ namespace ds4a {
 namespace {
 
 constexpr uint32_t kThreads = 256, kWarps = kThreads / 32;
-// Keys of a tile: 32 and two or three blocks a SM for 8 rows (8 x 8,000 tokens of 8 heads of 128 dims: 159 us,
-// 64 keys 251); 64 for 16 rows (3 x 1,024 tokens, 10 rows of 80 dims: 13.7 us, 32 keys 15.5).
+// Keys of a tile: 32 for 8 rows (8 x 8,000 tokens of 8 heads of 128 dims: 159 us, 64 keys, of which an SM holds one
+// block, 251); 64 for 16 rows (3 x 1,024 tokens, 10 rows of 80 dims: 13.7 us, 32 keys 15.5).
 __host__ __device__ constexpr uint32_t tile_of(uint32_t R) { return R == 8 ? 32 : 64; }
-// Blocks that an SM's registers have room for (16 rows of 256 dims take 249 a thread).
+// Blocks that an SM's registers have to have room for (16 rows of 256 dims take 249 a thread). Left to itself the
+// compiler takes 137 for 8 rows, and one block a SM needs 208 us for what two do in 155.
 __host__ __device__ constexpr uint32_t blocks_per_sm(int R, int DV) { return R == 16 && DV == 2 ? 1 : 2; }
 constexpr uint32_t kWsHead = 256;   // the status word's line
 constexpr uint32_t kSmemMost = 227 * 1024, kSmemSm = 228 * 1024, kSmemBlock = 1024;

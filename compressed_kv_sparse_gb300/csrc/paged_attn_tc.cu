@@ -22,11 +22,16 @@
 // Work. The tiles of all sequences, key heads and row groups are one list, of which each block
 // takes an even share, whatever the lengths. A part of a (sequence, key head, group) that a block
 // does not hold whole is left as sums with their reference, and a second launch joins
-// the parts in order. Bound by HBM: every visible key and value is read once.
+// the parts in order.
 //
-// Warps: 0 TMA, 1 MMA, 2 the block's list of segments, 3 queries, 4 .. 7 (4 .. 11)
-// softmax and output.
-// Every wait is bounded (tc.cuh).
+// Every visible key and value is read once. Bound by HBM for up to 16 rows in long sequences: 8 of
+// 131,072 tokens of 8 heads of 128 dims, bf16, 8 rows each 605 us (7.1 TB/s); 64 ragged ones up to
+// 32,768 over an 8-bit cache 101 (5.6 TB/s). With more rows by a tile's chain of scores, weights and output
+// product, of which an SM then has one: 16 ragged ones up to 16,384 with 40 rows each 40 us (4.0
+// TB/s). Short calls by some ten steps of 0.3 to 1 us with cold code: a sequence of 4,096 tokens 11 us.
+//
+// Warps: 0 TMA, 1 MMA, 2 the block's list of segments, 3 queries, 4 .. 7 (4 .. 11 from 32 rows on)
+// softmax and output. Every wait is bounded (tc.cuh).
 #include <cuda_fp8.h>
 
 #include "paged.cuh"
@@ -39,7 +44,9 @@ constexpr uint32_t kTile = 128, kBox = kTile * 128;   // keys; bytes of a 128-by
 constexpr uint32_t kSegs = 4, kMaxSlots = 16;
 constexpr uint32_t kSmemSm = 228 * 1024, kSmemBlock = 1024;   // shared memory of an SM; reserved per block
 constexpr uint32_t kLeast = 2;    // places of a share at least: fewer parts to join
-constexpr uint32_t kWholeTiles = 4;   // the most tiles of a sequence that is not divided
+// The most tiles of a sequence that is not divided: no parts and no join (28 sequences of 193 tokens, 2 heads: 11.2 us
+// divided, 8.4; 12 of 419, 8 heads 13.7, 10.8).
+constexpr uint32_t kWholeTiles = 4;
 constexpr float kNoRef = 3e38f;   // -reference of a row that has seen no key
 
 struct Segment {
@@ -79,11 +86,13 @@ struct Cfg {
   // softmax warps: four, which take a quarter of the keys each, or two such sets with every other
   // eight rows each
   static constexpr uint32_t kSets = RP >= 32 ? 2 : 1, kWarps = 4 * kSets, kThreads = 128 + 32 * kWarps;
-  // What a segment costs beside its tiles, in tiles, for even shares: measured, one tile takes
-  // 1.6 us (bf16, D 128) and 0.8 us (8 bits).
+  // What a segment costs beside its tiles, in tiles, for even shares: some 5 us where one block has the SM, in which a
+  // tile takes 1.6 us (bf16, 128 dims) or 0.8 (8 bits); two blocks hide most of it (64 ragged sequences over
+  // 8 bits: 140 us without it, 105 with it).
   static constexpr uint32_t kStart = RP <= 16 ? 1 : F8 ? 6 : 3;
   static constexpr int kRows = RP / kSets;
-  // few rows: two blocks a SM, so that one computes while the other starts, ends or waits
+  // few rows: two blocks a SM, so that one computes while the other starts, ends or waits (152 sequences of
+  // 128 tokens: 46 us with one, 23 with two); 32 rows and more take the shared memory of one
   static constexpr uint32_t kPerSm = RP <= 16 ? 2 : 1;
   static constexpr float kOff = F8 ? 5.f : 0.f;     // weights are 2^(s - m + kOff)
   static constexpr float kTop = F8 ? 8.75f : 8.f;   // ... and at most 2^kTop (448 for 8 bits)

@@ -10,7 +10,9 @@
 // per lane), sums its share of the row (each warp consecutive chunks of 512 tokens, whose sums it
 // keeps), and reads the others' sums through distributed shared memory; the warp in whose part
 // the sum passes the threshold finds the chunk, reads it again (it is in the caches) and finds the token.
-// Bound by HBM for many sequences: a row of p, and one of q where a draft fell, read once.
+// Bound by HBM for many sequences: a row of p, and one of q where a draft fell, read once (256 sequences of 131,072
+// tokens in fp32 39 us, 5.3 TB/s); for a few by the chain of drafts, a row's chunks, the cluster's sums and the second read
+// (8 sequences of 50,021 tokens 6.6 us).
 #include <type_traits>
 
 #include "common.cuh"

@@ -565,8 +565,8 @@ ds4a_status ds4a_rope_table_scaled(int kind, double base, double factor, double 
 /*
  * Rotates the heads of n tokens.
  *  dtype   of x and y (DS4A_F32 or DS4A_BF16)
- *  pos     [n] int32 DEVICE; a token whose position is negative or >= max_pos is skipped (y
- *          stays as it was)
+ *  pos     [n] int32 DEVICE; a token whose position is negative or, where n_rot > 0, >= max_pos
+ *          is skipped (y stays as it was)
  *  x, y    [n][n_heads][D], x_stride and y_stride elements from token to token (>= n_heads *
  *          D; a token's heads are contiguous). Dims that are not rotated are copied. y may be
  *          x with equal strides; it overlaps x in no other way.
