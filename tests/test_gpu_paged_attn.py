@@ -272,3 +272,48 @@ def test_offsets_beyond_32_bits():
     assert torch.equal(pk[blk, :, 5], k[0]) and torch.equal(pv[blk, :, 5], v[0])
 
 
+
+
+@pytest.mark.parametrize("kvd", ["bf16", "e4m3"])
+@pytest.mark.parametrize("D", [16, 64, 80, 128, 144, 256])
+@pytest.mark.parametrize("T,G", [(1, 3), (2, 7), (4, 8), (5, 8), (40, 5)])
+def test_every_row_count_and_width_divided(T, G, D, kvd):
+    """The same with sequences whose tiles several blocks share; groups that start inside a token."""
+    step = Step(lib_(), T * G + D + 1, [1500, 700, 3], [T, max(1, T - 2), T], G, 1, D, "bf16", kvd)
+    c, cu = step.on_gpu()
+    check(step, *run(step, c, cu), 1 / np.sqrt(D))
+
+
+@pytest.mark.parametrize("dtype,kvd", [("bf16", "bf16"), ("bf16", "e4m3"), ("f32", "f32")])
+@pytest.mark.parametrize("window", [1, 128, 378, 381, 384, 500])
+def test_windows_around_the_longest_undivided_sequence(window, dtype, kvd):
+    step = Step(lib_(), window, [1023, 895, 130, 640], [3, 2, 3, 1], 8, 2, 64, dtype, kvd, window=window)
+    c, cu = step.on_gpu()
+    check(step, *run(step, c, cu), 1 / 8)
+
+
+@pytest.mark.parametrize("kvd", ["bf16", "e4m3"])
+def test_more_undivided_sequences_than_blocks(kvd):
+    rng = np.random.default_rng(9)
+    B = 500
+    old, new = rng.integers(0, 500, B), rng.integers(0, 4, B)
+    old[new == 0] = 0
+    step = Step(lib_(), 23, list(old), list(new), 6, 2, 16, "bf16", kvd)
+    c, cu = step.on_gpu()
+    check(step, *run(step, c, cu), 0.25)
+
+
+@pytest.mark.parametrize("old", [[200, 30], [900, 30]])
+@pytest.mark.parametrize("shift", [0, 1])
+@pytest.mark.parametrize("D", [64, 144, 256])
+def test_unaligned_queries_over_8_bits(D, shift, old):
+    """Rows that do not start on 16 bytes give what aligned ones give, bit for bit."""
+    step = Step(lib_(), D + shift, old, [3, 2], 10, 2, D, "bf16", "e4m3")
+    c, cu = step.on_gpu()
+    want = run(step, c, cu)
+    check(step, *want, 1 / np.sqrt(D))
+    wide = torch.zeros(step.n * (10 * D + 3) + 8, dtype=torch.bfloat16, device=DEV)
+    q = wide.as_strided((step.n, 10, D), (10 * D + 3, D, 1), shift)
+    q.copy_(step.q)
+    got = run(step, c, cu, q=q)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
