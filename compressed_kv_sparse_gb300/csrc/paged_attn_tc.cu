@@ -718,43 +718,54 @@ __global__ void __launch_bounds__(Cfg<RP, F8>::kThreads, Cfg<RP, F8>::kPerSm)
         const bool in = c < P.nbox * 8;
         const float ks = __ldg(a.k_scale + sg.kh) * P.c2;
         __syncwarp();
-        for (uint32_t r = lane >> 4; r < rows; r += 2) {   // (both halves go on together)
-          uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
-          if (in) {
-            x0 = *reinterpret_cast<const uint4 *>(raw_place(r, 2 * c));
-            x1 = *reinterpret_cast<const uint4 *>(raw_place(r, 2 * c + 1));
+        for (uint32_t r0 = lane >> 4; r0 < rows; r0 += 4) {   // (both halves go on together, two rows each)
+          uint32_t w[2][8], top[2];
+#pragma unroll
+          for (uint32_t u = 0; u < 2; ++u) {
+            uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
+            if (in) {
+              x0 = *reinterpret_cast<const uint4 *>(raw_place(r0 + 2 * u, 2 * c));
+              x1 = *reinterpret_cast<const uint4 *>(raw_place(r0 + 2 * u, 2 * c + 1));
+            }
+            w[u][0] = x0.x, w[u][1] = x0.y, w[u][2] = x0.z, w[u][3] = x0.w;
+            w[u][4] = x1.x, w[u][5] = x1.y, w[u][6] = x1.z, w[u][7] = x1.w;
+            top[u] = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top[u] = max(top[u], max(w[u][i] & 0x7fffu, w[u][i] >> 16 & 0x7fffu));
           }
-          const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-          uint32_t top = 0;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) top = max(top, max(w[i] & 0x7fffu, w[i] >> 16 & 0x7fffu));
+          for (int o = 8; o > 0; o >>= 1)
 #pragma unroll
-          for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-          // (a row with a NaN or an infinity becomes NaN)
-          const int e = max((int)(top >> 7) - 127, -119);
-          const float up = top >= 0x7f80u ? NAN : __uint_as_float((uint32_t)(127 + 7 - e) << 23);
-          const float down = __uint_as_float((uint32_t)(127 - 7 + min(e, 127)) << 23);
-          uint32_t hi[4], lo[4];
+            for (uint32_t u = 0; u < 2; ++u) top[u] = max(top[u], __shfl_xor_sync(0xffffffffu, top[u], o));
+          __syncwarp();   // (the rows are in registers)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float2 x[2];
+          for (uint32_t u = 0; u < 2; ++u) {
+            const uint32_t r = r0 + 2 * u;
+            // (a row with a NaN or an infinity becomes NaN)
+            const int e = max((int)(top[u] >> 7) - 127, -119);
+            const float up = top[u] >= 0x7f80u ? NAN : __uint_as_float((uint32_t)(127 + 7 - e) << 23);
+            const float down = __uint_as_float((uint32_t)(127 - 7 + min(e, 127)) << 23);
+            uint32_t hi[4], lo[4];
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-              x[k] = mul2(make_float2(__uint_as_float(w[2 * i + k] << 16), __uint_as_float(w[2 * i + k] & 0xffff0000u)),
-                          make_float2(up, up));
-            const uint16_t h0 = pack_e4m3(x[0].x, x[0].y), h1 = pack_e4m3(x[1].x, x[1].y);
-            const float2 f0 = unpack_e4m3(h0), f1 = unpack_e4m3(h1);
-            const float2 r0 = mul2(add2(x[0], make_float2(-f0.x, -f0.y)), make_float2(16.f, 16.f));
-            const float2 s0 = mul2(add2(x[1], make_float2(-f1.x, -f1.y)), make_float2(16.f, 16.f));
-            hi[i] = h0 | (uint32_t)h1 << 16;
-            lo[i] = pack_e4m3(r0.x, r0.y) | (uint32_t)pack_e4m3(s0.x, s0.y) << 16;
+            for (int i = 0; i < 4; ++i) {
+              float2 x[2];
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+                x[k] = mul2(make_float2(__uint_as_float(w[u][2 * i + k] << 16), __uint_as_float(w[u][2 * i + k] & 0xffff0000u)),
+                            make_float2(up, up));
+              const uint16_t h0 = pack_e4m3(x[0].x, x[0].y), h1 = pack_e4m3(x[1].x, x[1].y);
+              const float2 f0 = unpack_e4m3(h0), f1 = unpack_e4m3(h1);
+              const float2 y0 = mul2(add2(x[0], make_float2(-f0.x, -f0.y)), make_float2(16.f, 16.f));
+              const float2 y1 = mul2(add2(x[1], make_float2(-f1.x, -f1.y)), make_float2(16.f, 16.f));
+              hi[i] = h0 | (uint32_t)h1 << 16;
+              lo[i] = pack_e4m3(y0.x, y0.y) | (uint32_t)pack_e4m3(y1.x, y1.y) << 16;
+            }
+            if (in) {
+              *reinterpret_cast<uint4 *>(place(r, c)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+              *reinterpret_cast<uint4 *>(place(RP + r, c)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
+            if (c == 0) S.qs[s % kSegs][r] = down * ks;
           }
-          __syncwarp();   // (the row is in registers)
-          if (in) {
-            *reinterpret_cast<uint4 *>(place(r, c)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4 *>(place(RP + r, c)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          }
-          if (c == 0) S.qs[s % kSegs][r] = down * ks;
         }
       }
       fence_proxy_async();
