@@ -11,8 +11,8 @@
 // keeps), and reads the others' sums through distributed shared memory; the warp in whose part
 // the sum passes the threshold finds the chunk, reads it again (it is in the caches) and finds the token.
 // Bound by HBM for many sequences: a row of p, and one of q where a draft fell, read once (256 sequences of 131,072
-// tokens in fp32 39 us, 5.3 TB/s); for a few by the chain of drafts, a row's chunks, the cluster's sums and the second read
-// (8 sequences of 50,021 tokens 6.6 us).
+// tokens in fp32 38.6 us, 5.4 TB/s); for a few by the chain of drafts, a row's chunks, the cluster's sums and the second read
+// (8 sequences of 50,021 tokens 6.2 us; with the chunk read again in four steps instead of one 6.6).
 #include <type_traits>
 
 #include "common.cuh"
@@ -231,13 +231,17 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(Params P) {
       uint64_t run = before;
       uint32_t i0 = w0;
       for (uint32_t n = 0; run + mine[n] <= thr; ++n, i0 += kChunk) run += mine[n];   // (it is there)
-#pragma unroll 1
-      for (uint32_t i = i0 + 4 * lane;; i += 128) {   // (it is in one of the four)
-        float p[4], q[4];
+      float p[4][4], q[4][4];   // (the whole chunk on its way at once)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        load4<T, VEC>(p[u], p_row, i0 + 128 * u + 4 * lane, w1);
+        if (has_q) load4<T, VEC>(q[u], q_row, i0 + 128 * u + 4 * lane, w1);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {   // (it is in one of the four)
+        const uint32_t i = i0 + 128 * u + 4 * lane;
         uint64_t w[4];
-        load4<T, VEC>(p, p_row, i, w1);
-        if (has_q) load4<T, VEC>(q, q_row, i, w1);
-        weights(w, p, q, has_q, i, drop, scale, hi_unit);
+        weights(w, p[u], q[u], has_q, i, drop, scale, hi_unit);
         const uint64_t four = (w[0] + w[1]) + (w[2] + w[3]);
         uint64_t inc = four;
 #pragma unroll
@@ -246,8 +250,8 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(Params P) {
           if (lane >= (uint32_t)o) inc += y;
         }
         const uint32_t hit = __ballot_sync(0xffffffffu, run + inc > thr);
-        if (hit || i - 4 * lane + 128 >= w1) {
-          if (hit && lane == (uint32_t)__ffs(hit) - 1) {
+        if (hit) {
+          if (lane == (uint32_t)__ffs(hit) - 1) {
             const uint64_t a0 = run + inc - four + w[0], a1 = a0 + w[1], a2 = a1 + w[2];
             const uint32_t k = a0 > thr ? 0u : a1 > thr ? 1u : a2 > thr ? 2u : 3u;
             a.tokens[(size_t)b * (N + 1) + acc] = (int32_t)(i + k);
