@@ -15,6 +15,19 @@ ds4a_status cuda_status(cudaError_t e) { return note_error(e) == cudaSuccess ? D
 bool is_row_type(int dtype) { return dtype == DS4A_F32 || dtype == DS4A_BF16; }
 uint32_t bytes_of(int dtype) { return dtype == DS4A_F32 ? 4u : dtype == DS4A_BF16 ? 2u : 1u; }
 
+// Whether n rows of `row` elements at x and at y, their strides apart, share memory without being the same rows: threads
+// would read what others have written.
+bool rows_clash(const void *x, uint64_t xs, const void *y, uint64_t ys, uint32_t n, uint64_t row, uint32_t es) {
+  typedef unsigned __int128 wide;
+  const wide a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y), last = n - 1u;
+  if (a + (last * xs + row) * es <= b || b + (last * ys + row) * es <= a) return false;
+  if (n == 1) return x != y;
+  if (xs != ys) return true;
+  if (x == y) return false;
+  const wide step = (wide)xs * es, d = (a < b ? b - a : a - b) % step, len = (wide)row * es;
+  return d < len || step - d < len;   // (else: other columns of the same rows)
+}
+
 // `inverse`: the flag is allowed.
 ds4a_status check_rope(const ds4a_rope_spec &r, uint32_t D, bool inverse) {
   if (r.flags & ~(DS4A_ROPE_HALF | (inverse ? DS4A_ROPE_INVERSE : 0u))) return DS4A_ERR_ARG;
@@ -134,7 +147,7 @@ ds4a_status ds4a_rope(const ds4a_rope_spec *rope, int dtype, uint32_t n, const i
   if (x_stride < row || y_stride < row || n > 0x7fffffffu) return DS4A_ERR_SHAPE;
   if (n == 0) return DS4A_OK;
   if (!pos || !x || !y || !aligned(4, {pos}) || !aligned(bytes_of(dtype), {x, y})) return DS4A_ERR_ARG;
-  if (x == y && x_stride != y_stride) return DS4A_ERR_ARG;
+  if ((x == y && x_stride != y_stride) || rows_clash(x, x_stride, y, y_stride, n, row, bytes_of(dtype))) return DS4A_ERR_ARG;
   RopeArgs a = {};
   a.dtype = a.kv_dtype = dtype;
   a.n = n;
@@ -169,6 +182,7 @@ ds4a_status ds4a_kv_append(const ds4a_kv_cache *c, uint32_t n, const int32_t *to
   if (n == 0) return DS4A_OK;
   if (!tok_seq || !tok_pos || !k || !v || !aligned(4, {tok_seq, tok_pos}) || !aligned(es, {k, v, q, q_out}))
     return DS4A_ERR_ARG;
+  if (q && rows_clash(q, q_stride, q_out, q_row, n, q_row, es)) return DS4A_ERR_ARG;
   RopeArgs a = {};
   a.dtype = c->dtype;
   a.kv_dtype = c->kv_dtype;

@@ -571,8 +571,8 @@ ds4a_status ds4a_rope_table_scaled(int kind, double base, double factor, double 
  *          D; a token's heads are contiguous). Dims that are not rotated are copied. y may be
  *          x with equal strides; it overlaps x in no other way.
  *  n_heads 1 .. 1024, D even, <= 512
- * n = 0 does nothing. Errors: DS4A_ERR_ARG (a missing or misaligned pointer, flags, in place
- * with other strides), DS4A_ERR_SHAPE, DS4A_ERR_DTYPE, DS4A_ERR_CUDA.
+ * n = 0 does nothing. Errors: DS4A_ERR_ARG (a missing or misaligned pointer, flags, x and y that
+ * overlap in another way), DS4A_ERR_SHAPE, DS4A_ERR_DTYPE, DS4A_ERR_CUDA.
  */
 ds4a_status ds4a_rope(const ds4a_rope_spec *rope, int dtype, uint32_t n, const int32_t *pos,
                       const void *x, uint64_t x_stride, uint32_t n_heads, uint32_t head_dim,
@@ -618,7 +618,8 @@ typedef struct {
  *               place either one, or a mix of both, remains.
  *  k, v         [n][K][D] (dtype), k_stride and v_stride elements from token to token
  *  q            [n][n_heads][D], q_stride elements; NULL: no queries (then n_heads 0)
- *  q_out        [n][n_heads][D], contiguous; may be q itself when q_stride == n_heads * D
+ *  q_out        [n][n_heads][D], contiguous; may be q itself when q_stride == n_heads * D;
+ *               overlaps q in no other way
  * With DS4A_E4M3 a value x becomes the code nearest x * (1 / scale), the reciprocal rounded to
  * fp32, ties to the even code, values beyond 448 held to 448, NaN kept.
  * n = 0 does nothing. Errors: DS4A_ERR_ARG, DS4A_ERR_SHAPE, DS4A_ERR_DTYPE, DS4A_ERR_CUDA.
@@ -639,7 +640,7 @@ ds4a_status ds4a_kv_append(const ds4a_kv_cache *cache, uint32_t n, const int32_t
  *  n_heads   H, a multiple of K, <= 1024: query head h reads key head h / (H / K)
  *  window    0: every position up to the token's own; W: the last W of them, its own included
  *  scale     of the products, before the softmax
- *  out       [tokens][H][D] (dtype), contiguous
+ *  out       [tokens][H][D] (dtype), contiguous; overlaps no input
  *  lse       [tokens][H] fp32, NULL: not wanted: the natural logarithm of the softmax's sum
  *            (for joining with attention over other keys)
  *  ws        ds4a_paged_attn_ws_bytes bytes on 16; its first 4 bytes count timed-out device

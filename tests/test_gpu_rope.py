@@ -193,3 +193,27 @@ def test_append_leaves_out_what_has_no_place():
     # queries of tokens without a block are rotated; those of skipped tokens stay
     done = (q_out != 9).flatten(1).any(1).tolist()
     assert done == [True, True, True, True, False, False, False, False, False]
+
+
+@pytest.mark.parametrize("swap", [False, True])
+def test_rope_between_columns_of_one_buffer(swap):
+    """Out beside in, in the same rows and behind them; what overlaps is refused."""
+    lib, n, H, D = lib_(), 9, 3, 64
+    rope = make_rope(64, 0, True)
+    pos = torch.arange(n, dtype=torch.int32, device=DEV) * 7
+    wide = torch.randn((2 * n, 2 * H * D + 8), device=DEV)
+    cols = [wide[:n, :H * D].view(n, H, D), wide[:n, H * D:2 * H * D].view(n, H, D)]
+    x, y = cols[::-1] if swap else cols
+    want = torch.empty((n, H, D), device=DEV)
+    lib.ds4a_rope(rope, pos, x, want)
+    lib.ds4a_rope(rope, pos, x, y)
+    assert torch.equal(y, want)
+    below = wide[n:, :H * D].view(n, H, D)
+    lib.ds4a_rope(rope, pos, x, below)
+    assert torch.equal(below, want)
+    before = wide.clone()
+    for other in (wide[1:n + 1, :H * D].view(n, H, D), wide[:n, 8:8 + H * D].view(n, H, D),
+                  wide.view(-1)[:n * H * D].view(n, H, D)):
+        with pytest.raises(lib.Ds4aError):
+            lib.ds4a_rope(rope, pos, cols[0], other)
+    assert torch.equal(wide, before)

@@ -239,3 +239,24 @@ def test_caches(L):
         lib.Rope(n_rot=8, max_pos=4, base=1e4, scaling="dynamic", device="cpu")
     with pytest.raises(lib.Ds4aError):
         lib.Rope(n_rot=7, max_pos=4, base=1e4, device="cpu")
+
+
+def test_overlapping_rows_are_refused(L):
+    """Out and in may be the same rows, or other columns of one buffer (test_gpu_rope.py); else they race."""
+    r, big = spec(), 1 << 20
+
+    def rope(x, xs, y, ys, n=3):   # rows of 512 bf16 elements
+        return L.ds4a_rope(ctypes.byref(r), 1, n, FAKE, x, xs, 4, 128, y, ys, None)
+
+    for x, xs, y, ys in [(big, 512, big + 2, 512), (big, 512, big + 1024, 512), (big, 512, big + 256, 512),
+                         (big + 256, 512, big, 512), (big, 600, big + 1000, 600), (big, 600, big + 1200, 600),
+                         (big, 600, big + 400, 600), (big, 512, big + 1024, 600), (big + 900, 600, big, 512)]:
+        assert rope(x, xs, y, ys) == -1, (x, xs, y, ys)
+    assert rope(big, 512, big + 1022, 512, n=1) == -1 and rope(big + 1022, 512, big, 512, n=1) == -1
+
+
+def test_overlapping_queries_are_refused(L):
+    c, big = cache(), 1 << 20
+    call = lambda q, qs, qo: L.ds4a_kv_append(ctypes.byref(c), 3, FAKE, FAKE, FAKE, 512, FAKE, 512, q, qs, 4, qo, None)  # noqa: E731
+    for q, qs, qo in [(big, 512, big + 2), (big, 1536, big + 1024), (big + 1024, 512, big)]:
+        assert call(q, qs, qo) == -1, (q, qs, qo)
