@@ -26,8 +26,8 @@
 //
 // Every visible key and value is read once. Bound by HBM for up to 16 rows in long sequences: 8 of
 // 131,072 tokens of 8 heads of 128 dims, bf16, 8 rows each 605 us (7.1 TB/s); 64 ragged ones up to
-// 32,768 over an 8-bit cache 101 (5.6 TB/s). With more rows by a tile's chain of scores, weights and output
-// product, of which an SM then has one: 16 ragged ones up to 16,384 with 40 rows each 41 us (3.9
+// 32,768 over an 8-bit cache 97 (5.8 TB/s). With more rows by a tile's chain of scores, weights and output
+// product, of which an SM then has one: 16 ragged ones up to 16,384 with 40 rows each 39 us (4.0
 // TB/s). Short calls by some ten steps of 0.3 to 1 us with cold code: a sequence of 4,096 tokens 11 us.
 //
 // Warps: 0 TMA, 1 MMA, 2 the block's list of segments, 3 queries, 4 .. 7 (4 .. 11 from 32 rows on)
@@ -86,10 +86,10 @@ struct Cfg {
   // softmax warps: four, which take a quarter of the keys each, or two such sets with every other
   // eight rows each
   static constexpr uint32_t kSets = RP >= 32 ? 2 : 1, kWarps = 4 * kSets, kThreads = 128 + 32 * kWarps;
-  // What a segment costs beside its tiles, in tiles, for even shares: some 5 us where one block has the SM, in which a
-  // tile takes 1.6 us (bf16, 128 dims) or 0.8 (8 bits); two blocks hide most of it (64 ragged sequences over
-  // 8 bits: 140 us without it, 105 with it).
-  static constexpr uint32_t kStart = RP <= 16 ? 1 : F8 ? 6 : 3;
+  // What a segment costs beside its tiles, in tiles, for even shares. 64 ragged sequences over 8 bits, 8 rows: 125 us
+  // with 0, 100.6 with 1, 96.6 with 2 or 3; 16 ragged ones with 40 rows: 60 with 1, 48 with 2, 40.6 with 3, 39.3 with 4,
+  // 39.9 with 5, over 8 bits 44.4 with 4, 45.9 with 6, 47.9 with 8.
+  static constexpr uint32_t kStart = RP <= 16 ? 2 : 4;
   static constexpr int kRows = RP / kSets;
   // few rows: two blocks a SM, so that one computes while the other starts, ends or waits (152 sequences of
   // 128 tokens: 46 us with one, 23 with two); 32 rows and more take the shared memory of one
