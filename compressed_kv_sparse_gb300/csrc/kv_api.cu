@@ -108,7 +108,7 @@ ds4a_status ds4a_rope_table_scaled(int kind, double base, double factor, double 
     const double two_pi = 6.283185307179586;
     auto at = [&](double turns) { return n_rot * std::log(orig_len / (two_pi * turns)) / (2.0 * std::log(base)); };
     low = std::fmax(std::floor(at(beta_fast)), 0.0);
-    high = std::fmin(std::ceil(at(beta_slow)), (double)half - 1.0);
+    high = std::fmin(std::ceil(at(beta_slow)), (double)n_rot - 1.0);   // (may lie behind the last pair)
     mag = magnitude > 0.0 ? magnitude : 0.1 * std::log(factor) + 1.0;
   }
   std::vector<double> theta;

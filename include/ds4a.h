@@ -551,9 +551,10 @@ typedef struct {
  *  DS4A_SCALE_NTK     theta_i of the base times factor^(n_rot / (n_rot - 2)); n_rot > 2
  *  DS4A_SCALE_YARN    theta_i (g_i + (1 - g_i) / factor): g_i falls linearly from 1 to 0
  *    between pairs low = max(floor(at(beta_fast)), 0) and high = min(ceil(at(beta_slow)),
- *    n_rot / 2 - 1), at(turns) = n_rot ln(orig_len / (2 pi turns)) / (2 ln base) being the
+ *    n_rot - 1), at(turns) = n_rot ln(orig_len / (2 pi turns)) / (2 ln base) being the
  *    pair that turns so often over orig_len positions (a distance below 0.001 counts as
- *    that). Cosines and sines are multiplied by magnitude; 0 stands for 0.1 ln(factor) + 1.
+ *    that). high may lie behind the last pair, which then keeps a part of its angle. Cosines
+ *    and sines are multiplied by magnitude; 0 stands for 0.1 ln(factor) + 1.
  *    (Peng et al., "YaRN: Efficient Context Window Extension of Large Language Models".)
  * factor >= 1, base > 1. Errors: DS4A_ERR_ARG.
  */

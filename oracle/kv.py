@@ -23,7 +23,7 @@ def theta(n_rot, base, kind="none", factor=1.0, orig_len=0.0, beta_fast=32.0, be
         return th, 1.0
     # pair i turns orig_len * th[i] / (2 pi) times over the trained positions
     at = lambda turns: n_rot / 2 * np.log(orig_len / (2 * np.pi * turns)) / np.log(base)  # noqa: E731
-    low, high = max(np.floor(at(beta_fast)), 0), min(np.ceil(at(beta_slow)), n_rot // 2 - 1)
+    low, high = max(np.floor(at(beta_fast)), 0), min(np.ceil(at(beta_slow)), n_rot - 1)
     keep = 1 - np.clip((i - low) / max(high - low, 0.001), 0, 1)
     return keep * th + (1 - keep) * th / factor, magnitude or 0.1 * np.log(factor) + 1
 
