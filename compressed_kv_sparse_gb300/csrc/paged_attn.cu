@@ -37,6 +37,11 @@ struct Params {
   float *part;                  // [batch * max_new * H][splits][D], then (max, sum) of each
 };
 
+// The weight of a key that a row does not see, or of a share without any that it sees: a zero, told apart from one of
+// a seen key that is too small for fp32.
+constexpr float kUnseen = -0.f;
+__device__ __forceinline__ bool is_unseen(float w) { return __float_as_uint(w) == 0x80000000u; }
+
 template <typename T>
 __device__ __forceinline__ float ld_kv(const T *p, size_t i) {
   return ld_f32(p, i);
@@ -176,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(R, DV)) paged_attn_ker
       float sum = 0.f;
 #pragma unroll
       for (uint32_t i = 0; i < kTile / 32; ++i) {
-        const float e = x[i] == -INFINITY ? 0.f : expf(x[i] - m1);
+        const float e = x[i] == -INFINITY ? kUnseen : expf(x[i] - m1);
         s_p[(lane + 32 * i) * PS + r] = e;
         sum += e;
       }
@@ -213,10 +218,10 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(R, DV)) paged_attn_ker
       for (int i = 0; i < DV; ++i) {
         const uint32_t c = lane + 32 * i;
         const float4 v = c < D4 ? *reinterpret_cast<const float4 *>(vt + k * VS + 4 * c) : make_float4(0.f, 0.f, 0.f, 0.f);
-        // (a key that only some rows see may hold a NaN)
+        // (a key that only some rows see may hold a NaN; a seen one's counts, however small its weight)
 #pragma unroll
         for (int r = 0; r < R; ++r)
-          if (plain || pr[r] != 0.f) {
+          if (plain || !is_unseen(pr[r])) {
             acc[r][i].x = fmaf(pr[r], v.x, acc[r][i].x);
             acc[r][i].y = fmaf(pr[r], v.y, acc[r][i].y);
             acc[r][i].z = fmaf(pr[r], v.z, acc[r][i].z);
@@ -278,7 +283,7 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(Params P) {
   m = __any_sync(0xffffffffu, nan) ? NAN : warp_max(m);
   for (uint32_t s0 = 0; s0 < S; s0 += 32) {
     const float ls = s0 + lane < S ? ml[2 * (s0 + lane) + 1] : 0.f;
-    const float w = ls == 0.f ? 0.f : expf(ml[2 * (s0 + lane)] - m);
+    const float w = ls == 0.f ? kUnseen : expf(ml[2 * (s0 + lane)] - m);
     l = fmaf(ls, w, l);
     for (uint32_t s = s0; s < min(S, s0 + 32); s += 8) {
       float v[8];
@@ -287,7 +292,7 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(Params P) {
 #pragma unroll
       for (uint32_t u = 0; u < 8; ++u) {
         const float f = __shfl_sync(0xffffffffu, w, (s - s0 + u) & 31);
-        if (s + u < S && f != 0.f) acc = fmaf(v[u], f, acc);
+        if (s + u < S && !is_unseen(f)) acc = fmaf(v[u], f, acc);   // (a NaN times 0 is one)
       }
     }
   }

@@ -1193,13 +1193,13 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_tc_kernel(Params P, u
         mine = i0 + lane < n ? ml[at(i0 + lane, r)] : make_float2(-kNoRef, 0.f);
         fetch(i0);
       }
-      const float w = mine.x <= -kNoRef ? 0.f : ex2_approx(mine.x - m);
+      const float w = mine.x <= -kNoRef ? -0.f : ex2_approx(mine.x - m);   // (-0: no key of the part is seen)
       l = fmaf(mine.y, w, l);
 #pragma unroll
       for (uint32_t u = 0; u < 8; ++u) {
         const uint32_t i = warp + kJoinWarps * u;
         const float f = __shfl_sync(0xffffffffu, w, i);
-        if (i0 + i < n && f != 0.f)
+        if (i0 + i < n && __float_as_uint(f) != 0x80000000u)   // (a NaN times 0 is one)
 #pragma unroll
           for (int k = 0; k < DV; ++k) {
             acc[k].x = fmaf(v[u][k].x, f, acc[k].x);

@@ -654,7 +654,7 @@ ds4a_status ds4a_kv_append(const ds4a_kv_cache *cache, uint32_t n, const int32_t
  * Runs on the tensor cores for bf16 layers (D a multiple of 8; of 16 with DS4A_E4M3), on the
  * CUDA cores otherwise, where weights are fp32 too. On the tensor cores a weight keeps 16 bits; with
  * DS4A_E4M3 8, and queries 8, from 2^-13 of a head's largest entry up. Weights there that are too small for
- * 8 bits (2^-10 of the largest weight of 128 neighbouring keys and less) are off by 2^-15 of that weight, or lost where all that a
+ * 8 bits (2^-6 of the largest weight of 128 neighbouring keys and less) are off by 2^-15 of that weight, or lost where all that a
  * token loses is less than 2^-7 of its weights' sum.
  * Errors: DS4A_ERR_ARG, DS4A_ERR_SHAPE, DS4A_ERR_DTYPE, DS4A_ERR_WORKSPACE, DS4A_ERR_CUDA.
  * ds4a_paged_attn_ws_bytes: 0 for sizes that no call takes; with the device of the call
