@@ -79,6 +79,16 @@ __device__ __forceinline__ void weights(uint64_t (&w)[4], const float (&p)[4], c
   }
 }
 
+// floor(u total), exactly, for total below 2^62 and u (held to [0, 1)) = m 2^-e with m below 2^24: a whole number is above
+// u total where it is above this. (In fp64 u total may round up to the running sum next to it.)
+__device__ __forceinline__ uint64_t threshold(float u, uint64_t total) {
+  const uint32_t bits = __float_as_uint(fminf(fmaxf(u, 0.f), 0x1.fffffep-1f));
+  const uint64_t m = bits >> 23 ? (bits & 0x7fffffu) | 0x800000u : bits;
+  const uint32_t e = 150 - max(bits >> 23, 1u);                    // 24 .. 149
+  const uint64_t lo = m * total, hi = __umul64hi(m, total);   // below 2^86
+  return e < 64 ? lo >> e | hi << (64 - e) : e < 128 ? hi >> (e - 64) : 0ull;
+}
+
 __device__ __forceinline__ uint64_t warp_sum64(uint64_t v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -224,8 +234,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(Params P) {
       if (rank == 0 && threadIdx.x == 0) a.tokens[(size_t)b * (N + 1) + acc] = (int32_t)V - 1;
       break;
     }
-    const float u = fminf(fmaxf(__ldg(a.u_sample + b), 0.f), 0x1.fffffep-1f);
-    const uint64_t thr = (uint64_t)((double)u * (double)total);   // below total
+    const uint64_t thr = threshold(__ldg(a.u_sample + b), total);
     if (before <= thr && thr < before + sum) {   // this warp's part (the whole warp)
       __syncwarp();
       uint64_t run = before;
