@@ -28,6 +28,15 @@ bool rows_clash(const void *x, uint64_t xs, const void *y, uint64_t ys, uint32_t
   return d < len || step - d < len;   // (else: other columns of the same rows)
 }
 
+// Whether any of n rows of `row` elements at x, xs apart, shares memory with the `len` contiguous elements at y.
+bool rows_meet(const void *x, uint64_t xs, uint64_t row, uint32_t n, const void *y, uint64_t len, uint32_t es) {
+  typedef unsigned __int128 wide;
+  const wide a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y), end = b + (wide)len * es;
+  const wide step = (wide)xs * es, width = (wide)row * es;
+  const wide i = b < a + width ? 0 : (b - a - width) / step + 1;   // the first row that ends behind y's start
+  return i < n && a + i * step < end;
+}
+
 // `inverse`: the flag is allowed.
 ds4a_status check_rope(const ds4a_rope_spec &r, uint32_t D, bool inverse) {
   if (r.flags & ~(DS4A_ROPE_HALF | (inverse ? DS4A_ROPE_INVERSE : 0u))) return DS4A_ERR_ARG;
@@ -182,7 +191,9 @@ ds4a_status ds4a_kv_append(const ds4a_kv_cache *c, uint32_t n, const int32_t *to
   if (n == 0) return DS4A_OK;
   if (!tok_seq || !tok_pos || !k || !v || !aligned(4, {tok_seq, tok_pos}) || !aligned(es, {k, v, q, q_out}))
     return DS4A_ERR_ARG;
-  if (q && rows_clash(q, q_stride, q_out, q_row, n, q_row, es)) return DS4A_ERR_ARG;
+  if (q && (rows_clash(q, q_stride, q_out, q_row, n, q_row, es) || rows_meet(k, k_stride, kv_row, n, q_out, n * q_row, es) ||
+            rows_meet(v, v_stride, kv_row, n, q_out, n * q_row, es)))
+    return DS4A_ERR_ARG;
   RopeArgs a = {};
   a.dtype = c->dtype;
   a.kv_dtype = c->kv_dtype;

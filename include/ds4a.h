@@ -620,7 +620,8 @@ typedef struct {
  *  k, v         [n][K][D] (dtype), k_stride and v_stride elements from token to token
  *  q            [n][n_heads][D], q_stride elements; NULL: no queries (then n_heads 0)
  *  q_out        [n][n_heads][D], contiguous; may be q itself when q_stride == n_heads * D;
- *               overlaps q in no other way
+ *               overlaps q in no other way, and neither k nor v
+ * No row of k, v and q lies where the call writes in the pools, nor q_out in them (not checked).
  * With DS4A_E4M3 a value x becomes the code nearest x * (1 / scale), the reciprocal rounded to
  * fp32, ties to the even code, values beyond 448 held to 448, NaN kept.
  * n = 0 does nothing. Errors: DS4A_ERR_ARG, DS4A_ERR_SHAPE, DS4A_ERR_DTYPE, DS4A_ERR_CUDA.
@@ -693,7 +694,8 @@ size_t ds4a_paged_attn_ws_bytes(const ds4a_kv_cache *cache, uint32_t max_new, ui
  * u_sample times the sum. For these sums p and q are each rounded to a multiple of 2^-s, s = 45 (62 -
  * ceil(log2 V) beyond 131,072 tokens), and added as whole numbers, so the order of sums changes
  * nothing; probabilities above 1 count as 1, negative ones and NaN as 0. A w that is zero everywhere
- * gives way to p, and a p that is zero everywhere to token V - 1.
+ * gives way to p, and a p that is zero everywhere to token V - 1. No output overlaps an input or another
+ * output (not checked); ctx_out may be seq_pos.
  * Errors: DS4A_ERR_ARG, DS4A_ERR_SHAPE, DS4A_ERR_DTYPE, DS4A_ERR_CUDA.
  */
 ds4a_status ds4a_verify_drafts(int dtype, uint32_t batch, uint32_t max_drafts, uint32_t vocab,
