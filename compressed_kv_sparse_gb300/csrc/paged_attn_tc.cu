@@ -130,7 +130,7 @@ struct Shared {
   alignas(16) float wmax[4][RP];
   alignas(16) uint32_t fine[2][8];   // rows with a weight of 2^kLow or more: of each warp, in this tile and the one before
   uint32_t enough[2][2], settled[2];   // rows whose sum is enough, of each set (halves of 64 rows); whether all are for all tiles
-  uint32_t row_out[RP];              // packed token * H + head of each row
+  uint64_t row_out[RP];              // packed token * H + head of each row (passes 2^32 where steps hold 2^22 tokens)
 };
 
 // Products with 8-bit operands, both E4M3, fp32 sums; from code that the whole warp runs.
@@ -824,7 +824,7 @@ __global__ void __launch_bounds__(Cfg<RP, F8>::kThreads, Cfg<RP, F8>::kPerSm)
       const uint32_t p_first = sg.pos0 + tok_a, p_last = sg.pos0 + by_group(P, sg.r0 + sg.nr - 1);
       if (half == 0 && me < RP) {
         const uint32_t tok = by_group(P, sg.r0 + me);
-        S.row_out[me] = (sg.first + tok) * a.n_heads + sg.kh * P.G + sg.r0 + me - tok * P.G;
+        S.row_out[me] = (uint64_t)(sg.first + tok) * a.n_heads + (sg.kh * P.G + sg.r0 + me - tok * P.G);
       }
       float l[R], nm[R];   // sums of this thread's keys, -references
 #pragma unroll
@@ -1116,7 +1116,7 @@ __global__ void __launch_bounds__(Cfg<RP, F8>::kThreads, Cfg<RP, F8>::kPerSm)
               __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + d;
 #pragma unroll
               for (int i = 0; i < 8; ++i)
-                if (i < nr) out[(size_t)S.row_out[r0 + i] * D] = __float2bfloat16_rn(o[i] * S.fac[r0 + i]);
+                if (i < nr) out[S.row_out[r0 + i] * D] = __float2bfloat16_rn(o[i] * S.fac[r0 + i]);
             } else {
               float *out = sums + (size_t)r0 * D + d;
 #pragma unroll
@@ -1214,7 +1214,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_tc_kernel(Params P, u
     __syncthreads();
     l = warp_sum(l);
     const uint32_t row = part.r0 + r, tok = by_group(P, row);
-    const uint32_t out = (part.first + tok) * a.n_heads + part.kh * P.G + row - tok * P.G;
+    const size_t out = (size_t)(part.first + tok) * a.n_heads + (part.kh * P.G + row - tok * P.G);
     const float scale = l == 0.f ? 0.f : (F8 ? __ldg(a.v_scale + part.kh) : 1.f) / l;
     if (r0 + sub < part.nr) {
       const float *sums = reinterpret_cast<const float *>(s_acc[sub]);
@@ -1222,7 +1222,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_tc_kernel(Params P, u
         float o = 0.f;
 #pragma unroll
         for (uint32_t w = 0; w < kJoinWarps; ++w) o += sums[w * 128 * DV + d];
-        static_cast<__nv_bfloat16 *>(a.out)[(size_t)out * D + d] = __float2bfloat16_rn(o * scale);
+        static_cast<__nv_bfloat16 *>(a.out)[out * D + d] = __float2bfloat16_rn(o * scale);
       }
       if (a.lse && warp == 0 && lane == 0) a.lse[out] = l == 0.f ? -INFINITY : (log2f(l) + m) * 0.6931471805599453f;
     }
