@@ -19,13 +19,13 @@
 // query has 8 significant bits, hi and lo 4 each; the largest entry of a row is brought to 2^7 .. 2^8
 // and lo's step is 2^-13, so only entries below 2^-13 of the largest lose bits. A weight keeps 8 bits
 // too, and below 2^-5 steps of 2^-13: a weight of 2^-14 is lost. So the reference there follows the row's weights
-// down as well as up, by whole powers of two, and the sums, which have fp32's range, are brought along. A row
+// down as well as up, and the sums, which have fp32's range, are brought along. A row
 // whose weights of a tile all fall below 2 is noticed one tile later, and its reference lowered, unless the row's sum
 // is 2 for each tile up to the next power of two: what all these tiles' keys can lose is then 2^-8 of it. Only while some
 // row's sum is not enough are single tiles watched. (A key with 0.95 of the weight before 131,070 others: 0.05 of the
-// output lost with a reference that only rises, 0.001 now. 19 sequences of 8,192 tokens with 1 / 4 / 8 new ones: 58.0 / 76.8 /
-// 110 us, 57.8 / 72.3 / 105 with one that only rises; where scores spread by 5 around their mean, 8 new
-// ones 197 against 139.) Sums are fp32.
+// output lost with a reference that only rises, 0.001 now. 19 sequences of 8,192 tokens with 1 / 4 / 8 new ones: 58.2 / 76.4 /
+// 111 us, 58.0 / 72.6 / 106 with one that only rises; where scores spread by 5 around their mean, 8 new
+// ones 195 against 139.) Sums are fp32.
 //
 // Work. The tiles of all sequences, key heads and row groups are one list, of which each block
 // takes an even share, whatever the lengths. A part of a (sequence, key head, group) that a block
@@ -57,9 +57,9 @@ constexpr uint32_t kLeast = 2;    // places of a share at least: fewer parts to 
 constexpr uint32_t kWholeTiles = 4;
 constexpr float kNoRef = 3e38f;   // -reference of a row that has seen no key
 // 8 bits: a row's reference is lowered where a tile's weights are below 2^kLow, unless its sum is kEnough a tile. The
-// largest weight of the first tile, 2^4.5 or more, is that for kSure tiles. (kEnough 4, kSure 4: 8 new tokens as above 114 us.)
+// largest weight of the first tile, 2^5, is that for kSure tiles. (kEnough 4, kSure 4: 8 new tokens as above 114 us.)
 constexpr float kLow = 1.f, kEnough = 2.f;
-constexpr uint32_t kSure = 8;
+constexpr uint32_t kSure = 16;
 
 struct Segment {
   uint32_t b, kh, r0, nr;          // sequence, key head, first row and rows
@@ -968,7 +968,7 @@ __global__ void __launch_bounds__(Cfg<RP, F8>::kThreads, Cfg<RP, F8>::kPerSm)
             const float was = j ? S.negm[me] : kNoRef;
             float now;
             if constexpr (F8) {
-              const float to = C::kOff - rintf(m), all = kEnough * (float)sg.nt;
+              const float to = C::kOff - m, all = kEnough * (float)sg.nt;
               now = m == -INFINITY ? was : fminf(was, to);
               if (j && m + was < kLow && m != -INFINITY && known < kEnough * (float)min(next_look(j), sg.nt))
                 now = fminf(to, was + ceilf(log2f(all / known)));   // (no lower than is enough for all tiles)
