@@ -8,9 +8,10 @@
 // rows), so that a key or value is read from shared memory once for all rows. A sequence's
 // tiles are shared among several blocks where there are few rows; each leaves its sums
 // with their maximum, and a second launch joins them in order.
-// Up to 8 rows half bound by HBM (8 sequences of 8,000 fp32 tokens, 8 heads of 128 dims, one row each 155 us, 3.4
-// TB/s; 8 rows 164), beyond by the fp32 units and shared memory (128 rows 1,504 us, 22 TFLOP/s); short calls by two
-// launches and a tile's steps (3 of a 1,024-token window 11.9 us).
+// Up to 8 rows half bound by HBM (8 sequences of 8,000 fp32 tokens, 8 heads of 128 dims, one row each 147 us, 3.6
+// TB/s; 8 rows 156), beyond by the fp32 units and shared memory (128 rows 1,501 us, 22 TFLOP/s); short calls by two
+// launches and a tile's steps (3 of a 1,024-token window 11.9 us). Other types than fp32 come one element a load (8 x 8,000
+// tokens, 64 heads over 8 of 100 dims: bf16 454 us, 8 bits 326).
 #include <cuda_fp8.h>
 
 #include "paged.cuh"
@@ -21,11 +22,13 @@ namespace ds4a {
 namespace {
 
 constexpr uint32_t kThreads = 256, kWarps = kThreads / 32;
-// Keys of a tile: 32 for 8 rows (8 x 8,000 tokens of 8 heads of 128 dims: 159 us, 64 keys, of which an SM holds one
-// block, 251); 64 for 16 rows (3 x 1,024 tokens, 10 rows of 80 dims: 13.7 us, 32 keys 15.5).
+// Keys of a tile: 32 for 8 rows (8 x 8,000 tokens of 8 heads of 128 dims: 156 us, 64 keys 159; of 256 dims, where an SM
+// holds one block of 64, 287 and 358); 64 for 16 rows (3 x 1,024 tokens, 10 rows of 80 dims: 11.8 us, 32 keys 15.4).
 __host__ __device__ constexpr uint32_t tile_of(uint32_t R) { return R == 8 ? 32 : 64; }
 // Blocks that an SM's registers have to have room for (16 rows of 256 dims take 249 a thread). Left to itself the
-// compiler takes 137 for 8 rows, and one block a SM needs 208 us for what two do in 155.
+// compiler takes 137 for 8 rows, and one block a SM needs 222 us for what two do in 156. With 8 rows of more than 128
+// dims two blocks cost 70 to 100 bytes of spills a thread, and are faster all the same (8 x 8,000 tokens of 256 dims 287 us,
+// one block without spills 327; bf16 of 250 dims 745 and 1,027).
 __host__ __device__ constexpr uint32_t blocks_per_sm(int R, int DV) { return R == 16 && DV == 2 ? 1 : 2; }
 constexpr uint32_t kWsHead = 256;   // the status word's line
 constexpr uint32_t kSmemMost = 227 * 1024, kSmemSm = 228 * 1024, kSmemBlock = 1024;
@@ -312,8 +315,8 @@ uint64_t blocks_unsplit(const PagedArgs &a) {
 
 // Shares of a sequence of `tiles` tiles at most: as many as fill the SMs (three blocks each, two for 16 rows),
 // and up to eight blocks a SM where eight tiles are left to each, so that short sequences' SMs go on with
-// long ones' shares (8 ragged sequences of 5,104 with 8 new tokens: 140 us with the former alone, 78); beyond 32 the
-// join takes more than it saves (a sequence of 8,000 tokens, 8 heads of 64 dims: 57 shares 31 us, 32 26).
+// long ones' shares (8 ragged sequences of 5,104 with 8 new tokens: 134 us with the former alone, 68); beyond 32 the
+// join takes more than it saves (a sequence of 8,000 tokens, 8 heads of 64 dims: 57 shares 31 us, 32 25).
 uint32_t splits_for(const PagedArgs &a, uint64_t tiles) {
   const uint64_t blocks = blocks_unsplit(a), sms = (uint64_t)num_sms();
   const uint64_t fill = ((group_rows(a) == 8 ? 3 : 2) * sms + blocks - 1) / blocks;
@@ -349,7 +352,7 @@ cudaError_t launch_r(const PagedArgs &a, cudaStream_t s) {
   P.part = reinterpret_cast<float *>(static_cast<uint8_t *>(a.ws) + kWsHead);
   const uint32_t D4 = (a.head_dim + 3) / 4;
   // the next tile on its way, unless that leaves one block a SM and without it there are two (4 sequences of
-  // 7,000, 48 rows of 128 dims: 112 us with one, 103 with two)
+  // 7,000, 48 rows of 128 dims, 2 / 8 heads: 125 / 373 us with one, 120 / 279 with two)
   auto per_sm = [&](uint32_t stages) { return kSmemSm / (smem_floats(D4, R, stages) * 4 + kSmemBlock); };
   P.stages = per_sm(2) >= 2 || per_sm(1) < 2 || blocks_per_sm(R, DV) < 2 ? 2 : 1;
   if (P.stages == 2 && smem_floats(D4, R, 2) * 4 > kSmemMost) P.stages = 1;

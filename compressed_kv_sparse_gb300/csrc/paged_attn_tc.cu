@@ -98,9 +98,9 @@ struct Cfg {
   // softmax warps: four, which take a quarter of the keys each, or two such sets with every other
   // eight rows each
   static constexpr uint32_t kSets = RP >= 32 ? 2 : 1, kWarps = 4 * kSets, kThreads = 128 + 32 * kWarps;
-  // What a segment costs beside its tiles, in tiles, for even shares. 64 ragged sequences over 8 bits, 8 rows: 125 us
-  // with 0, 100.6 with 1, 96.6 with 2 or 3; 16 ragged ones with 40 rows: 60 with 1, 48 with 2, 40.6 with 3, 39.3 with 4,
-  // 39.9 with 5, over 8 bits 44.4 with 4, 45.9 with 6, 47.9 with 8.
+  // What a segment costs beside its tiles, in tiles, for even shares. 64 ragged sequences over 8 bits, 8 rows: 129 us
+  // with 0, 102 with 1, 97 with 2, 96 with 3; 16 ragged ones with 40 rows: 48.4 with 2, 40.9 with 3, 39.3 with 4, 40.0 with
+  // 5, 41.7 with 8, over 8 bits 55.1, 47.2, 47.1, 47.7 and 50.1.
   static constexpr uint32_t kStart = RP <= 16 ? 2 : 4;
   static constexpr int kRows = RP / kSets;
   // few rows: two blocks a SM, so that one computes while the other starts, ends or waits (152 sequences of
@@ -1231,8 +1231,8 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_tc_kernel(Params P, u
 }
 
 // Rows of a group: the fewest that hold a sequence's, up to 64 (19 sequences of 8,192 tokens, 8 heads of 128 dims: 64 rows
-// in groups of 64 / 32 / 16 take 105 / 189 / 193 us in bf16 and 98 / 128 / 135 over 8 bits; 8 rows in groups of 8 / 16 / 32
-// 58 / 58 / 62 over 8 bits, with 128 tokens each 8.3 / 9.7 / 9.5).
+// in groups of 64 / 32 / 16 take 108 / 189 / 192 us in bf16 and 111 / 140 / 145 over 8 bits; 8 rows in groups of 8 / 16 / 32
+// 59 / 60 / 65 over 8 bits, with 128 tokens each 8.7 / 10.2 / 10.0).
 uint32_t rows_of(const PagedArgs &a) {
   const uint32_t r = a.max_new * (a.n_heads / a.n_kv);
   return r <= 8 ? 8 : r <= 16 ? 16 : r <= 32 ? 32 : 64;

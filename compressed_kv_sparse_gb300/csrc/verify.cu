@@ -11,8 +11,8 @@
 // keeps), and reads the others' sums through distributed shared memory; the warp in whose part
 // the sum passes the threshold finds the chunk, reads it again (it is in the caches) and finds the token.
 // Bound by HBM for many sequences: a row of p, and one of q where a draft fell, read once (256 sequences of 131,072
-// tokens in fp32 38.6 us, 5.4 TB/s); for a few by the chain of drafts, a row's chunks, the cluster's sums and the second read
-// (8 sequences of 50,021 tokens 6.2 us; with the chunk read again in four steps instead of one 6.6).
+// tokens in fp32 38.1 us, 5.4 TB/s); for a few by the chain of drafts, a row's chunks, the cluster's sums and the second read
+// (8 sequences of 50,021 tokens 6.1 us; with the chunk read again in four steps instead of one 6.6).
 #include <type_traits>
 
 #include "common.cuh"
@@ -102,8 +102,8 @@ __device__ __forceinline__ uint64_t ld_cluster_u64(uint32_t addr) {
 }
 
 // (Four blocks a SM hide the loads: 256 sequences of 131,072 tokens, three quarters with a draft that fell,
-// take 43 us, with three blocks 55, two 121; with the next chunks on their way in registers or shared
-// memory, which leave room for two or three blocks, 54 to 60.)
+// take 38 us, with registers for three or two blocks a SM 50. Next chunks on their way in registers or shared memory leave
+// room for two or three blocks: 54 to 60 on an earlier version that took 43.)
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads, 4) verify_kernel(Params P) {
   extern __shared__ uint64_t s_chunks[];   // [warp][chunks of a warp]
@@ -285,8 +285,8 @@ cudaError_t launch_verify(const VerifyArgs &a, cudaStream_t s) {
   const uintptr_t all = reinterpret_cast<uintptr_t>(a.target) | reinterpret_cast<uintptr_t>(a.draft_probs);
   const uint32_t es = a.dtype == DS4A_BF16 ? 2 : 4;
   const bool vec = all % (4 * es) == 0 && a.vocab % 4 == 0 && a.target_stride % 4 == 0;
-  // up to eight blocks a sequence while no more than four a SM come of it, which run at once (eight
-  // for every one of 256 sequences: 46 us, two 43)
+  // up to eight blocks a sequence while no more than four a SM come of it, which run at once (256 sequences of 131,072
+  // tokens with eight each 46.6 us, four 40.2, two, as here, 38.1, one 46.6)
   uint32_t cluster = 8;
   while (cluster > 1 && (uint64_t)a.batch * cluster > 4ull * num_sms()) cluster /= 2;
   constexpr uint32_t kStep = kChunk * kWarps;
